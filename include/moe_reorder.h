@@ -79,6 +79,7 @@ typedef int32_t mr_status;
 #define MR_DTYPE_F32   3
 #define MR_DTYPE_INT32 4 /* expert ids of moe_update_expert */
 #define MR_DTYPE_INT64 5
+#define MR_DTYPE_E4M3  6 /* 8-bit rows and weights of the expert products */
 
 /* Sentinel-free limits from the pages' constraint tables. */
 #define MR_MAX_EXPERT_NUM 8192 /* expertNum in (0, 8192] */
@@ -88,6 +89,8 @@ typedef int32_t mr_status;
 #define MR_MAX_UPDATE_BS      512  /* moe_update_expert: BS in (0, 512] */
 #define MR_MAX_UPDATE_K       16   /* K in (0, 16], K <= moeExpertNum */
 #define MR_MAX_UPDATE_EXPERTS 1024 /* moeExpertNum in (0, 1024] */
+#define MR_MAX_EXPERT_ROWS    (1 << 30) /* rows of an expert product */
+#define MR_MAX_EXPERT_COLS    (1 << 24) /* columns of its operands */
 
 /* ------------------------------------------------------------------------ */
 /* FFN-worker batching                                                      */
@@ -469,6 +472,117 @@ mr_status moe_update_expert(const void* expertIds, int32_t idDtype, const int32_
                             void* balancedExpertIds, uint8_t* balancedActiveMask, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Expert products (no counterpart on the pages: what runs between the       */
+/* batching or the permute and the unpermute)                                */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * 8-bit blocks. The expert products take rows and weights as e4m3 values with
+ * fp32 scales: one scale per 128 consecutive values of a row (the row's last
+ * block may be shorter), and one per 128 x 128 block of a weight matrix. A
+ * value stands for its e4m3 value times its scale.
+ *
+ * Operands of the matrix instructions (e4m3 rows given to moe_grouped_matmul
+ * or moe_expert_ffn, and all weights) start on 16 bytes and have row strides
+ * that are multiples of 16 bytes; a length that is not is padded by the stride,
+ * and the padding is never read as values. Every other tensor may start
+ * anywhere its element type may, with any row stride.
+ */
+
+/*
+ * moe_quantize -- rows or weights to 8-bit blocks.
+ *   s = the smallest power of two with max(max |x|, 2^-96) <= 448 s over the
+ *   block, value = e4m3(x / s) to nearest even: dividing by s is exact, so each
+ *   element is rounded once. A block that holds an infinity or a NaN gets
+ *   s = NaN, and all of its values are NaN.
+ *
+ *   x            [batch, rows, cols] of dtype (F16, BF16, F32), device.
+ *   xStrides     host array {batch, row} of element strides, nullable
+ *                (contiguous); a row's elements are adjacent.
+ *   blockRows    1: a scale per row and 128 columns (batch must be 1).
+ *                128: a scale per 128 x 128 block, for weights.
+ *   numRows      device int64 [1], nullable (blockRows 1 only): rows at or past
+ *                it (e.g. the batching's actualTokenNum) are not written.
+ *   values       e4m3 [batch, rows, cols]; valueStrides as xStrides, in bytes.
+ *   scales       float32. blockRows 1: [rows, ceil(cols/128)], scaleStrides =
+ *                host {row, block} element strides, nullable (contiguous).
+ *                blockRows 128: [batch, ceil(rows/128), ceil(cols/128)],
+ *                contiguous (scaleStrides NULL).
+ *   Returns MR_OK, MR_ERR_PARAM_NULLPTR, MR_ERR_PARAM_INVALID or MR_ERR_CUDA.
+ */
+mr_status moe_quantize(const void* x, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                       const int64_t* xStrides, int32_t blockRows, const int64_t* numRows, void* values,
+                       const int64_t* valueStrides, float* scales, const int64_t* scaleStrides,
+                       void* stream);
+
+/*
+ * moe_grouped_matmul_get_workspace_size / moe_grouped_matmul
+ *   y[r, n] = sum_b xs[r, b] ws[e, n/128, b] sum_{k in block b} x[r, k] w[e, n, k]
+ *   for the rows of each group. Sums over the blocks are fp32; the result is
+ *   rounded once to yDtype.
+ *
+ *   x             [rows, cols], row stride xStride elements: E4M3 with xScales,
+ *                 or F16, BF16 or F32 (xScales NULL), which the call quantizes
+ *                 first as moe_quantize does, into the workspace.
+ *   xScales       float32 [rows, ceil(cols/128)]; xScaleStrides = host {row,
+ *                 block} element strides, nullable (contiguous).
+ *   weights       e4m3 [experts, outCols, cols]; weightStrides = host {row,
+ *                 matrix} byte strides, nullable (contiguous).
+ *   weightScales  float32 [experts, ceil(outCols/128), ceil(cols/128)].
+ *   groupList     int64 [numGroups, 2] of (expert, rows), device, 16-byte
+ *                 aligned: the batching's group_list, or one row per expert.
+ *                 Groups are consecutive rows from row 0 on; a count of 0 or
+ *                 less is an empty group, and no group reaches past `rows`.
+ *                 numGroups -1 (groupList unused): one group of all rows with
+ *                 expert 0. The list is read on the device only.
+ *   numRows       device int64 [1], nullable: the rows in use (the batching's
+ *                 actualTokenNum), so that no others are quantized.
+ *   expertBase    subtracted from the list's expert ids: the key of the first
+ *                 matrix of `weights` (layer_id * experts per layer).
+ *   y             [rows, outCols] of yDtype (F16, BF16, F32), row stride yStride
+ *                 elements. Rows of no group, and of a group whose expert is not
+ *                 in `weights`, are not written.
+ *   rows in [0, 2^30], outCols and cols in [1, 2^24], experts in [1, 8192].
+ *   workspace     256-byte aligned; not needed (NULL) for E4M3 rows.
+ *   Returns MR_OK, MR_ERR_PARAM_NULLPTR, MR_ERR_PARAM_INVALID,
+ *   MR_ERR_WORKSPACE or MR_ERR_CUDA.
+ */
+mr_status moe_grouped_matmul_get_workspace_size(int64_t rows, int64_t cols, int32_t xDtype,
+                                                uint64_t* workspaceSize);
+mr_status moe_grouped_matmul(const void* x, int32_t xDtype, int64_t xStride, const float* xScales,
+                             const int64_t* xScaleStrides, const void* weights,
+                             const int64_t* weightStrides, const float* weightScales,
+                             const int64_t* groupList, int64_t numGroups, const int64_t* numRows,
+                             int64_t expertBase, int64_t rows, int64_t experts, int64_t outCols,
+                             int64_t cols, void* y, int32_t yDtype, int64_t yStride, void* workspace,
+                             uint64_t workspaceSize, void* stream);
+
+/*
+ * moe_expert_ffn_get_workspace_size / moe_expert_ffn
+ *   h = silu(x W1^T) * (x W3^T), quantized as moe_quantize does (from fp32),
+ *   y = h W2^T, for the rows of each group. Two products as in
+ *   moe_grouped_matmul; h exists only as 8-bit blocks, in the workspace.
+ *
+ *   w13           e4m3 [experts, 2, inter, hidden]: W1 then W3; w13Strides =
+ *                 host {row, matrix} byte strides, nullable.
+ *   w13Scales     float32 [experts, 2, ceil(inter/128), ceil(hidden/128)].
+ *   w2            e4m3 [experts, hidden, inter]; w2Strides as w13Strides.
+ *   w2Scales      float32 [experts, ceil(hidden/128), ceil(inter/128)].
+ *   y             [rows, hidden] of yDtype.
+ *   The other arguments, limits and errors are moe_grouped_matmul's; the
+ *   workspace is always needed.
+ */
+mr_status moe_expert_ffn_get_workspace_size(int64_t rows, int64_t hidden, int64_t inter,
+                                            uint64_t* workspaceSize);
+mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const float* xScales,
+                         const int64_t* xScaleStrides, const void* w13, const int64_t* w13Strides,
+                         const float* w13Scales, const void* w2, const int64_t* w2Strides,
+                         const float* w2Scales, const int64_t* groupList, int64_t numGroups,
+                         const int64_t* numRows, int64_t expertBase, int64_t rows, int64_t experts,
+                         int64_t hidden, int64_t inter, void* y, int32_t yDtype, int64_t yStride,
+                         void* workspace, uint64_t workspaceSize, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Utilities (no counterpart on the pages)                                  */
 /* ------------------------------------------------------------------------ */
 
@@ -510,6 +624,17 @@ mr_status mr_profile_set_events(void* const* events, int32_t count);
  *   MR_ERR_UNSUPPORTED in a regular build (which has no checks; it writes 0).
  */
 mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, int32_t reset);
+
+/*
+ * mr_waits_out -- blocks of the expert products that gave up a wait.
+ *   Those kernels wait on copies and matrix instructions of their own block;
+ *   every such wait ends after two seconds at the latest. A block whose wait
+ *   ran out leaves its remaining tiles unwritten and is counted here. The count
+ *   stays 0 on a working device. This call synchronises with the device, writes
+ *   the count since the last reset to *count (host pointer), and with
+ *   reset != 0 clears it. Returns MR_OK, MR_ERR_PARAM_NULLPTR or MR_ERR_CUDA.
+ */
+mr_status mr_waits_out(uint32_t* count, int32_t reset);
 
 #ifdef __cplusplus
 }

@@ -43,6 +43,14 @@ SIGNATURES = {
                            _P]),
     "moe_update_expert": (_I32, [_P, _I32, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
                                  _I64, _PI64, _P, _P, _P]),
+    "moe_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _PI64, _I32, _P, _P, _PI64, _P, _PI64, _P]),
+    "moe_grouped_matmul_get_workspace_size": (_I32, [_I64, _I64, _I32, _PU64]),
+    "moe_grouped_matmul": (_I32, [_P, _I32, _I64, _P, _PI64, _P, _PI64, _P, _P, _I64, _P, _I64, _I64,
+                                  _I64, _I64, _I64, _P, _I32, _I64, _P, _U64, _P]),
+    "moe_expert_ffn_get_workspace_size": (_I32, [_I64, _I64, _I64, _PU64]),
+    "moe_expert_ffn": (_I32, [_P, _I32, _I64, _P, _PI64, _P, _PI64, _P, _P, _PI64, _P, _P, _I64, _P,
+                              _I64, _I64, _I64, _I64, _I64, _P, _I32, _I64, _P, _U64, _P]),
+    "mr_waits_out": (_I32, [ctypes.POINTER(_U32), _I32]),
     "mr_status_string": (ctypes.c_char_p, [_I32]),
     "mr_version": (_I32, []),
     "mr_profile_set_events": (_I32, [ctypes.POINTER(_P), _I32]),

@@ -324,6 +324,229 @@ def moe_update_expert(expert_ids, eplb_table, *, local_rank: int = 0, world_size
     return out
 
 
+# ---------------------------------------------------------------------------
+# Expert products
+# ---------------------------------------------------------------------------
+
+DT_E4M3 = 6
+_E4M3 = torch.float8_e4m3fn
+_FLOAT_OR_E4M3 = {**_TORCH_TO_DT, _E4M3: DT_E4M3}
+_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return -(-n // _BLOCK)
+
+
+def _float_dt(name, t, table=None):
+    dt = (table or _TORCH_TO_DT).get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} dtype {t.dtype} is not f16/bf16/f32" + ("/e4m3" if table else ""))
+    return dt
+
+
+def _require_rows(name, t, dims):
+    """A CUDA tensor of `dims` dimensions whose rows have adjacent elements."""
+    _require_cuda(name, t, strided=True)
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have adjacent elements in a row")
+
+
+def _row_stride(t):
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def _matrix_strides(name, t):
+    """{row, matrix} strides of weights [..., rows, cols] with evenly spaced matrices."""
+    row = _row_stride(t)
+    if t.dim() == 4 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+        raise ValueError(f"{name} must have evenly spaced matrices")
+    matrix = t.stride(-3) if t.shape[-3] > 1 else t.shape[-2] * row
+    return row, matrix
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _aligned_rows(rows: int, cols: int, device):
+    """e4m3 [rows, cols] whose rows start on 16 bytes."""
+    return torch.empty((rows, -(-cols // 16) * 16), dtype=_E4M3, device=device)[:, :cols]
+
+
+def quantize_outputs(shape, device, block_rows: int = 1) -> dict:
+    """Allocate the output tensors of one moe_quantize call for x of `shape`:
+    rows start on 16 bytes, as the expert products take them."""
+    *lead, rows, cols = (int(v) for v in shape)
+    wide = -(-cols // 16) * 16
+    values = torch.empty((*lead, rows, wide), dtype=_E4M3, device=device)[..., :cols]
+    return dict(values=values, scales=torch.empty((*lead, rows if block_rows == 1 else _blocks(rows), _blocks(cols)),
+                                                  dtype=torch.float32, device=device))
+
+
+def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = None, stream=None) -> dict:
+    """Quantize x (f16/bf16/f32) to e4m3 blocks on the current stream. Returns
+    values and scales.
+
+    block_rows 1: x [rows, cols], a scale per row and 128 columns. block_rows
+    128: weights x [..., rows, cols], a scale per 128 x 128 block. num_rows
+    (int64 [1] on the device): rows at or past it are not written."""
+    if block_rows not in (1, _BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    _require_rows("x", x, 2 if block_rows == 1 else x.dim())
+    if x.dim() < 2 or x.dim() > 4:
+        raise ValueError("x must have 2 to 4 dimensions")
+    dt = _float_dt("x", x)
+    _require_cuda("num_rows", num_rows, torch.int64)
+    rows, cols = int(x.shape[-2]), int(x.shape[-1])
+    batch = x.numel() // max(1, rows * cols)
+    dev = x.device
+    if out is None:
+        out = quantize_outputs(x.shape, dev, block_rows)
+    values, scales = out["values"], out["scales"]
+    _require_rows("values", values, x.dim())
+    _require_cuda("values", values, _E4M3, strided=True)
+    _require_cuda("scales", scales, torch.float32, strided=block_rows == 1)
+    if values.shape != x.shape or tuple(scales.shape) != (*x.shape[:-2], rows if block_rows == 1 else _blocks(rows),
+                                                          _blocks(cols)):
+        raise ValueError("values and scales must have the shapes of quantize_outputs")
+    _same_device(dev, num_rows=num_rows, values=values, scales=scales)
+    xs = vs = ss = None
+    if x.dim() == 2:
+        xs, vs = (rows * _row_stride(x), _row_stride(x)), (rows * _row_stride(values), _row_stride(values))
+    else:
+        (xr, xm), (vr, vm) = _matrix_strides("x", x), _matrix_strides("values", values)
+        xs, vs = (xm, xr), (vm, vr)
+    if block_rows == 1:
+        ss = int64_array((max(1, scales.stride(0)), max(1, scales.stride(1))))
+    st = lib().moe_quantize(_ptr(x), dt, max(1, batch), rows, cols, int64_array(xs), block_rows, _ptr(num_rows),
+                            _ptr(values), int64_array(vs), _ptr(scales), ss, _stream(stream, dev))
+    _check(st, "moe_quantize")
+    return out
+
+
+def grouped_matmul_workspace_size(rows: int, cols: int, x_dtype: int) -> int:
+    ws = ctypes.c_uint64(0)
+    _check(lib().moe_grouped_matmul_get_workspace_size(rows, cols, x_dtype, ctypes.byref(ws)),
+           "moe_grouped_matmul_get_workspace_size")
+    return int(ws.value)
+
+
+def _expert_rows(x, x_scales, group_list, num_rows):
+    """Checks of the rows and groups that both products take."""
+    _require_rows("x", x, 2)
+    dt = _float_dt("x", x, _FLOAT_OR_E4M3)
+    _require_cuda("group_list", group_list, torch.int64)
+    _require_cuda("num_rows", num_rows, torch.int64)
+    if group_list is not None and (group_list.dim() != 2 or group_list.shape[1] != 2):
+        raise ValueError("group_list must be [groups, 2]")
+    strides = None
+    if dt == DT_E4M3:
+        if x_scales is None:
+            raise ValueError("e4m3 rows need x_scales")
+        _require_cuda("x_scales", x_scales, torch.float32, strided=True)
+        if tuple(x_scales.shape) != (x.shape[0], _blocks(int(x.shape[1]))):
+            raise ValueError("x_scales must be [rows, ceil(cols/128)]")
+        strides = int64_array(x_scales.stride())
+    elif x_scales is not None:
+        raise ValueError("x_scales belong to e4m3 rows")
+    _same_device(x.device, x_scales=x_scales, group_list=group_list, num_rows=num_rows)
+    return dt, strides
+
+
+def _expert_weights(name, w, scales, shape):
+    _require_rows(name, w, len(shape))
+    _require_cuda(name, w, _E4M3, strided=True)
+    _require_cuda(name + "_scales", scales, torch.float32)
+    if tuple(w.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(w.shape)}")
+    want = (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1]))
+    if scales is None or tuple(scales.shape) != want:
+        raise ValueError(f"{name}_scales must be {list(want)}")
+    return int64_array(_matrix_strides(name, w))
+
+
+def _out_rows(out, rows, cols, dtype, dev):
+    if out is None:
+        out = dict(y=torch.empty((rows, cols), dtype=dtype, device=dev))
+    y = out["y"]
+    _require_rows("y", y, 2)
+    if tuple(y.shape) != (rows, cols):
+        raise ValueError(f"y must be [{rows}, {cols}]")
+    return out, y, _float_dt("y", y)
+
+
+def moe_grouped_matmul(x, weights, weight_scales, group_list=None, *, x_scales=None, num_rows=None,
+                       expert_base: int = 0, out_dtype=torch.bfloat16, out: dict | None = None,
+                       workspace=None, stream=None) -> dict:
+    """Product of each group's rows with its expert's e4m3 weights [experts,
+    out_cols, cols] on the current stream. Returns y [rows, out_cols].
+
+    x: e4m3 rows with x_scales, or f16/bf16/f32 rows, which the call quantizes.
+    group_list: int64 [groups, 2] of (expert, rows) on the device (the
+    batching's groupList); None: all rows with expert 0. num_rows: the
+    batching's actualTokenNum. expert_base: the list's id of weights[0]."""
+    dt, xss = _expert_rows(x, x_scales, group_list, num_rows)
+    if weights.dim() != 3 or weights.shape[2] != x.shape[1]:
+        raise ValueError("weights must be [experts, out_cols, cols]")
+    E, N, K = (int(v) for v in weights.shape)
+    rows, dev = int(x.shape[0]), x.device
+    wst = _expert_weights("weights", weights, weight_scales, (E, N, K))
+    out, y, ydt = _out_rows(out, rows, N, out_dtype, dev)
+    _same_device(dev, weights=weights, weight_scales=weight_scales, y=y)
+    if workspace is None and dt != DT_E4M3:
+        workspace = torch.empty(max(grouped_matmul_workspace_size(rows, K, dt), 1), dtype=torch.uint8, device=dev)
+    st = lib().moe_grouped_matmul(
+        _ptr(x), dt, _row_stride(x), _ptr(x_scales), xss, _ptr(weights), wst, _ptr(weight_scales),
+        _ptr(group_list), -1 if group_list is None else int(group_list.shape[0]), _ptr(num_rows),
+        int(expert_base), rows, E, N, K, _ptr(y), ydt, _row_stride(y), _ptr(workspace),
+        0 if workspace is None else int(workspace.numel()), _stream(stream, dev))
+    _check(st, "moe_grouped_matmul")
+    return out
+
+
+def expert_ffn_workspace_size(rows: int, hidden: int, inter: int) -> int:
+    ws = ctypes.c_uint64(0)
+    _check(lib().moe_expert_ffn_get_workspace_size(rows, hidden, inter, ctypes.byref(ws)),
+           "moe_expert_ffn_get_workspace_size")
+    return int(ws.value)
+
+
+def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scales=None, num_rows=None,
+                   expert_base: int = 0, out_dtype=None, out: dict | None = None, workspace=None,
+                   stream=None) -> dict:
+    """The experts' network, y = quantized(silu(x W1^T) * (x W3^T)) W2^T, for
+    each group's rows on the current stream. Returns y [rows, hidden].
+
+    w13: e4m3 [experts, 2, inter, hidden]; w2: e4m3 [experts, hidden, inter].
+    out_dtype: x's by default (bf16 for e4m3 rows). The other arguments are
+    moe_grouped_matmul's."""
+    dt, xss = _expert_rows(x, x_scales, group_list, num_rows)
+    rows, H, dev = int(x.shape[0]), int(x.shape[1]), x.device
+    if w13.dim() != 4 or w13.shape[1] != 2 or w13.shape[3] != H:
+        raise ValueError("w13 must be [experts, 2, inter, hidden]")
+    E, inter = int(w13.shape[0]), int(w13.shape[2])
+    st13 = _expert_weights("w13", w13, w13_scales, (E, 2, inter, H))
+    st2 = _expert_weights("w2", w2, w2_scales, (E, H, inter))
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if dt == DT_E4M3 else x.dtype
+    out, y, ydt = _out_rows(out, rows, H, out_dtype, dev)
+    _same_device(dev, w13=w13, w13_scales=w13_scales, w2=w2, w2_scales=w2_scales, y=y)
+    if workspace is None:
+        workspace = torch.empty(max(expert_ffn_workspace_size(rows, H, inter), 1), dtype=torch.uint8, device=dev)
+    st = lib().moe_expert_ffn(
+        _ptr(x), dt, _row_stride(x), _ptr(x_scales), xss, _ptr(w13), st13, _ptr(w13_scales), _ptr(w2), st2,
+        _ptr(w2_scales), _ptr(group_list), -1 if group_list is None else int(group_list.shape[0]), _ptr(num_rows),
+        int(expert_base), rows, E, H, inter, _ptr(y), ydt, _row_stride(y), _ptr(workspace),
+        int(workspace.numel()), _stream(stream, dev))
+    _check(st, "moe_expert_ffn")
+    return out
+
+
 def profile_set_events(events) -> None:
     """Attach cudaEvents (torch.cuda.Event, created with enable_timing) to the
     library's phase markers for this thread; None to detach."""

@@ -83,6 +83,7 @@ extern "C" const char* mr_status_string(mr_status status) {
 namespace mr {
 cudaError_t mr_check_words_batching(unsigned* out, bool reset);
 cudaError_t mr_check_words_context(unsigned* out, bool reset);
+cudaError_t mr_check_words_grouped_matmul(unsigned* out, bool reset);
 cudaError_t mr_check_words_permute(unsigned* out, bool reset);
 cudaError_t mr_check_words_unpermute(unsigned* out, bool reset);
 cudaError_t mr_check_words_update_expert(unsigned* out, bool reset);
@@ -93,6 +94,7 @@ extern "C" mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, 
 #ifdef MR_CHECKED
     if (!failures) return MR_ERR_PARAM_NULLPTR;
     cudaError_t (*readers[])(unsigned*, bool) = {mr::mr_check_words_batching, mr::mr_check_words_context,
+                                                 mr::mr_check_words_grouped_matmul,
                                                  mr::mr_check_words_permute, mr::mr_check_words_unpermute,
                                                  mr::mr_check_words_update_expert};
     uint32_t total = 0u, first = 0u;
@@ -111,6 +113,22 @@ extern "C" mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, 
     if (firstSite) *firstSite = 0u;
     return MR_ERR_UNSUPPORTED;
 #endif
+}
+
+namespace mr {
+cudaError_t waits_out_grouped_matmul(unsigned* out, bool reset);
+}  // namespace mr
+
+extern "C" mr_status mr_waits_out(uint32_t* count, int32_t reset) {
+    if (!count) return MR_ERR_PARAM_NULLPTR;
+    cudaError_t (*readers[])(unsigned*, bool) = {mr::waits_out_grouped_matmul};
+    *count = 0u;
+    for (auto rd : readers) {
+        unsigned n = 0u;
+        MR_TRY_CUDA(rd(&n, reset != 0));
+        *count += n;
+    }
+    return MR_OK;
 }
 
 extern "C" int32_t mr_version(void) { return 100; }
