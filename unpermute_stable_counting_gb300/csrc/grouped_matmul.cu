@@ -9,17 +9,17 @@
 // e4m3 operands. The scales change every step, so a step's product goes to its
 // own columns of tensor memory (two to four such buffers), and two warpgroups
 // add it to the fp32 sums that they keep in registers, times the scales:
-//   warp 0     TMA loads of the tiles' operands (a ring of stages)
-//   warp 1     matrix instructions
-//   warps 2-3  products of row and weight scales, in shared memory, four
-//              steps at a time
-//   warps 4-11 sums; at the end of a tile the result
+//   warp 0      TMA loads of the tiles' operands (a ring of stages)
+//   warp 1      matrix instructions
+//   warp 2      hands the tiles to the sums
+//   warps 4-11  sums; at the end of a tile the result
 // One persistent block per SM takes tiles round robin; every warp walks the
 // group list for itself (32 groups at a time, one per lane), so there is no
 // scheduling traffic and the host never reads the list.
 #include "tensor.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 namespace mr {
 
@@ -27,8 +27,9 @@ namespace {
 
 __device__ unsigned g_waits_out;  // blocks that left early, see mbar_wait
 
-constexpr int kTileM = 128, kTileK = 128, kScaleBatch = 4, kScaleRing = 3;
-constexpr int kThreads = 384;
+constexpr int kTileM = 128, kTileK = 128;
+constexpr int kThreads = 384, kSumWarps = 8;
+constexpr int kOutBytes = 2048;  // of each summing warp, to turn its rows into whole segments
 
 struct GroupArgs {
     const float* x_scales;     // [r * xs_row + b * xs_block]
@@ -52,39 +53,42 @@ struct Tile {
     int expert, row0, rows, n0;
 };
 
-// Walks the group list. Every lane of the warp calls next() with the same t,
-// ascending over the calls.
-struct Walk {
+// Walks the group list in tiles of TM rows. Every lane of the warp calls next()
+// with the same t, ascending over the calls.
+template <int TM> struct Walk {
     int first, base_tile, total;      // window of 32 groups; tiles before it, tiles in it
-    int64_t base_row, window_rows;
+    int base_row, window_rows;        // rows before it, rows in it
     int expert, count, row0, tiles;   // this lane's group
     int end;                          // inclusive sum of tiles over the window
 
     __device__ __forceinline__ void load(const GroupArgs& a, int lane) {
         const int g = first + lane;
-        int64_t e = 0, c = 0;
+        int64_t e = 0;
+        int c = 0;
         if (g < a.G) {
             if (a.groups) {
                 const longlong2 v = reinterpret_cast<const longlong2*>(a.groups)[g];
                 e = v.x - a.expert_base;
-                c = min(max((int64_t)v.y, (int64_t)0), (int64_t)a.rows);
+                c = (int)min(max((int64_t)v.y, (int64_t)0), (int64_t)a.rows);
             } else {
                 c = a.rows;
             }
         }
-        int64_t sum = c;
+        // rows up to and with this group, at most a.rows (sums of two such values fit 32 bits)
+        int sum = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += up;
+            const int up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum = min(sum + up, a.rows);
         }
+        int before = __shfl_up_sync(0xffffffffu, sum, 1);
+        if (lane == 0) before = 0;
         window_rows = __shfl_sync(0xffffffffu, sum, 31);
-        const int64_t start = min(base_row + sum - c, (int64_t)a.rows);
-        row0 = (int)start;
-        count = (int)min(c, a.rows - start);
-        expert = (int)e;
+        row0 = min(base_row + before, a.rows);
+        count = min(c, a.rows - row0);
         const bool ok = e >= 0 && e < a.experts;
-        tiles = ok ? (count + kTileM - 1) / kTileM * a.n_tiles : 0;
+        expert = ok ? (int)e : 0;
+        tiles = ok ? (count + TM - 1) / TM * a.n_tiles : 0;
         end = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -94,15 +98,14 @@ struct Walk {
         total = __shfl_sync(0xffffffffu, end, 31);
     }
     __device__ __forceinline__ void begin(const GroupArgs& a, int lane) {
-        first = base_tile = 0;
-        base_row = 0;
+        first = base_tile = base_row = 0;
         load(a, lane);
     }
     __device__ __forceinline__ bool next(const GroupArgs& a, int lane, int t, int bn, Tile& out) {
         while (t >= base_tile + total) {
             if (first + 32 >= a.G) return false;
             base_tile += total;
-            base_row = min(base_row + window_rows, (int64_t)a.rows);
+            base_row = min(base_row + window_rows, a.rows);
             first += 32;
             load(a, lane);
         }
@@ -110,265 +113,335 @@ struct Walk {
         const int src = __ffs(__ballot_sync(0xffffffffu, in < end)) - 1;
         const int i = in - __shfl_sync(0xffffffffu, end - tiles, src);
         const int c = __shfl_sync(0xffffffffu, count, src);
-        const int mt = (c + kTileM - 1) / kTileM;
-        const int n = i / mt, m = i - n * mt;  // a weight tile's row tiles side by side: it is read once
+        const int mt = (c + TM - 1) / TM;
+        // Bands of 8 row tiles, column tiles within a band, the band's row tiles side by side: the
+        // tiles in flight share rows and weights through L2.
+        const int band = i / (8 * a.n_tiles);
+        const int bm = min(8, mt - 8 * band);
+        const int j = i - band * 8 * a.n_tiles;
+        const int n = j / bm, m = 8 * band + j - n * bm;
         out.expert = __shfl_sync(0xffffffffu, expert, src);
-        out.row0 = __shfl_sync(0xffffffffu, row0, src) + m * kTileM;
-        out.rows = min(c - m * kTileM, kTileM);
+        out.row0 = __shfl_sync(0xffffffffu, row0, src) + m * TM;
+        out.rows = min(c - m * TM, TM);
         out.n0 = n * bn;
         return true;
     }
 };
 
-template <int BN> struct Cfg {
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+// PAIR: two blocks share a tile of 256 rows. Each loads its own 128 rows and half
+// of the weight columns, and the matrix instructions read both halves.
+template <int BN, bool SWIGLU, bool PAIR> struct Cfg {
+    static constexpr int kLoadN = PAIR ? BN / 2 : BN;                // weight columns this block loads
+    static constexpr int kStages = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 8;
     static constexpr int kBufs = BN == 256 ? 2 : 4;                  // tensor memory buffers
-    static constexpr int kScaleCols = BN == 256 ? 2 : 1;             // scale products per row and step
-    static constexpr int kChunks = BN == 256 ? 2 : 1;                // column chunks per warpgroup
-    static constexpr int kChunk = BN == 256 ? 64 : BN / 2;           // columns of a chunk
-    static constexpr int kStageBytes = (kTileM + BN) * kTileK;
-    static constexpr int kRingFloats = kScaleRing * kScaleBatch * kScaleCols * kTileM;
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kRingFloats * 4 + 2 * 2 * kTileM * 4;
+    static constexpr int kHalves = BN == 256 ? 2 : 1;                // column halves with barriers of their own
+    static constexpr int kHalf = BN / kHalves;
+    static constexpr int kChunks = SWIGLU ? 2 : 1;                   // column chunks per warpgroup
+    static constexpr int kChunk = BN / 2 / kChunks;                  // columns of a chunk
+    static constexpr int kLoad = kChunk < 16 ? kChunk : 16;          // columns per tensor memory load
+    static constexpr int kLoads = kChunks * kChunk / kLoad;
+    static constexpr int kStageBytes = (kTileM + kLoadN) * kTileK;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kSumWarps * kOutBytes;
 };
 
-// 16-bit or fp32 stores of one row's columns [0, CW) from `p`, `left` of them real.
-template <int CW>
-__device__ __forceinline__ void store_row(const float2 (&acc)[CW / 2], void* y, int64_t at, int dt, int vec,
-                                          int left) {
-    if (left <= 0) return;
-    if (dt == MR_DTYPE_F32) {
-        float* p = reinterpret_cast<float*>(y) + at;
-        if (vec && left >= CW) {
+// Stores a warp's 32 rows (lane: row) of U 16-byte pieces, U <= 4, so that the
+// lanes of an instruction write whole segments of a few rows: straight from the
+// registers every lane would write to a row of its own, 32 lines per
+// instruction. `at`: bytes of this lane's row; row_step: bytes from row to row;
+// rows, left: real rows and real bytes of a row; vec: 16-byte stores are aligned.
+template <int U>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4 (&v)[U], uint8_t* row0, int64_t row_step,
+                                           int rows, int64_t left, int elem, bool vec, int lane) {
+    // 64-byte rows, pieces permuted so that eight lanes hit different banks
+    const int key = (lane >> 1) & 3;
 #pragma unroll
-            for (int j = 0; j < CW / 4; ++j)
-                reinterpret_cast<float4*>(p)[j] =
-                    make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+    for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ key) << 4)) = v[u];
+    __syncwarp();
+    constexpr int kRows = 32 / U;  // rows per instruction
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int r = i * kRows + lane / U, u = lane % U;
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+        if (r >= rows || u * 16 >= left) continue;
+        uint8_t* p = row0 + r * row_step + u * 16;
+        if (vec && u * 16 + 16 <= left) {
+            *reinterpret_cast<uint4*>(p) = w;
         } else {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < CW / 2; ++j) {
-                if (2 * j < left) p[2 * j] = acc[j].x;
-                if (2 * j + 1 < left) p[2 * j + 1] = acc[j].y;
+            for (int k = 0; k < 4; ++k) {
+                if (elem == 4) {
+                    if (u * 16 + 4 * k < left) reinterpret_cast<uint32_t*>(p)[k] = x[k];
+                } else {
+                    if (u * 16 + 4 * k < left) reinterpret_cast<uint16_t*>(p)[2 * k] = (uint16_t)(x[k] & 0xFFFFu);
+                    if (u * 16 + 4 * k + 2 < left) reinterpret_cast<uint16_t*>(p)[2 * k + 1] = (uint16_t)(x[k] >> 16);
+                }
             }
+        }
+    }
+    __syncwarp();
+}
+
+template <int DT> __device__ __forceinline__ uint32_t pack2(float2 v) {
+    return (uint32_t)Elem<DT>::from_f32(v.x) | ((uint32_t)Elem<DT>::from_f32(v.y) << 16);
+}
+
+// CW columns of the warp's rows, from `row0` (first row, first column) on.
+template <int CW>
+__device__ __forceinline__ void store_columns(uint8_t* stage, const float2 (&acc)[CW / 2], uint8_t* row0,
+                                              int64_t row_step, int rows, int cols, int dt, bool vec, int lane) {
+    if (dt == MR_DTYPE_F32) {
+        constexpr int F = CW < 16 ? CW : 16;
+#pragma unroll
+        for (int c = 0; c < CW; c += F) {
+            uint4 v[F / 4];
+#pragma unroll
+            for (int u = 0; u < F / 4; ++u)
+                v[u] = make_uint4(__float_as_uint(acc[c / 2 + 2 * u].x), __float_as_uint(acc[c / 2 + 2 * u].y),
+                                  __float_as_uint(acc[c / 2 + 2 * u + 1].x), __float_as_uint(acc[c / 2 + 2 * u + 1].y));
+            store_rows<F / 4>(stage, v, row0 + 4 * c, row_step, rows, 4 * (int64_t)(cols - c), 4, vec, lane);
         }
         return;
     }
-    uint32_t w[CW / 2];
+    constexpr int W = CW < 32 ? CW : 32;
 #pragma unroll
-    for (int j = 0; j < CW / 2; ++j) {
-        uint32_t lo, hi;
-        if (dt == MR_DTYPE_F16) {
-            lo = Elem<MR_DTYPE_F16>::from_f32(acc[j].x), hi = Elem<MR_DTYPE_F16>::from_f32(acc[j].y);
-        } else {
-            lo = Elem<MR_DTYPE_BF16>::from_f32(acc[j].x), hi = Elem<MR_DTYPE_BF16>::from_f32(acc[j].y);
+    for (int c = 0; c < CW; c += W) {
+        uint4 v[W / 8];
+#pragma unroll
+        for (int u = 0; u < W / 8; ++u) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 p = acc[c / 2 + 4 * u + k];
+                x[k] = dt == MR_DTYPE_F16 ? pack2<MR_DTYPE_F16>(p) : pack2<MR_DTYPE_BF16>(p);
+            }
+            v[u] = make_uint4(x[0], x[1], x[2], x[3]);
         }
-        w[j] = lo | (hi << 16);
-    }
-    uint16_t* p = reinterpret_cast<uint16_t*>(y) + at;
-    if (vec && left >= CW) {
-#pragma unroll
-        for (int j = 0; j < CW / 8; ++j)
-            reinterpret_cast<uint4*>(p)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < CW / 2; ++j) {
-            if (2 * j < left) p[2 * j] = (uint16_t)(w[j] & 0xFFFFu);
-            if (2 * j + 1 < left) p[2 * j + 1] = (uint16_t)(w[j] >> 16);
-        }
+        store_rows<W / 8>(stage, v, row0 + 2 * c, row_step, rows, 2 * (int64_t)(cols - c), 2, vec, lane);
     }
 }
 
-template <int BN, bool SWIGLU>
+template <int BN, bool SWIGLU, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                           const GroupArgs a) {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, SWIGLU, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages];
-    __shared__ __align__(8) uint64_t t_full[C::kBufs], t_empty[C::kBufs];
-    __shared__ __align__(8) uint64_t r_full[kScaleRing], r_empty[kScaleRing];
+    __shared__ __align__(8) uint64_t t_full[C::kBufs * C::kHalves], t_empty[C::kBufs * C::kHalves];
+    __shared__ __align__(8) uint64_t i_full[2], i_empty[2];
+    __shared__ Tile info[2];
     __shared__ __align__(8) uint64_t max_bar, drain_bar;
     __shared__ uint32_t tmem_base, abort_word;
+    __shared__ uint32_t row_max[SWIGLU ? 2 : 1][SWIGLU ? 2 : 1][SWIGLU ? kTileM : 1];  // [tile parity][warpgroup][row]
 
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    static_assert(C::kSmem + 512 <= 232448, "shared memory of a block");
-    float* ring = reinterpret_cast<float*>(tiles + C::kStages * C::kStageBytes);
-    uint32_t* row_max = reinterpret_cast<uint32_t*>(ring + C::kRingFloats);  // [tile parity][warpgroup][128]
+    static_assert(C::kSmem + 512 + (SWIGLU ? 4 * kTileM * 4 : 0) <= 232448, "shared memory of a block");
+    uint8_t* out_stage = tiles + C::kStages * C::kStageBytes;
     volatile uint32_t* abort = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) mbar_init(smem_u32(&s_full[i]), 1), mbar_init(smem_u32(&s_empty[i]), 1);
-        for (int i = 0; i < C::kBufs; ++i) mbar_init(smem_u32(&t_full[i]), 1), mbar_init(smem_u32(&t_empty[i]), 8);
-        for (int i = 0; i < kScaleRing; ++i) mbar_init(smem_u32(&r_full[i]), 2), mbar_init(smem_u32(&r_empty[i]), 8);
-        mbar_init(smem_u32(&max_bar), 8);
+        for (int i = 0; i < C::kBufs * C::kHalves; ++i)
+            mbar_init(smem_u32(&t_full[i]), 1), mbar_init(smem_u32(&t_empty[i]), (PAIR ? 2 : 1) * kSumWarps / C::kHalves);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&i_full[i]), 1), mbar_init(smem_u32(&i_empty[i]), kSumWarps);
+        mbar_init(smem_u32(&max_bar), kSumWarps);
         mbar_init(smem_u32(&drain_bar), 1);
         abort_word = 0u;
         mbar_init_fence();
         tma_prefetch(&map_x);
         tma_prefetch(&map_w);
     }
-    if (warp == 1) tmem_alloc(smem_u32(&tmem_base), BN * C::kBufs);
+    if (warp == 1) tmem_alloc<PAIR>(smem_u32(&tmem_base), BN * C::kBufs);
     tc_fence_before();
+    if (PAIR) cluster_sync();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    const uint32_t rank = PAIR ? cluster_rank() : 0u;
+    const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
     pdl_enter();
 
-    Walk walk;
+    Walk<PAIR ? 2 * kTileM : kTileM> walk;
     Tile tile;
     uint32_t it = 0;  // steps that this warp has taken, over all of its tiles
 
     if (warp < 4) {
-        regs_dec<80>();
+        regs_dec<104>();
         if (warp == 0) {
             walk.begin(a, lane);
             bool ok = true;
-            for (int t = blockIdx.x; ok && walk.next(a, lane, t, BN, tile); t += gridDim.x) {
-                const int boxes = (tile.rows + 31) / 32;
-                const uint32_t bytes = (uint32_t)(boxes * 32 + BN) * kTileK;
-                for (int kb = 0; kb < a.KB; ++kb, ++it) {
-                    const uint32_t st = it % C::kStages;
-                    ok = mbar_wait(smem_u32(&s_empty[st]), ((it / C::kStages) & 1) ^ 1, abort);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        const uint32_t bar = smem_u32(&s_full[st]);
+            for (int t = first; ok && walk.next(a, lane, t, BN, tile); t += step) {
+                // every block's boxes of 32 rows; the first block of a pair expects the bytes of both
+                const int all = (tile.rows + 31) / 32;
+                const int boxes = PAIR ? max(0, min(4, all - 4 * (int)rank)) : all;
+                const int row0 = tile.row0 + (int)rank * kTileM;
+                const uint32_t bytes = (uint32_t)(all * 32 + BN) * kTileK;
+                if (elect_one()) {  // one thread for all steps: issuing costs a third of what a branch per step does
+                    for (int kb = 0; kb < a.KB; ++kb, ++it) {
+                        const uint32_t st = it % C::kStages;
+                        ok = mbar_wait<PAIR>(smem_u32(&s_empty[st]), ((it / C::kStages) & 1) ^ 1, abort);
+                        if (!ok) break;
+                        const uint32_t own = smem_u32(&s_full[st]);
+                        const uint32_t bar = PAIR ? map_cluster(own, 0) : own;
                         const uint32_t dst = smem_u32(tiles + st * C::kStageBytes);
-                        mbar_expect(bar, bytes);
-                        if (SWIGLU) {
-                            tma_load_3d(dst + kTileM * kTileK, &map_w, bar, kb * kTileK, tile.n0 / 2, tile.expert * 2);
-                            tma_load_3d(dst + 2 * kTileM * kTileK, &map_w, bar, kb * kTileK, tile.n0 / 2,
-                                        tile.expert * 2 + 1);
+                        if (rank == 0) mbar_expect(own, bytes);
+                        const uint32_t wdst = dst + kTileM * kTileK;
+                        const int k = kb * kTileK, n = SWIGLU ? tile.n0 / 2 : tile.n0;
+                        if (PAIR) {
+                            // halves of 128 columns: 64 of each in this block; the network's: 64 columns
+                            // of the gate in the first block, the same of the other factor in the second
+                            const int plane = SWIGLU ? tile.expert * 2 + (int)rank : tile.expert;
+                            const int n1 = SWIGLU ? n : n + 64 * (int)rank;
+                            tma_load_3d<PAIR>(wdst, &map_w, bar, k, n1, plane);
+                            tma_load_3d<PAIR>(wdst + 64 * kTileK, &map_w, bar, k, n1 + (SWIGLU ? 64 : 128), plane);
+                        } else if (SWIGLU) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                tma_load_3d(wdst + j * 64 * kTileK, &map_w, bar, k, n + (j >> 1) * 64,
+                                            tile.expert * 2 + (j & 1));
                         } else {
-                            tma_load_3d(dst + kTileM * kTileK, &map_w, bar, kb * kTileK, tile.n0, tile.expert);
+                            tma_load_3d(wdst, &map_w, bar, k, n, tile.expert);
                         }
                         for (int j = 0; j < boxes; ++j)
-                            tma_load_2d(dst + j * 32 * kTileK, &map_x, bar, kb * kTileK, tile.row0 + 32 * j);
+                            tma_load_2d<PAIR>(dst + j * 32 * kTileK, &map_x, bar, kb * kTileK, row0 + 32 * j);
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
+                it = __reduce_max_sync(0xffffffffu, it);
+                ok = __all_sync(0xffffffffu, ok);
             }
         } else if (warp == 1) {
             walk.begin(a, lane);
-            bool ok = true;
-            for (int t = blockIdx.x; ok && walk.next(a, lane, t, BN, tile); t += gridDim.x) {
-                for (int kb = 0; kb < a.KB; ++kb, ++it) {
-                    const uint32_t st = it % C::kStages, buf = it % C::kBufs;
-                    ok = mbar_wait(smem_u32(&t_empty[buf]), ((it / C::kBufs) & 1) ^ 1, abort) &&
-                         mbar_wait(smem_u32(&s_full[st]), (it / C::kStages) & 1, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (lane == 0) {
+            bool ok = rank == 0;
+            for (int t = first; ok && walk.next(a, lane, t, BN, tile); t += step) {
+                if (elect_one()) {
+                    for (int kb = 0; kb < a.KB; ++kb, ++it) {
+                        const uint32_t st = it % C::kStages, buf = it % C::kBufs;
                         const uint32_t at = smem_u32(tiles + st * C::kStageBytes);
                         const uint64_t da = smem_desc(at), db = smem_desc(at + kTileM * kTileK);
+                        ok = mbar_wait<PAIR>(smem_u32(&s_full[st]), (it / C::kStages) & 1, abort);
 #pragma unroll
-                        for (int k = 0; k < kTileK / 32; ++k)
-                            mma_e4m3(tmem + buf * BN, da + 2 * k, db + 2 * k, idesc_e4m3(kTileM, BN), k > 0);
-                        tc_commit(smem_u32(&s_empty[st]));
-                        tc_commit(smem_u32(&t_full[buf]));
-                    }
-                    __syncwarp();
-                }
-            }
-        } else {
-            // Products of the scales: this warp's 64 rows, two per lane.
-            walk.begin(a, lane);
-            uint32_t batch = 0;
-            bool ok = true;
-            const int r0 = (warp - 2) * 64 + lane;
-            for (int t = blockIdx.x; ok && walk.next(a, lane, t, BN, tile); t += gridDim.x) {
-                const float* ws[C::kScaleCols];
-                bool real[C::kScaleCols];
+                        for (int h = 0; h < C::kHalves; ++h) {
+                            const uint32_t th = buf * C::kHalves + h;
+                            ok = ok && mbar_wait<PAIR>(smem_u32(&t_empty[th]), ((it / C::kBufs) & 1) ^ 1, abort);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t dh = db + h * (C::kHalf / (PAIR ? 2 : 1) * kTileK / 16);
 #pragma unroll
-                for (int c = 0; c < C::kScaleCols; ++c) {
-                    const int nb = (SWIGLU ? tile.n0 / 2 : tile.n0 + c * 128) / kScaleBlock;
-                    real[c] = nb < a.scale_rows;
-                    const int64_t row = SWIGLU ? ((int64_t)tile.expert * 2 + c) * a.scale_rows + nb
-                                               : (int64_t)tile.expert * a.scale_rows + nb;
-                    ws[c] = a.w_scales + row * a.KB;
-                }
-                const float* xs = a.x_scales + (int64_t)(tile.row0 + r0) * a.xs_row;
-                const bool in0 = r0 < tile.rows, in1 = r0 + 32 < tile.rows;
-                for (int kb = 0; kb < a.KB; kb += kScaleBatch, ++batch) {
-                    float x0[kScaleBatch], x1[kScaleBatch], w[kScaleBatch][C::kScaleCols];
-#pragma unroll
-                    for (int j = 0; j < kScaleBatch; ++j) {
-                        const bool k_in = kb + j < a.KB;
-                        x0[j] = k_in && in0 ? xs[(kb + j) * a.xs_block] : 0.0f;
-                        x1[j] = k_in && in1 ? xs[32 * a.xs_row + (kb + j) * a.xs_block] : 0.0f;
-#pragma unroll
-                        for (int c = 0; c < C::kScaleCols; ++c) w[j][c] = k_in && real[c] ? ws[c][kb + j] : 0.0f;
-                    }
-                    const uint32_t slot = batch % kScaleRing;
-                    ok = mbar_wait(smem_u32(&r_empty[slot]), ((batch / kScaleRing) & 1) ^ 1, abort);
-                    if (!ok) break;
-#pragma unroll
-                    for (int j = 0; j < kScaleBatch; ++j)
-#pragma unroll
-                        for (int c = 0; c < C::kScaleCols; ++c) {
-                            float* dst = ring + ((slot * kScaleBatch + j) * C::kScaleCols + c) * kTileM;
-                            dst[r0] = x0[j] * w[j][c];
-                            dst[r0 + 32] = x1[j] * w[j][c];
+                            for (int k = 0; k < kTileK / 32; ++k)
+                                mma_e4m3<PAIR>(tmem + buf * BN + h * C::kHalf, da + 2 * k, dh + 2 * k,
+                                               idesc_e4m3(PAIR ? 2 * kTileM : kTileM, C::kHalf), k > 0);
+                            if (h == C::kHalves - 1) tc_commit<PAIR>(smem_u32(&s_empty[st]));
+                            tc_commit<PAIR>(smem_u32(&t_full[th]));
                         }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&r_full[slot]));
+                        if (!ok) break;
+                    }
                 }
+                __syncwarp();
+                it = __reduce_max_sync(0xffffffffu, it);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+        } else if (warp == 2) {
+            // tiles for the sums; one of no rows ends them
+            walk.begin(a, lane);
+            uint32_t n = 0;
+            for (int t = first;; t += step, ++n) {
+                const bool more = walk.next(a, lane, t, BN, tile);
+                if (!mbar_wait<PAIR>(smem_u32(&i_empty[n & 1]), ((n >> 1) & 1) ^ 1, abort)) break;
+                if (lane == 0) {
+                    if (!more) tile.rows = 0;
+                    info[n & 1] = tile;
+                    mbar_arrive(smem_u32(&i_full[n & 1]));
+                }
+                if (!more) break;
             }
         }
     } else {
-        regs_inc<208>();
-        walk.begin(a, lane);
+        regs_inc<200>();
         const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes << 16
-        // first column and scale of each chunk
-        int col[C::kChunks], sc[C::kChunks];
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
-            if (BN != 256) col[c] = group * C::kChunk, sc[c] = 0;
-            else if (SWIGLU) col[c] = c * 128 + group * 64, sc[c] = c;
-            else col[c] = group * 128 + c * 64, sc[c] = group;
-        }
-        uint32_t batch = 0, done = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && walk.next(a, lane, t, BN, tile); t += gridDim.x, ++done) {
+        // this warpgroup's half of the columns (narrow tiles: half of the chunk), its two chunks'
+        // weight scales
+        const int half = C::kHalves == 2 ? group : 0;
+        const uint32_t from = lanes + (C::kHalves == 2 ? group * C::kHalf : group * C::kChunk);
+        uint8_t* stage = out_stage + (warp - 4) * kOutBytes;
+        uint32_t done = 0;
+        for (bool ok = true;; ++done) {
+            ok = mbar_wait<PAIR>(smem_u32(&i_full[done & 1]), (done >> 1) & 1, abort);
+            if (!ok) break;
+            tile = info[done & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&i_empty[done & 1]));
+            if (tile.rows == 0) break;
+            // Scales come straight from memory, two steps ahead: through shared memory, whose
+            // bandwidth the operands take, they cost the sums more than the loads do.
+            // Rows and columns past the tile's take its last ones' scales: their sums are not stored.
+            const float* xp =
+                a.x_scales + (int64_t)(tile.row0 + min((int)rank * kTileM + row, tile.rows - 1)) * a.xs_row;
+            const int nb = min(SWIGLU ? tile.n0 / 2 / kScaleBlock : tile.n0 / kScaleBlock + half, a.scale_rows - 1);
+            const float* wp =
+                a.w_scales + ((int64_t)(SWIGLU ? tile.expert * 2 : tile.expert) * a.scale_rows + nb) * a.KB;
+            const int64_t w_other = SWIGLU ? (int64_t)a.scale_rows * a.KB : 0;
+            float xs[2], ws[2][C::kChunks];  // of the next two steps
+            xs[0] = *xp;
+            ws[0][0] = *wp;
+            if (SWIGLU) ws[0][C::kChunks - 1] = wp[w_other];
+            if (a.KB > 1) xp += a.xs_block, ++wp;
+            xs[1] = *xp;
+            ws[1][0] = *wp;
+            if (SWIGLU) ws[1][C::kChunks - 1] = wp[w_other];
             float2 acc[C::kChunks][C::kChunk / 2];
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
                 for (int j = 0; j < C::kChunk / 2; ++j) acc[c][j] = make_float2(0.0f, 0.0f);
+            // (A wait that gives up does not leave this loop, whose sums would then have to be kept in
+            // place at every way out; the tile is dropped after it.)
             for (int kb = 0; kb < a.KB; ++kb, ++it) {
-                const uint32_t buf = it % C::kBufs, slot = batch % kScaleRing;
-                if (kb % kScaleBatch == 0) ok = mbar_wait(smem_u32(&r_full[slot]), (batch / kScaleRing) & 1, abort);
-                ok = ok && mbar_wait(smem_u32(&t_full[buf]), (it / C::kBufs) & 1, abort);
-                if (!ok) break;
+                const uint32_t buf = it % C::kBufs, th = buf * C::kHalves + half;
+                float s[C::kChunks];
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c) s[c] = xs[0] * ws[0][c], ws[0][c] = ws[1][c];
+                xs[0] = xs[1];
+                if (kb + 2 < a.KB) xp += a.xs_block, ++wp;
+                xs[1] = *xp;
+                ws[1][0] = *wp;
+                if (SWIGLU) ws[1][C::kChunks - 1] = wp[w_other];
+                mbar_wait<PAIR>(smem_u32(&t_full[th]), (it / C::kBufs) & 1, abort);
                 tc_fence_after();
-                const float* rs = ring + (slot * kScaleBatch + kb % kScaleBatch) * C::kScaleCols * kTileM + row;
+                // a load in flight while the one before it is added
+                uint32_t v[2][C::kLoad];
+                tmem_load(v[0], from + buf * BN);
 #pragma unroll
-                for (int c = 0; c < C::kChunks; ++c) {
-                    const float s = rs[sc[c] * kTileM];
-                    const float2 s2 = make_float2(s, s);
-#pragma unroll
-                    for (int q = 0; q < C::kChunk / 16; ++q) {
-                        uint32_t v[16];
-                        tmem_ld16(v, lanes + buf * BN + col[c] + 16 * q);
-                        tmem_ld_wait(v);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            acc[c][8 * q + j] = fma2(
-                                make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), s2,
-                                acc[c][8 * q + j]);
+                for (int q = 0; q < C::kLoads; ++q) {
+                    tmem_ld_wait(v[q & 1]);
+                    if (q + 1 < C::kLoads) {
+                        tmem_load(v[(q + 1) & 1], from + buf * BN + (q + 1) * C::kLoad);
+                    } else {
+                        // everything is in registers: hand the buffer back before the last additions
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&t_empty[th]), 0));
+                            else mbar_arrive(smem_u32(&t_empty[th]));
+                        }
                     }
+                    const int c = q * C::kLoad / C::kChunk, base = q * C::kLoad % C::kChunk / 2;
+                    const float2 s2 = make_float2(s[c], s[c]);
+#pragma unroll
+                    for (int j = 0; j < C::kLoad / 2; ++j)
+                        acc[c][base + j] = fma2(make_float2(__uint_as_float(v[q & 1][2 * j]),
+                                                            __uint_as_float(v[q & 1][2 * j + 1])),
+                                                s2, acc[c][base + j]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                const bool last = kb % kScaleBatch == kScaleBatch - 1 || kb == a.KB - 1;
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&t_empty[buf]));
-                    if (last) mbar_arrive(smem_u32(&r_empty[slot]));
-                }
-                batch += last;
             }
-            if (!ok) break;
-            const int64_t r = (int64_t)tile.row0 + row;
+            if (*abort) break;
+            // this warp's rows of the tile
+            const int wrow = (int)rank * kTileM + (warp & 3) * 32;
+            const int wrows = min(32, tile.rows - wrow);
+            const int64_t r = (int64_t)tile.row0 + wrow;
             if (SWIGLU) {
                 // chunk 0 holds the gate's columns, chunk 1 the same columns of the other factor
                 uint32_t m = 0u;
@@ -379,68 +452,101 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = max(m, max(abs_bits(acc[0][j].x), abs_bits(acc[0][j].y)));
                 }
                 // a block of 128 is half in each warpgroup
-                uint32_t* mx = row_max + (done & 1) * 2 * kTileM;
-                mx[group * kTileM + row] = m;
+                uint32_t (*mx)[SWIGLU ? kTileM : 1] = row_max[done & 1];
+                mx[group][row] = m;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&max_bar));
-                ok = mbar_wait(smem_u32(&max_bar), done & 1, abort);
+                ok = mbar_wait<PAIR>(smem_u32(&max_bar), done & 1, abort);
                 if (!ok) break;
-                m = max(m, mx[(group ^ 1) * kTileM + row]);
+                m = max(m, mx[group ^ 1][row]);
                 float s, inv;
                 block_scale(m, &s, &inv);
-                if (row < tile.rows) {
-                    const int n = tile.n0 / 2 + group * 64;
-                    if (group == 0) a.hs[(tile.n0 / 2 / kScaleBlock) * a.hs_block + r] = s;
-                    uint4* dst = reinterpret_cast<uint4*>(a.hq + r * a.hq_stride + n);
+                const int n = tile.n0 / 2 + group * 64;
+                if (group == 0 && lane < wrows) a.hs[(tile.n0 / 2 / kScaleBlock) * a.hs_block + r + lane] = s;
+                uint4 w[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t x[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 p = acc[0][8 * j + 2 * i], q = acc[0][8 * j + 2 * i + 1];
-                            w[i] = e4m3x4(p.x * inv, p.y * inv, q.x * inv, q.y * inv);
-                        }
-                        dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 p = acc[0][8 * j + 2 * i], q = acc[0][8 * j + 2 * i + 1];
+                        x[i] = e4m3x4(p.x * inv, p.y * inv, q.x * inv, q.y * inv);
                     }
+                    w[j] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
-            } else if (row < tile.rows && MR_IN_RANGE(r, a.rows, 901)) {
+                store_rows<4>(stage, w, a.hq + r * a.hq_stride + n, a.hq_stride, wrows, 64, 4, true, lane);
+            } else if (wrows > 0 && MR_IN_RANGE(r + wrows - 1, a.rows, 901)) {
+                const int elem = a.y_dtype == MR_DTYPE_F32 ? 4 : 2;
 #pragma unroll
-                for (int c = 0; c < C::kChunks; ++c)
-                    store_row<C::kChunk>(acc[c], a.y, r * a.y_stride + tile.n0 + col[c], a.y_dtype, a.y_vec,
-                                         a.N - tile.n0 - col[c]);
+                for (int c = 0; c < C::kChunks; ++c) {
+                    const int n = tile.n0 + group * C::kChunks * C::kChunk + c * C::kChunk;
+                    if (n < a.N)
+                        store_columns<C::kChunk>(stage, acc[c],
+                                                 reinterpret_cast<uint8_t*>(a.y) + (r * a.y_stride + n) * elem,
+                                                 a.y_stride * elem, wrows, a.N - n, a.y_dtype, a.y_vec, lane);
+                }
             }
         }
     }
     __syncthreads();
+    if (PAIR) cluster_sync();
     if (abort_word) {  // let what is in flight land
-        if (warp == 0)
+        if (warp == 0 && rank == 0)
             for (uint32_t k = it > C::kStages ? it - C::kStages : 0; k < it; ++k)
                 mbar_drain(smem_u32(&s_full[k % C::kStages]), (k / C::kStages) & 1);
-        if (warp == 1) {
-            if (lane == 0) tc_commit(smem_u32(&drain_bar));
+        if (warp == 1 && rank == 0) {
+            if (elect_one()) tc_commit<PAIR>(smem_u32(&drain_bar));
             mbar_drain(smem_u32(&drain_bar), 0);
         }
         if (threadIdx.x == 0) atomicAdd(&g_waits_out, 1u);
     }
     tc_fence_before();
+    if (PAIR) cluster_sync();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_free(tmem, BN * C::kBufs);
+    if (warp == 1) tmem_free<PAIR>(tmem, BN * C::kBufs);
 }
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <int BN, bool SWIGLU>
+template <int BN, bool SWIGLU, bool PAIR>
 cudaError_t launch_grouped(const CUtensorMap& mx, const CUtensorMap& mw, const GroupArgs& a, int64_t tiles,
                            cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(grouped_matmul_kernel<BN, SWIGLU>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem);
-    if (e != cudaSuccess) return e;
-    const int64_t sms = device_sm_count();
-    return launch_pdl(grouped_matmul_kernel<BN, SWIGLU>, dim3((unsigned)(tiles < sms ? tiles : sms)),
-                      dim3(kThreads), Cfg<BN>::kSmem, s, mx, mw, a);
+    auto kernel = grouped_matmul_kernel<BN, SWIGLU, PAIR>;
+    constexpr int smem = Cfg<BN, SWIGLU, PAIR>::kSmem;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    // blocks (pairs) the device holds at once, found once per device
+    static std::atomic<int> resident[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    int n = resident[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return e;
+        n = device_sm_count();
+        if (PAIR) {
+            cfg.gridDim = dim3(n / 2 * 2);
+            if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+            if (n < 1) return cudaErrorInvalidConfiguration;
+        }
+        resident[dev].store(n, std::memory_order_release);
+    }
+    cfg.gridDim = dim3((unsigned)(tiles < n ? tiles : n) * (PAIR ? 2 : 1));
+    return cudaLaunchKernelEx(&cfg, kernel, mx, mw, a);
 }
 
 // One product over the groups. x: e4m3 rows, w: e4m3 [experts][N][K]; the first
@@ -455,10 +561,13 @@ struct Product {
 };
 
 mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
-    const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, kTileM) + a.G, a.rows);
+    // Pairs of blocks where the groups fill their 256 rows
+    const bool pair = (int64_t)a.rows >= 192 * (int64_t)a.G;
+    const int tile_m = pair ? 2 * kTileM : kTileM;
+    const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G, a.rows);
     const int sms = device_sm_count();
     int bn = 256;
-    if (!p.swiglu) {
+    if (!p.swiglu && !pair) {
         // the widest tile that still gives every SM one (narrower ones read the rows more often)
         while (bn > 32 && m_tiles * ceil_div(a.N, bn) < sms) bn /= 2;
     }
@@ -470,16 +579,18 @@ mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
     const uint32_t xb[2] = {kTileK, 32};
     const uint64_t wd[3] = {(uint64_t)p.K, (uint64_t)a.N, (uint64_t)a.experts * (p.swiglu ? 2 : 1)};
     const uint64_t ws[2] = {(uint64_t)p.w_row, (uint64_t)p.w_matrix};
-    const uint32_t wb[3] = {kTileK, (uint32_t)(p.swiglu ? 128 : bn), 1};
+    const uint32_t wb[3] = {kTileK, (uint32_t)(p.swiglu || pair ? 64 : bn), 1};
     if (!make_tensor_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.x, 2, xd, xs, xb) ||
         !make_tensor_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, 3, wd, ws, wb))
         return MR_ERR_CUDA;
     cudaError_t e;
-    if (p.swiglu) e = launch_grouped<256, true>(mx, mw, a, tiles, s);
-    else if (bn == 256) e = launch_grouped<256, false>(mx, mw, a, tiles, s);
-    else if (bn == 128) e = launch_grouped<128, false>(mx, mw, a, tiles, s);
-    else if (bn == 64) e = launch_grouped<64, false>(mx, mw, a, tiles, s);
-    else e = launch_grouped<32, false>(mx, mw, a, tiles, s);
+    if (pair) e = p.swiglu ? launch_grouped<256, true, true>(mx, mw, a, tiles, s)
+                           : launch_grouped<256, false, true>(mx, mw, a, tiles, s);
+    else if (p.swiglu) e = launch_grouped<256, true, false>(mx, mw, a, tiles, s);
+    else if (bn == 256) e = launch_grouped<256, false, false>(mx, mw, a, tiles, s);
+    else if (bn == 128) e = launch_grouped<128, false, false>(mx, mw, a, tiles, s);
+    else if (bn == 64) e = launch_grouped<64, false, false>(mx, mw, a, tiles, s);
+    else e = launch_grouped<32, false, false>(mx, mw, a, tiles, s);
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
 
