@@ -91,6 +91,12 @@ typedef int32_t mr_status;
 #define MR_MAX_UPDATE_EXPERTS 1024 /* moeExpertNum in (0, 1024] */
 #define MR_MAX_EXPERT_ROWS    (1 << 30) /* rows of an expert product */
 #define MR_MAX_EXPERT_COLS    (1 << 24) /* columns of its operands */
+#define MR_MAX_LAYER_TOKENS   64    /* moe_layer: tokens in [0, 64] */
+#define MR_MAX_LAYER_EXPERTS  1024  /* experts in [1, 1024] */
+#define MR_MAX_LAYER_TOPK     16    /* topK in [1, 16], topK <= experts */
+#define MR_MAX_LAYER_COLS     16384 /* hidden and inter in [1, 16384] */
+#define MR_LAYER_SIGMOID      1u
+#define MR_LAYER_KEEP_WEIGHTS 2u
 
 /* ------------------------------------------------------------------------ */
 /* FFN-worker batching                                                      */
@@ -581,6 +587,48 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
                          const int64_t* numRows, int64_t expertBase, int64_t rows, int64_t experts,
                          int64_t hidden, int64_t inter, void* y, int32_t yDtype, int64_t yStride,
                          void* workspace, uint64_t workspaceSize, void* stream);
+
+/*
+ * moe_layer_get_workspace_size / moe_layer
+ *   A whole mixture-of-experts layer for up to 64 tokens (a decode step), in
+ *   one launch:
+ *     logits[t, e] = sum_k x[t, k] router[e, k]   (fp32)
+ *     each token's topK experts by logit (by score + selectBias[e], if given),
+ *     ties to the lowest expert, a NaN logit below every other;
+ *     weight = score / (sum of the token's taken scores) * routedScale, the
+ *     score softmax(logits[t])[e], or 1 / (1 + exp(-logit)) with
+ *     MR_LAYER_SIGMOID; MR_LAYER_KEEP_WEIGHTS: weight = score * routedScale;
+ *     y[t] = sum over the taken experts, ascending, of weight * ffn_e(x[t]).
+ *   e4m3 weights: ffn_e is moe_expert_ffn's, its quantizations of x and h
+ *   included. 16-bit weights: silu(x W1^T) * (x W3^T) W2^T with fp32 sums, h
+ *   held to at least 16 bits of precision in two 16-bit parts.
+ *
+ *   x             [tokens, hidden] of xDtype (F16, BF16, F32; with 16-bit
+ *                 weights, theirs), row stride xStride elements.
+ *   router        [experts, hidden] of routerDtype (F16, BF16, F32).
+ *   selectBias    float32 [experts], nullable.
+ *   w13, w2       as in moe_expert_ffn, of weightDtype: E4M3 with w13Scales and
+ *                 w2Scales, or F16 / BF16 without (NULL). They start on 16
+ *                 bytes; byte strides are multiples of 16.
+ *   flags         MR_LAYER_SIGMOID, MR_LAYER_KEEP_WEIGHTS.
+ *   y             [tokens, hidden] of xDtype, row stride yStride elements.
+ *   expertIds     int32 [tokens, topK], by descending choice.
+ *   expertWeights float32 [tokens, topK].
+ *   tokens in [0, 64], hidden and inter in [1, 16384], experts in [1, 1024],
+ *   topK in [1, 16], topK <= experts. workspace: 256-byte aligned.
+ *   Returns MR_OK, MR_ERR_PARAM_NULLPTR, MR_ERR_PARAM_INVALID,
+ *   MR_ERR_WORKSPACE, MR_ERR_UNSUPPORTED (the sizes do not fit this device's
+ *   SMs) or MR_ERR_CUDA.
+ */
+mr_status moe_layer_get_workspace_size(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts,
+                                       int64_t topK, int32_t weightDtype, uint64_t* workspaceSize);
+mr_status moe_layer(const void* x, int32_t xDtype, int64_t xStride, const void* router,
+                    int32_t routerDtype, int64_t routerStride, const float* selectBias, const void* w13,
+                    int32_t weightDtype, const int64_t* w13Strides, const float* w13Scales, const void* w2,
+                    const int64_t* w2Strides, const float* w2Scales, int64_t tokens, int64_t hidden,
+                    int64_t inter, int64_t experts, int64_t topK, uint32_t flags, float routedScale,
+                    void* y, int64_t yStride, int32_t* expertIds, float* expertWeights, void* workspace,
+                    uint64_t workspaceSize, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Utilities (no counterpart on the pages)                                  */

@@ -547,6 +547,82 @@ def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scal
     return out
 
 
+MR_LAYER_SIGMOID, MR_LAYER_KEEP_WEIGHTS = 1, 2
+
+
+def layer_workspace_size(tokens: int, hidden: int, inter: int, experts: int, topk: int, weight_dtype: int) -> int:
+    ws = ctypes.c_uint64(0)
+    _check(lib().moe_layer_get_workspace_size(tokens, hidden, inter, experts, topk, weight_dtype, ctypes.byref(ws)),
+           "moe_layer_get_workspace_size")
+    return int(ws.value)
+
+
+def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None, score: str = "softmax",
+              renormalize: bool = True, routed_scale: float = 1.0, select_bias=None, out: dict | None = None,
+              workspace=None, stream=None) -> dict:
+    """A whole mixture-of-experts layer for up to 64 tokens, in one launch on the
+    current stream. Returns y [tokens, hidden], expertIds and expertWeights
+    [tokens, topk].
+
+    router [experts, hidden]; w13 [experts, 2, inter, hidden] and w2 [experts,
+    hidden, inter], e4m3 with their scales or of x's 16-bit dtype. score:
+    "softmax" (over all experts) or "sigmoid"; renormalize: a token's weights
+    sum to routed_scale. select_bias float32 [experts]: experts are chosen by
+    score + select_bias."""
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError("score must be softmax or sigmoid")
+    _require_rows("x", x, 2)
+    _require_rows("router", router, 2)
+    xdt, rdt = _float_dt("x", x), _float_dt("router", router)
+    T, H, dev = int(x.shape[0]), int(x.shape[1]), x.device
+    E = int(router.shape[0])
+    if router.shape[1] != H or w13.dim() != 4 or w13.shape[1] != 2:
+        raise ValueError("router must be [experts, hidden], w13 [experts, 2, inter, hidden]")
+    inter = int(w13.shape[2])
+    if w13.dtype == _E4M3:
+        wdt = DT_E4M3
+        st13 = _expert_weights("w13", w13, w13_scales, (E, 2, inter, H))
+        st2 = _expert_weights("w2", w2, w2_scales, (E, H, inter))
+    else:
+        wdt = _float_dt("w13", w13)
+        if w13.dtype != x.dtype or w2.dtype != x.dtype:
+            raise TypeError("16-bit weights must have x's dtype")
+        if w13_scales is not None or w2_scales is not None:
+            raise ValueError("scales belong to e4m3 weights")
+        _require_rows("w13", w13, 4)
+        _require_rows("w2", w2, 3)
+        if tuple(w13.shape) != (E, 2, inter, H) or tuple(w2.shape) != (E, H, inter):
+            raise ValueError("w13 must be [experts, 2, inter, hidden], w2 [experts, hidden, inter]")
+        size = w13.element_size()
+        st13 = int64_array([size * v for v in _matrix_strides("w13", w13)])
+        st2 = int64_array([size * v for v in _matrix_strides("w2", w2)])
+    _require_cuda("select_bias", select_bias, torch.float32)
+    if select_bias is not None and tuple(select_bias.shape) != (E,):
+        raise ValueError("select_bias must be [experts]")
+    if out is None:
+        out = dict(y=torch.empty((T, H), dtype=x.dtype, device=dev),
+                   expertIds=torch.empty((T, topk), dtype=torch.int32, device=dev),
+                   expertWeights=torch.empty((T, topk), dtype=torch.float32, device=dev))
+    y, ids, weights = out["y"], out["expertIds"], out["expertWeights"]
+    _require_rows("y", y, 2)
+    _require_cuda("y", y, x.dtype, strided=True)
+    _require_cuda("expertIds", ids, torch.int32)
+    _require_cuda("expertWeights", weights, torch.float32)
+    if tuple(y.shape) != (T, H) or tuple(ids.shape) != (T, topk) or tuple(weights.shape) != (T, topk):
+        raise ValueError("y must be [tokens, hidden], expertIds and expertWeights [tokens, topk]")
+    _same_device(dev, router=router, w13=w13, w2=w2, w13_scales=w13_scales, w2_scales=w2_scales,
+                 select_bias=select_bias, y=y, expertIds=ids, expertWeights=weights)
+    if workspace is None:
+        workspace = torch.empty(max(layer_workspace_size(T, H, inter, E, topk, wdt), 1), dtype=torch.uint8, device=dev)
+    flags = (MR_LAYER_SIGMOID if score == "sigmoid" else 0) | (0 if renormalize else MR_LAYER_KEEP_WEIGHTS)
+    st = lib().moe_layer(_ptr(x), xdt, _row_stride(x), _ptr(router), rdt, _row_stride(router), _ptr(select_bias),
+                         _ptr(w13), wdt, st13, _ptr(w13_scales), _ptr(w2), st2, _ptr(w2_scales), T, H, inter, E,
+                         int(topk), flags, float(routed_scale), _ptr(y), _row_stride(y), _ptr(ids), _ptr(weights),
+                         _ptr(workspace), int(workspace.numel()), _stream(stream, dev))
+    _check(st, "moe_layer")
+    return out
+
+
 def profile_set_events(events) -> None:
     """Attach cudaEvents (torch.cuda.Event, created with enable_timing) to the
     library's phase markers for this thread; None to detach."""

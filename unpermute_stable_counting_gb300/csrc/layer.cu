@@ -1,0 +1,1023 @@
+// A whole mixture-of-experts layer for a few tokens in one launch:
+//   logits = x R^T; the top-k experts of each token and their weights;
+//   y[t] = sum over its experts e of weight * (silu(x W1e^T) * (x W3e^T)) W2e^T
+// with e4m3 weights in blocks (rows quantized as moe_expert_ffn does) or
+// 16-bit weights.
+//
+// With few tokens the time is that of reading the taken experts' weights once,
+// so the weights are the wide operand: their rows fill the 128 lanes of the
+// tcgen05 instructions, and the tokens are the columns (16 to 64). One
+// cooperative grid of a block per SM runs three steps, a grid barrier between:
+//   1. logits (a block per few experts and tokens, its warps along k), and the
+//      rows of x as the second step's operand
+//   2. every block finds all tokens' experts for itself, and takes an equal
+//      share of the taken experts' W1/W3 rows, 8 rows at a time: rows of
+//      several experts share an instruction, since all of them meet all tokens,
+//      and a token keeps the products of its own experts
+//   3. every block takes an equal share of the rows of y and reads those rows
+//      of every taken expert's W2; a block so holds its rows' whole sum, and no
+//      sum crosses blocks
+// Equal shares matter more than whole tiles: with 8 experts of 2048 rows on
+// 152 SMs, tiles of 128 rows would leave one SM in six idle.
+// Copies run through a ring of TMA stages (one thread), instructions are
+// issued by one thread, and two warpgroups take the results out of tensor
+// memory. The first stages of step 3 are requested before its barrier.
+#include "tensor.cuh"
+
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <atomic>
+
+namespace mr {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+__device__ unsigned g_waits_out;
+
+constexpr int kThreads = 384, kWarps = kThreads / 32;
+constexpr int kMaxTokens = MR_MAX_LAYER_TOKENS, kMaxExperts = MR_MAX_LAYER_EXPERTS;
+constexpr int kLine = 128;            // bytes of a row per stage (the swizzle's width)
+constexpr int kMaxStages = 24;
+constexpr int kBufs = 4, kBufCols = 128;  // tensor memory
+static_assert(kMaxTokens == 64, "a token set is a 64-bit mask");
+
+struct LayerArgs {
+    const void* x;
+    int64_t x_stride;
+    const void* router;
+    int64_t router_stride;
+    int x_dt, router_dt, vec_logits;
+    const float* bias;
+    int T, H, I, E, K;
+    int sigmoid, keep;                // flags
+    float scale;
+    const float* s13;                 // [E][2][ceil(I/128)][ceil(H/128)]
+    const float* s2;                  // [E][ceil(H/128)][ceil(I/128)]
+    uint32_t bf16;                    // 16-bit weights: bf16 (1) or f16 (0)
+    void* y;
+    int64_t y_stride;
+    int32_t* ids;
+    float* weights;
+    // workspace
+    float* logits;                    // [T][E]
+    uint8_t* xs;                      // staged rows, xs_stride bytes apart
+    int64_t xs_stride;
+    float* sx;                        // [ceil(H/128)][64]
+    float* hf;                        // fp32 h, [slot][h_cols] (8-bit weights)
+    uint8_t* hs;                      // staged h, hs_stride bytes apart; 16-bit: high parts, then low parts
+    int64_t hs_stride;
+    int h_cols, slots;                // slots: rows of a part
+    float* sh;                        // [ceil(I/128)][slots]
+    unsigned* count;                  // [E][ceil(I/128)] row groups of h done
+    int rows2;                        // rows of y per block
+    int n1, stages1, stage1, stage2_a, ring_bytes;  // columns and stages of step 2, bytes
+    int off_sx, off_acc, off_ring;    // dynamic shared memory, from its 1024-byte boundary
+};
+
+// Tables of the tokens' experts, at the start of dynamic shared memory.
+struct Tables {
+    unsigned long long mask[kMaxExperts];  // tokens that take the expert
+    uint16_t start[kMaxExperts];           // its first slot: slots are sorted by expert, then token
+    uint16_t active[kMaxTokens * MR_MAX_LAYER_TOPK];
+    float weight[kMaxTokens * MR_MAX_LAYER_TOPK];  // by slot
+    uint8_t token[kMaxTokens * MR_MAX_LAYER_TOPK];
+};
+
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// Step 1
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void load8(const void* base, int64_t at, int dt, float (&v)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + at);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint16_t lo = (uint16_t)(u[j] & 0xFFFFu), hi = (uint16_t)(u[j] >> 16);
+        v[2 * j] = dt == MR_DTYPE_F16 ? Elem<MR_DTYPE_F16>::to_f32(lo) : Elem<MR_DTYPE_BF16>::to_f32(lo);
+        v[2 * j + 1] = dt == MR_DTYPE_F16 ? Elem<MR_DTYPE_F16>::to_f32(hi) : Elem<MR_DTYPE_BF16>::to_f32(hi);
+    }
+}
+
+// Logits of EB experts x TB tokens per block; its threads along k.
+template <int EB, int TB>
+__device__ void logits_step(const LayerArgs& a, float (*part)[16]) {
+    const int nt = (a.T + TB - 1) / TB, tasks = (a.E + EB - 1) / EB * nt;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const int e0 = task / nt * EB, t0 = task % nt * TB;
+        float acc[EB][TB] = {};
+        // past the last expert or token: the last one again, not stored
+        if (a.vec_logits) {
+            for (int k = threadIdx.x * 8; k < a.H; k += kThreads * 8) {
+                float w[EB][8], x[8];
+#pragma unroll
+                for (int i = 0; i < EB; ++i)
+                    load8(a.router, min(e0 + i, a.E - 1) * a.router_stride + k, a.router_dt, w[i]);
+#pragma unroll
+                for (int j = 0; j < TB; ++j) {
+                    load8(a.x, min(t0 + j, a.T - 1) * a.x_stride + k, a.x_dt, x);
+#pragma unroll
+                    for (int i = 0; i < EB; ++i)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) acc[i][j] = fmaf(w[i][q], x[q], acc[i][j]);
+                }
+            }
+        } else {
+            for (int k = threadIdx.x; k < a.H; k += kThreads) {
+                float w[EB];
+#pragma unroll
+                for (int i = 0; i < EB; ++i)
+                    w[i] = load_f32(a.router, min(e0 + i, a.E - 1) * a.router_stride + k, a.router_dt);
+#pragma unroll
+                for (int j = 0; j < TB; ++j) {
+                    const float x = load_f32(a.x, min(t0 + j, a.T - 1) * a.x_stride + k, a.x_dt);
+#pragma unroll
+                    for (int i = 0; i < EB; ++i) acc[i][j] = fmaf(w[i], x, acc[i][j]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < EB; ++i)
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], o);
+                if (lane == 0) part[warp][i * TB + j] = acc[i][j];
+            }
+        __syncthreads();
+        if (threadIdx.x < EB * TB) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += part[w][threadIdx.x];
+            const int e = e0 + threadIdx.x / TB, t = t0 + threadIdx.x % TB;
+            if (e < a.E && t < a.T) a.logits[t * a.E + e] = s;
+        }
+        __syncthreads();
+    }
+}
+
+// Rows of x as the tensor operand: e4m3 blocks with scales, or the same 16 bits.
+template <bool EIGHT>
+__device__ void stage_rows(const LayerArgs& a) {
+    const int lane = threadIdx.x & 31;
+    const int kb = (a.H + kScaleBlock - 1) / kScaleBlock;
+    // blocks from the last one down: the first ones have logits to do
+    for (int i = (gridDim.x - 1 - blockIdx.x) * kWarps + (threadIdx.x >> 5); i < a.T * kb; i += gridDim.x * kWarps) {
+        const int t = i / kb, b = i - t * kb, c = b * kScaleBlock + lane * 4;
+        if (EIGHT) {
+            float v[4];
+            uint32_t m = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = c + j < a.H ? load_f32(a.x, t * a.x_stride + c + j, a.x_dt) : 0.0f;
+                m = max(m, abs_bits(v[j]));
+            }
+            m = __reduce_max_sync(0xffffffffu, m);
+            float s, inv;
+            block_scale(m, &s, &inv);
+            if (lane == 0) a.sx[b * kMaxTokens + t] = s;
+            *reinterpret_cast<uint32_t*>(a.xs + t * a.xs_stride + c) =
+                e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+        } else {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(a.x) + t * a.x_stride;
+            uint16_t* dst = reinterpret_cast<uint16_t*>(a.xs + t * a.xs_stride);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < a.H) dst[c + j] = src[c + j];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Step 2: the tokens' experts
+// ---------------------------------------------------------------------------
+// Bits that order as the values do; NaN below everything.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+    if (v != v) return 0u;
+    const uint32_t b = __float_as_uint(v);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+// One token per warp: the K experts of highest logit (or score + bias), ties to
+// the lowest index. V: values per lane.
+template <int V>
+__device__ void choose(const LayerArgs& a, Tables& tb, int t, bool write) {
+    const int lane = threadIdx.x & 31;
+    float v[V];
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int e = lane + 32 * j;
+        v[j] = e < a.E ? __ldcg(a.logits + t * a.E + e) : -INFINITY;
+        if (e < a.E) top = fmaxf(top, v[j]);
+    }
+    float sum = 1.0f;
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (lane + 32 * j < a.E) sum += expf(v[j] - top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    auto score = [&](float l) { return a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / sum; };
+    uint32_t key[V];  // 0: taken, or no expert
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int e = lane + 32 * j;
+        key[j] = e < a.E ? max(order_bits(a.bias ? score(v[j]) + a.bias[e] : v[j]), 1u) : 0u;
+    }
+    float mine = 0.0f, total = 0.0f;  // lane r: the r-th expert's score
+    int expert = 0;
+    for (int r = 0; r < a.K; ++r) {
+        uint32_t best = 0u;
+#pragma unroll
+        for (int j = 0; j < V; ++j) best = max(best, key[j]);
+        const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+        uint32_t at = 0xffffffffu;
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j)
+            if (key[j] == most) at = lane + 32 * j;
+        const int e = (int)__reduce_min_sync(0xffffffffu, at);
+        float l = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (e == lane + 32 * j) {
+                key[j] = 0u;
+                l = v[j];
+            }
+        const float s = score(__shfl_sync(0xffffffffu, l, e & 31));
+        total += s;
+        if (lane == r) mine = s, expert = e;
+    }
+    if (lane < a.K) {
+        const float w = (a.keep ? mine : mine / fmaxf(total, 1.17549435e-38f)) * a.scale;
+        atomicOr(&tb.mask[expert], 1ull << t);
+        tb.weight[t * a.K + lane] = w;  // by token until the slots are known
+        tb.active[t * a.K + lane] = (uint16_t)expert;
+        if (write) {
+            a.ids[t * a.K + lane] = expert;
+            a.weights[t * a.K + lane] = w;
+        }
+    }
+}
+
+__device__ __forceinline__ int rank_of(unsigned long long mask, int t) {
+    return __popcll(mask & ((1ull << t) - 1ull));
+}
+
+// Fills the tables; returns the number of experts taken, *most the largest number of tokens of one.
+__device__ int make_tables(const LayerArgs& a, Tables& tb, uint32_t* warp_sums, int* most_smem, int* most) {
+    for (int e = threadIdx.x; e < a.E; e += kThreads) tb.mask[e] = 0ull;
+    if (threadIdx.x == 0) *most_smem = 0;
+    __syncthreads();
+    for (int t = threadIdx.x >> 5; t < a.T; t += kWarps) {
+        const bool write = blockIdx.x == 0;
+        if (a.E <= 64) choose<2>(a, tb, t, write);
+        else if (a.E <= 256) choose<8>(a, tb, t, write);
+        else choose<kMaxExperts / 32>(a, tb, t, write);
+    }
+    __syncthreads();
+    // each thread's pairs, before the tables by slot take their place
+    constexpr int kMine = (kMaxTokens * MR_MAX_LAYER_TOPK + kThreads - 1) / kThreads;
+    float w[kMine];
+    int ex[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        ex[j] = i < a.T * a.K ? tb.active[i] : -1;
+        w[j] = i < a.T * a.K ? tb.weight[i] : 0.0f;
+    }
+    // experts of this thread: their slots, and their places among the taken ones
+    constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
+    uint32_t slots = 0u, taken = 0u;
+    int biggest = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = threadIdx.x * kPer + j;
+        const int n = e < a.E ? __popcll(tb.mask[e]) : 0;
+        slots += n;
+        taken += n > 0;
+        biggest = max(biggest, n);
+    }
+    biggest = (int)__reduce_max_sync(0xffffffffu, (unsigned)biggest);
+    if ((threadIdx.x & 31) == 0) atomicMax(most_smem, biggest);
+    uint32_t experts = 0u;
+    uint32_t before = block_exclusive_scan((taken << 16) | slots, warp_sums, &experts);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = threadIdx.x * kPer + j;
+        if (e >= a.E) continue;
+        const int n = __popcll(tb.mask[e]);
+        tb.start[e] = (uint16_t)(before & 0xFFFFu);
+        if (n) tb.active[before >> 16] = (uint16_t)e;
+        before += (n ? 0x10000u : 0u) + n;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        if (ex[j] < 0) continue;
+        const int t = i / a.K, slot = tb.start[ex[j]] + rank_of(tb.mask[ex[j]], t);
+        tb.weight[slot] = w[j];
+        tb.token[slot] = (uint8_t)t;
+    }
+    __syncthreads();
+    *most = *most_smem;
+    return (int)(experts >> 16);
+}
+
+// ---------------------------------------------------------------------------
+// Barriers of the ring and of tensor memory
+// ---------------------------------------------------------------------------
+struct Bars {
+    uint64_t full[kMaxStages], empty[kMaxStages], t_full[kBufs], t_empty[kBufs];
+};
+__device__ void init_bars(Bars& b) {
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(smem_u32(&b.full[i]), 1), mbar_init(smem_u32(&b.empty[i]), 1);
+    for (int i = 0; i < kBufs; ++i) mbar_init(smem_u32(&b.t_full[i]), 1), mbar_init(smem_u32(&b.t_empty[i]), 8);
+}
+
+// ---------------------------------------------------------------------------
+// Step 2: h. Row groups of 8 (of one expert) [g0, g1) of all taken experts.
+// ---------------------------------------------------------------------------
+template <bool EIGHT, int COLS>
+__device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* map_x, const CUtensorMap* map_w8,
+                       const CUtensorMap* map_w64, uint8_t* ring, const float* sx, Bars& bars, uint32_t tmem,
+                       volatile uint32_t* abort, uint32_t* flag, int g0, int g1) {
+    constexpr int kLineElems = EIGHT ? kLine : kLine / 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (a.I + 7) / 8;  // row groups of an expert
+    const int kbs = (a.H + kLineElems - 1) / kLineElems;
+    const int tiles = (g1 - g0 + 15) / 16;
+    const int x_bytes = 2 * COLS * kLine;
+    if (warp == 0) {
+        if (elect_one()) {
+            proxy_fence();
+            uint32_t it = 0;
+            for (int n = 0; n < tiles; ++n) {
+                const int f = g0 + n * 16, l = min(f + 16, g1);
+                for (int kb = 0; kb < kbs; ++kb, ++it) {
+                    const uint32_t st = it % a.stages1, bar = smem_u32(&bars.full[st]);
+                    if (!mbar_wait(smem_u32(&bars.empty[st]), ((it / a.stages1) & 1) ^ 1, abort)) break;
+                    const uint32_t dst = smem_u32(ring) + st * a.stage1;
+                    mbar_expect(bar, (l - f) * 2048 + x_bytes);
+                    for (int g = f; g < l;) {
+                        const int j = g / per, r = g - j * per;
+                        const int run = min(l - g, per - r);
+                        const int plane = tb.active[j] * 2;
+                        int done = 0;
+                        for (; done + 8 <= run; done += 8) {
+                            const uint32_t to = dst + (g - f + done) * 1024;
+                            tma_load_3d(to, map_w64, bar, kb * kLineElems, (r + done) * 8, plane);
+                            tma_load_3d(to + 16384, map_w64, bar, kb * kLineElems, (r + done) * 8, plane + 1);
+                        }
+                        for (; done < run; ++done) {
+                            const uint32_t to = dst + (g - f + done) * 1024;
+                            tma_load_3d(to, map_w8, bar, kb * kLineElems, (r + done) * 8, plane);
+                            tma_load_3d(to + 16384, map_w8, bar, kb * kLineElems, (r + done) * 8, plane + 1);
+                        }
+                        g += run;
+                    }
+                    tma_load_2d(dst + 32768, map_x, bar, kb * kLineElems, 0);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            uint32_t it = 0, use = 0;  // stages and tensor memory buffers used
+            for (int n = 0; n < tiles; ++n) {
+                for (int kb = 0; kb < kbs; ++kb, ++it) {
+                    const uint32_t st = it % a.stages1, buf = use % kBufs;
+                    if (EIGHT || kb == 0) mbar_wait(smem_u32(&bars.t_empty[buf]), ((use / kBufs) & 1) ^ 1, abort);
+                    if (!mbar_wait(smem_u32(&bars.full[st]), (it / a.stages1) & 1, abort)) break;
+                    tc_fence_after();
+                    const uint32_t at = smem_u32(ring) + st * a.stage1;
+                    const uint64_t dg = smem_desc(at), du = smem_desc(at + 16384), dx = smem_desc(at + 32768);
+                    const uint32_t d = tmem + buf * kBufCols;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t add = EIGHT ? k > 0 : k > 0 || kb > 0;
+                        if (EIGHT) {
+                            mma_e4m3(d, dg + 2 * k, dx + 2 * k, idesc_e4m3(128, 2 * COLS), add);
+                            mma_e4m3(d + 64, du + 2 * k, dx + 2 * k, idesc_e4m3(128, 2 * COLS), add);
+                        } else {
+                            mma_16(d, dg + 2 * k, dx + 2 * k, idesc_16(128, 2 * COLS, a.bf16), add);
+                            mma_16(d + 64, du + 2 * k, dx + 2 * k, idesc_16(128, 2 * COLS, a.bf16), add);
+                        }
+                    }
+                    tc_commit(smem_u32(&bars.empty[st]));
+                    if (EIGHT || kb == kbs - 1) {
+                        tc_commit(smem_u32(&bars.t_full[buf]));
+                        ++use;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + half * COLS;
+        const int hb = (a.H + kScaleBlock - 1) / kScaleBlock, ib = (a.I + kScaleBlock - 1) / kScaleBlock;
+        uint32_t use = 0;
+        for (int n = 0; n < tiles; ++n) {
+            const int f = g0 + n * 16, l = min(f + 16, g1);
+            const int g = min(f + row / 8, l - 1);
+            const int e = tb.active[g / per], i = g % per * 8 + (row & 7);
+            const bool real = f + row / 8 < l && i < a.I;
+            float hg[COLS], hu[COLS];
+            if (EIGHT) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) hg[c] = hu[c] = 0.0f;
+                const float* wg = a.s13 + ((int64_t)(2 * e) * ib + min(i, a.I - 1) / kScaleBlock) * hb;
+                const float* wu = wg + (int64_t)ib * hb;
+                float ng = wg[0], nu = wu[0];
+                for (int kb = 0; kb < kbs; ++kb, ++use) {
+                    const uint32_t buf = use % kBufs;
+                    const float sg = ng, su = nu;
+                    if (kb + 1 < kbs) ng = wg[kb + 1], nu = wu[kb + 1];
+                    mbar_wait(smem_u32(&bars.t_full[buf]), (use / kBufs) & 1, abort);
+                    tc_fence_after();
+                    uint32_t vg[COLS], vu[COLS];
+                    tmem_load(vg, from + buf * kBufCols);
+                    tmem_load(vu, from + buf * kBufCols + 64);
+                    tmem_ld_wait(vg);
+                    tmem_ld_wait(vu);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[buf]));
+                    const float4* s4 = reinterpret_cast<const float4*>(sx + kb * 2 * COLS + half * COLS);
+#pragma unroll
+                    for (int c = 0; c < COLS / 4; ++c) {
+                        const float4 s = s4[c];
+                        const float t[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            hg[4 * c + q] = fmaf(__uint_as_float(vg[4 * c + q]), sg * t[q], hg[4 * c + q]);
+                            hu[4 * c + q] = fmaf(__uint_as_float(vu[4 * c + q]), su * t[q], hu[4 * c + q]);
+                        }
+                    }
+                }
+            } else {
+                const uint32_t buf = use % kBufs;
+                mbar_wait(smem_u32(&bars.t_full[buf]), (use / kBufs) & 1, abort);
+                tc_fence_after();
+                uint32_t vg[COLS], vu[COLS];
+                tmem_load(vg, from + buf * kBufCols);
+                tmem_load(vu, from + buf * kBufCols + 64);
+                tmem_ld_wait(vg);
+                tmem_ld_wait(vu);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[buf]));
+                ++use;
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) hg[c] = __uint_as_float(vg[c]), hu[c] = __uint_as_float(vu[c]);
+            }
+            // h of the tokens that take this row's expert
+            const unsigned long long mask = real ? tb.mask[e] : 0ull;
+            const int start = tb.start[e];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                const int t = half * COLS + c;
+                if (t >= a.T || !((mask >> t) & 1ull)) continue;
+                const int slot = start + rank_of(mask, t);
+                if (!MR_IN_RANGE(slot, a.T * a.K, 950)) continue;
+                const float h = silu(hg[c]) * hu[c];
+                if (EIGHT) {
+                    a.hf[(int64_t)slot * a.h_cols + i] = h;
+                } else {
+                    // the value in two 16-bit parts: the second product loses nothing of the 32 bits but
+                    // their last few
+                    uint16_t* p = reinterpret_cast<uint16_t*>(a.hs + (int64_t)slot * a.hs_stride) + i;
+                    uint16_t* q = reinterpret_cast<uint16_t*>(a.hs + (int64_t)(a.slots + slot) * a.hs_stride) + i;
+                    if (a.bf16) {
+                        const uint16_t hi = Elem<MR_DTYPE_BF16>::from_f32(h);
+                        *p = hi;
+                        *q = Elem<MR_DTYPE_BF16>::from_f32(h - Elem<MR_DTYPE_BF16>::to_f32(hi));
+                    } else {
+                        const uint16_t hi = Elem<MR_DTYPE_F16>::from_f32(h);
+                        *p = hi;
+                        *q = Elem<MR_DTYPE_F16>::from_f32(h - Elem<MR_DTYPE_F16>::to_f32(hi));
+                    }
+                }
+            }
+            if (EIGHT) {
+                // Blocks of 128 columns of h are quantized by whoever completes them.
+                __threadfence();
+                for (int g = f; g < l;) {
+                    const int j = g / per, r = g - j * per, b = r / 16;
+                    const int run = min(min(l - g, per - r), (b + 1) * 16 - r);
+                    const int ex = tb.active[j], whole = min(16, per - b * 16);
+                    named_barrier(1, 256);  // the tile's rows are stored; *flag is free
+                    if (threadIdx.x == 128) {
+                        *flag = atomicAdd(&a.count[ex * ib + b], (unsigned)run) + run == (unsigned)whole;
+                        __threadfence();
+                    }
+                    named_barrier(1, 256);
+                    if (*flag) {
+                        const int tokens = __popcll(tb.mask[ex]), s0 = tb.start[ex];
+                        for (int s = warp - 4; s < tokens; s += 8) {
+                            const int64_t at = (int64_t)(s0 + s) * a.h_cols + b * kScaleBlock + lane * 4;
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.hf + at));
+                            // columns past I hold nothing
+                            const int left = a.I - b * kScaleBlock - lane * 4;
+                            const float x[4] = {left > 0 ? v.x : 0.0f, left > 1 ? v.y : 0.0f,
+                                                left > 2 ? v.z : 0.0f, left > 3 ? v.w : 0.0f};
+                            uint32_t m = max(max(abs_bits(x[0]), abs_bits(x[1])), max(abs_bits(x[2]), abs_bits(x[3])));
+                            m = __reduce_max_sync(0xffffffffu, m);
+                            float sc, inv;
+                            block_scale(m, &sc, &inv);
+                            *reinterpret_cast<uint32_t*>(a.hs + (int64_t)(s0 + s) * a.hs_stride + b * kScaleBlock +
+                                                         lane * 4) =
+                                e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                            if (lane == 0) a.sh[b * a.slots + s0 + s] = sc;
+                        }
+                    }
+                    g += run;
+                }
+            }
+        }
+        proxy_fence();  // h is read by copies of the async proxy
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Step 3: y. Rows [row0, row0 + rows2) of every taken expert's W2. The second
+// product's columns are the expert's slots; COLS of them per warpgroup, and
+// (8-bit weights) 32 / COLS lines of k per tensor memory buffer.
+// ---------------------------------------------------------------------------
+template <bool EIGHT, int COLS>
+__device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* map_w2, const CUtensorMap* map_h,
+                       uint8_t* ring, float* acc, Bars& bars, uint32_t tmem, volatile uint32_t* abort, int experts,
+                       int row0, cg::grid_group& grid) {
+    constexpr int kLineElems = EIGHT ? kLine : kLine / 2;
+    constexpr int kUnits = EIGHT ? 32 / COLS : 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kbs = (a.I + kLineElems - 1) / kLineElems;
+    const int stage = a.stage2_a + 2 * COLS * kLine * (EIGHT ? 1 : 2);
+    // the instructions read 128 rows from a stage's start on, whatever rows2 is: 16 KB of slack
+    const int stages = min(kMaxStages, (a.ring_bytes - 16384) / stage);
+    const int total = row0 < a.H ? experts * kbs : 0;
+    const uint32_t a_bytes = a.rows2 * kLine;
+    const uint32_t base = smem_u32(ring);
+    auto boxes = [&](int j) { return (__popcll(tb.mask[tb.active[j]]) + 15) / 16; };
+    auto request_h = [&](int unit, int j, int kb) {
+        const uint32_t st = unit % stages, dst = base + st * stage + a.stage2_a, bar = smem_u32(&bars.full[st]);
+        const int nb = boxes(j), s0 = tb.start[tb.active[j]];
+        for (int b = 0; b < nb; ++b) {
+            tma_load_2d(dst + b * 2048, map_h, bar, kb * kLineElems, s0 + 16 * b);
+            if (!EIGHT) tma_load_2d(dst + (nb + b) * 2048, map_h, bar, kb * kLineElems, a.slots + s0 + 16 * b);
+        }
+    };
+    auto request_w = [&](int unit, int j, int kb) {
+        const uint32_t st = unit % stages, bar = smem_u32(&bars.full[st]);
+        mbar_expect(bar, a_bytes + boxes(j) * 2048 * (EIGHT ? 1 : 2));
+        tma_load_3d(base + st * stage, map_w2, bar, kb * kLineElems, row0, tb.active[j]);
+    };
+    const int ahead = min(stages, total);
+    if (warp == 0) {
+        if (elect_one())
+            for (int u = 0, j = 0, kb = 0; u < ahead; ++u) {
+                request_w(u, j, kb);
+                if (++kb == kbs) kb = 0, ++j;
+            }
+        __syncwarp();
+    }
+    for (int i = threadIdx.x; i < 2 * a.T * a.rows2; i += kThreads) acc[i] = 0.0f;
+    grid.sync();
+    if (warp == 0) {
+        if (elect_one()) {
+            proxy_fence();
+            for (int u = 0, j = 0, kb = 0; u < total; ++u) {
+                if (u >= ahead) {
+                    if (!mbar_wait(smem_u32(&bars.empty[u % stages]), ((u / stages) & 1) ^ 1, abort)) break;
+                    request_w(u, j, kb);
+                }
+                request_h(u, j, kb);
+                if (++kb == kbs) kb = 0, ++j;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            uint32_t u = 0, use = 0;
+            for (int j = 0; j < (total ? experts : 0); ++j) {
+                const int nb = boxes(j);
+                const uint32_t idesc = EIGHT ? idesc_e4m3(128, 16 * nb) : idesc_16(128, 32 * nb, a.bf16);
+                for (int kb = 0; kb < kbs; ++kb, ++u) {
+                    const uint32_t st = u % stages, buf = use % kBufs;
+                    const int part = kb % kUnits;
+                    if (EIGHT ? part == 0 : kb == 0)
+                        mbar_wait(smem_u32(&bars.t_empty[buf]), ((use / kBufs) & 1) ^ 1, abort);
+                    if (!mbar_wait(smem_u32(&bars.full[st]), (u / stages) & 1, abort)) break;
+                    tc_fence_after();
+                    const uint64_t dw = smem_desc(base + st * stage), dh = smem_desc(base + st * stage + a.stage2_a);
+                    const uint32_t d = tmem + buf * kBufCols + (EIGHT ? part * 2 * COLS : 0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (EIGHT) mma_e4m3(d, dw + 2 * k, dh + 2 * k, idesc, k > 0);
+                        else mma_16(d, dw + 2 * k, dh + 2 * k, idesc, k > 0 || kb > 0);
+                    }
+                    tc_commit(smem_u32(&bars.empty[st]));
+                    if (kb == kbs - 1 || (EIGHT && part == kUnits - 1)) {
+                        tc_commit(smem_u32(&bars.t_full[buf]));
+                        ++use;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + half * COLS;
+        const int hb = (a.H + kScaleBlock - 1) / kScaleBlock, ib = (a.I + kScaleBlock - 1) / kScaleBlock;
+        const int wrow = min(row0 + row, a.H - 1);
+        float* mine = acc + half * a.T * a.rows2 + row;  // [token][row]
+        uint32_t use = 0;
+        for (int j = 0; j < (total ? experts : 0); ++j) {
+            const int e = tb.active[j], s0 = tb.start[e], tokens = __popcll(tb.mask[e]);
+            float y[COLS];
+            if (EIGHT) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) y[c] = 0.0f;
+                const float* w = a.s2 + ((int64_t)e * hb + wrow / kScaleBlock) * ib;
+                const int lc = half * COLS + lane % COLS;
+                for (int kb = 0; kb < kbs; kb += kUnits, ++use) {
+                    const uint32_t buf = use % kBufs;
+                    // lane: the scale of one column and line
+                    const int lk = kb + lane / COLS;
+                    const float sv = lk < kbs && lc < tokens ? __ldcg(a.sh + lk * a.slots + s0 + lc) : 0.0f;
+                    float sw[kUnits];
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) sw[u] = kb + u < kbs ? w[kb + u] : 0.0f;
+                    mbar_wait(smem_u32(&bars.t_full[buf]), (use / kBufs) & 1, abort);
+                    tc_fence_after();
+                    uint32_t v[kUnits][COLS];
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) tmem_load(v[u], from + buf * kBufCols + u * 2 * COLS);
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) tmem_ld_wait(v[u]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[buf]));
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) {
+                        if (kb + u >= kbs) break;  // lines past the end: whatever the buffer held
+#pragma unroll
+                        for (int c = 0; c < COLS; ++c)
+                            y[c] = fmaf(__uint_as_float(v[u][c]), sw[u] * __shfl_sync(0xffffffffu, sv, u * COLS + c),
+                                        y[c]);
+                    }
+                }
+            } else {
+                const uint32_t buf = use % kBufs;
+                mbar_wait(smem_u32(&bars.t_full[buf]), (use / kBufs) & 1, abort);
+                tc_fence_after();
+                uint32_t hi[COLS], lo[COLS];
+                tmem_load(hi, from + buf * kBufCols);
+                tmem_load(lo, from + buf * kBufCols + 16 * boxes(j));
+                tmem_ld_wait(hi);
+                tmem_ld_wait(lo);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[buf]));
+                ++use;
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) y[c] = __uint_as_float(hi[c]) + __uint_as_float(lo[c]);
+            }
+            if (row < a.rows2) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) {
+                    if (half * COLS + c >= tokens) break;
+                    const int slot = s0 + half * COLS + c;
+                    float* p = mine + tb.token[slot] * a.rows2;
+                    *p = fmaf(tb.weight[slot], y[c], *p);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T * a.rows2; i += kThreads) {
+        const int t = i / a.rows2, r = row0 + i - t * a.rows2;
+        if (r >= a.H) continue;
+        const float v = acc[i] + acc[a.T * a.rows2 + i];
+        const int64_t at = t * a.y_stride + r;
+        if (a.x_dt == MR_DTYPE_F32) reinterpret_cast<float*>(a.y)[at] = v;
+        else if (a.x_dt == MR_DTYPE_F16) reinterpret_cast<uint16_t*>(a.y)[at] = Elem<MR_DTYPE_F16>::from_f32(v);
+        else reinterpret_cast<uint16_t*>(a.y)[at] = Elem<MR_DTYPE_BF16>::from_f32(v);
+    }
+}
+
+struct LayerMaps {
+    CUtensorMap x, w8, w64, w2, h;
+};
+
+template <bool EIGHT, int COLS>
+__global__ void __launch_bounds__(kThreads, 1)
+    layer_kernel(const __grid_constant__ LayerMaps maps, const __grid_constant__ LayerArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) Bars bars1, bars2;
+    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ uint32_t tmem_base, abort_word, flag, warp_sums[32];
+    __shared__ int most_smem;
+    __shared__ float part[kWarps][16];
+    cg::grid_group grid = cg::this_grid();
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Tables& tb = *reinterpret_cast<Tables*>(smem);
+    float* sx = reinterpret_cast<float*>(smem + a.off_sx);
+    float* acc = reinterpret_cast<float*>(smem + a.off_acc);
+    uint8_t* ring = smem + a.off_ring;
+    volatile uint32_t* abort = &abort_word;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        init_bars(bars1);
+        init_bars(bars2);
+        mbar_init(smem_u32(&drain_bar), 1);
+        abort_word = 0u;
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&tmem_base), kBufs * kBufCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    pdl_enter();
+
+    // 1
+    const int ib = (a.I + kScaleBlock - 1) / kScaleBlock, hb = (a.H + kScaleBlock - 1) / kScaleBlock;
+    if (EIGHT)
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.E * ib; i += gridDim.x * kThreads) a.count[i] = 0u;
+    stage_rows<EIGHT>(a);
+    if (a.T * a.E <= 4 * (int)gridDim.x) logits_step<1, 1>(a, part);
+    else logits_step<4, 4>(a, part);
+    proxy_fence();
+    grid.sync();
+
+    // 2
+    int most = 0;
+    const int experts = make_tables(a, tb, warp_sums, &most_smem, &most);
+    if (EIGHT)
+        for (int i = threadIdx.x; i < hb * 2 * COLS; i += kThreads) {
+            const int t = i % (2 * COLS);
+            sx[i] = t < a.T ? __ldcg(a.sx + i / (2 * COLS) * kMaxTokens + t) : 0.0f;
+        }
+    __syncthreads();
+    const int groups = experts * ((a.I + 7) / 8);
+    const int g0 = (int)((int64_t)groups * blockIdx.x / gridDim.x);
+    const int g1 = (int)((int64_t)groups * (blockIdx.x + 1) / gridDim.x);
+    step_h<EIGHT, COLS>(a, tb, &maps.x, &maps.w8, &maps.w64, ring, sx, bars1, tmem, abort, &flag, g0, g1);
+    tc_fence_before();
+    __syncthreads();  // the ring changes its layout, tensor memory its use
+    tc_fence_after();
+
+    // 3
+    const int row0 = blockIdx.x * a.rows2;
+    if (most <= 16) step_y<EIGHT, 8>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, grid);
+    else if (most <= 32) step_y<EIGHT, 16>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, grid);
+    else step_y<EIGHT, 32>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, grid);
+
+    __syncthreads();
+    if (abort_word) {
+        // A wait gave up: let the instructions in flight end, and give the copies the time that
+        // mbar_drain gives a barrier, before the block's memory goes.
+        if (warp == 1) {
+            if (elect_one()) tc_commit(smem_u32(&drain_bar));
+            mbar_drain(smem_u32(&drain_bar), 0);
+        }
+        if (threadIdx.x == 0) {
+            const uint64_t start = global_ns();
+            while (global_ns() - start < 100000000ull) {
+            }
+            atomicAdd(&g_waits_out, 1u);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free(tmem, kBufs * kBufCols);
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+bool float_dtype(int32_t dt) { return dt == MR_DTYPE_F16 || dt == MR_DTYPE_BF16 || dt == MR_DTYPE_F32; }
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Workspace regions, 256-byte aligned.
+struct LayerPlan {
+    int64_t xs_stride, hs_stride, h_cols, slots;
+    uint64_t logits, xs, sx, hf, hs, sh, count, bytes;
+    LayerPlan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t K, bool eight) {
+        const int64_t ib = ceil_div(I, kScaleBlock), hb = ceil_div(H, kScaleBlock);
+        slots = ceil_div(T * K, 16) * 16 + 64;  // a box of 16 slots may start at any slot
+        h_cols = ib * kScaleBlock;
+        xs_stride = eight ? hb * kScaleBlock : (int64_t)align_up(2 * H, 128);
+        hs_stride = eight ? h_cols : (int64_t)align_up(2 * I, 128);
+        uint64_t at = 0;
+        auto take = [&](uint64_t n) {
+            const uint64_t p = at;
+            at += align_up(n, 256);
+            return p;
+        };
+        logits = take(T * E * 4);
+        xs = take(kMaxTokens * xs_stride);
+        sx = take(hb * kMaxTokens * 4);
+        hf = take(eight ? slots * h_cols * 4 : 0);
+        hs = take((eight ? 1 : 2) * slots * hs_stride);
+        sh = take(eight ? ib * slots * 4 : 0);
+        count = take(eight ? E * ib * 4 : 0);
+        bytes = at;
+    }
+};
+
+template <bool EIGHT, int COLS>
+cudaError_t launch_layer(const LayerMaps& maps, const LayerArgs& a, int smem, int grid, cudaStream_t s) {
+    auto kernel = layer_kernel<EIGHT, COLS>;
+    static std::atomic<int> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        cudaFuncAttributes at;
+        if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      232448 - (int)at.sharedSizeBytes)) != cudaSuccess)
+            return e;
+        ready[dev].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
+bool layer_sizes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t K, int32_t dt) {
+    return T >= 0 && T <= MR_MAX_LAYER_TOKENS && H >= 1 && H <= MR_MAX_LAYER_COLS && I >= 1 &&
+           I <= MR_MAX_LAYER_COLS && E >= 1 && E <= MR_MAX_LAYER_EXPERTS && K >= 1 && K <= MR_MAX_LAYER_TOPK &&
+           K <= E && (dt == MR_DTYPE_E4M3 || dt == MR_DTYPE_F16 || dt == MR_DTYPE_BF16);
+}
+
+}  // namespace
+
+MR_CHECK_ACCESSOR(layer)
+
+cudaError_t waits_out_layer(unsigned* out, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_waits_out, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0u;
+        e = cudaMemcpyToSymbol(g_waits_out, &zero, sizeof(zero));
+    }
+    return e;
+}
+
+}  // namespace mr
+
+using namespace mr;
+
+extern "C" mr_status moe_layer_get_workspace_size(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts,
+                                                  int64_t topK, int32_t weightDtype, uint64_t* workspaceSize) {
+    if (!layer_sizes(tokens, hidden, inter, experts, topK, weightDtype)) return MR_ERR_PARAM_INVALID;
+    if (!workspaceSize) return MR_ERR_PARAM_NULLPTR;
+    *workspaceSize = LayerPlan(tokens, hidden, inter, experts, topK, weightDtype == MR_DTYPE_E4M3).bytes;
+    return MR_OK;
+}
+
+extern "C" mr_status moe_layer(const void* x, int32_t xDtype, int64_t xStride, const void* router,
+                               int32_t routerDtype, int64_t routerStride, const float* selectBias, const void* w13,
+                               int32_t weightDtype, const int64_t* w13Strides, const float* w13Scales,
+                               const void* w2, const int64_t* w2Strides, const float* w2Scales, int64_t tokens,
+                               int64_t hidden, int64_t inter, int64_t experts, int64_t topK, uint32_t flags,
+                               float routedScale, void* y, int64_t yStride, int32_t* expertIds, float* expertWeights,
+                               void* workspace, uint64_t workspaceSize, void* stream) {
+    const bool eight = weightDtype == MR_DTYPE_E4M3;
+    if (!layer_sizes(tokens, hidden, inter, experts, topK, weightDtype)) return MR_ERR_PARAM_INVALID;
+    if (!float_dtype(xDtype) || !float_dtype(routerDtype) || (!eight && xDtype != weightDtype))
+        return MR_ERR_PARAM_INVALID;
+    if (flags & ~(MR_LAYER_SIGMOID | MR_LAYER_KEEP_WEIGHTS)) return MR_ERR_PARAM_INVALID;
+    const int64_t top = INT64_C(1) << 40;
+    if (xStride < hidden || xStride > top || routerStride < hidden || routerStride > top || yStride < hidden ||
+        yStride > top)
+        return MR_ERR_PARAM_INVALID;
+    const int64_t el = eight ? 1 : 2;
+    int64_t ar = hidden * el, am = inter * ar, br = inter * el, bm = hidden * br;
+    if (w13Strides) ar = w13Strides[0], am = w13Strides[1];
+    if (w2Strides) br = w2Strides[0], bm = w2Strides[1];
+    if (ar < hidden * el || ar % 16 || am % 16 || ar > top || am > top || am < (inter - 1) * ar + hidden * el)
+        return MR_ERR_PARAM_INVALID;
+    if (br < inter * el || br % 16 || bm % 16 || br > top || bm > top ||
+        (experts > 1 && bm < (hidden - 1) * br + inter * el))
+        return MR_ERR_PARAM_INVALID;
+    if (tokens == 0) return MR_OK;
+    if (!x || !router || !w13 || !w2 || !y || !expertIds || !expertWeights || !workspace) return MR_ERR_PARAM_NULLPTR;
+    if (eight != (w13Scales != nullptr) || eight != (w2Scales != nullptr)) return MR_ERR_PARAM_NULLPTR;
+    const LayerPlan p(tokens, hidden, inter, experts, topK, eight);
+    if (workspaceSize < p.bytes) return MR_ERR_WORKSPACE;
+    if (!aligned16(w13) || !aligned16(w2) || reinterpret_cast<uintptr_t>(workspace) % 256) return MR_ERR_PARAM_INVALID;
+    const uintptr_t xe = xDtype == MR_DTYPE_F32 ? 4 : 2, re = routerDtype == MR_DTYPE_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(x) % xe || reinterpret_cast<uintptr_t>(y) % xe ||
+        reinterpret_cast<uintptr_t>(router) % re)
+        return MR_ERR_PARAM_INVALID;
+
+    const int grid = device_sm_count();
+    LayerArgs a{};
+    a.x = x;
+    a.x_stride = xStride;
+    a.router = router;
+    a.router_stride = routerStride;
+    a.x_dt = xDtype;
+    a.router_dt = routerDtype;
+    a.vec_logits = xe == 2 && re == 2 && aligned16(x) && aligned16(router) && xStride % 8 == 0 &&
+                   routerStride % 8 == 0 && hidden % 8 == 0;
+    a.bias = selectBias;
+    a.T = (int)tokens;
+    a.H = (int)hidden;
+    a.I = (int)inter;
+    a.E = (int)experts;
+    a.K = (int)topK;
+    a.sigmoid = (flags & MR_LAYER_SIGMOID) != 0;
+    a.keep = (flags & MR_LAYER_KEEP_WEIGHTS) != 0;
+    a.scale = routedScale;
+    a.s13 = w13Scales;
+    a.s2 = w2Scales;
+    a.bf16 = weightDtype == MR_DTYPE_BF16;
+    a.y = y;
+    a.y_stride = yStride;
+    a.ids = expertIds;
+    a.weights = expertWeights;
+    uint8_t* w = reinterpret_cast<uint8_t*>(workspace);
+    a.logits = reinterpret_cast<float*>(w + p.logits);
+    a.xs = w + p.xs;
+    a.xs_stride = p.xs_stride;
+    a.sx = reinterpret_cast<float*>(w + p.sx);
+    a.hf = reinterpret_cast<float*>(w + p.hf);
+    a.hs = w + p.hs;
+    a.hs_stride = p.hs_stride;
+    a.h_cols = (int)p.h_cols;
+    a.slots = (int)p.slots;
+    a.sh = reinterpret_cast<float*>(w + p.sh);
+    a.count = reinterpret_cast<unsigned*>(w + p.count);
+    a.rows2 = ceil_div(ceil_div(hidden, grid), 8) * 8;
+    if (a.rows2 > 128) return MR_ERR_UNSUPPORTED;  // a device with fewer SMs
+    a.n1 = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
+
+    // shared memory: tables, scales of x, sums of y, then the ring
+    a.off_sx = (int)align_up(sizeof(Tables), 128);
+    a.off_acc = a.off_sx + (eight ? ceil_div(hidden, kScaleBlock) * a.n1 * 4 : 0);
+    a.off_ring = (int)align_up(a.off_acc + 2 * tokens * a.rows2 * 4, 1024);
+    constexpr int kStatic = 4096;  // at least the kernel's static shared memory and alignment
+    const int room = 232448 - kStatic;
+    a.ring_bytes = (room - a.off_ring) / 1024 * 1024;
+    a.stage1 = 32768 + a.n1 * kLine;
+    a.stages1 = std::min(kMaxStages, a.ring_bytes / a.stage1);
+    a.stage2_a = (int)align_up(a.rows2 * kLine, 1024);
+    // the widest stage of step 3: 64 columns, in two parts for 16-bit weights
+    const int widest = a.stage2_a + 64 * kLine * (eight ? 1 : 2);
+    if (a.stages1 < 2 || (a.ring_bytes - 16384) / widest < 2) return MR_ERR_UNSUPPORTED;
+
+    LayerMaps m;
+    const CUtensorMapDataType type = eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    const uint32_t line = (uint32_t)(kLine / el);
+    const uint64_t xd[2] = {(uint64_t)hidden, (uint64_t)kMaxTokens}, xst[1] = {(uint64_t)p.xs_stride};
+    const uint32_t xb[2] = {line, (uint32_t)a.n1};
+    const uint64_t ad[3] = {(uint64_t)hidden, (uint64_t)inter, (uint64_t)experts * 2};
+    const uint64_t ast[2] = {(uint64_t)ar, (uint64_t)am};
+    const uint32_t a8[3] = {line, 8, 1}, a64[3] = {line, 64, 1};
+    const uint64_t bd[3] = {(uint64_t)inter, (uint64_t)hidden, (uint64_t)experts};
+    const uint64_t bst[2] = {(uint64_t)br, (uint64_t)bm};
+    const uint32_t bb[3] = {line, (uint32_t)a.rows2, 1};
+    const uint64_t hd[2] = {(uint64_t)inter, (uint64_t)(p.slots * (eight ? 1 : 2))}, hst[1] = {(uint64_t)p.hs_stride};
+    const uint32_t hbx[2] = {line, 16};
+    const int eb = (int)el;
+    if (!make_tensor_map(&m.x, type, eb, a.xs, 2, xd, xst, xb) || !make_tensor_map(&m.w8, type, eb, w13, 3, ad, ast, a8) ||
+        !make_tensor_map(&m.w64, type, eb, w13, 3, ad, ast, a64) ||
+        !make_tensor_map(&m.w2, type, eb, w2, 3, bd, bst, bb) || !make_tensor_map(&m.h, type, eb, a.hs, 2, hd, hst, hbx))
+        return MR_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int smem = 1024 + a.off_ring + a.ring_bytes;
+    cudaError_t e;
+    if (eight) {
+        e = a.n1 == 16   ? launch_layer<true, 8>(m, a, smem, grid, s)
+            : a.n1 == 32 ? launch_layer<true, 16>(m, a, smem, grid, s)
+                         : launch_layer<true, 32>(m, a, smem, grid, s);
+    } else {
+        e = a.n1 == 16   ? launch_layer<false, 8>(m, a, smem, grid, s)
+            : a.n1 == 32 ? launch_layer<false, 16>(m, a, smem, grid, s)
+                         : launch_layer<false, 32>(m, a, smem, grid, s);
+    }
+    return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+}

@@ -84,6 +84,7 @@ namespace mr {
 cudaError_t mr_check_words_batching(unsigned* out, bool reset);
 cudaError_t mr_check_words_context(unsigned* out, bool reset);
 cudaError_t mr_check_words_grouped_matmul(unsigned* out, bool reset);
+cudaError_t mr_check_words_layer(unsigned* out, bool reset);
 cudaError_t mr_check_words_permute(unsigned* out, bool reset);
 cudaError_t mr_check_words_unpermute(unsigned* out, bool reset);
 cudaError_t mr_check_words_update_expert(unsigned* out, bool reset);
@@ -94,7 +95,7 @@ extern "C" mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, 
 #ifdef MR_CHECKED
     if (!failures) return MR_ERR_PARAM_NULLPTR;
     cudaError_t (*readers[])(unsigned*, bool) = {mr::mr_check_words_batching, mr::mr_check_words_context,
-                                                 mr::mr_check_words_grouped_matmul,
+                                                 mr::mr_check_words_grouped_matmul, mr::mr_check_words_layer,
                                                  mr::mr_check_words_permute, mr::mr_check_words_unpermute,
                                                  mr::mr_check_words_update_expert};
     uint32_t total = 0u, first = 0u;
@@ -117,11 +118,12 @@ extern "C" mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, 
 
 namespace mr {
 cudaError_t waits_out_grouped_matmul(unsigned* out, bool reset);
+cudaError_t waits_out_layer(unsigned* out, bool reset);
 }  // namespace mr
 
 extern "C" mr_status mr_waits_out(uint32_t* count, int32_t reset) {
     if (!count) return MR_ERR_PARAM_NULLPTR;
-    cudaError_t (*readers[])(unsigned*, bool) = {mr::waits_out_grouped_matmul};
+    cudaError_t (*readers[])(unsigned*, bool) = {mr::waits_out_grouped_matmul, mr::waits_out_layer};
     *count = 0u;
     for (auto rd : readers) {
         unsigned n = 0u;
