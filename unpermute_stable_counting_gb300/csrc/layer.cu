@@ -91,8 +91,7 @@ __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;
 // ---------------------------------------------------------------------------
 // Step 1
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void load8(const void* base, int64_t at, int dt, float (&v)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + at);
+__device__ __forceinline__ void widen8(uint4 w, int dt, float (&v)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -112,19 +111,39 @@ __device__ void logits_step(const LayerArgs& a, float (*part)[16]) {
         float acc[EB][TB] = {};
         // past the last expert or token: the last one again, not stored
         if (a.vec_logits) {
-            for (int k = threadIdx.x * 8; k < a.H; k += kThreads * 8) {
-                float w[EB][8], x[8];
+            // rows as 16-byte pieces, the next pieces requested before these are used
+            const uint16_t* wp[EB];
+            const uint16_t* xp[TB];
+#pragma unroll
+            for (int i = 0; i < EB; ++i)
+                wp[i] = reinterpret_cast<const uint16_t*>(a.router) + min(e0 + i, a.E - 1) * a.router_stride;
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+                xp[j] = reinterpret_cast<const uint16_t*>(a.x) + min(t0 + j, a.T - 1) * a.x_stride;
+            uint4 wn[EB], xn[TB];
+            int k = threadIdx.x * 8;
+            auto fetch = [&](int at) {
+                at = min(at, a.H - 8);
+#pragma unroll
+                for (int i = 0; i < EB; ++i) wn[i] = *reinterpret_cast<const uint4*>(wp[i] + at);
+#pragma unroll
+                for (int j = 0; j < TB; ++j) xn[j] = *reinterpret_cast<const uint4*>(xp[j] + at);
+            };
+            fetch(k);
+            while (k < a.H) {
+                float w[EB][8], x[TB][8];
+#pragma unroll
+                for (int i = 0; i < EB; ++i) widen8(wn[i], a.router_dt, w[i]);
+#pragma unroll
+                for (int j = 0; j < TB; ++j) widen8(xn[j], a.x_dt, x[j]);
+                k += kThreads * 8;
+                fetch(k);
 #pragma unroll
                 for (int i = 0; i < EB; ++i)
-                    load8(a.router, min(e0 + i, a.E - 1) * a.router_stride + k, a.router_dt, w[i]);
 #pragma unroll
-                for (int j = 0; j < TB; ++j) {
-                    load8(a.x, min(t0 + j, a.T - 1) * a.x_stride + k, a.x_dt, x);
+                    for (int j = 0; j < TB; ++j)
 #pragma unroll
-                    for (int i = 0; i < EB; ++i)
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) acc[i][j] = fmaf(w[i][q], x[q], acc[i][j]);
-                }
+                        for (int q = 0; q < 8; ++q) acc[i][j] = fmaf(w[i][q], x[j][q], acc[i][j]);
             }
         } else {
             for (int k = threadIdx.x; k < a.H; k += kThreads) {
@@ -233,7 +252,7 @@ __device__ void choose(const LayerArgs& a, Tables& tb, int t, bool write) {
         const int e = lane + 32 * j;
         key[j] = e < a.E ? max(order_bits(a.bias ? score(v[j]) + a.bias[e] : v[j]), 1u) : 0u;
     }
-    float mine = 0.0f, total = 0.0f;  // lane r: the r-th expert's score
+    float mine = 0.0f;  // lane r: the r-th expert's logit, then its score
     int expert = 0;
     for (int r = 0; r < a.K; ++r) {
         uint32_t best = 0u;
@@ -252,10 +271,13 @@ __device__ void choose(const LayerArgs& a, Tables& tb, int t, bool write) {
                 key[j] = 0u;
                 l = v[j];
             }
-        const float s = score(__shfl_sync(0xffffffffu, l, e & 31));
-        total += s;
-        if (lane == r) mine = s, expert = e;
+        l = __shfl_sync(0xffffffffu, l, e & 31);
+        if (lane == r) mine = l, expert = e;
     }
+    mine = lane < a.K ? score(mine) : 0.0f;
+    float total = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane < a.K) {
         const float w = (a.keep ? mine : mine / fmaxf(total, 1.17549435e-38f)) * a.scale;
         atomicOr(&tb.mask[expert], 1ull << t);
@@ -347,6 +369,14 @@ __device__ void init_bars(Bars& b) {
 // ---------------------------------------------------------------------------
 // Step 2: h. Row groups of 8 (of one expert) [g0, g1) of all taken experts.
 // ---------------------------------------------------------------------------
+// A place in a ring of n stages, and the parity of its current round.
+struct Place {
+    uint32_t at = 0, round = 0;
+    __device__ __forceinline__ void next(uint32_t n) {
+        if (++at == n) at = 0, round ^= 1;
+    }
+};
+
 template <bool EIGHT, int COLS>
 __device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* map_x, const CUtensorMap* map_w8,
                        const CUtensorMap* map_w64, uint8_t* ring, const float* sx, Bars& bars, uint32_t tmem,
@@ -360,13 +390,13 @@ __device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
     if (warp == 0) {
         if (elect_one()) {
             proxy_fence();
-            uint32_t it = 0;
+            Place p;
             for (int n = 0; n < tiles; ++n) {
                 const int f = g0 + n * 16, l = min(f + 16, g1);
-                for (int kb = 0; kb < kbs; ++kb, ++it) {
-                    const uint32_t st = it % a.stages1, bar = smem_u32(&bars.full[st]);
-                    if (!mbar_wait(smem_u32(&bars.empty[st]), ((it / a.stages1) & 1) ^ 1, abort)) break;
-                    const uint32_t dst = smem_u32(ring) + st * a.stage1;
+                for (int kb = 0; kb < kbs; ++kb, p.next(a.stages1)) {
+                    const uint32_t bar = smem_u32(&bars.full[p.at]);
+                    if (!mbar_wait(smem_u32(&bars.empty[p.at]), p.round ^ 1, abort)) break;
+                    const uint32_t dst = smem_u32(ring) + p.at * a.stage1;
                     mbar_expect(bar, (l - f) * 2048 + x_bytes);
                     for (int g = f; g < l;) {
                         const int j = g / per, r = g - j * per;
@@ -392,14 +422,15 @@ __device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
         __syncwarp();
     } else if (warp == 1) {
         if (elect_one()) {
-            uint32_t it = 0, use = 0;  // stages and tensor memory buffers used
+            Place p;
+            uint32_t use = 0;  // tensor memory buffers used
             for (int n = 0; n < tiles; ++n) {
-                for (int kb = 0; kb < kbs; ++kb, ++it) {
-                    const uint32_t st = it % a.stages1, buf = use % kBufs;
+                for (int kb = 0; kb < kbs; ++kb, p.next(a.stages1)) {
+                    const uint32_t buf = use % kBufs;
                     if (EIGHT || kb == 0) mbar_wait(smem_u32(&bars.t_empty[buf]), ((use / kBufs) & 1) ^ 1, abort);
-                    if (!mbar_wait(smem_u32(&bars.full[st]), (it / a.stages1) & 1, abort)) break;
+                    if (!mbar_wait(smem_u32(&bars.full[p.at]), p.round, abort)) break;
                     tc_fence_after();
-                    const uint32_t at = smem_u32(ring) + st * a.stage1;
+                    const uint32_t at = smem_u32(ring) + p.at * a.stage1;
                     const uint64_t dg = smem_desc(at), du = smem_desc(at + 16384), dx = smem_desc(at + 32768);
                     const uint32_t d = tmem + buf * kBufCols;
 #pragma unroll
@@ -413,7 +444,7 @@ __device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
                             mma_16(d + 64, du + 2 * k, dx + 2 * k, idesc_16(128, 2 * COLS, a.bf16), add);
                         }
                     }
-                    tc_commit(smem_u32(&bars.empty[st]));
+                    tc_commit(smem_u32(&bars.empty[p.at]));
                     if (EIGHT || kb == kbs - 1) {
                         tc_commit(smem_u32(&bars.t_full[buf]));
                         ++use;
@@ -568,27 +599,31 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
     const int total = row0 < a.H ? experts * kbs : 0;
     const uint32_t a_bytes = a.rows2 * kLine;
     const uint32_t base = smem_u32(ring);
-    auto boxes = [&](int j) { return (__popcll(tb.mask[tb.active[j]]) + 15) / 16; };
-    auto request_h = [&](int unit, int j, int kb) {
-        const uint32_t st = unit % stages, dst = base + st * stage + a.stage2_a, bar = smem_u32(&bars.full[st]);
-        const int nb = boxes(j), s0 = tb.start[tb.active[j]];
+    auto boxes = [&](int e) { return (__popcll(tb.mask[e]) + 15) / 16; };
+    // the expert's weights of a stage, and its bytes of both operands announced
+    auto request_w = [&](const Place& p, int e, int nb, int kb) {
+        const uint32_t bar = smem_u32(&bars.full[p.at]);
+        mbar_expect(bar, a_bytes + nb * 2048 * (EIGHT ? 1 : 2));
+        tma_load_3d(base + p.at * stage, map_w2, bar, kb * kLineElems, row0, e);
+    };
+    auto request_h = [&](const Place& p, int nb, int s0, int kb) {
+        const uint32_t dst = base + p.at * stage + a.stage2_a, bar = smem_u32(&bars.full[p.at]);
         for (int b = 0; b < nb; ++b) {
             tma_load_2d(dst + b * 2048, map_h, bar, kb * kLineElems, s0 + 16 * b);
             if (!EIGHT) tma_load_2d(dst + (nb + b) * 2048, map_h, bar, kb * kLineElems, a.slots + s0 + 16 * b);
         }
     };
-    auto request_w = [&](int unit, int j, int kb) {
-        const uint32_t st = unit % stages, bar = smem_u32(&bars.full[st]);
-        mbar_expect(bar, a_bytes + boxes(j) * 2048 * (EIGHT ? 1 : 2));
-        tma_load_3d(base + st * stage, map_w2, bar, kb * kLineElems, row0, tb.active[j]);
-    };
     const int ahead = min(stages, total);
     if (warp == 0) {
-        if (elect_one())
-            for (int u = 0, j = 0, kb = 0; u < ahead; ++u) {
-                request_w(u, j, kb);
+        if (elect_one()) {
+            Place p;
+            int e = 0, nb = 0;
+            for (int u = 0, j = 0, kb = 0; u < ahead; ++u, p.next(stages)) {
+                if (kb == 0) e = tb.active[j], nb = boxes(e);
+                request_w(p, e, nb, kb);
                 if (++kb == kbs) kb = 0, ++j;
             }
+        }
         __syncwarp();
     }
     for (int i = threadIdx.x; i < 2 * a.T * a.rows2; i += kThreads) acc[i] = 0.0f;
@@ -596,37 +631,41 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
     if (warp == 0) {
         if (elect_one()) {
             proxy_fence();
-            for (int u = 0, j = 0, kb = 0; u < total; ++u) {
-                if (u >= ahead) {
-                    if (!mbar_wait(smem_u32(&bars.empty[u % stages]), ((u / stages) & 1) ^ 1, abort)) break;
-                    request_w(u, j, kb);
+            Place p;
+            for (int u = 0, j = 0; u < total; ++j) {
+                const int e = tb.active[j], nb = boxes(e), s0 = tb.start[e];
+                for (int kb = 0; kb < kbs; ++kb, ++u, p.next(stages)) {
+                    if (u >= ahead) {
+                        if (!mbar_wait(smem_u32(&bars.empty[p.at]), p.round ^ 1, abort)) continue;
+                        request_w(p, e, nb, kb);
+                    }
+                    request_h(p, nb, s0, kb);
                 }
-                request_h(u, j, kb);
-                if (++kb == kbs) kb = 0, ++j;
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (elect_one()) {
-            uint32_t u = 0, use = 0;
+            Place p;
+            uint32_t use = 0;
             for (int j = 0; j < (total ? experts : 0); ++j) {
-                const int nb = boxes(j);
+                const int nb = boxes(tb.active[j]);
                 const uint32_t idesc = EIGHT ? idesc_e4m3(128, 16 * nb) : idesc_16(128, 32 * nb, a.bf16);
-                for (int kb = 0; kb < kbs; ++kb, ++u) {
-                    const uint32_t st = u % stages, buf = use % kBufs;
+                for (int kb = 0; kb < kbs; ++kb, p.next(stages)) {
+                    const uint32_t buf = use % kBufs;
                     const int part = kb % kUnits;
                     if (EIGHT ? part == 0 : kb == 0)
                         mbar_wait(smem_u32(&bars.t_empty[buf]), ((use / kBufs) & 1) ^ 1, abort);
-                    if (!mbar_wait(smem_u32(&bars.full[st]), (u / stages) & 1, abort)) break;
+                    if (!mbar_wait(smem_u32(&bars.full[p.at]), p.round, abort)) break;
                     tc_fence_after();
-                    const uint64_t dw = smem_desc(base + st * stage), dh = smem_desc(base + st * stage + a.stage2_a);
+                    const uint64_t dw = smem_desc(base + p.at * stage), dh = smem_desc(base + p.at * stage + a.stage2_a);
                     const uint32_t d = tmem + buf * kBufCols + (EIGHT ? part * 2 * COLS : 0);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (EIGHT) mma_e4m3(d, dw + 2 * k, dh + 2 * k, idesc, k > 0);
                         else mma_16(d, dw + 2 * k, dh + 2 * k, idesc, k > 0 || kb > 0);
                     }
-                    tc_commit(smem_u32(&bars.empty[st]));
+                    tc_commit(smem_u32(&bars.empty[p.at]));
                     if (kb == kbs - 1 || (EIGHT && part == kUnits - 1)) {
                         tc_commit(smem_u32(&bars.t_full[buf]));
                         ++use;
@@ -683,7 +722,7 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
                 tc_fence_after();
                 uint32_t hi[COLS], lo[COLS];
                 tmem_load(hi, from + buf * kBufCols);
-                tmem_load(lo, from + buf * kBufCols + 16 * boxes(j));
+                tmem_load(lo, from + buf * kBufCols + 16 * boxes(e));
                 tmem_ld_wait(hi);
                 tmem_ld_wait(lo);
                 tc_fence_before();
@@ -763,12 +802,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // 2
     int most = 0;
-    const int experts = make_tables(a, tb, warp_sums, &most_smem, &most);
-    if (EIGHT)
-        for (int i = threadIdx.x; i < hb * 2 * COLS; i += kThreads) {
-            const int t = i % (2 * COLS);
-            sx[i] = t < a.T ? __ldcg(a.sx + i / (2 * COLS) * kMaxTokens + t) : 0.0f;
+    if (EIGHT)  // the scales of x, on their way while the experts are chosen
+        for (int i = threadIdx.x; i < hb * COLS / 2; i += kThreads) {
+            const int b = i / (COLS / 2), t = i % (COLS / 2) * 4;
+            copy_16(smem_u32(sx + b * 2 * COLS + t), a.sx + b * kMaxTokens + t);
         }
+    const int experts = make_tables(a, tb, warp_sums, &most_smem, &most);
+    copy_wait();
     __syncthreads();
     const int groups = experts * ((a.I + 7) / 8);
     const int g0 = (int)((int64_t)groups * blockIdx.x / gridDim.x);

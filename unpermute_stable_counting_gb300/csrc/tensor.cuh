@@ -105,17 +105,13 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
 }
 
 // ---------------------------------------------------------------------------
-// Asynchronous copies of single words (0 where `real` is false), and the
-// arrival on a barrier once the thread's earlier ones have landed.
+// Asynchronous copies of 16 bytes to shared memory (through L2 alone), and the
+// wait for the thread's earlier ones.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void copy_word(uint32_t dst, const float* src, bool real) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0)
-                 : "memory");
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy_words_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void copy_words_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // TMA tile loads (global -> shared, counted on an mbarrier)
