@@ -14,9 +14,9 @@
 //      share of the taken experts' W1/W3 rows, 8 rows at a time: rows of
 //      several experts share an instruction, since all of them meet all tokens,
 //      and a token keeps the products of its own experts
-//   3. every block takes an equal share of the rows of y and reads those rows
-//      of every taken expert's W2; a block so holds its rows' whole sum, and no
-//      sum crosses blocks
+//   3. every block takes about 100 rows of y and a share of the taken experts'
+//      W2 along k (lines of 128 bytes, over all experts); the shares' sums meet
+//      in memory after a last barrier
 // Equal shares matter more than whole tiles: with 8 experts of 2048 rows on
 // 152 SMs, tiles of 128 rows would leave one SM in six idle.
 // Copies run through a ring of TMA stages (one thread), instructions are
@@ -40,7 +40,7 @@ __device__ unsigned g_waits_out;
 constexpr int kThreads = 384, kWarps = kThreads / 32;
 constexpr int kMaxTokens = MR_MAX_LAYER_TOKENS, kMaxExperts = MR_MAX_LAYER_EXPERTS;
 constexpr int kLine = 128;            // bytes of a row per stage (the swizzle's width)
-constexpr int kMaxStages = 24;
+constexpr int kMaxStages = 24, kMaxSplits = 8;
 constexpr int kBufs = 4, kBufCols = 128;  // tensor memory
 static_assert(kMaxTokens == 64, "a token set is a 64-bit mask");
 
@@ -72,7 +72,8 @@ struct LayerArgs {
     int h_cols, slots;                // slots: rows of a part
     float* sh;                        // [ceil(I/128)][slots]
     unsigned* count;                  // [E][ceil(I/128)] row groups of h done
-    int rows2;                        // rows of y per block
+    int rows2, splits;                // step 3: rows of y per block, blocks that share them
+    float* part;                      // [splits][T][H] their sums
     int n1, stages1, stage1, stage2_a, ring_bytes;  // columns and stages of step 2, bytes
     int off_sx, off_acc, off_ring;    // dynamic shared memory, from its 1024-byte boundary
 };
@@ -103,7 +104,7 @@ __device__ __forceinline__ void widen8(uint4 w, int dt, float (&v)[8]) {
 
 // Logits of EB experts x TB tokens per block; its threads along k.
 template <int EB, int TB>
-__device__ void logits_step(const LayerArgs& a, float (*part)[16]) {
+__device__ void logits_step(const LayerArgs& a, float (*part)[32]) {
     const int nt = (a.T + TB - 1) / TB, tasks = (a.E + EB - 1) / EB * nt;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
@@ -224,7 +225,7 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 // One token per warp: the K experts of highest logit (or score + bias), ties to
 // the lowest index. V: values per lane.
 template <int V>
-__device__ void choose(const LayerArgs& a, Tables& tb, int t, bool write) {
+__device__ void choose(const LayerArgs& a, int t, bool write, uint16_t* ids, float* weights) {
     const int lane = threadIdx.x & 31;
     float v[V];
     float top = -INFINITY;
@@ -280,9 +281,10 @@ __device__ void choose(const LayerArgs& a, Tables& tb, int t, bool write) {
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane < a.K) {
         const float w = (a.keep ? mine : mine / fmaxf(total, 1.17549435e-38f)) * a.scale;
-        atomicOr(&tb.mask[expert], 1ull << t);
-        tb.weight[t * a.K + lane] = w;  // by token until the slots are known
-        tb.active[t * a.K + lane] = (uint16_t)expert;
+        if (ids) {
+            ids[t * a.K + lane] = (uint16_t)expert;
+            weights[t * a.K + lane] = w;
+        }
         if (write) {
             a.ids[t * a.K + lane] = expert;
             a.weights[t * a.K + lane] = w;
@@ -290,32 +292,38 @@ __device__ void choose(const LayerArgs& a, Tables& tb, int t, bool write) {
     }
 }
 
+__device__ void choose_any(const LayerArgs& a, int t, bool write, uint16_t* ids, float* weights) {
+    if (a.E <= 64) choose<2>(a, t, write, ids, weights);
+    else if (a.E <= 256) choose<8>(a, t, write, ids, weights);
+    else choose<kMaxExperts / 32>(a, t, write, ids, weights);
+}
+
 __device__ __forceinline__ int rank_of(unsigned long long mask, int t) {
     return __popcll(mask & ((1ull << t) - 1ull));
 }
 
 // Fills the tables; returns the number of experts taken, *most the largest number of tokens of one.
-__device__ int make_tables(const LayerArgs& a, Tables& tb, uint32_t* warp_sums, int* most_smem, int* most) {
-    for (int e = threadIdx.x; e < a.E; e += kThreads) tb.mask[e] = 0ull;
-    if (threadIdx.x == 0) *most_smem = 0;
-    __syncthreads();
-    for (int t = threadIdx.x >> 5; t < a.T; t += kWarps) {
-        const bool write = blockIdx.x == 0;
-        if (a.E <= 64) choose<2>(a, tb, t, write);
-        else if (a.E <= 256) choose<8>(a, tb, t, write);
-        else choose<kMaxExperts / 32>(a, tb, t, write);
-    }
-    __syncthreads();
-    // each thread's pairs, before the tables by slot take their place
+// chosen: the experts are in a.ids and a.weights; otherwise by token in the tables' place.
+__device__ int make_tables(const LayerArgs& a, Tables& tb, bool chosen, uint32_t* warp_sums, int* most_smem,
+                           int* most) {
+    // each thread's pairs of a token and an expert
     constexpr int kMine = (kMaxTokens * MR_MAX_LAYER_TOPK + kThreads - 1) / kThreads;
     float w[kMine];
     int ex[kMine];
+    const int pairs = a.T * a.K;
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
         const int i = threadIdx.x + j * kThreads;
-        ex[j] = i < a.T * a.K ? tb.active[i] : -1;
-        w[j] = i < a.T * a.K ? tb.weight[i] : 0.0f;
+        ex[j] = i >= pairs ? -1 : chosen ? __ldcg(a.ids + i) : tb.active[i];
+        w[j] = i >= pairs ? 0.0f : chosen ? __ldcg(a.weights + i) : tb.weight[i];
     }
+    for (int e = threadIdx.x; e < a.E; e += kThreads) tb.mask[e] = 0ull;
+    if (threadIdx.x == 0) *most_smem = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMine; ++j)
+        if (ex[j] >= 0) atomicOr(&tb.mask[ex[j]], 1ull << ((threadIdx.x + j * kThreads) / a.K));
+    __syncthreads();
     // experts of this thread: their slots, and their places among the taken ones
     constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
     uint32_t slots = 0u, taken = 0u;
@@ -581,14 +589,15 @@ __device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
 }
 
 // ---------------------------------------------------------------------------
-// Step 3: y. Rows [row0, row0 + rows2) of every taken expert's W2. The second
-// product's columns are the expert's slots; COLS of them per warpgroup, and
-// (8-bit weights) 32 / COLS lines of k per tensor memory buffer.
+// Step 3: y. Rows [row0, row0 + rows2) of the taken experts' W2, lines [u0, u1)
+// of k, counted over all of them. The second product's columns are an expert's
+// slots; COLS of them per warpgroup, and (8-bit weights) 32 / COLS lines per
+// tensor memory buffer.
 // ---------------------------------------------------------------------------
 template <bool EIGHT, int COLS>
 __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* map_w2, const CUtensorMap* map_h,
                        uint8_t* ring, float* acc, Bars& bars, uint32_t tmem, volatile uint32_t* abort, int experts,
-                       int row0, cg::grid_group& grid) {
+                       int row0, int split, cg::grid_group& grid) {
     constexpr int kLineElems = EIGHT ? kLine : kLine / 2;
     constexpr int kUnits = EIGHT ? 32 / COLS : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -596,7 +605,13 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
     const int stage = a.stage2_a + 2 * COLS * kLine * (EIGHT ? 1 : 2);
     // the instructions read 128 rows from a stage's start on, whatever rows2 is: 16 KB of slack
     const int stages = min(kMaxStages, (a.ring_bytes - 16384) / stage);
-    const int total = row0 < a.H ? experts * kbs : 0;
+    const bool real = row0 < a.H && split < a.splits;
+    const int u0 = real ? (int)((int64_t)experts * kbs * split / a.splits) : 0;
+    const int u1 = real ? (int)((int64_t)experts * kbs * (split + 1) / a.splits) : 0;
+    // experts with lines of this share (few lines: it may have none)
+    const int j0 = u0 / kbs, j1 = u1 > u0 ? (u1 + kbs - 1) / kbs : j0;
+    auto first_line = [&](int j) { return j == j0 ? u0 - j0 * kbs : 0; };
+    auto last_line = [&](int j) { return min(kbs, u1 - j * kbs); };
     const uint32_t a_bytes = a.rows2 * kLine;
     const uint32_t base = smem_u32(ring);
     auto boxes = [&](int e) { return (__popcll(tb.mask[e]) + 15) / 16; };
@@ -613,15 +628,13 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
             if (!EIGHT) tma_load_2d(dst + (nb + b) * 2048, map_h, bar, kb * kLineElems, a.slots + s0 + 16 * b);
         }
     };
-    const int ahead = min(stages, total);
+    const int ahead = min(stages, u1 - u0);
     if (warp == 0) {
         if (elect_one()) {
             Place p;
-            int e = 0, nb = 0;
-            for (int u = 0, j = 0, kb = 0; u < ahead; ++u, p.next(stages)) {
-                if (kb == 0) e = tb.active[j], nb = boxes(e);
-                request_w(p, e, nb, kb);
-                if (++kb == kbs) kb = 0, ++j;
+            for (int j = j0, u = 0; u < ahead; ++j) {
+                const int e = tb.active[j], nb = boxes(e), end = last_line(j);
+                for (int kb = first_line(j); kb < end && u < ahead; ++kb, ++u, p.next(stages)) request_w(p, e, nb, kb);
             }
         }
         __syncwarp();
@@ -632,9 +645,9 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
         if (elect_one()) {
             proxy_fence();
             Place p;
-            for (int u = 0, j = 0; u < total; ++j) {
-                const int e = tb.active[j], nb = boxes(e), s0 = tb.start[e];
-                for (int kb = 0; kb < kbs; ++kb, ++u, p.next(stages)) {
+            for (int j = j0, u = 0; j < j1; ++j) {
+                const int e = tb.active[j], nb = boxes(e), s0 = tb.start[e], end = last_line(j);
+                for (int kb = first_line(j); kb < end; ++kb, ++u, p.next(stages)) {
                     if (u >= ahead) {
                         if (!mbar_wait(smem_u32(&bars.empty[p.at]), p.round ^ 1, abort)) continue;
                         request_w(p, e, nb, kb);
@@ -648,13 +661,13 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
         if (elect_one()) {
             Place p;
             uint32_t use = 0;
-            for (int j = 0; j < (total ? experts : 0); ++j) {
-                const int nb = boxes(tb.active[j]);
+            for (int j = j0; j < j1; ++j) {
+                const int nb = boxes(tb.active[j]), k0 = first_line(j), end = last_line(j);
                 const uint32_t idesc = EIGHT ? idesc_e4m3(128, 16 * nb) : idesc_16(128, 32 * nb, a.bf16);
-                for (int kb = 0; kb < kbs; ++kb, p.next(stages)) {
+                for (int kb = k0; kb < end; ++kb, p.next(stages)) {
                     const uint32_t buf = use % kBufs;
-                    const int part = kb % kUnits;
-                    if (EIGHT ? part == 0 : kb == 0)
+                    const int part = (kb - k0) % kUnits;
+                    if (EIGHT ? part == 0 : kb == k0)
                         mbar_wait(smem_u32(&bars.t_empty[buf]), ((use / kBufs) & 1) ^ 1, abort);
                     if (!mbar_wait(smem_u32(&bars.full[p.at]), p.round, abort)) break;
                     tc_fence_after();
@@ -663,10 +676,10 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (EIGHT) mma_e4m3(d, dw + 2 * k, dh + 2 * k, idesc, k > 0);
-                        else mma_16(d, dw + 2 * k, dh + 2 * k, idesc, k > 0 || kb > 0);
+                        else mma_16(d, dw + 2 * k, dh + 2 * k, idesc, k > 0 || kb > k0);
                     }
                     tc_commit(smem_u32(&bars.empty[p.at]));
-                    if (kb == kbs - 1 || (EIGHT && part == kUnits - 1)) {
+                    if (kb == end - 1 || (EIGHT && part == kUnits - 1)) {
                         tc_commit(smem_u32(&bars.t_full[buf]));
                         ++use;
                     }
@@ -681,22 +694,22 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
         const int wrow = min(row0 + row, a.H - 1);
         float* mine = acc + half * a.T * a.rows2 + row;  // [token][row]
         uint32_t use = 0;
-        for (int j = 0; j < (total ? experts : 0); ++j) {
-            const int e = tb.active[j], s0 = tb.start[e], tokens = __popcll(tb.mask[e]);
+        for (int j = j0; j < j1; ++j) {
+            const int e = tb.active[j], s0 = tb.start[e], tokens = __popcll(tb.mask[e]), end = last_line(j);
             float y[COLS];
             if (EIGHT) {
 #pragma unroll
                 for (int c = 0; c < COLS; ++c) y[c] = 0.0f;
                 const float* w = a.s2 + ((int64_t)e * hb + wrow / kScaleBlock) * ib;
                 const int lc = half * COLS + lane % COLS;
-                for (int kb = 0; kb < kbs; kb += kUnits, ++use) {
+                for (int kb = first_line(j); kb < end; kb += kUnits, ++use) {
                     const uint32_t buf = use % kBufs;
                     // lane: the scale of one column and line
                     const int lk = kb + lane / COLS;
-                    const float sv = lk < kbs && lc < tokens ? __ldcg(a.sh + lk * a.slots + s0 + lc) : 0.0f;
+                    const float sv = lk < end && lc < tokens ? __ldcg(a.sh + lk * a.slots + s0 + lc) : 0.0f;
                     float sw[kUnits];
 #pragma unroll
-                    for (int u = 0; u < kUnits; ++u) sw[u] = kb + u < kbs ? w[kb + u] : 0.0f;
+                    for (int u = 0; u < kUnits; ++u) sw[u] = kb + u < end ? w[kb + u] : 0.0f;
                     mbar_wait(smem_u32(&bars.t_full[buf]), (use / kBufs) & 1, abort);
                     tc_fence_after();
                     uint32_t v[kUnits][COLS];
@@ -709,7 +722,7 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
                     if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[buf]));
 #pragma unroll
                     for (int u = 0; u < kUnits; ++u) {
-                        if (kb + u >= kbs) break;  // lines past the end: whatever the buffer held
+                        if (kb + u >= end) break;  // lines past the end: whatever the buffer held
 #pragma unroll
                         for (int c = 0; c < COLS; ++c)
                             y[c] = fmaf(__uint_as_float(v[u][c]), sw[u] * __shfl_sync(0xffffffffu, sv, u * COLS + c),
@@ -744,14 +757,27 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * a.rows2; i += kThreads) {
-        const int t = i / a.rows2, r = row0 + i - t * a.rows2;
-        if (r >= a.H) continue;
-        const float v = acc[i] + acc[a.T * a.rows2 + i];
-        const int64_t at = t * a.y_stride + r;
+    auto store = [&](int64_t at, float v) {
         if (a.x_dt == MR_DTYPE_F32) reinterpret_cast<float*>(a.y)[at] = v;
         else if (a.x_dt == MR_DTYPE_F16) reinterpret_cast<uint16_t*>(a.y)[at] = Elem<MR_DTYPE_F16>::from_f32(v);
         else reinterpret_cast<uint16_t*>(a.y)[at] = Elem<MR_DTYPE_BF16>::from_f32(v);
+    };
+    if (real)
+        for (int i = threadIdx.x; i < a.T * a.rows2; i += kThreads) {
+            const int t = i / a.rows2, r = row0 + i - t * a.rows2;
+            if (r >= a.H) continue;
+            const float v = acc[i] + acc[a.T * a.rows2 + i];
+            if (a.splits == 1) store(t * a.y_stride + r, v);
+            else a.part[((int64_t)split * a.T + t) * a.H + r] = v;
+        }
+    if (a.splits == 1) return;
+    grid.sync();
+    const int n = a.T * a.H;
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) {
+        float v = __ldcg(a.part + i);
+        for (int k = 1; k < a.splits; ++k) v += __ldcg(a.part + (int64_t)k * n + i);
+        const int t = i / a.H;
+        store(t * a.y_stride + i - t * a.H, v);
     }
 }
 
@@ -767,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t drain_bar;
     __shared__ uint32_t tmem_base, abort_word, flag, warp_sums[32];
     __shared__ int most_smem;
-    __shared__ float part[kWarps][16];
+    __shared__ float part[kWarps][32];
     cg::grid_group grid = cg::this_grid();
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Tables& tb = *reinterpret_cast<Tables*>(smem);
@@ -795,19 +821,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (EIGHT)
         for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.E * ib; i += gridDim.x * kThreads) a.count[i] = 0u;
     stage_rows<EIGHT>(a);
+    // few pairs: a block per pair; else the fewest rows read that still occupy every block once
     if (a.T * a.E <= 4 * (int)gridDim.x) logits_step<1, 1>(a, part);
-    else logits_step<4, 4>(a, part);
+    else if ((a.T + 3) / 4 * ((a.E + 3) / 4) <= (int)gridDim.x) logits_step<4, 4>(a, part);
+    else logits_step<4, 8>(a, part);
     proxy_fence();
     grid.sync();
 
     // 2
+    // Up to a token per warp every block chooses all tokens' experts for itself, which saves a
+    // barrier (1.3 us); more tokens are a block's each.
+    const bool shared_choice = a.T > kWarps;
+    const int token = shared_choice ? (warp == 0 ? (int)blockIdx.x : a.T) : warp;
+    if (token < a.T)
+        choose_any(a, token, shared_choice || blockIdx.x == 0, shared_choice ? nullptr : tb.active, tb.weight);
+    if (shared_choice) grid.sync();
+    else __syncthreads();
     int most = 0;
     if (EIGHT)  // the scales of x, on their way while the experts are chosen
         for (int i = threadIdx.x; i < hb * COLS / 2; i += kThreads) {
             const int b = i / (COLS / 2), t = i % (COLS / 2) * 4;
             copy_16(smem_u32(sx + b * 2 * COLS + t), a.sx + b * kMaxTokens + t);
         }
-    const int experts = make_tables(a, tb, warp_sums, &most_smem, &most);
+    const int experts = make_tables(a, tb, shared_choice, warp_sums, &most_smem, &most);
     copy_wait();
     __syncthreads();
     const int groups = experts * ((a.I + 7) / 8);
@@ -819,10 +855,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
 
     // 3
-    const int row0 = blockIdx.x * a.rows2;
-    if (most <= 16) step_y<EIGHT, 8>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, grid);
-    else if (most <= 32) step_y<EIGHT, 16>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, grid);
-    else step_y<EIGHT, 32>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, grid);
+    const int row0 = blockIdx.x / a.splits * a.rows2, split = blockIdx.x % a.splits;
+    if (most <= 16)
+        step_y<EIGHT, 8>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, split, grid);
+    else if (most <= 32)
+        step_y<EIGHT, 16>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, split, grid);
+    else
+        step_y<EIGHT, 32>(a, tb, &maps.w2, &maps.h, ring, acc, bars2, tmem, abort, experts, row0, split, grid);
 
     __syncthreads();
     if (abort_word) {
@@ -852,13 +891,21 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 // Workspace regions, 256-byte aligned.
 struct LayerPlan {
     int64_t xs_stride, hs_stride, h_cols, slots;
-    uint64_t logits, xs, sx, hf, hs, sh, count, bytes;
+    int rows2, splits;
+    uint64_t logits, xs, sx, hf, hs, sh, count, part, bytes;
     LayerPlan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t K, bool eight) {
         const int64_t ib = ceil_div(I, kScaleBlock), hb = ceil_div(H, kScaleBlock);
         slots = ceil_div(T * K, 16) * 16 + 64;  // a box of 16 slots may start at any slot
         h_cols = ib * kScaleBlock;
         xs_stride = eight ? hb * kScaleBlock : (int64_t)align_up(2 * H, 128);
         hs_stride = eight ? h_cols : (int64_t)align_up(2 * I, 128);
+        // Step 3: the most shares of k with at most 128 rows per block: a line of W2 then has about 100
+        // rows, and the fixed cost of a line (waits, four instructions) stays below its time in HBM. With
+        // one share and 48 rows (hidden 7168) step 3 of one token took 39 us, its bytes 17 us.
+        const int grid = device_sm_count();
+        splits = 1;
+        while (splits < kMaxSplits && ceil_div(H, grid / (splits + 1)) <= 128) ++splits;
+        rows2 = ceil_div(ceil_div(H, grid / splits), 8) * 8;
         uint64_t at = 0;
         auto take = [&](uint64_t n) {
             const uint64_t p = at;
@@ -872,6 +919,7 @@ struct LayerPlan {
         hs = take((eight ? 1 : 2) * slots * hs_stride);
         sh = take(eight ? ib * slots * 4 : 0);
         count = take(eight ? E * ib * 4 : 0);
+        part = take(splits > 1 ? splits * T * H * 4 : 0);
         bytes = at;
     }
 };
@@ -1011,7 +1059,9 @@ extern "C" mr_status moe_layer(const void* x, int32_t xDtype, int64_t xStride, c
     a.slots = (int)p.slots;
     a.sh = reinterpret_cast<float*>(w + p.sh);
     a.count = reinterpret_cast<unsigned*>(w + p.count);
-    a.rows2 = ceil_div(ceil_div(hidden, grid), 8) * 8;
+    a.rows2 = p.rows2;
+    a.splits = p.splits;
+    a.part = reinterpret_cast<float*>(w + p.part);
     if (a.rows2 > 128) return MR_ERR_UNSUPPORTED;  // a device with fewer SMs
     a.n1 = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
 
