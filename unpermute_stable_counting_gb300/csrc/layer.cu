@@ -104,7 +104,7 @@ __device__ __forceinline__ void widen8(uint4 w, int dt, float (&v)[8]) {
 
 // Logits of EB experts x TB tokens per block; its threads along k.
 template <int EB, int TB>
-__device__ void logits_step(const LayerArgs& a, float (*part)[32]) {
+__device__ __forceinline__ void logits_step(const LayerArgs& a, float (*part)[32]) {
     const int nt = (a.T + TB - 1) / TB, tasks = (a.E + EB - 1) / EB * nt;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
@@ -182,7 +182,7 @@ __device__ void logits_step(const LayerArgs& a, float (*part)[32]) {
 
 // Rows of x as the tensor operand: e4m3 blocks with scales, or the same 16 bits.
 template <bool EIGHT>
-__device__ void stage_rows(const LayerArgs& a) {
+__device__ __forceinline__ void stage_rows(const LayerArgs& a) {
     const int lane = threadIdx.x & 31;
     const int kb = (a.H + kScaleBlock - 1) / kScaleBlock;
     // blocks from the last one down: the first ones have logits to do
@@ -225,7 +225,7 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 // One token per warp: the K experts of highest logit (or score + bias), ties to
 // the lowest index. V: values per lane.
 template <int V>
-__device__ void choose(const LayerArgs& a, int t, bool write, uint16_t* ids, float* weights) {
+__device__ __forceinline__ void choose(const LayerArgs& a, int t, bool write, uint16_t* ids, float* weights) {
     const int lane = threadIdx.x & 31;
     float v[V];
     float top = -INFINITY;
@@ -292,7 +292,7 @@ __device__ void choose(const LayerArgs& a, int t, bool write, uint16_t* ids, flo
     }
 }
 
-__device__ void choose_any(const LayerArgs& a, int t, bool write, uint16_t* ids, float* weights) {
+__device__ __forceinline__ void choose_any(const LayerArgs& a, int t, bool write, uint16_t* ids, float* weights) {
     if (a.E <= 64) choose<2>(a, t, write, ids, weights);
     else if (a.E <= 256) choose<8>(a, t, write, ids, weights);
     else choose<kMaxExperts / 32>(a, t, write, ids, weights);
@@ -304,7 +304,7 @@ __device__ __forceinline__ int rank_of(unsigned long long mask, int t) {
 
 // Fills the tables; returns the number of experts taken, *most the largest number of tokens of one.
 // chosen: the experts are in a.ids and a.weights; otherwise by token in the tables' place.
-__device__ int make_tables(const LayerArgs& a, Tables& tb, bool chosen, uint32_t* warp_sums, int* most_smem,
+__device__ __forceinline__ int make_tables(const LayerArgs& a, Tables& tb, bool chosen, uint32_t* warp_sums, int* most_smem,
                            int* most) {
     // each thread's pairs of a token and an expert
     constexpr int kMine = (kMaxTokens * MR_MAX_LAYER_TOPK + kThreads - 1) / kThreads;
@@ -369,7 +369,7 @@ __device__ int make_tables(const LayerArgs& a, Tables& tb, bool chosen, uint32_t
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages], t_full[kBufs], t_empty[kBufs];
 };
-__device__ void init_bars(Bars& b) {
+__device__ __forceinline__ void init_bars(Bars& b) {
     for (int i = 0; i < kMaxStages; ++i) mbar_init(smem_u32(&b.full[i]), 1), mbar_init(smem_u32(&b.empty[i]), 1);
     for (int i = 0; i < kBufs; ++i) mbar_init(smem_u32(&b.t_full[i]), 1), mbar_init(smem_u32(&b.t_empty[i]), 8);
 }
@@ -386,7 +386,7 @@ struct Place {
 };
 
 template <bool EIGHT, int COLS>
-__device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* map_x, const CUtensorMap* map_w8,
+__device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* map_x, const CUtensorMap* map_w8,
                        const CUtensorMap* map_w64, uint8_t* ring, const float* sx, Bars& bars, uint32_t tmem,
                        volatile uint32_t* abort, uint32_t* flag, int g0, int g1) {
     constexpr int kLineElems = EIGHT ? kLine : kLine / 2;
@@ -398,6 +398,7 @@ __device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
     if (warp == 0) {
         if (elect_one()) {
             proxy_fence();
+            const uint64_t policy = evict_first();
             Place p;
             for (int n = 0; n < tiles; ++n) {
                 const int f = g0 + n * 16, l = min(f + 16, g1);
@@ -413,13 +414,13 @@ __device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
                         int done = 0;
                         for (; done + 8 <= run; done += 8) {
                             const uint32_t to = dst + (g - f + done) * 1024;
-                            tma_load_3d(to, map_w64, bar, kb * kLineElems, (r + done) * 8, plane);
-                            tma_load_3d(to + 16384, map_w64, bar, kb * kLineElems, (r + done) * 8, plane + 1);
+                            tma_load_3d_hint(to, map_w64, bar, kb * kLineElems, (r + done) * 8, plane, policy);
+                            tma_load_3d_hint(to + 16384, map_w64, bar, kb * kLineElems, (r + done) * 8, plane + 1, policy);
                         }
                         for (; done < run; ++done) {
                             const uint32_t to = dst + (g - f + done) * 1024;
-                            tma_load_3d(to, map_w8, bar, kb * kLineElems, (r + done) * 8, plane);
-                            tma_load_3d(to + 16384, map_w8, bar, kb * kLineElems, (r + done) * 8, plane + 1);
+                            tma_load_3d_hint(to, map_w8, bar, kb * kLineElems, (r + done) * 8, plane, policy);
+                            tma_load_3d_hint(to + 16384, map_w8, bar, kb * kLineElems, (r + done) * 8, plane + 1, policy);
                         }
                         g += run;
                     }
@@ -595,7 +596,7 @@ __device__ void step_h(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
 // tensor memory buffer.
 // ---------------------------------------------------------------------------
 template <bool EIGHT, int COLS>
-__device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* map_w2, const CUtensorMap* map_h,
+__device__ __forceinline__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* map_w2, const CUtensorMap* map_h,
                        uint8_t* ring, float* acc, Bars& bars, uint32_t tmem, volatile uint32_t* abort, int experts,
                        int row0, int split, cg::grid_group& grid) {
     constexpr int kLineElems = EIGHT ? kLine : kLine / 2;
@@ -614,12 +615,13 @@ __device__ void step_y(const LayerArgs& a, const Tables& tb, const CUtensorMap* 
     auto last_line = [&](int j) { return min(kbs, u1 - j * kbs); };
     const uint32_t a_bytes = a.rows2 * kLine;
     const uint32_t base = smem_u32(ring);
+    const uint64_t policy = evict_first();
     auto boxes = [&](int e) { return (__popcll(tb.mask[e]) + 15) / 16; };
     // the expert's weights of a stage, and its bytes of both operands announced
     auto request_w = [&](const Place& p, int e, int nb, int kb) {
         const uint32_t bar = smem_u32(&bars.full[p.at]);
         mbar_expect(bar, a_bytes + nb * 2048 * (EIGHT ? 1 : 2));
-        tma_load_3d(base + p.at * stage, map_w2, bar, kb * kLineElems, row0, e);
+        tma_load_3d_hint(base + p.at * stage, map_w2, bar, kb * kLineElems, row0, e, policy);
     };
     auto request_h = [&](const Place& p, int nb, int s0, int kb) {
         const uint32_t dst = base + p.at * stage + a.stage2_a, bar = smem_u32(&bars.full[p.at]);
