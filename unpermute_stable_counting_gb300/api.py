@@ -8,6 +8,7 @@ workspace, when the caller does not pass them) and the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -338,54 +339,102 @@ def _blocks(n: int) -> int:
     return -(-n // _BLOCK)
 
 
-def _float_dt(name, t, table=None):
-    dt = (table or _TORCH_TO_DT).get(t.dtype)
+# The expert products are called per layer of a decode step: what a call costs on
+# the host is part of its latency. So their checks read each tensor's attributes
+# once, pointers go to ctypes as plain ints, pairs of strides as arrays of one
+# type, and workspace sizes (pure functions of the sizes) are kept.
+_Pair = ctypes.c_int64 * 2
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, index):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _float_dt(name, t, table=_TORCH_TO_DT):
+    dt = table.get(t.dtype)
     if dt is None:
-        raise TypeError(f"{name} dtype {t.dtype} is not f16/bf16/f32" + ("/e4m3" if table else ""))
+        raise TypeError(f"{name} dtype {t.dtype} is not f16/bf16/f32" + ("/e4m3" if DT_E4M3 in table.values() else ""))
     return dt
 
 
-def _require_rows(name, t, dims):
-    """A CUDA tensor of `dims` dimensions whose rows have adjacent elements."""
-    _require_cuda(name, t, strided=True)
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _rows_of(name, t, dims):
+    """Shape and strides of a CUDA tensor of `dims` dimensions whose rows have
+    adjacent elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have adjacent elements in a row")
+    return shape, strides
 
 
-def _row_stride(t):
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+def _row_stride(shape, strides):
+    return strides[-2] if shape[-2] > 1 else max(strides[-2], shape[-1])
 
 
-def _matrix_strides(name, t):
-    """{row, matrix} strides of weights [..., rows, cols] with evenly spaced matrices."""
-    row = _row_stride(t)
-    if t.dim() == 4 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+def _matrix_strides(name, shape, strides, size=1):
+    """{row, matrix} byte strides of weights [..., rows, cols] with evenly spaced matrices."""
+    row = _row_stride(shape, strides)
+    if len(shape) == 4 and shape[0] > 1 and strides[0] != shape[1] * strides[1]:
         raise ValueError(f"{name} must have evenly spaced matrices")
-    matrix = t.stride(-3) if t.shape[-3] > 1 else t.shape[-2] * row
-    return row, matrix
+    matrix = strides[-3] if shape[-3] > 1 else shape[-2] * row
+    return _Pair(row * size, matrix * size)
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _vector(name, t, dtype, index, shape=None):
+    """The address of a contiguous tensor (None: no tensor)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    _same_device(name, t, index)
+    return t.data_ptr()
 
 
-def _aligned_rows(rows: int, cols: int, device):
-    """e4m3 [rows, cols] whose rows start on 16 bytes."""
-    return torch.empty((rows, -(-cols // 16) * 16), dtype=_E4M3, device=device)[:, :cols]
+def _same_device(name, t, index):
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+
+
+def _workspace(workspace, size, index):
+    if workspace is None:
+        return torch.empty(max(size, 1), dtype=torch.uint8, device=f"cuda:{index}")
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.dtype != torch.uint8:
+        raise TypeError("workspace must be a CUDA tensor of uint8")
+    _same_device("workspace", workspace, index)
+    return workspace
+
+
+def _wide_rows(lead, cols, index):
+    """e4m3 [*lead, cols] whose rows start on 16 bytes."""
+    wide = -(-cols // 16) * 16
+    t = torch.empty((*lead, wide), dtype=_E4M3, device=f"cuda:{index}")
+    return t if wide == cols else t[..., :cols]
 
 
 def quantize_outputs(shape, device, block_rows: int = 1) -> dict:
     """Allocate the output tensors of one moe_quantize call for x of `shape`:
     rows start on 16 bytes, as the expert products take them."""
     *lead, rows, cols = (int(v) for v in shape)
-    wide = -(-cols // 16) * 16
-    values = torch.empty((*lead, rows, wide), dtype=_E4M3, device=device)[..., :cols]
-    return dict(values=values, scales=torch.empty((*lead, rows if block_rows == 1 else _blocks(rows), _blocks(cols)),
-                                                  dtype=torch.float32, device=device))
+    device = torch.device(device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    return dict(values=_wide_rows((*lead, rows), cols, index),
+                scales=torch.empty((*lead, rows if block_rows == 1 else _blocks(rows), _blocks(cols)),
+                                   dtype=torch.float32, device=f"cuda:{index}"))
 
 
 def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = None, stream=None) -> dict:
@@ -397,38 +446,50 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
     (int64 [1] on the device): rows at or past it are not written."""
     if block_rows not in (1, _BLOCK):
         raise ValueError("block_rows must be 1 or 128")
-    _require_rows("x", x, 2 if block_rows == 1 else x.dim())
-    if x.dim() < 2 or x.dim() > 4:
+    dims = 2 if block_rows == 1 else x.dim()
+    shape, strides = _rows_of("x", x, dims)
+    if not 2 <= dims <= 4:
         raise ValueError("x must have 2 to 4 dimensions")
-    dt = _float_dt("x", x)
-    _require_cuda("num_rows", num_rows, torch.int64)
-    rows, cols = int(x.shape[-2]), int(x.shape[-1])
-    batch = x.numel() // max(1, rows * cols)
-    dev = x.device
+    dt, index = _float_dt("x", x), x.get_device()
+    rows, cols = shape[-2], shape[-1]
+    sshape = (*shape[:-2], rows if block_rows == 1 else _blocks(rows), _blocks(cols))
     if out is None:
-        out = quantize_outputs(x.shape, dev, block_rows)
-    values, scales = out["values"], out["scales"]
-    _require_rows("values", values, x.dim())
-    _require_cuda("values", values, _E4M3, strided=True)
-    _require_cuda("scales", scales, torch.float32, strided=block_rows == 1)
-    if values.shape != x.shape or tuple(scales.shape) != (*x.shape[:-2], rows if block_rows == 1 else _blocks(rows),
-                                                          _blocks(cols)):
-        raise ValueError("values and scales must have the shapes of quantize_outputs")
-    _same_device(dev, num_rows=num_rows, values=values, scales=scales)
-    xs = vs = ss = None
-    if x.dim() == 2:
-        xs, vs = (rows * _row_stride(x), _row_stride(x)), (rows * _row_stride(values), _row_stride(values))
+        values = _wide_rows(shape[:-1], cols, index)
+        scales = torch.empty(sshape, dtype=torch.float32, device=f"cuda:{index}")
+        out = dict(values=values, scales=scales)
     else:
-        (xr, xm), (vr, vm) = _matrix_strides("x", x), _matrix_strides("values", values)
-        xs, vs = (xm, xr), (vm, vr)
+        values, scales = out["values"], out["scales"]
+    vshape, vstrides = _rows_of("values", values, dims)
+    if values.dtype != _E4M3 or vshape != shape:
+        raise ValueError("values must be e4m3 of x's shape")
+    _same_device("values", values, index)
+    ss = None
     if block_rows == 1:
-        ss = int64_array((max(1, scales.stride(0)), max(1, scales.stride(1))))
-    st = lib().moe_quantize(_ptr(x), dt, max(1, batch), rows, cols, int64_array(xs), block_rows, _ptr(num_rows),
-                            _ptr(values), int64_array(vs), _ptr(scales), ss, _stream(stream, dev))
+        if not scales.is_cuda or scales.dtype != torch.float32 or scales.shape != sshape:
+            raise ValueError(f"scales must be float32 {list(sshape)}")
+        _same_device("scales", scales, index)
+        s0, s1 = scales.stride()
+        ss = _Pair(max(1, s0), max(1, s1))
+        saddr = scales.data_ptr()
+        xs, vs = _Pair(0, _row_stride(shape, strides)), _Pair(0, _row_stride(vshape, vstrides))
+        batch = 1
+    else:
+        saddr = _vector("scales", scales, torch.float32, index, sshape)
+        batch = x.numel() // max(1, rows * cols)
+        if dims == 2:
+            xs, vs = _Pair(0, _row_stride(shape, strides)), _Pair(0, _row_stride(vshape, vstrides))
+        else:
+            xs, vs = _matrix_strides("x", shape, strides), _matrix_strides("values", vshape, vstrides)
+            xs[0], xs[1] = xs[1], xs[0]
+            vs[0], vs[1] = vs[1], vs[0]
+    st = lib().moe_quantize(x.data_ptr(), dt, max(1, batch), rows, cols, xs, block_rows,
+                            _vector("num_rows", num_rows, torch.int64, index), values.data_ptr(), vs, saddr, ss,
+                            _raw_stream(stream, index))
     _check(st, "moe_quantize")
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def grouped_matmul_workspace_size(rows: int, cols: int, x_dtype: int) -> int:
     ws = ctypes.c_uint64(0)
     _check(lib().moe_grouped_matmul_get_workspace_size(rows, cols, x_dtype, ctypes.byref(ws)),
@@ -436,48 +497,53 @@ def grouped_matmul_workspace_size(rows: int, cols: int, x_dtype: int) -> int:
     return int(ws.value)
 
 
-def _expert_rows(x, x_scales, group_list, num_rows):
+def _expert_rows(x, x_scales, group_list):
     """Checks of the rows and groups that both products take."""
-    _require_rows("x", x, 2)
-    dt = _float_dt("x", x, _FLOAT_OR_E4M3)
-    _require_cuda("group_list", group_list, torch.int64)
-    _require_cuda("num_rows", num_rows, torch.int64)
-    if group_list is not None and (group_list.dim() != 2 or group_list.shape[1] != 2):
-        raise ValueError("group_list must be [groups, 2]")
-    strides = None
+    shape, strides = _rows_of("x", x, 2)
+    dt, index = _float_dt("x", x, _FLOAT_OR_E4M3), x.get_device()
+    sa = ss = None
     if dt == DT_E4M3:
         if x_scales is None:
             raise ValueError("e4m3 rows need x_scales")
-        _require_cuda("x_scales", x_scales, torch.float32, strided=True)
-        if tuple(x_scales.shape) != (x.shape[0], _blocks(int(x.shape[1]))):
+        if not isinstance(x_scales, torch.Tensor) or not x_scales.is_cuda or x_scales.dtype != torch.float32:
+            raise TypeError("x_scales must be a CUDA tensor of float32")
+        if x_scales.shape != (shape[0], _blocks(shape[1])):
             raise ValueError("x_scales must be [rows, ceil(cols/128)]")
-        strides = int64_array(x_scales.stride())
+        _same_device("x_scales", x_scales, index)
+        sa, ss = x_scales.data_ptr(), _Pair(*x_scales.stride())
     elif x_scales is not None:
         raise ValueError("x_scales belong to e4m3 rows")
-    _same_device(x.device, x_scales=x_scales, group_list=group_list, num_rows=num_rows)
-    return dt, strides
+    ga, groups = _vector("group_list", group_list, torch.int64, index), -1
+    if group_list is not None:
+        if group_list.dim() != 2 or group_list.shape[1] != 2:
+            raise ValueError("group_list must be [groups, 2]")
+        groups = group_list.shape[0]
+    return dt, index, shape, _row_stride(shape, strides), sa, ss, ga, groups
 
 
-def _expert_weights(name, w, scales, shape):
-    _require_rows(name, w, len(shape))
-    _require_cuda(name, w, _E4M3, strided=True)
-    _require_cuda(name + "_scales", scales, torch.float32)
-    if tuple(w.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(w.shape)}")
-    want = (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1]))
-    if scales is None or tuple(scales.shape) != want:
-        raise ValueError(f"{name}_scales must be {list(want)}")
-    return int64_array(_matrix_strides(name, w))
+def _expert_weights(name, w, scales, shape, index):
+    """Address and strides of e4m3 weights of `shape`, address of their scales."""
+    wshape, strides = _rows_of(name, w, len(shape))
+    if w.dtype != _E4M3:
+        raise TypeError(f"{name} must have dtype {_E4M3}, got {w.dtype}")
+    if wshape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(wshape)}")
+    _same_device(name, w, index)
+    if scales is None:
+        raise ValueError(f"{name} needs its scales")
+    sa = _vector(name + "_scales", scales, torch.float32, index, (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1])))
+    return w.data_ptr(), _matrix_strides(name, wshape, strides), sa
 
 
-def _out_rows(out, rows, cols, dtype, dev):
+def _out_rows(out, rows, cols, dtype, index):
     if out is None:
-        out = dict(y=torch.empty((rows, cols), dtype=dtype, device=dev))
+        out = dict(y=torch.empty((rows, cols), dtype=dtype, device=f"cuda:{index}"))
     y = out["y"]
-    _require_rows("y", y, 2)
-    if tuple(y.shape) != (rows, cols):
+    shape, strides = _rows_of("y", y, 2)
+    if shape != (rows, cols):
         raise ValueError(f"y must be [{rows}, {cols}]")
-    return out, y, _float_dt("y", y)
+    _same_device("y", y, index)
+    return out, y.data_ptr(), _float_dt("y", y), _row_stride(shape, strides)
 
 
 def moe_grouped_matmul(x, weights, weight_scales, group_list=None, *, x_scales=None, num_rows=None,
@@ -490,25 +556,24 @@ def moe_grouped_matmul(x, weights, weight_scales, group_list=None, *, x_scales=N
     group_list: int64 [groups, 2] of (expert, rows) on the device (the
     batching's groupList); None: all rows with expert 0. num_rows: the
     batching's actualTokenNum. expert_base: the list's id of weights[0]."""
-    dt, xss = _expert_rows(x, x_scales, group_list, num_rows)
-    if weights.dim() != 3 or weights.shape[2] != x.shape[1]:
+    dt, index, (rows, K), xst, xsa, xss, ga, groups = _expert_rows(x, x_scales, group_list)
+    if weights.dim() != 3 or weights.shape[2] != K:
         raise ValueError("weights must be [experts, out_cols, cols]")
-    E, N, K = (int(v) for v in weights.shape)
-    rows, dev = int(x.shape[0]), x.device
-    wst = _expert_weights("weights", weights, weight_scales, (E, N, K))
-    out, y, ydt = _out_rows(out, rows, N, out_dtype, dev)
-    _same_device(dev, weights=weights, weight_scales=weight_scales, y=y)
-    if workspace is None and dt != DT_E4M3:
-        workspace = torch.empty(max(grouped_matmul_workspace_size(rows, K, dt), 1), dtype=torch.uint8, device=dev)
-    st = lib().moe_grouped_matmul(
-        _ptr(x), dt, _row_stride(x), _ptr(x_scales), xss, _ptr(weights), wst, _ptr(weight_scales),
-        _ptr(group_list), -1 if group_list is None else int(group_list.shape[0]), _ptr(num_rows),
-        int(expert_base), rows, E, N, K, _ptr(y), ydt, _row_stride(y), _ptr(workspace),
-        0 if workspace is None else int(workspace.numel()), _stream(stream, dev))
+    E, N = weights.shape[0], weights.shape[1]
+    wa, wst, wsa = _expert_weights("weights", weights, weight_scales, (E, N, K), index)
+    out, ya, ydt, yst = _out_rows(out, rows, N, out_dtype, index)
+    wsp, size = None, 0
+    if dt != DT_E4M3 or workspace is not None:
+        workspace = _workspace(workspace, grouped_matmul_workspace_size(rows, K, dt), index)
+        wsp, size = workspace.data_ptr(), workspace.numel()
+    st = lib().moe_grouped_matmul(x.data_ptr(), dt, xst, xsa, xss, wa, wst, wsa, ga, groups,
+                                  _vector("num_rows", num_rows, torch.int64, index), expert_base, rows, E, N, K, ya,
+                                  ydt, yst, wsp, size, _raw_stream(stream, index))
     _check(st, "moe_grouped_matmul")
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def expert_ffn_workspace_size(rows: int, hidden: int, inter: int) -> int:
     ws = ctypes.c_uint64(0)
     _check(lib().moe_expert_ffn_get_workspace_size(rows, hidden, inter, ctypes.byref(ws)),
@@ -525,24 +590,19 @@ def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scal
     w13: e4m3 [experts, 2, inter, hidden]; w2: e4m3 [experts, hidden, inter].
     out_dtype: x's by default (bf16 for e4m3 rows). The other arguments are
     moe_grouped_matmul's."""
-    dt, xss = _expert_rows(x, x_scales, group_list, num_rows)
-    rows, H, dev = int(x.shape[0]), int(x.shape[1]), x.device
+    dt, index, (rows, H), xst, xsa, xss, ga, groups = _expert_rows(x, x_scales, group_list)
     if w13.dim() != 4 or w13.shape[1] != 2 or w13.shape[3] != H:
         raise ValueError("w13 must be [experts, 2, inter, hidden]")
-    E, inter = int(w13.shape[0]), int(w13.shape[2])
-    st13 = _expert_weights("w13", w13, w13_scales, (E, 2, inter, H))
-    st2 = _expert_weights("w2", w2, w2_scales, (E, H, inter))
+    E, inter = w13.shape[0], w13.shape[2]
+    a13, st13, s13 = _expert_weights("w13", w13, w13_scales, (E, 2, inter, H), index)
+    a2, st2, s2 = _expert_weights("w2", w2, w2_scales, (E, H, inter), index)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if dt == DT_E4M3 else x.dtype
-    out, y, ydt = _out_rows(out, rows, H, out_dtype, dev)
-    _same_device(dev, w13=w13, w13_scales=w13_scales, w2=w2, w2_scales=w2_scales, y=y)
-    if workspace is None:
-        workspace = torch.empty(max(expert_ffn_workspace_size(rows, H, inter), 1), dtype=torch.uint8, device=dev)
-    st = lib().moe_expert_ffn(
-        _ptr(x), dt, _row_stride(x), _ptr(x_scales), xss, _ptr(w13), st13, _ptr(w13_scales), _ptr(w2), st2,
-        _ptr(w2_scales), _ptr(group_list), -1 if group_list is None else int(group_list.shape[0]), _ptr(num_rows),
-        int(expert_base), rows, E, H, inter, _ptr(y), ydt, _row_stride(y), _ptr(workspace),
-        int(workspace.numel()), _stream(stream, dev))
+    out, ya, ydt, yst = _out_rows(out, rows, H, out_dtype, index)
+    workspace = _workspace(workspace, expert_ffn_workspace_size(rows, H, inter), index)
+    st = lib().moe_expert_ffn(x.data_ptr(), dt, xst, xsa, xss, a13, st13, s13, a2, st2, s2, ga, groups,
+                              _vector("num_rows", num_rows, torch.int64, index), expert_base, rows, E, H, inter, ya,
+                              ydt, yst, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, index))
     _check(st, "moe_expert_ffn")
     return out
 
@@ -550,6 +610,7 @@ def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scal
 MR_LAYER_SIGMOID, MR_LAYER_KEEP_WEIGHTS = 1, 2
 
 
+@functools.lru_cache(maxsize=1024)
 def layer_workspace_size(tokens: int, hidden: int, inter: int, experts: int, topk: int, weight_dtype: int) -> int:
     ws = ctypes.c_uint64(0)
     _check(lib().moe_layer_get_workspace_size(tokens, hidden, inter, experts, topk, weight_dtype, ctypes.byref(ws)),
@@ -571,54 +632,54 @@ def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None,
     score + select_bias."""
     if score not in ("softmax", "sigmoid"):
         raise ValueError("score must be softmax or sigmoid")
-    _require_rows("x", x, 2)
-    _require_rows("router", router, 2)
-    xdt, rdt = _float_dt("x", x), _float_dt("router", router)
-    T, H, dev = int(x.shape[0]), int(x.shape[1]), x.device
-    E = int(router.shape[0])
-    if router.shape[1] != H or w13.dim() != 4 or w13.shape[1] != 2:
+    (T, H), xstrides = _rows_of("x", x, 2)
+    rshape, rstrides = _rows_of("router", router, 2)
+    xdt, rdt, index = _float_dt("x", x), _float_dt("router", router), x.get_device()
+    E = rshape[0]
+    if rshape[1] != H or w13.dim() != 4 or w13.shape[1] != 2:
         raise ValueError("router must be [experts, hidden], w13 [experts, 2, inter, hidden]")
-    inter = int(w13.shape[2])
+    _same_device("router", router, index)
+    inter = w13.shape[2]
     if w13.dtype == _E4M3:
         wdt = DT_E4M3
-        st13 = _expert_weights("w13", w13, w13_scales, (E, 2, inter, H))
-        st2 = _expert_weights("w2", w2, w2_scales, (E, H, inter))
+        a13, st13, s13 = _expert_weights("w13", w13, w13_scales, (E, 2, inter, H), index)
+        a2, st2, s2 = _expert_weights("w2", w2, w2_scales, (E, H, inter), index)
     else:
         wdt = _float_dt("w13", w13)
         if w13.dtype != x.dtype or w2.dtype != x.dtype:
             raise TypeError("16-bit weights must have x's dtype")
         if w13_scales is not None or w2_scales is not None:
             raise ValueError("scales belong to e4m3 weights")
-        _require_rows("w13", w13, 4)
-        _require_rows("w2", w2, 3)
-        if tuple(w13.shape) != (E, 2, inter, H) or tuple(w2.shape) != (E, H, inter):
+        shape13, strides13 = _rows_of("w13", w13, 4)
+        shape2, strides2 = _rows_of("w2", w2, 3)
+        if shape13 != (E, 2, inter, H) or shape2 != (E, H, inter):
             raise ValueError("w13 must be [experts, 2, inter, hidden], w2 [experts, hidden, inter]")
+        _same_device("w13", w13, index)
+        _same_device("w2", w2, index)
         size = w13.element_size()
-        st13 = int64_array([size * v for v in _matrix_strides("w13", w13)])
-        st2 = int64_array([size * v for v in _matrix_strides("w2", w2)])
-    _require_cuda("select_bias", select_bias, torch.float32)
-    if select_bias is not None and tuple(select_bias.shape) != (E,):
-        raise ValueError("select_bias must be [experts]")
+        st13, st2 = _matrix_strides("w13", shape13, strides13, size), _matrix_strides("w2", shape2, strides2, size)
+        a13, a2, s13, s2 = w13.data_ptr(), w2.data_ptr(), None, None
+    bias = _vector("select_bias", select_bias, torch.float32, index, (E,))
+    # (the size call refuses what the layer does not take before anything is allocated)
+    size = layer_workspace_size(T, H, inter, E, topk, wdt)
     if out is None:
+        dev = f"cuda:{index}"
         out = dict(y=torch.empty((T, H), dtype=x.dtype, device=dev),
                    expertIds=torch.empty((T, topk), dtype=torch.int32, device=dev),
                    expertWeights=torch.empty((T, topk), dtype=torch.float32, device=dev))
-    y, ids, weights = out["y"], out["expertIds"], out["expertWeights"]
-    _require_rows("y", y, 2)
-    _require_cuda("y", y, x.dtype, strided=True)
-    _require_cuda("expertIds", ids, torch.int32)
-    _require_cuda("expertWeights", weights, torch.float32)
-    if tuple(y.shape) != (T, H) or tuple(ids.shape) != (T, topk) or tuple(weights.shape) != (T, topk):
-        raise ValueError("y must be [tokens, hidden], expertIds and expertWeights [tokens, topk]")
-    _same_device(dev, router=router, w13=w13, w2=w2, w13_scales=w13_scales, w2_scales=w2_scales,
-                 select_bias=select_bias, y=y, expertIds=ids, expertWeights=weights)
-    if workspace is None:
-        workspace = torch.empty(max(layer_workspace_size(T, H, inter, E, topk, wdt), 1), dtype=torch.uint8, device=dev)
+    y = out["y"]
+    yshape, ystrides = _rows_of("y", y, 2)
+    if yshape != (T, H) or y.dtype != x.dtype:
+        raise ValueError("y must be [tokens, hidden] of x's dtype")
+    _same_device("y", y, index)
+    ids = _vector("expertIds", out["expertIds"], torch.int32, index, (T, topk))
+    weights = _vector("expertWeights", out["expertWeights"], torch.float32, index, (T, topk))
+    workspace = _workspace(workspace, size, index)
     flags = (MR_LAYER_SIGMOID if score == "sigmoid" else 0) | (0 if renormalize else MR_LAYER_KEEP_WEIGHTS)
-    st = lib().moe_layer(_ptr(x), xdt, _row_stride(x), _ptr(router), rdt, _row_stride(router), _ptr(select_bias),
-                         _ptr(w13), wdt, st13, _ptr(w13_scales), _ptr(w2), st2, _ptr(w2_scales), T, H, inter, E,
-                         int(topk), flags, float(routed_scale), _ptr(y), _row_stride(y), _ptr(ids), _ptr(weights),
-                         _ptr(workspace), int(workspace.numel()), _stream(stream, dev))
+    st = lib().moe_layer(x.data_ptr(), xdt, _row_stride((T, H), xstrides), router.data_ptr(), rdt,
+                         _row_stride(rshape, rstrides), bias, a13, wdt, st13, s13, a2, st2, s2, T, H, inter, E, topk,
+                         flags, routed_scale, y.data_ptr(), _row_stride(yshape, ystrides), ids, weights,
+                         workspace.data_ptr(), workspace.numel(), _raw_stream(stream, index))
     _check(st, "moe_layer")
     return out
 

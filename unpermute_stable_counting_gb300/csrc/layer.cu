@@ -222,80 +222,77 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// One token per warp: the K experts of highest logit (or score + bias), ties to
-// the lowest index. V: values per lane.
-template <int V>
-__device__ __forceinline__ void choose(const LayerArgs& a, int t, bool write, uint16_t* ids, float* weights) {
+// The choice, in the ring's memory while it is free: a warp's logits as keys,
+// and what was chosen, by token.
+struct Choice {
+    uint32_t key[kWarps][kMaxExperts];
+    float weight[kMaxTokens][MR_MAX_LAYER_TOPK];
+    uint16_t expert[kMaxTokens][MR_MAX_LAYER_TOPK];
+};
+
+// One token by a warp: the K experts of highest logit (or score + bias), ties to
+// the lowest index. Rolled loops throughout: this runs once per launch, with the
+// instructions not yet in the SM's cache, and takes the time of fetching them (3 us
+// of the 5 us that an unrolled form with the logits in registers took).
+__device__ __forceinline__ void choose(const LayerArgs& a, Choice& c, int t, bool write) {
     const int lane = threadIdx.x & 31;
-    float v[V];
-    float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int e = lane + 32 * j;
-        v[j] = e < a.E ? __ldcg(a.logits + t * a.E + e) : -INFINITY;
-        if (e < a.E) top = fmaxf(top, v[j]);
-    }
-    float sum = 1.0f;
+    uint32_t* key = c.key[threadIdx.x >> 5];
+    const float* logits = a.logits + t * a.E;
+    float top = -INFINITY, sum = 1.0f;
     if (!a.sigmoid) {
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) top = fmaxf(top, __ldcg(logits + e));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (lane + 32 * j < a.E) sum += expf(v[j] - top);
+    }
+    // softmax: exp(l - top) / sum; sigmoid: 1 / (1 + exp(-l))
+    const float sign = a.sigmoid ? -1.0f : 1.0f, shift = a.sigmoid ? 0.0f : top;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32) {
+        const float l = __ldcg(logits + e);
+        if (!a.sigmoid) sum += expf(l - shift);
+        key[e] = __float_as_uint(l);
+    }
+    if (!a.sigmoid) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    auto score = [&](float l) { return a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / sum; };
-    uint32_t key[V];  // 0: taken, or no expert
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int e = lane + 32 * j;
-        key[j] = e < a.E ? max(order_bits(a.bias ? score(v[j]) + a.bias[e] : v[j]), 1u) : 0u;
+    auto score = [&](float l) {
+        const float x = expf(sign * (l - shift));
+        return a.sigmoid ? 1.0f / (1.0f + x) : x / sum;
+    };
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32) {
+        float v = __uint_as_float(key[e]);
+        if (a.bias) v = score(v) + a.bias[e];
+        key[e] = max(order_bits(v), 1u);  // 0: taken
     }
-    float mine = 0.0f;  // lane r: the r-th expert's logit, then its score
-    int expert = 0;
+    int mine = 0;  // lane r: the r-th expert
+#pragma unroll 1
     for (int r = 0; r < a.K; ++r) {
-        uint32_t best = 0u;
-#pragma unroll
-        for (int j = 0; j < V; ++j) best = max(best, key[j]);
+        uint32_t best = 0u, at = 0u;
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32)
+            if (key[e] > best) best = key[e], at = e;
         const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-        uint32_t at = 0xffffffffu;
-#pragma unroll
-        for (int j = V - 1; j >= 0; --j)
-            if (key[j] == most) at = lane + 32 * j;
-        const int e = (int)__reduce_min_sync(0xffffffffu, at);
-        float l = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e == lane + 32 * j) {
-                key[j] = 0u;
-                l = v[j];
-            }
-        l = __shfl_sync(0xffffffffu, l, e & 31);
-        if (lane == r) mine = l, expert = e;
+        const int e = (int)__reduce_min_sync(0xffffffffu, best == most ? at : 0xffffffffu);
+        if ((e & 31) == lane) key[e] = 0u;
+        if (lane == r) mine = e;
     }
-    mine = lane < a.K ? score(mine) : 0.0f;
-    float total = mine;
+    const float s = lane < a.K ? score(__ldcg(logits + mine)) : 0.0f;
+    float total = s;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane < a.K) {
-        const float w = (a.keep ? mine : mine / fmaxf(total, 1.17549435e-38f)) * a.scale;
-        if (ids) {
-            ids[t * a.K + lane] = (uint16_t)expert;
-            weights[t * a.K + lane] = w;
-        }
+        const float w = (a.keep ? s : s / fmaxf(total, 1.17549435e-38f)) * a.scale;
+        c.expert[t][lane] = (uint16_t)mine;
+        c.weight[t][lane] = w;
         if (write) {
-            a.ids[t * a.K + lane] = expert;
+            a.ids[t * a.K + lane] = mine;
             a.weights[t * a.K + lane] = w;
         }
     }
-}
-
-__device__ __forceinline__ void choose_any(const LayerArgs& a, int t, bool write, uint16_t* ids, float* weights) {
-    if (a.E <= 64) choose<2>(a, t, write, ids, weights);
-    else if (a.E <= 256) choose<8>(a, t, write, ids, weights);
-    else choose<kMaxExperts / 32>(a, t, write, ids, weights);
 }
 
 __device__ __forceinline__ int rank_of(unsigned long long mask, int t) {
@@ -303,64 +300,68 @@ __device__ __forceinline__ int rank_of(unsigned long long mask, int t) {
 }
 
 // Fills the tables; returns the number of experts taken, *most the largest number of tokens of one.
-// chosen: the experts are in a.ids and a.weights; otherwise by token in the tables' place.
-__device__ __forceinline__ int make_tables(const LayerArgs& a, Tables& tb, bool chosen, uint32_t* warp_sums, int* most_smem,
-                           int* most) {
-    // each thread's pairs of a token and an expert
+// shared: the experts were chosen by other blocks and are in a.ids and a.weights.
+__device__ __forceinline__ int make_tables(const LayerArgs& a, Tables& tb, Choice& c, bool shared,
+                                           uint32_t* warp_sums, int* most_smem, int* most) {
+    const int lane = threadIdx.x & 31;
+    // pair i: token i / 16, its choice i % 16
     constexpr int kMine = (kMaxTokens * MR_MAX_LAYER_TOPK + kThreads - 1) / kThreads;
-    float w[kMine];
-    int ex[kMine];
-    const int pairs = a.T * a.K;
+    static_assert(MR_MAX_LAYER_TOPK == 16, "pairs are numbered by shifts");
+    if (shared) {
+        int ex[kMine];
+        float w[kMine];
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int i = threadIdx.x + j * kThreads;
-        ex[j] = i >= pairs ? -1 : chosen ? __ldcg(a.ids + i) : tb.active[i];
-        w[j] = i >= pairs ? 0.0f : chosen ? __ldcg(a.weights + i) : tb.weight[i];
+        for (int j = 0; j < kMine; ++j) {
+            const int i = threadIdx.x + j * kThreads, at = min((i >> 4) * a.K + min(i & 15, a.K - 1), a.T * a.K - 1);
+            ex[j] = __ldcg(a.ids + at);
+            w[j] = __ldcg(a.weights + at);
+        }
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            const int i = threadIdx.x + j * kThreads;
+            if (i < kMaxTokens * 16) c.expert[i >> 4][i & 15] = (uint16_t)ex[j], c.weight[i >> 4][i & 15] = w[j];
+        }
     }
     for (int e = threadIdx.x; e < a.E; e += kThreads) tb.mask[e] = 0ull;
     if (threadIdx.x == 0) *most_smem = 0;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-        if (ex[j] >= 0) atomicOr(&tb.mask[ex[j]], 1ull << ((threadIdx.x + j * kThreads) / a.K));
+#pragma unroll 1
+    for (int i = threadIdx.x; i < a.T * 16; i += kThreads)
+        if ((i & 15) < a.K) atomicOr(&tb.mask[c.expert[i >> 4][i & 15]], 1ull << (i >> 4));
     __syncthreads();
     // experts of this thread: their slots, and their places among the taken ones
     constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
-    uint32_t slots = 0u, taken = 0u;
+    const int e0 = threadIdx.x * kPer, e1 = min(e0 + kPer, a.E);
+    uint32_t sum = 0u;  // experts taken << 16 | slots
     int biggest = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int e = threadIdx.x * kPer + j;
-        const int n = e < a.E ? __popcll(tb.mask[e]) : 0;
-        slots += n;
-        taken += n > 0;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+        const int n = __popcll(tb.mask[e]);
+        sum += (n ? 0x10000u : 0u) + n;
         biggest = max(biggest, n);
     }
     biggest = (int)__reduce_max_sync(0xffffffffu, (unsigned)biggest);
-    if ((threadIdx.x & 31) == 0) atomicMax(most_smem, biggest);
-    uint32_t experts = 0u;
-    uint32_t before = block_exclusive_scan((taken << 16) | slots, warp_sums, &experts);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int e = threadIdx.x * kPer + j;
-        if (e >= a.E) continue;
+    if (lane == 0 && biggest) atomicMax(most_smem, biggest);
+    uint32_t all = 0u;
+    uint32_t before = block_exclusive_scan(sum, warp_sums, &all);
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
         const int n = __popcll(tb.mask[e]);
         tb.start[e] = (uint16_t)(before & 0xFFFFu);
         if (n) tb.active[before >> 16] = (uint16_t)e;
         before += (n ? 0x10000u : 0u) + n;
     }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int i = threadIdx.x + j * kThreads;
-        if (ex[j] < 0) continue;
-        const int t = i / a.K, slot = tb.start[ex[j]] + rank_of(tb.mask[ex[j]], t);
-        tb.weight[slot] = w[j];
+#pragma unroll 1
+    for (int i = threadIdx.x; i < a.T * 16; i += kThreads) {
+        const int t = i >> 4, r = i & 15;
+        if (r >= a.K) continue;
+        const int e = c.expert[t][r], slot = tb.start[e] + rank_of(tb.mask[e], t);
+        tb.weight[slot] = c.weight[t][r];
         tb.token[slot] = (uint8_t)t;
     }
-    __syncthreads();
     *most = *most_smem;
-    return (int)(experts >> 16);
+    return (int)(all >> 16);
 }
 
 // ---------------------------------------------------------------------------
@@ -835,8 +836,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // barrier (1.3 us); more tokens are a block's each.
     const bool shared_choice = a.T > kWarps;
     const int token = shared_choice ? (warp == 0 ? (int)blockIdx.x : a.T) : warp;
-    if (token < a.T)
-        choose_any(a, token, shared_choice || blockIdx.x == 0, shared_choice ? nullptr : tb.active, tb.weight);
+    Choice& choice = *reinterpret_cast<Choice*>(ring);
+    if (token < a.T) choose(a, choice, token, shared_choice || blockIdx.x == 0);
     if (shared_choice) grid.sync();
     else __syncthreads();
     int most = 0;
@@ -845,8 +846,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b = i / (COLS / 2), t = i % (COLS / 2) * 4;
             copy_16(smem_u32(sx + b * 2 * COLS + t), a.sx + b * kMaxTokens + t);
         }
-    const int experts = make_tables(a, tb, shared_choice, warp_sums, &most_smem, &most);
+    const int experts = make_tables(a, tb, choice, shared_choice, warp_sums, &most_smem, &most);
     copy_wait();
+    proxy_fence();  // the ring's memory goes to copies of the async proxy
     __syncthreads();
     const int groups = experts * ((a.I + 7) / 8);
     const int g0 = (int)((int64_t)groups * blockIdx.x / gridDim.x);
@@ -1079,7 +1081,8 @@ extern "C" mr_status moe_layer(const void* x, int32_t xDtype, int64_t xStride, c
     a.stage2_a = (int)align_up(a.rows2 * kLine, 1024);
     // the widest stage of step 3: 64 columns, in two parts for 16-bit weights
     const int widest = a.stage2_a + 64 * kLine * (eight ? 1 : 2);
-    if (a.stages1 < 2 || (a.ring_bytes - 16384) / widest < 2) return MR_ERR_UNSUPPORTED;
+    static_assert(sizeof(Choice) <= 65536, "fits the ring");
+    if (a.ring_bytes < 65536 || a.stages1 < 2 || (a.ring_bytes - 16384) / widest < 2) return MR_ERR_UNSUPPORTED;
 
     LayerMaps m;
     const CUtensorMapDataType type = eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
