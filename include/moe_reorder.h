@@ -514,6 +514,7 @@ mr_status moe_update_expert(const void* expertIds, int32_t idDtype, const int32_
  *                host {row, block} element strides, nullable (contiguous).
  *                blockRows 128: [batch, ceil(rows/128), ceil(cols/128)],
  *                contiguous (scaleStrides NULL).
+ *   rows and batch at most 2^30, cols at most 2^24, blocks of 128 below 2^31.
  *   Returns MR_OK, MR_ERR_PARAM_NULLPTR, MR_ERR_PARAM_INVALID or MR_ERR_CUDA.
  */
 mr_status moe_quantize(const void* x, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,

@@ -346,8 +346,9 @@ def _blocks(n: int) -> int:
 _Pair = ctypes.c_int64 * 2
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
+@functools.lru_cache(maxsize=64)
+def _device(index):
+    return torch.device("cuda", index)
 
 
 def _raw_stream(stream, index):
@@ -412,7 +413,7 @@ def _same_device(name, t, index):
 
 def _workspace(workspace, size, index):
     if workspace is None:
-        return torch.empty(max(size, 1), dtype=torch.uint8, device=f"cuda:{index}")
+        return torch.empty(max(size, 1), dtype=torch.uint8, device=_device(index))
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.dtype != torch.uint8:
         raise TypeError("workspace must be a CUDA tensor of uint8")
     _same_device("workspace", workspace, index)
@@ -422,7 +423,7 @@ def _workspace(workspace, size, index):
 def _wide_rows(lead, cols, index):
     """e4m3 [*lead, cols] whose rows start on 16 bytes."""
     wide = -(-cols // 16) * 16
-    t = torch.empty((*lead, wide), dtype=_E4M3, device=f"cuda:{index}")
+    t = torch.empty((*lead, wide), dtype=_E4M3, device=_device(index))
     return t if wide == cols else t[..., :cols]
 
 
@@ -434,7 +435,7 @@ def quantize_outputs(shape, device, block_rows: int = 1) -> dict:
     index = torch.cuda.current_device() if device.index is None else device.index
     return dict(values=_wide_rows((*lead, rows), cols, index),
                 scales=torch.empty((*lead, rows if block_rows == 1 else _blocks(rows), _blocks(cols)),
-                                   dtype=torch.float32, device=f"cuda:{index}"))
+                                   dtype=torch.float32, device=_device(index)))
 
 
 def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = None, stream=None) -> dict:
@@ -455,7 +456,7 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
     sshape = (*shape[:-2], rows if block_rows == 1 else _blocks(rows), _blocks(cols))
     if out is None:
         values = _wide_rows(shape[:-1], cols, index)
-        scales = torch.empty(sshape, dtype=torch.float32, device=f"cuda:{index}")
+        scales = torch.empty(sshape, dtype=torch.float32, device=_device(index))
         out = dict(values=values, scales=scales)
     else:
         values, scales = out["values"], out["scales"]
@@ -537,7 +538,7 @@ def _expert_weights(name, w, scales, shape, index):
 
 def _out_rows(out, rows, cols, dtype, index):
     if out is None:
-        out = dict(y=torch.empty((rows, cols), dtype=dtype, device=f"cuda:{index}"))
+        out = dict(y=torch.empty((rows, cols), dtype=dtype, device=_device(index)))
     y = out["y"]
     shape, strides = _rows_of("y", y, 2)
     if shape != (rows, cols):
@@ -663,7 +664,7 @@ def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None,
     # (the size call refuses what the layer does not take before anything is allocated)
     size = layer_workspace_size(T, H, inter, E, topk, wdt)
     if out is None:
-        dev = f"cuda:{index}"
+        dev = _device(index)
         out = dict(y=torch.empty((T, H), dtype=x.dtype, device=dev),
                    expertIds=torch.empty((T, topk), dtype=torch.int32, device=dev),
                    expertWeights=torch.empty((T, topk), dtype=torch.float32, device=dev))

@@ -685,6 +685,7 @@ extern "C" mr_status moe_grouped_matmul(const void* x, int32_t xDtype, int64_t x
     int64_t sr = blocks_of(cols), sb = 1;
     if (xScaleStrides) sr = xScaleStrides[0], sb = xScaleStrides[1];
     if (eight && (xStride % 16 || sr < 0 || sb < 0 || sr > top || sb > top)) return MR_ERR_PARAM_INVALID;
+    if (!eight && rows * blocks_of(cols) > INT32_MAX) return MR_ERR_PARAM_INVALID;  // moe_quantize's limit
     const Quantized ws(rows, cols);
     if (rows == 0) return MR_OK;
     if (!x || !weights || !weightScales || !y || (eight && !xScales)) return MR_ERR_PARAM_NULLPTR;
@@ -759,6 +760,7 @@ extern "C" mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStri
     int64_t sr = blocks_of(hidden), sb = 1;
     if (xScaleStrides) sr = xScaleStrides[0], sb = xScaleStrides[1];
     if (eight && (xStride % 16 || sr < 0 || sb < 0 || sr > top || sb > top)) return MR_ERR_PARAM_INVALID;
+    if (!eight && rows * blocks_of(hidden) > INT32_MAX) return MR_ERR_PARAM_INVALID;  // moe_quantize's limit
     if (rows == 0) return MR_OK;
     if (!x || !w13 || !w13Scales || !w2 || !w2Scales || !y || !workspace || (eight && !xScales))
         return MR_ERR_PARAM_NULLPTR;

@@ -3,41 +3,55 @@
 //     s = the smallest power of two with max(max |x|, 2^-96) <= 448 s
 //     q = e4m3(x / s), round to nearest even
 //
-// One pass: 8 threads hold a block's 128 values in registers (16 each), find
-// the maximum with three shuffles, and write 16 bytes each. HBM bound.
+// One pass: 8 lanes hold a block's 128 values in registers, find the maximum with
+// three shuffles, and write them.
 #include "tensor.cuh"
 
 namespace mr {
 
-template <int DT> struct Wide;  // 16 consecutive values of a row as floats
-template <> struct Wide<MR_DTYPE_F32> {
-    static __device__ __forceinline__ void load(const void* p, float (&v)[16]) {
+// max(m, |v|), NaN if either is (one instruction).
+__device__ __forceinline__ float max_abs(float m, float v) {
+    float r;
+    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(m), "f"(v));
+    return r;
+}
+
+// A lane's 16 values of a block, as 16-byte pieces 128 bytes apart (8 lanes read
+// whole lines).
+template <int DT> struct Piece {
+    static constexpr int kValues = DT == MR_DTYPE_F32 ? 4 : 8;  // of a piece
+    static constexpr int kPieces = 16 / kValues;
+    static constexpr int kStep = 8 * kValues;                   // values from piece to piece
+
+    static __device__ __forceinline__ uint4 load(const void* row, int64_t col, int64_t K, bool vec) {
+        if (vec && col + kValues <= K)
+            return ld_stream_v4(reinterpret_cast<const char*>(row) + col * (DT == MR_DTYPE_F32 ? 4 : 2));
+        uint32_t u[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint4 w = ld_stream_v4(reinterpret_cast<const char*>(p) + 16 * j);
-            v[4 * j] = __uint_as_float(w.x);
-            v[4 * j + 1] = __uint_as_float(w.y);
-            v[4 * j + 2] = __uint_as_float(w.z);
-            v[4 * j + 3] = __uint_as_float(w.w);
+        for (int j = 0; j < kValues; ++j) {
+            if (col + j >= K) break;
+            if (DT == MR_DTYPE_F32) u[j & 3] = reinterpret_cast<const uint32_t*>(row)[col + j];
+            else u[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[col + j] << (16 * (j & 1));
         }
+        return make_uint4(u[0], u[1], u[2], u[3]);
     }
-};
-template <int DT> struct Wide16 {
-    static __device__ __forceinline__ void load(const void* p, float (&v)[16]) {
+    static __device__ __forceinline__ void widen(const uint4& w, float* v) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint4 w = ld_stream_v4(reinterpret_cast<const char*>(p) + 16 * j);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[8 * j + 2 * i] = Elem<DT>::to_f32((uint16_t)(u[i] & 0xFFFFu));
-                v[8 * j + 2 * i + 1] = Elem<DT>::to_f32((uint16_t)(u[i] >> 16));
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == MR_DTYPE_F32) {
+                v[i] = __uint_as_float(u[i]);
+            } else if constexpr (DT == MR_DTYPE_BF16) {
+                v[2 * i] = __uint_as_float(u[i] << 16);
+                v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+            } else {
+                const float2 f = __half22float2(reinterpret_cast<const __half2&>(u[i]));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
             }
         }
     }
 };
-template <> struct Wide<MR_DTYPE_F16> : Wide16<MR_DTYPE_F16> {};
-template <> struct Wide<MR_DTYPE_BF16> : Wide16<MR_DTYPE_BF16> {};
 
 struct QuantArgs {
     const void* x;
@@ -47,55 +61,80 @@ struct QuantArgs {
     int64_t q_stride;
     float* scales;
     int64_t row_step, block_step;
-    int blocks;    // ceil(K / 128)
-    int vec_in;    // rows readable as 16-byte vectors
-    int vec_out;   // q rows start on 16 bytes
+    uint32_t blocks;        // ceil(K / 128)
+    uint32_t magic, shift;  // i / blocks = umulhi(i, magic) >> shift for i < 2^31 (magic 0: blocks is 1)
+    int vec_in;             // rows readable as 16-byte vectors
+    int vec_out;            // q rows start on 16 bytes
 };
 
-template <int DT>
+// kItems blocks per 8 lanes, all loads before the first use. The instructions
+// bound this kernel before HBM does: about 6 per value here; with 8 values per lane
+// and 64-bit index arithmetic it was 19, and 32768 x 4096 bf16 rows took 84 us.
+template <int DT, int kItems>
 __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     pdl_enter();
+    using P = Piece<DT>;
+    constexpr int kElem = DT == MR_DTYPE_F32 ? 4 : 2;
     int64_t rows = a.rows;
     if (a.num_rows) rows = max((int64_t)0, min(rows, *a.num_rows));
-    const int64_t total = rows * a.blocks * 8;
-    // a block's 8 threads are in one warp and leave together: total is a multiple of 8
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * blockDim.x) {
-        const unsigned group = 0xFFu << (threadIdx.x & 24);
-        const int64_t rb = i >> 3;
-        const int64_t r = rb / a.blocks;
-        const int b = (int)(rb - r * a.blocks);
-        const int64_t c0 = (int64_t)b * kScaleBlock + (i & 7) * 16;
-        constexpr int kElem = DT == MR_DTYPE_F32 ? 4 : 2;
-        float v[16];
-        if (a.vec_in && c0 + 16 <= a.K) {
-            Wide<DT>::load(reinterpret_cast<const char*>(a.x) + (r * a.x_stride + c0) * kElem, v);
-        } else {
+    const uint32_t total = (uint32_t)(rows * a.blocks);
+    const uint32_t first = blockIdx.x * (32 * kItems) + (threadIdx.x >> 3);
+    if (blockIdx.x * (32 * kItems) >= total) return;
+    const int sub = threadIdx.x & 7;
+    uint4 raw[kItems][P::kPieces];
+    uint32_t row[kItems], col[kItems];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                v[j] = c0 + j < a.K ? load_f32(a.x, r * a.x_stride + c0 + j, DT) : 0.0f;
-        }
-        uint32_t m = 0u;
+    for (int n = 0; n < kItems; ++n) {
+        const uint32_t i = min(first + n * 32, total - 1);  // past the end: the last block again, not stored
+        row[n] = a.magic ? __umulhi(i, a.magic) >> a.shift : i;
+        col[n] = (i - row[n] * a.blocks) * kScaleBlock + sub * P::kValues;
+        const char* src = reinterpret_cast<const char*>(a.x) + row[n] * a.x_stride * kElem;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[j]));
+        for (int p = 0; p < P::kPieces; ++p) raw[n][p] = P::load(src, col[n] + p * P::kStep, a.K, a.vec_in);
+    }
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(group, m, o));
+    for (int n = 0; n < kItems; ++n) {
+        float v[16], m = 0.0f;
+#pragma unroll
+        for (int p = 0; p < P::kPieces; ++p) P::widen(raw[n][p], v + p * P::kValues);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max_abs(m, v[j]);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (first + n * 32 >= total) continue;
         float s, inv;
-        block_scale(m, &s, &inv);
-        if ((i & 7) == 0) a.scales[r * a.row_step + b * a.block_step] = s;
-        uint32_t w[4];
+        block_scale(__float_as_uint(m), &s, &inv);
+        if (sub == 0) a.scales[row[n] * a.row_step + (col[n] / kScaleBlock) * a.block_step] = s;
+        uint8_t* dst = a.q + row[n] * a.q_stride + col[n];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = e4m3x4(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv, v[4 * j + 3] * inv);
-        uint8_t* dst = a.q + r * a.q_stride + c0;
-        if (c0 < a.K) {
-            if (a.vec_out && c0 + 16 <= a.K) {
-                *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int p = 0; p < P::kPieces; ++p) {
+            uint32_t q[P::kValues / 4];
+#pragma unroll
+            for (int j = 0; j < P::kValues / 4; ++j) {
+                const float* f = v + p * P::kValues + 4 * j;
+                q[j] = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+            }
+            if (a.vec_out && col[n] + p * P::kStep + P::kValues <= a.K) {
+                if constexpr (P::kValues == 8)
+                    *reinterpret_cast<uint2*>(dst + p * P::kStep) = make_uint2(q[0], q[1]);
+                else *reinterpret_cast<uint32_t*>(dst + p * P::kStep) = q[0];
             } else {
-                for (int j = 0; j < 16 && c0 + j < a.K; ++j) dst[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+#pragma unroll
+                for (int j = 0; j < P::kValues; ++j)
+                    if (col[n] + p * P::kStep + j < a.K)
+                        dst[p * P::kStep + j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
             }
         }
     }
+}
+
+template <int DT>
+cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s) {
+    // two blocks per 8 lanes once that still fills the SMs twice over
+    const int64_t total = a.rows * a.blocks;
+    if (total >= (int64_t)device_sm_count() * 8 * 64 * 2)
+        return launch_pdl(quantize_kernel<DT, 2>, dim3((unsigned)((total + 63) / 64)), dim3(256), 0, s, a);
+    return launch_pdl(quantize_kernel<DT, 1>, dim3((unsigned)((total + 31) / 32)), dim3(256), 0, s, a);
 }
 
 // 128 x 128 blocks (weights, quantized once when a model is loaded): one block
@@ -145,16 +184,17 @@ cudaError_t enqueue_quantize(const void* x, int dt, int64_t rows, int64_t K, int
     a.scales = scales;
     a.row_step = rowStep;
     a.block_step = blockStep;
-    a.blocks = (int)((K + kScaleBlock - 1) / kScaleBlock);
+    a.blocks = (uint32_t)((K + kScaleBlock - 1) / kScaleBlock);
     a.vec_in = (reinterpret_cast<uintptr_t>(x) % 16 == 0) && (xStride * elem) % 16 == 0;
     a.vec_out = (reinterpret_cast<uintptr_t>(q) % 16 == 0) && qStride % 16 == 0;
-    const int64_t total = rows * a.blocks * 8;
-    const int64_t grid = (total + 255) / 256;
-    auto kernel = dt == MR_DTYPE_F32   ? quantize_kernel<MR_DTYPE_F32>
-                  : dt == MR_DTYPE_F16 ? quantize_kernel<MR_DTYPE_F16>
-                                       : quantize_kernel<MR_DTYPE_BF16>;
-    const int64_t most = (int64_t)device_sm_count() * 8 * 16;
-    return launch_pdl(kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(256), 0, stream, a);
+    // ceil(2^(31 + l) / blocks) for 2^(l - 1) < blocks <= 2^l: below 2^32, and exact for i < 2^31
+    int l = 0;
+    while ((1u << l) < a.blocks) ++l;
+    a.magic = l ? (uint32_t)(((1ull << (31 + l)) + a.blocks - 1) / a.blocks) : 0u;
+    a.shift = l ? l - 1 : 0;
+    return dt == MR_DTYPE_F32   ? launch_quantize<MR_DTYPE_F32>(a, stream)
+           : dt == MR_DTYPE_F16 ? launch_quantize<MR_DTYPE_F16>(a, stream)
+                                : launch_quantize<MR_DTYPE_BF16>(a, stream);
 }
 
 }  // namespace mr
@@ -168,8 +208,9 @@ extern "C" mr_status moe_quantize(const void* x, int32_t dtype, int64_t batch, i
     if (dtype != MR_DTYPE_F16 && dtype != MR_DTYPE_BF16 && dtype != MR_DTYPE_F32) return MR_ERR_PARAM_INVALID;
     if (batch < 1 || rows < 0 || cols < 1 || (blockRows != 1 && blockRows != kScaleBlock))
         return MR_ERR_PARAM_INVALID;
-    if (rows > MR_MAX_EXPERT_ROWS || cols > MR_MAX_EXPERT_ROWS || batch > MR_MAX_EXPERT_ROWS)
+    if (rows > MR_MAX_EXPERT_ROWS || cols > MR_MAX_EXPERT_COLS || batch > MR_MAX_EXPERT_ROWS)
         return MR_ERR_PARAM_INVALID;
+    if (blockRows == 1 && rows * ((cols + kScaleBlock - 1) / kScaleBlock) > INT32_MAX) return MR_ERR_PARAM_INVALID;
     if (blockRows == 1 && batch != 1) return MR_ERR_PARAM_INVALID;
     if (blockRows != 1 && numRows) return MR_ERR_PARAM_INVALID;
     const int64_t cb = (cols + kScaleBlock - 1) / kScaleBlock, rb = (rows + kScaleBlock - 1) / kScaleBlock;
