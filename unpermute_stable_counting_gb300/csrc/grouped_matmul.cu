@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool more = walk.next(a, lane, t, BN, tile);
                 if (!mbar_wait<PAIR>(smem_u32(&i_empty[n & 1]), ((n >> 1) & 1) ^ 1, abort)) break;
                 if (lane == 0) {
-                    if (!more) tile.rows = 0;
+                    if (!more) tile = Tile{0, 0, 0, 0};
                     info[n & 1] = tile;
                     mbar_arrive(smem_u32(&i_full[n & 1]));
                 }
@@ -368,23 +368,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t from = lanes + (C::kHalves == 2 ? group * C::kHalf : group * C::kChunk);
         uint8_t* stage = out_stage + (warp - 4) * kOutBytes;
         uint32_t done = 0;
-        for (bool ok = true;; ++done) {
-            ok = mbar_wait<PAIR>(smem_u32(&i_full[done & 1]), (done >> 1) & 1, abort);
-            if (!ok) break;
-            tile = info[done & 1];
+        // Scales come straight from memory, two steps ahead (through shared memory, whose bandwidth
+        // the operands take, they cost the sums more than the loads do), and a tile's first ones
+        // before the tile before it is stored. Rows and columns past the tile's take its last ones'
+        // scales: their sums are not stored.
+        const float *xp, *wp;
+        float xs[2], ws[2][C::kChunks];  // of the next two steps
+        const int64_t w_other = SWIGLU ? (int64_t)a.scale_rows * a.KB : 0;
+        bool ok = true;
+        auto take = [&](uint32_t n) {
+            ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
+            if (!ok) return;
+            tile = info[n & 1];
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&i_empty[done & 1]));
-            if (tile.rows == 0) break;
-            // Scales come straight from memory, two steps ahead: through shared memory, whose
-            // bandwidth the operands take, they cost the sums more than the loads do.
-            // Rows and columns past the tile's take its last ones' scales: their sums are not stored.
-            const float* xp =
-                a.x_scales + (int64_t)(tile.row0 + min((int)rank * kTileM + row, tile.rows - 1)) * a.xs_row;
+            if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
+            xp = a.x_scales + (int64_t)(tile.row0 + max(0, min((int)rank * kTileM + row, tile.rows - 1))) * a.xs_row;
             const int nb = min(SWIGLU ? tile.n0 / 2 / kScaleBlock : tile.n0 / kScaleBlock + half, a.scale_rows - 1);
-            const float* wp =
-                a.w_scales + ((int64_t)(SWIGLU ? tile.expert * 2 : tile.expert) * a.scale_rows + nb) * a.KB;
-            const int64_t w_other = SWIGLU ? (int64_t)a.scale_rows * a.KB : 0;
-            float xs[2], ws[2][C::kChunks];  // of the next two steps
+            wp = a.w_scales + ((int64_t)(SWIGLU ? tile.expert * 2 : tile.expert) * a.scale_rows + nb) * a.KB;
             xs[0] = *xp;
             ws[0][0] = *wp;
             if (SWIGLU) ws[0][C::kChunks - 1] = wp[w_other];
@@ -392,6 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             xs[1] = *xp;
             ws[1][0] = *wp;
             if (SWIGLU) ws[1][C::kChunks - 1] = wp[w_other];
+        };
+        take(0);
+        while (ok && tile.rows != 0) {
             float2 acc[C::kChunks][C::kChunk / 2];
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
@@ -442,6 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int wrow = (int)rank * kTileM + (warp & 3) * 32;
             const int wrows = min(32, tile.rows - wrow);
             const int64_t r = (int64_t)tile.row0 + wrow;
+            const int n0 = tile.n0;
+            take(done + 1);
             if (SWIGLU) {
                 // chunk 0 holds the gate's columns, chunk 1 the same columns of the other factor
                 uint32_t m = 0u;
@@ -456,13 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx[group][row] = m;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&max_bar));
-                ok = mbar_wait<PAIR>(smem_u32(&max_bar), done & 1, abort);
-                if (!ok) break;
+                if (!mbar_wait<PAIR>(smem_u32(&max_bar), done & 1, abort)) break;
                 m = max(m, mx[group ^ 1][row]);
                 float s, inv;
                 block_scale(m, &s, &inv);
-                const int n = tile.n0 / 2 + group * 64;
-                if (group == 0 && lane < wrows) a.hs[(tile.n0 / 2 / kScaleBlock) * a.hs_block + r + lane] = s;
+                const int n = n0 / 2 + group * 64;
+                if (group == 0 && lane < wrows) a.hs[(n0 / 2 / kScaleBlock) * a.hs_block + r + lane] = s;
                 uint4 w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -479,13 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int elem = a.y_dtype == MR_DTYPE_F32 ? 4 : 2;
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c) {
-                    const int n = tile.n0 + group * C::kChunks * C::kChunk + c * C::kChunk;
+                    const int n = n0 + group * C::kChunks * C::kChunk + c * C::kChunk;
                     if (n < a.N)
                         store_columns<C::kChunk>(stage, acc[c],
                                                  reinterpret_cast<uint8_t*>(a.y) + (r * a.y_stride + n) * elem,
                                                  a.y_stride * elem, wrows, a.N - n, a.y_dtype, a.y_vec, lane);
                 }
             }
+            ++done;
         }
     }
     __syncthreads();
