@@ -147,77 +147,91 @@ template <int BN, bool SWIGLU, bool PAIR> struct Cfg {
 // Stores a warp's 32 rows (lane: row) of U 16-byte pieces, U <= 4, so that the
 // lanes of an instruction write whole segments of a few rows: straight from the
 // registers every lane would write to a row of its own, 32 lines per
-// instruction. `at`: bytes of this lane's row; row_step: bytes from row to row;
-// rows, left: real rows and real bytes of a row; vec: 16-byte stores are aligned.
+// instruction. `to`: this lane's piece of its first row, bytes; step: bytes from
+// one of its rows to the next (32 / U rows on). `whole`: every row and piece is
+// real and aligned; otherwise `rows` rows and `left` bytes of each are.
 template <int U>
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4 (&v)[U], uint8_t* row0, int64_t row_step,
-                                           int rows, int64_t left, int elem, bool vec, int lane) {
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4 (&v)[U], uint8_t* to, int64_t step,
+                                           bool whole, int rows, int64_t left, int elem, bool vec, int lane) {
     // 64-byte rows, pieces permuted so that eight lanes hit different banks
     const int key = (lane >> 1) & 3;
 #pragma unroll
     for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ key) << 4)) = v[u];
     __syncwarp();
     constexpr int kRows = 32 / U;  // rows per instruction
+    uint4 w[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         const int r = i * kRows + lane / U, u = lane % U;
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
-        if (r >= rows || u * 16 >= left) continue;
-        uint8_t* p = row0 + r * row_step + u * 16;
-        if (vec && u * 16 + 16 <= left) {
-            *reinterpret_cast<uint4*>(p) = w;
-        } else {
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        w[i] = *reinterpret_cast<const uint4*>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+    }
+    __syncwarp();
+    if (whole) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (elem == 4) {
-                    if (u * 16 + 4 * k < left) reinterpret_cast<uint32_t*>(p)[k] = x[k];
-                } else {
-                    if (u * 16 + 4 * k < left) reinterpret_cast<uint16_t*>(p)[2 * k] = (uint16_t)(x[k] & 0xFFFFu);
-                    if (u * 16 + 4 * k + 2 < left) reinterpret_cast<uint16_t*>(p)[2 * k + 1] = (uint16_t)(x[k] >> 16);
-                }
+        for (int i = 0; i < U; ++i, to += step) *reinterpret_cast<uint4*>(to) = w[i];
+        return;
+    }
+    left -= lane % U * 16;
+#pragma unroll
+    for (int i = 0; i < U; ++i, to += step) {
+        if (i * kRows + lane / U >= rows || left <= 0) continue;
+        if (vec && left >= 16) {
+            *reinterpret_cast<uint4*>(to) = w[i];
+            continue;
+        }
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (elem == 4) {
+                if (4 * k < left) reinterpret_cast<uint32_t*>(to)[k] = x[k];
+            } else {
+                if (4 * k < left) reinterpret_cast<uint16_t*>(to)[2 * k] = (uint16_t)(x[k] & 0xFFFFu);
+                if (4 * k + 2 < left) reinterpret_cast<uint16_t*>(to)[2 * k + 1] = (uint16_t)(x[k] >> 16);
             }
         }
     }
-    __syncwarp();
 }
 
 template <int DT> __device__ __forceinline__ uint32_t pack2(float2 v) {
-    return (uint32_t)Elem<DT>::from_f32(v.x) | ((uint32_t)Elem<DT>::from_f32(v.y) << 16);
+    uint32_t r;
+    if constexpr (DT == MR_DTYPE_F16) {
+        const __half2 h = __floats2half2_rn(v.x, v.y);
+        r = reinterpret_cast<const uint32_t&>(h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+        r = reinterpret_cast<const uint32_t&>(h);
+    }
+    return r;
 }
 
 // CW columns of the warp's rows, from `row0` (first row, first column) on.
-template <int CW>
+template <int DT, int CW>
 __device__ __forceinline__ void store_columns(uint8_t* stage, const float2 (&acc)[CW / 2], uint8_t* row0,
-                                              int64_t row_step, int rows, int cols, int dt, bool vec, int lane) {
-    if (dt == MR_DTYPE_F32) {
-        constexpr int F = CW < 16 ? CW : 16;
-#pragma unroll
-        for (int c = 0; c < CW; c += F) {
-            uint4 v[F / 4];
-#pragma unroll
-            for (int u = 0; u < F / 4; ++u)
-                v[u] = make_uint4(__float_as_uint(acc[c / 2 + 2 * u].x), __float_as_uint(acc[c / 2 + 2 * u].y),
-                                  __float_as_uint(acc[c / 2 + 2 * u + 1].x), __float_as_uint(acc[c / 2 + 2 * u + 1].y));
-            store_rows<F / 4>(stage, v, row0 + 4 * c, row_step, rows, 4 * (int64_t)(cols - c), 4, vec, lane);
-        }
-        return;
-    }
-    constexpr int W = CW < 32 ? CW : 32;
+                                              int64_t row_step, int rows, int cols, bool vec, int lane) {
+    constexpr int kElem = DT == MR_DTYPE_F32 ? 4 : 2;
+    constexpr int kMost = 64 / kElem;                // columns per 64-byte segment
+    constexpr int W = CW < kMost ? CW : kMost, U = W * kElem / 16;
+    const bool whole = vec && rows == 32 && cols >= CW;
+    uint8_t* to = row0 + lane / U * row_step + lane % U * 16;
+    const int64_t step = 32 / U * row_step;
 #pragma unroll
     for (int c = 0; c < CW; c += W) {
-        uint4 v[W / 8];
+        uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < W / 8; ++u) {
+        for (int u = 0; u < U; ++u) {
             uint32_t x[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 p = acc[c / 2 + 4 * u + k];
-                x[k] = dt == MR_DTYPE_F16 ? pack2<MR_DTYPE_F16>(p) : pack2<MR_DTYPE_BF16>(p);
+                if constexpr (DT == MR_DTYPE_F32) {
+                    const float2 p = acc[c / 2 + 2 * u + k / 2];
+                    x[k] = __float_as_uint(k % 2 ? p.y : p.x);
+                } else {
+                    x[k] = pack2<DT>(acc[c / 2 + 4 * u + k]);
+                }
             }
             v[u] = make_uint4(x[0], x[1], x[2], x[3]);
         }
-        store_rows<W / 8>(stage, v, row0 + 2 * c, row_step, rows, 2 * (int64_t)(cols - c), 2, vec, lane);
+        store_rows<U>(stage, v, to + kElem * c, step, whole, rows, kElem * (int64_t)(cols - c), kElem, vec, lane);
     }
 }
 
@@ -478,16 +492,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     w[j] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
-                store_rows<4>(stage, w, a.hq + r * a.hq_stride + n, a.hq_stride, wrows, 64, 4, true, lane);
+                store_rows<4>(stage, w, a.hq + (r + lane / 4) * a.hq_stride + n + lane % 4 * 16, 8 * a.hq_stride,
+                              wrows == 32, wrows, 64, 4, true, lane);
             } else if (wrows > 0 && MR_IN_RANGE(r + wrows - 1, a.rows, 901)) {
                 const int elem = a.y_dtype == MR_DTYPE_F32 ? 4 : 2;
-#pragma unroll
-                for (int c = 0; c < C::kChunks; ++c) {
-                    const int n = n0 + group * C::kChunks * C::kChunk + c * C::kChunk;
-                    if (n < a.N)
-                        store_columns<C::kChunk>(stage, acc[c],
-                                                 reinterpret_cast<uint8_t*>(a.y) + (r * a.y_stride + n) * elem,
-                                                 a.y_stride * elem, wrows, a.N - n, a.y_dtype, a.y_vec, lane);
+                const int n = n0 + group * C::kChunk;
+                uint8_t* to = reinterpret_cast<uint8_t*>(a.y) + (r * a.y_stride + n) * elem;
+                const int64_t step = a.y_stride * elem;
+                if (n < a.N) {
+                    if (a.y_dtype == MR_DTYPE_BF16)
+                        store_columns<MR_DTYPE_BF16, C::kChunk>(stage, acc[0], to, step, wrows, a.N - n, a.y_vec, lane);
+                    else if (a.y_dtype == MR_DTYPE_F16)
+                        store_columns<MR_DTYPE_F16, C::kChunk>(stage, acc[0], to, step, wrows, a.N - n, a.y_vec, lane);
+                    else
+                        store_columns<MR_DTYPE_F32, C::kChunk>(stage, acc[0], to, step, wrows, a.N - n, a.y_vec, lane);
                 }
             }
             ++done;
