@@ -454,10 +454,18 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
     dt, index = _float_dt("x", x), x.get_device()
     rows, cols = shape[-2], shape[-1]
     sshape = (*shape[:-2], rows if block_rows == 1 else _blocks(rows), _blocks(cols))
+    num_rows = _vector("num_rows", num_rows, torch.int64, index)
     if out is None:
         values = _wide_rows(shape[:-1], cols, index)
         scales = torch.empty(sshape, dtype=torch.float32, device=_device(index))
         out = dict(values=values, scales=scales)
+        if block_rows == 1:
+            st = lib().moe_quantize(x.data_ptr(), dt, 1, rows, cols, _Pair(0, _row_stride(shape, strides)), 1, num_rows,
+                                    values.data_ptr(), _Pair(0, -(-cols // 16) * 16), scales.data_ptr(), None,
+                                    _raw_stream(stream, index))
+            if st:
+                _check(st, "moe_quantize")
+            return out
     else:
         values, scales = out["values"], out["scales"]
     vshape, vstrides = _rows_of("values", values, dims)
@@ -484,8 +492,7 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
             xs[0], xs[1] = xs[1], xs[0]
             vs[0], vs[1] = vs[1], vs[0]
     st = lib().moe_quantize(x.data_ptr(), dt, max(1, batch), rows, cols, xs, block_rows,
-                            _vector("num_rows", num_rows, torch.int64, index), values.data_ptr(), vs, saddr, ss,
-                            _raw_stream(stream, index))
+                            num_rows, values.data_ptr(), vs, saddr, ss, _raw_stream(stream, index))
     _check(st, "moe_quantize")
     return out
 
@@ -538,7 +545,11 @@ def _expert_weights(name, w, scales, shape, index):
 
 def _out_rows(out, rows, cols, dtype, index):
     if out is None:
-        out = dict(y=torch.empty((rows, cols), dtype=dtype, device=_device(index)))
+        dt = _TORCH_TO_DT.get(dtype)
+        if dt is None:
+            raise TypeError(f"y dtype {dtype} is not f16/bf16/f32")
+        y = torch.empty((rows, cols), dtype=dtype, device=_device(index))
+        return dict(y=y), y.data_ptr(), dt, cols
     y = out["y"]
     shape, strides = _rows_of("y", y, 2)
     if shape != (rows, cols):
