@@ -29,7 +29,6 @@ __device__ unsigned g_waits_out;  // blocks that left early, see mbar_wait
 
 constexpr int kTileM = 128, kTileK = 128;
 constexpr int kThreads = 384, kSumWarps = 8;
-constexpr int kOutBytes = 2048;  // of each summing warp, to turn its rows into whole segments
 
 struct GroupArgs {
     const float* x_scales;     // [r * xs_row + b * xs_block]
@@ -42,7 +41,7 @@ struct GroupArgs {
     int n_tiles;
     void* y;
     int64_t y_stride;
-    int y_dtype, y_vec;        // y_vec: rows can be stored as 16-byte vectors
+    int y_dtype, y_vec, y_map; // y_vec: rows can be stored as 16-byte vectors; y_map: there is a map of y
     uint8_t* hq;               // quantized result of the network's first product
     int64_t hq_stride;
     float* hs;                 // its scales, [b * hs_block + r]
@@ -132,7 +131,7 @@ template <int TM> struct Walk {
 // of the weight columns, and the matrix instructions read both halves.
 template <int BN, bool SWIGLU, bool PAIR> struct Cfg {
     static constexpr int kLoadN = PAIR ? BN / 2 : BN;                // weight columns this block loads
-    static constexpr int kStages = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kStages = PAIR ? (SWIGLU ? 6 : 5) : BN == 256 ? 4 : BN == 128 ? 6 : 8;
     static constexpr int kBufs = BN == 256 ? 2 : 4;                  // tensor memory buffers
     static constexpr int kHalves = BN == 256 ? 2 : 1;                // column halves with barriers of their own
     static constexpr int kHalf = BN / kHalves;
@@ -141,6 +140,11 @@ template <int BN, bool SWIGLU, bool PAIR> struct Cfg {
     static constexpr int kLoad = kChunk < 16 ? kChunk : 16;          // columns per tensor memory load
     static constexpr int kLoads = kChunks * kChunk / kLoad;
     static constexpr int kStageBytes = (kTileM + kLoadN) * kTileK;
+    // a summing warp's rows on their way out: a pair's 16-bit results leave whole (send_columns),
+    // others 64 bytes of a row at a time, which leaves a fourth stage for the weights of few rows
+    // (decode batch: 294 against 306 us)
+    static constexpr bool kSend = PAIR && !SWIGLU;
+    static constexpr int kOutBytes = kSend ? 32 * kChunk * 2 : 2048;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kSumWarps * kOutBytes;
 };
 
@@ -235,10 +239,33 @@ __device__ __forceinline__ void store_columns(uint8_t* stage, const float2 (&acc
     }
 }
 
+// The same for 32 real rows of 16-bit results and a map of y: the columns go to
+// shared memory, 64 at a time as a tile of 128-byte rows in the map's swizzle, and
+// from there by asynchronous copies beside the next tile's sums. (Stores from
+// registers took 3400 cycles of a tile's 27500 at 32 steps, these take a third.)
+template <int DT, int CW>
+__device__ __forceinline__ void send_columns(uint8_t* stage, const float2 (&acc)[CW / 2], const CUtensorMap* map,
+                                             int row, int col, int cols, int lane) {
+    if (lane == 0) tma_store_read();  // the tile before has left
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < CW; c += 64) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const float2* p = &acc[c / 2 + 4 * u];
+            *reinterpret_cast<uint4*>(stage + c * 64 + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                make_uint4(pack2<DT>(p[0]), pack2<DT>(p[1]), pack2<DT>(p[2]), pack2<DT>(p[3]));
+        }
+        smem_proxy_fence();
+        __syncwarp();
+        if (lane == 0 && c < cols) tma_store_2d(map, smem_u32(stage + c * 64), col + c, row);
+    }
+}
+
 template <int BN, bool SWIGLU, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                          const GroupArgs a) {
+                          const __grid_constant__ CUtensorMap map_y, const GroupArgs a) {
     using C = Cfg<BN, SWIGLU, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages];
@@ -380,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // weight scales
         const int half = C::kHalves == 2 ? group : 0;
         const uint32_t from = lanes + (C::kHalves == 2 ? group * C::kHalf : group * C::kChunk);
-        uint8_t* stage = out_stage + (warp - 4) * kOutBytes;
+        uint8_t* stage = out_stage + (warp - 4) * C::kOutBytes;
         uint32_t done = 0;
         // Scales come straight from memory, two steps ahead (through shared memory, whose bandwidth
         // the operands take, they cost the sums more than the loads do), and a tile's first ones
@@ -499,7 +526,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = n0 + group * C::kChunk;
                 uint8_t* to = reinterpret_cast<uint8_t*>(a.y) + (r * a.y_stride + n) * elem;
                 const int64_t step = a.y_stride * elem;
-                if (n < a.N) {
+                bool sent = false;
+                if constexpr (C::kSend) {
+                    if (a.y_map && wrows == 32) {
+                        sent = true;
+                        if (n < a.N) {
+                            if (a.y_dtype == MR_DTYPE_BF16)
+                                send_columns<MR_DTYPE_BF16, C::kChunk>(stage, acc[0], &map_y, (int)r, n, a.N - n, lane);
+                            else
+                                send_columns<MR_DTYPE_F16, C::kChunk>(stage, acc[0], &map_y, (int)r, n, a.N - n, lane);
+                        }
+                    } else if (a.y_map) {
+                        if (lane == 0) tma_store_read();
+                        __syncwarp();
+                    }
+                }
+                if (!sent && n < a.N) {
                     if (a.y_dtype == MR_DTYPE_BF16)
                         store_columns<MR_DTYPE_BF16, C::kChunk>(stage, acc[0], to, step, wrows, a.N - n, a.y_vec, lane);
                     else if (a.y_dtype == MR_DTYPE_F16)
@@ -510,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++done;
         }
+        if (C::kSend && lane == 0) tma_store_done();
     }
     __syncthreads();
     if (PAIR) cluster_sync();
@@ -535,7 +578,7 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <int BN, bool SWIGLU, bool PAIR>
-cudaError_t launch_grouped(const CUtensorMap& mx, const CUtensorMap& mw, const GroupArgs& a, int64_t tiles,
+cudaError_t launch_grouped(const CUtensorMap (&m)[3], const GroupArgs& a, int64_t tiles,
                            cudaStream_t s) {
     auto kernel = grouped_matmul_kernel<BN, SWIGLU, PAIR>;
     constexpr int smem = Cfg<BN, SWIGLU, PAIR>::kSmem;
@@ -569,7 +612,7 @@ cudaError_t launch_grouped(const CUtensorMap& mx, const CUtensorMap& mw, const G
         resident[dev].store(n, std::memory_order_release);
     }
     cfg.gridDim = dim3((unsigned)(tiles < n ? tiles : n) * (PAIR ? 2 : 1));
-    return cudaLaunchKernelEx(&cfg, kernel, mx, mw, a);
+    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], a);
 }
 
 // One product over the groups. x: e4m3 rows, w: e4m3 [experts][N][K]; the first
@@ -602,23 +645,30 @@ mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
     a.n_tiles = p.swiglu ? ceil_div(a.N, 128) : ceil_div(a.N, bn);
     const int64_t tiles = m_tiles * a.n_tiles;
     if (tiles > INT32_MAX) return MR_ERR_PARAM_INVALID;
-    CUtensorMap mx, mw;
+    CUtensorMap m[3];
     const uint64_t xd[2] = {(uint64_t)p.K, (uint64_t)p.x_rows}, xs[1] = {(uint64_t)p.x_stride};
     const uint32_t xb[2] = {kTileK, 32};
     const uint64_t wd[3] = {(uint64_t)p.K, (uint64_t)a.N, (uint64_t)a.experts * (p.swiglu ? 2 : 1)};
     const uint64_t ws[2] = {(uint64_t)p.w_row, (uint64_t)p.w_matrix};
     const uint32_t wb[3] = {kTileK, (uint32_t)(p.swiglu || pair ? 64 : bn), 1};
-    if (!make_tensor_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.x, 2, xd, xs, xb) ||
-        !make_tensor_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, 3, wd, ws, wb))
+    if (!make_tensor_map(&m[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.x, 2, xd, xs, xb) ||
+        !make_tensor_map(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, 3, wd, ws, wb))
         return MR_ERR_CUDA;
+    m[2] = m[0];  // not read
+    a.y_map = pair && !p.swiglu && a.y_vec && a.y_dtype != MR_DTYPE_F32;
+    if (a.y_map) {
+        const uint64_t yd[2] = {(uint64_t)a.N, (uint64_t)a.rows}, ys[1] = {(uint64_t)a.y_stride * 2};
+        const uint32_t yb[2] = {64, 32};
+        if (!make_tensor_map(&m[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.y, 2, yd, ys, yb)) return MR_ERR_CUDA;
+    }
     cudaError_t e;
-    if (pair) e = p.swiglu ? launch_grouped<256, true, true>(mx, mw, a, tiles, s)
-                           : launch_grouped<256, false, true>(mx, mw, a, tiles, s);
-    else if (p.swiglu) e = launch_grouped<256, true, false>(mx, mw, a, tiles, s);
-    else if (bn == 256) e = launch_grouped<256, false, false>(mx, mw, a, tiles, s);
-    else if (bn == 128) e = launch_grouped<128, false, false>(mx, mw, a, tiles, s);
-    else if (bn == 64) e = launch_grouped<64, false, false>(mx, mw, a, tiles, s);
-    else e = launch_grouped<32, false, false>(mx, mw, a, tiles, s);
+    if (pair) e = p.swiglu ? launch_grouped<256, true, true>(m, a, tiles, s)
+                           : launch_grouped<256, false, true>(m, a, tiles, s);
+    else if (p.swiglu) e = launch_grouped<256, true, false>(m, a, tiles, s);
+    else if (bn == 256) e = launch_grouped<256, false, false>(m, a, tiles, s);
+    else if (bn == 128) e = launch_grouped<128, false, false>(m, a, tiles, s);
+    else if (bn == 64) e = launch_grouped<64, false, false>(m, a, tiles, s);
+    else e = launch_grouped<32, false, false>(m, a, tiles, s);
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
 
@@ -673,10 +723,10 @@ bool make_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes,
         return reinterpret_cast<Encode>(f);
     }();
     if (!encode) return false;
-    (void)elem_bytes;
+    const bool wide = box[0] * elem_bytes == 128;
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     return encode(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

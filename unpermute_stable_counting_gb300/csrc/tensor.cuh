@@ -153,6 +153,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// A tile from shared memory to global memory, by one thread; the thread's earlier
+// ones have been read (their shared memory is free) / are complete.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void smem_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // Weights that one launch reads once leave L2 first, so that what is small and used again (rows,
 // scales, the code itself) stays there.
 __device__ __forceinline__ uint64_t evict_first() {
@@ -364,9 +376,9 @@ __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __e
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// A tiled tensor map of `rank` dimensions (innermost first) with the 128-byte
-// swizzle; strides[i] is the byte stride of dimension i + 1. False if the
-// driver refuses it.
+// A tiled tensor map of `rank` dimensions (innermost first) with the swizzle of
+// its rows' width (128 or 64 bytes); strides[i] is the byte stride of dimension
+// i + 1. False if the driver refuses it.
 bool make_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, const void* base, int rank,
                      const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
 
