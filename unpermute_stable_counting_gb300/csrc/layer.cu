@@ -394,15 +394,18 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per = (a.I + 7) / 8;  // row groups of an expert
     const int kbs = (a.H + kLineElems - 1) / kLineElems;
+    // tiles of at most 16 groups, all alike: 17 groups as 16 and 1 would take the short one's steps,
+    // bound by their latency, on top
     const int tiles = (g1 - g0 + 15) / 16;
+    auto tile_end = [&](int n) { return g0 + (n + 1) * (g1 - g0) / tiles; };
     const int x_bytes = 2 * COLS * kLine;
     if (warp == 0) {
         if (elect_one()) {
             proxy_fence();
             const uint64_t policy = evict_first();
             Place p;
-            for (int n = 0; n < tiles; ++n) {
-                const int f = g0 + n * 16, l = min(f + 16, g1);
+            for (int n = 0, f = g0; n < tiles; ++n) {
+                const int l = tile_end(n);
                 for (int kb = 0; kb < kbs; ++kb, p.next(a.stages1)) {
                     const uint32_t bar = smem_u32(&bars.full[p.at]);
                     if (!mbar_wait(smem_u32(&bars.empty[p.at]), p.round ^ 1, abort)) break;
@@ -427,6 +430,7 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
                     }
                     tma_load_2d(dst + 32768, map_x, bar, kb * kLineElems, 0);
                 }
+                f = l;
             }
         }
         __syncwarp();
@@ -468,8 +472,8 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
         const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + half * COLS;
         const int hb = (a.H + kScaleBlock - 1) / kScaleBlock, ib = (a.I + kScaleBlock - 1) / kScaleBlock;
         uint32_t use = 0;
-        for (int n = 0; n < tiles; ++n) {
-            const int f = g0 + n * 16, l = min(f + 16, g1);
+        for (int n = 0, f = g0; n < tiles; ++n) {
+            const int l = tile_end(n);
             const int g = min(f + row / 8, l - 1);
             const int e = tb.active[g / per], i = g % per * 8 + (row & 7);
             const bool real = f + row / 8 < l && i < a.I;
@@ -585,6 +589,7 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
                     g += run;
                 }
             }
+            f = l;
         }
         proxy_fence();  // h is read by copies of the async proxy
     }
@@ -777,8 +782,11 @@ __device__ __forceinline__ void step_y(const LayerArgs& a, const Tables& tb, con
     grid.sync();
     const int n = a.T * a.H;
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) {
-        float v = __ldcg(a.part + i);
-        for (int k = 1; k < a.splits; ++k) v += __ldcg(a.part + (int64_t)k * n + i);
+        float p[kMaxSplits], v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kMaxSplits; ++k) p[k] = k < a.splits ? __ldcg(a.part + (int64_t)k * n + i) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kMaxSplits; ++k) v += p[k];
         const int t = i / a.H;
         store(t * a.y_stride + i - t * a.H, v);
     }
