@@ -13,7 +13,10 @@
  *                      返回值与错误码, Kernel 实现 (skip rules, fp32 math).
  * and around them: the batching from a ScheduleContext, its full-tail option,
  * the routing-map permute that produces the unpermute's input, and
- * MoeUpdateExpert ("MoeUpdateExpert"), declared further down.
+ * MoeUpdateExpert ("MoeUpdateExpert"), declared further down; and the experts
+ * between the two: rows and weights in 8-bit blocks, the product of each
+ * expert's rows with its weights, the experts' network, and a whole layer for a
+ * few tokens.
  *
  * Conventions shared by every entry point
  *  - Pointers named as device pointers must point to device memory of the
@@ -41,9 +44,9 @@
  *  - Results are deterministic: identical inputs give identical bits.
  *  - Execute calls can be captured into a CUDA graph (stream capture): they
  *    only enqueue kernels (the not-padded moe_unpermute's maskedSelect and
- *    the batching's one-launch sort of up to 32768 slots are cooperative
- *    launches, whose grids never exceed the blocks the device can hold at
- *    once), memsets and event records/waits on `stream` and its auxiliary
+ *    the batching's one-launch sort of up to 32768 slots and moe_layer are
+ *    cooperative launches, whose grids never exceed the blocks the device can
+ *    hold at once), memsets and event records/waits on `stream` and its auxiliary
  *    stream, which joins back. Make one call of each kind on each caller
  *    stream outside any capture first (it creates that stream's auxiliary
  *    stream and caches device queries), and capture ffnwb_batching_noalloc
@@ -602,7 +605,8 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
  *     y[t] = sum over the taken experts, ascending, of weight * ffn_e(x[t]).
  *   e4m3 weights: ffn_e is moe_expert_ffn's, its quantizations of x and h
  *   included. 16-bit weights: silu(x W1^T) * (x W3^T) W2^T with fp32 sums, h
- *   held to at least 16 bits of precision in two 16-bit parts.
+ *   held to at least 16 bits of precision in two 16-bit parts (with F16 an h
+ *   past its range is an infinity).
  *
  *   x             [tokens, hidden] of xDtype (F16, BF16, F32; with 16-bit
  *                 weights, theirs), row stride xStride elements.

@@ -210,6 +210,46 @@ def test_many_groups_and_expert_base():
     eu.assert_close(got, *reference(x, w, ws, pairs, base=3 * 96))
 
 
+@pytest.mark.parametrize("total,present", [(1024, [0, 1, 2]), (1024, [5, 700, 1023]), (257, [255, 256]), (288, [31, 287]),
+                                           (600, [])])
+def test_long_lists_of_empty_groups(total, present):
+    """Whole windows of empty groups before, between and after the others."""
+    g = gen(total + len(present))
+    n, N, k = 3 + 40 * len(present), 64, 128
+    q, s, x = eight(n, k, g)
+    w, ws = weights((4,), N, k, g)
+    lst = torch.zeros(total, 2, dtype=torch.int64)
+    lst[:, 1] = -(torch.arange(total) % 2)                # empty: 0 and -1
+    pairs = []
+    for j, i in enumerate(present):
+        lst[i] = torch.tensor([j, 40])
+        pairs.append((j, 40))
+    y = torch.full((n, N), 77.0, dtype=F32, device="cuda")
+    usc.moe_grouped_matmul(q.cuda(), w.cuda(), ws.cuda(), lst.cuda(), x_scales=s.cuda(), out=dict(y=y))
+    ref, b = reference(x, w, ws, pairs)
+    real = ~ref[:, 0].isnan()
+    if present:
+        eu.assert_close(y[real.cuda()], ref[real], b[real])
+    assert (y[~real.cuda()] == 77.0).all()
+
+
+def test_memory_of_a_call_on_another_stream_is_kept_until_it_is_done():
+    g = gen(77)
+    n, N, k = 4000, 512, 1024
+    w, ws = weights((1,), N, k, g)
+    w, ws, x = w.cuda(), ws.cuda(), rows(n, k, BF16, g).cuda()
+    want = usc.moe_grouped_matmul(x, w, ws)["y"]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        got.append(usc.moe_grouped_matmul(x, w, ws, stream=side)["y"])
+        # as large as the call's workspace, on the current stream: must not be its memory
+        torch.full((usc.grouped_matmul_workspace_size(n, k, 1),), 0x7F, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(as_bytes(want), as_bytes(y)) for y in got)
+
+
 def test_experts_outside_and_counts_past_the_rows():
     g = gen(10)
     n, N, k = 150, 64, 128

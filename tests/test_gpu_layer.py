@@ -182,6 +182,15 @@ def test_nan_logits_and_tokens():
     assert y[2].isnan().all() and int(y.isnan().any(1).sum()) == 1
 
 
+def test_f16_values_past_the_range_are_infinities():
+    c = make(3, 4, 128, 32, F16, F16, 14)
+    c["x"][1] = 300.0
+    c["w13"][:] = 2.0                            # h of token 1: (128 * 600)^2
+    c["w2"][:] = 1.0
+    y = run(c, 2)["y"].float().cpu()
+    assert y[1].isinf().all() and (y[1] > 0).all()
+
+
 def test_strided_rows_and_no_tokens():
     c = make(10, 8, 264, 72, BF16, BF16, 10)
     big = torch.full((20, 300), float("nan"), dtype=BF16, device="cuda")

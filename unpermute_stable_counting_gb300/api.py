@@ -411,6 +411,17 @@ def _same_device(name, t, index):
         raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
+def _used_on(stream, *tensors):
+    """Tensors that a call allocated for work on another stream than the current
+    one: their memory is not reused before that work is done."""
+    if stream is None:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        t.record_stream(stream)
+
+
 def _workspace(workspace, size, index):
     if workspace is None:
         return torch.empty(max(size, 1), dtype=torch.uint8, device=_device(index))
@@ -465,6 +476,7 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
                                     _raw_stream(stream, index))
             if st:
                 _check(st, "moe_quantize")
+            _used_on(stream, values, scales)
             return out
     else:
         values, scales = out["values"], out["scales"]
@@ -494,6 +506,7 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
     st = lib().moe_quantize(x.data_ptr(), dt, max(1, batch), rows, cols, xs, block_rows,
                             num_rows, values.data_ptr(), vs, saddr, ss, _raw_stream(stream, index))
     _check(st, "moe_quantize")
+    _used_on(stream, values, scales)
     return out
 
 
@@ -579,9 +592,11 @@ def moe_grouped_matmul(x, weights, weight_scales, group_list=None, *, x_scales=N
         workspace = _workspace(workspace, grouped_matmul_workspace_size(rows, K, dt), index)
         wsp, size = workspace.data_ptr(), workspace.numel()
     st = lib().moe_grouped_matmul(x.data_ptr(), dt, xst, xsa, xss, wa, wst, wsa, ga, groups,
-                                  _vector("num_rows", num_rows, torch.int64, index), expert_base, rows, E, N, K, ya,
+                                  _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, N, K, ya,
                                   ydt, yst, wsp, size, _raw_stream(stream, index))
     _check(st, "moe_grouped_matmul")
+    if stream is not None:
+        _used_on(stream, out["y"], *([] if workspace is None else [workspace]))
     return out
 
 
@@ -613,9 +628,10 @@ def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scal
     out, ya, ydt, yst = _out_rows(out, rows, H, out_dtype, index)
     workspace = _workspace(workspace, expert_ffn_workspace_size(rows, H, inter), index)
     st = lib().moe_expert_ffn(x.data_ptr(), dt, xst, xsa, xss, a13, st13, s13, a2, st2, s2, ga, groups,
-                              _vector("num_rows", num_rows, torch.int64, index), expert_base, rows, E, H, inter, ya,
+                              _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, H, inter, ya,
                               ydt, yst, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, index))
     _check(st, "moe_expert_ffn")
+    _used_on(stream, out["y"], workspace)
     return out
 
 
@@ -644,6 +660,7 @@ def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None,
     score + select_bias."""
     if score not in ("softmax", "sigmoid"):
         raise ValueError("score must be softmax or sigmoid")
+    topk = int(topk)
     (T, H), xstrides = _rows_of("x", x, 2)
     rshape, rstrides = _rows_of("router", router, 2)
     xdt, rdt, index = _float_dt("x", x), _float_dt("router", router), x.get_device()
@@ -693,6 +710,8 @@ def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None,
                          flags, routed_scale, y.data_ptr(), _row_stride(yshape, ystrides), ids, weights,
                          workspace.data_ptr(), workspace.numel(), _raw_stream(stream, index))
     _check(st, "moe_layer")
+    if stream is not None:
+        _used_on(stream, workspace, *out.values())
     return out
 
 

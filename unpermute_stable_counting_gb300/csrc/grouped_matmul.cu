@@ -5,17 +5,28 @@
 // the experts' network built on it (silu(x W1^T) * (x W3^T), quantized again,
 // times W2^T), whose first product quantizes its result in its epilogue.
 //
-// Tiles of 128 rows x BN columns, 128 values of k per step, on tcgen05 with
-// e4m3 operands. The scales change every step, so a step's product goes to its
-// own columns of tensor memory (two to four such buffers), and two warpgroups
-// add it to the fp32 sums that they keep in registers, times the scales:
+// Tiles of 128 rows x BN columns, or of 256 rows on a pair of blocks (each loads
+// its own rows and half of the weights, which halves what L2 and shared memory
+// carry per product), 128 values of k per step, on tcgen05 with e4m3 operands. The
+// scales change every step, so a step's product goes to its own columns of tensor
+// memory (two to four such buffers), and two warpgroups add it to the fp32 sums
+// that they keep in registers, times the scales:
 //   warp 0      TMA loads of the tiles' operands (a ring of stages)
 //   warp 1      matrix instructions
 //   warp 2      hands the tiles to the sums
 //   warps 4-11  sums; at the end of a tile the result
-// One persistent block per SM takes tiles round robin; every warp walks the
-// group list for itself (32 groups at a time, one per lane), so there is no
-// scheduling traffic and the host never reads the list.
+// One persistent block per SM takes tiles round robin; the loads, the instructions
+// and the tiles' warp each walk the group list (32 groups at a time, one per
+// lane), so the host never reads it.
+//
+// What bounds it: with many rows the sums. A step of a pair's tile is 512 cycles of
+// the tensor cores, and 128 columns of loads from tensor memory and fp32 additions
+// for each of two warps per scheduler take about 690; the tensor pipe is active
+// 66 % of the time (4096 x 7168 x 7168). Sums of more warps with fewer columns, loads
+// of 32 columns and a step unrolled twice were all slower: they spill. Without the
+// additions the same kernel takes 516 us for 16384 x 7168 x 7168 (with them 572 us
+// = 2.94 PFLOP/s). With few rows per group the weights' way from HBM: 576 rows over
+// 64 experts, 7168 -> 4096, 285 us = 0.98 of the measured copy rate.
 #include "tensor.cuh"
 
 #include <algorithm>
@@ -96,6 +107,24 @@ template <int TM> struct Walk {
         }
         total = __shfl_sync(0xffffffffu, end, 31);
     }
+    // The first window from g on that has rows, or the list's last one: eight windows per round trip
+    // to memory (a batching's list ends in a row of empty groups for every absent expert).
+    static __device__ __forceinline__ int skip(const GroupArgs& a, int lane, int g) {
+        while (g + 32 < a.G) {
+            int64_t c[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = g + 32 * j + lane;
+                c[j] = i < a.G ? a.groups[2 * (int64_t)i + 1] : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (g + 32 >= a.G || __ballot_sync(0xffffffffu, c[j] > 0)) return g;
+                g += 32;
+            }
+        }
+        return g;
+    }
     __device__ __forceinline__ void begin(const GroupArgs& a, int lane) {
         first = base_tile = base_row = 0;
         load(a, lane);
@@ -105,7 +134,7 @@ template <int TM> struct Walk {
             if (first + 32 >= a.G) return false;
             base_tile += total;
             base_row = min(base_row + window_rows, a.rows);
-            first += 32;
+            first = skip(a, lane, first + 32);
             load(a, lane);
         }
         const int in = t - base_tile;
@@ -403,8 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_inc<200>();
         const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes << 16
-        // this warpgroup's half of the columns (narrow tiles: half of the chunk), its two chunks'
-        // weight scales
+        // this warpgroup's half of the columns, of narrow tiles its chunk
         const int half = C::kHalves == 2 ? group : 0;
         const uint32_t from = lanes + (C::kHalves == 2 ? group * C::kHalf : group * C::kChunk);
         uint8_t* stage = out_stage + (warp - 4) * C::kOutBytes;

@@ -22,6 +22,12 @@
 // Copies run through a ring of TMA stages (one thread), instructions are
 // issued by one thread, and two warpgroups take the results out of tensor
 // memory. The first stages of step 3 are requested before its barrier.
+//
+// What bounds it: HBM in steps 2 and 3 (one token, 8 experts of 7168 x 2048 in 8
+// bits: 235 MB in 39 us and 117 MB in 25 us with their starts and ends), and around
+// them about 12 us of latency: the launch, the logits, three to four barriers of 1.3 us, and
+// the choice, whose instructions come from L2. 76 us, 0.68 of the time that the copy
+// rate gives the bytes; 64 tokens, 64 experts of 7168 x 1024 in 16 bits: 480 us, 0.86.
 #include "tensor.cuh"
 
 #include <cooperative_groups.h>
@@ -550,7 +556,9 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
                     } else {
                         const uint16_t hi = Elem<MR_DTYPE_F16>::from_f32(h);
                         *p = hi;
-                        *q = Elem<MR_DTYPE_F16>::from_f32(h - Elem<MR_DTYPE_F16>::to_f32(hi));
+                        // past f16's range the high part is an infinity, and the whole value
+                        *q = (hi & 0x7FFFu) == 0x7C00u ? 0
+                                                       : Elem<MR_DTYPE_F16>::from_f32(h - Elem<MR_DTYPE_F16>::to_f32(hi));
                     }
                 }
             }
