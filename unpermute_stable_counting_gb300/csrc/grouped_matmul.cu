@@ -169,11 +169,11 @@ template <int BN, bool SWIGLU, bool PAIR> struct Cfg {
     static constexpr int kLoad = kChunk < 16 ? kChunk : 16;          // columns per tensor memory load
     static constexpr int kLoads = kChunks * kChunk / kLoad;
     static constexpr int kStageBytes = (kTileM + kLoadN) * kTileK;
-    // a summing warp's rows on their way out: a pair's 16-bit results leave whole (send_columns),
-    // others 64 bytes of a row at a time, which leaves a fourth stage for the weights of few rows
+    // a summing warp's rows on their way out: a pair's results leave by 8 KB (send_columns), others
+    // 64 bytes of a row at a time, which leaves a fourth stage for the weights of few rows
     // (decode batch: 294 against 306 us)
     static constexpr bool kSend = PAIR && !SWIGLU;
-    static constexpr int kOutBytes = kSend ? 32 * kChunk * 2 : 2048;
+    static constexpr int kOutBytes = kSend ? 8192 : 2048;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kSumWarps * kOutBytes;
 };
 
@@ -268,26 +268,36 @@ __device__ __forceinline__ void store_columns(uint8_t* stage, const float2 (&acc
     }
 }
 
-// The same for 32 real rows of 16-bit results and a map of y: the columns go to
-// shared memory, 64 at a time as a tile of 128-byte rows in the map's swizzle, and
-// from there by asynchronous copies beside the next tile's sums. (Stores from
-// registers took 3400 cycles of a tile's 27500 at 32 steps, these take a third.)
+// The same for 32 real rows and a map of y: the columns go to shared memory as
+// tiles of 128-byte rows in the map's swizzle, two of them at a time (all of a
+// warp's 16-bit columns, half of its fp32 ones), and from there by asynchronous
+// copies beside the next tile's sums. (Stores from registers took 3400 cycles of a
+// tile's 27500 at 32 steps, these take half.)
 template <int DT, int CW>
 __device__ __forceinline__ void send_columns(uint8_t* stage, const float2 (&acc)[CW / 2], const CUtensorMap* map,
                                              int row, int col, int cols, int lane) {
-    if (lane == 0) tma_store_read();  // the tile before has left
-    __syncwarp();
+    constexpr int kCols = DT == MR_DTYPE_F32 ? 32 : 64;
 #pragma unroll
-    for (int c = 0; c < CW; c += 64) {
+    for (int b = 0; b < CW / kCols; ++b) {
+        if (b % 2 == 0) {  // what was sent from here has left
+            if (lane == 0) tma_store_read();
+            __syncwarp();
+        }
+        uint8_t* tile = stage + b % 2 * 4096;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const float2* p = &acc[c / 2 + 4 * u];
-            *reinterpret_cast<uint4*>(stage + c * 64 + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-                make_uint4(pack2<DT>(p[0]), pack2<DT>(p[1]), pack2<DT>(p[2]), pack2<DT>(p[3]));
+            const float2* p = &acc[(b * kCols + u * kCols / 8) / 2];
+            uint4 v;
+            if constexpr (DT == MR_DTYPE_F32)
+                v = make_uint4(__float_as_uint(p[0].x), __float_as_uint(p[0].y), __float_as_uint(p[1].x),
+                               __float_as_uint(p[1].y));
+            else
+                v = make_uint4(pack2<DT>(p[0]), pack2<DT>(p[1]), pack2<DT>(p[2]), pack2<DT>(p[3]));
+            *reinterpret_cast<uint4*>(tile + lane * 128 + ((u ^ (lane & 7)) << 4)) = v;
         }
         smem_proxy_fence();
         __syncwarp();
-        if (lane == 0 && c < cols) tma_store_2d(map, smem_u32(stage + c * 64), col + c, row);
+        if (lane == 0 && b * kCols < cols) tma_store_2d(map, smem_u32(tile), col + b * kCols, row);
     }
 }
 
@@ -561,8 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (n < a.N) {
                             if (a.y_dtype == MR_DTYPE_BF16)
                                 send_columns<MR_DTYPE_BF16, C::kChunk>(stage, acc[0], &map_y, (int)r, n, a.N - n, lane);
-                            else
+                            else if (a.y_dtype == MR_DTYPE_F16)
                                 send_columns<MR_DTYPE_F16, C::kChunk>(stage, acc[0], &map_y, (int)r, n, a.N - n, lane);
+                            else
+                                send_columns<MR_DTYPE_F32, C::kChunk>(stage, acc[0], &map_y, (int)r, n, a.N - n, lane);
                         }
                     } else if (a.y_map) {
                         if (lane == 0) tma_store_read();
@@ -683,11 +695,15 @@ mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
         !make_tensor_map(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, 3, wd, ws, wb))
         return MR_ERR_CUDA;
     m[2] = m[0];  // not read
-    a.y_map = pair && !p.swiglu && a.y_vec && a.y_dtype != MR_DTYPE_F32;
+    a.y_map = pair && !p.swiglu && a.y_vec;
     if (a.y_map) {
-        const uint64_t yd[2] = {(uint64_t)a.N, (uint64_t)a.rows}, ys[1] = {(uint64_t)a.y_stride * 2};
-        const uint32_t yb[2] = {64, 32};
-        if (!make_tensor_map(&m[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.y, 2, yd, ys, yb)) return MR_ERR_CUDA;
+        const bool wide = a.y_dtype == MR_DTYPE_F32;
+        const int elem = wide ? 4 : 2;
+        const uint64_t yd[2] = {(uint64_t)a.N, (uint64_t)a.rows}, ys[1] = {(uint64_t)a.y_stride * elem};
+        const uint32_t yb[2] = {(uint32_t)(128 / elem), 32};
+        if (!make_tensor_map(&m[2], wide ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, elem, a.y, 2,
+                             yd, ys, yb))
+            return MR_ERR_CUDA;
     }
     cudaError_t e;
     if (pair) e = p.swiglu ? launch_grouped<256, true, true>(m, a, tiles, s)
