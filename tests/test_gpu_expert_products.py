@@ -295,6 +295,40 @@ def test_strided_operands_and_results(xdt):
     assert (ybuf[:, :3] == 77).all() and (ybuf[:, 3 + N:] == 77).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("lead", [0, 1, 2, 3, 5, 7])
+def test_quantize_rows_that_start_anywhere(lead, dtype):
+    """Rows whose 16-byte words are shared with their neighbours: what lies beside them is not used."""
+    g = gen(41)
+    n, k = 37, 261
+    x = rows(n, k, dtype, g)
+    buf = torch.full((lead + n * (k + 2),), float("nan"), dtype=dtype, device="cuda")
+    xv = buf[lead:].view(n, k + 2)[:, :k]
+    xv.copy_(x.cuda())
+    v, s = eu.quantize(x.double())
+    r = usc.moe_quantize(xv)
+    assert torch.equal(r["scales"].double().cpu(), s)
+    assert torch.equal(r["values"].float().double().cpu(), v)
+
+
+@pytest.mark.parametrize("out", [BF16, F16, F32])
+@pytest.mark.parametrize("N,lead,step", [(131, 1, 2), (515, 0, 0), (514, 3, 1), (96, 1, 1), (33, 2, 3), (1, 1, 1)])
+@pytest.mark.parametrize("pairs", [[(0, 33), (1, 1), (2, 100)], [(1, 700)]])
+def test_results_that_start_anywhere(N, lead, step, out, pairs):
+    """Rows of results that share their words with what lies beside them, which stays as it is."""
+    g = gen(42)
+    n, k, E = sum(c for _, c in pairs), 130, 3
+    q, s, x = eight(n, k, g)
+    w, ws = weights((E,), N, k, g)
+    ybuf = torch.full((lead + n * (N + step) + 1,), 77.0, dtype=out, device="cuda")
+    body = ybuf[lead:lead + n * (N + step)].view(n, N + step)
+    usc.moe_grouped_matmul(padded_cuda(q), padded_cuda(w), ws.cuda(), group_list(pairs, len(pairs)), x_scales=s.cuda(),
+                           out=dict(y=body[:, :N]))
+    ref, b = reference(x, w, ws, pairs)
+    eu.assert_close(body[:, :N], ref, b)
+    assert (body[:, N:] == 77).all() and (ybuf[:lead] == 77).all() and ybuf[-1] == 77
+
+
 def test_non_finite_rows_stay_in_their_rows():
     g = gen(12)
     n, N, k = 200, 130, 256

@@ -52,7 +52,7 @@ struct GroupArgs {
     int n_tiles;
     void* y;
     int64_t y_stride;
-    int y_dtype, y_vec, y_map; // y_vec: rows can be stored as 16-byte vectors; y_map: there is a map of y
+    int y_dtype, y_loose;  // y_loose: rows that cannot be stored as 16-byte vectors
     uint8_t* hq;               // quantized result of the network's first product
     int64_t hq_stride;
     float* hs;                 // its scales, [b * hs_block + r]
@@ -158,9 +158,12 @@ template <int TM> struct Walk {
 
 // PAIR: two blocks share a tile of 256 rows. Each loads its own 128 rows and half
 // of the weight columns, and the matrix instructions read both halves.
-template <int BN, bool SWIGLU, bool PAIR> struct Cfg {
+// LOOSE: rows of results that do not start on 16 bytes, in kernels of their own: in
+// the others the code beside the sums cost aligned rows up to 14 percent (3026 rows
+// x 3705 x 5396 fp32 out: 106 us without, 120 with it).
+template <int BN, bool SWIGLU, bool PAIR, bool LOOSE> struct Cfg {
     static constexpr int kLoadN = PAIR ? BN / 2 : BN;                // weight columns this block loads
-    static constexpr int kStages = PAIR ? (SWIGLU ? 6 : 5) : BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kStages = PAIR ? (SWIGLU || LOOSE ? 6 : 5) : BN == 256 ? 4 : BN == 128 ? 6 : 8;
     static constexpr int kBufs = BN == 256 ? 2 : 4;                  // tensor memory buffers
     static constexpr int kHalves = BN == 256 ? 2 : 1;                // column halves with barriers of their own
     static constexpr int kHalf = BN / kHalves;
@@ -172,26 +175,71 @@ template <int BN, bool SWIGLU, bool PAIR> struct Cfg {
     // a summing warp's rows on their way out: a pair's results leave by 8 KB (send_columns), others
     // 64 bytes of a row at a time, which leaves a fourth stage for the weights of few rows
     // (decode batch: 294 against 306 us)
-    static constexpr bool kSend = PAIR && !SWIGLU;
+    static constexpr bool kSend = PAIR && !SWIGLU && !LOOSE;
     static constexpr int kOutBytes = kSend ? 8192 : 2048;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kSumWarps * kOutBytes;
 };
 
+// Rows of U 16-byte pieces from shared memory (store_rows' layout) to rows that
+// start anywhere: 4-byte words side by side, a word between two of the source's
+// where a row of 16-bit values starts in the middle of one, whose first and last
+// value then go alone. Not inlined: one copy that stays in the instruction cache.
+template <int U, int ELEM>
+__device__ __noinline__ void store_words(const uint8_t* stage, uint8_t* row0, int64_t row_step, int rows, int left) {
+    constexpr int kWords = 4 * U, kRows = 32 / kWords, kBatch = 4;
+    const int lane = threadIdx.x & 31, j = lane % kWords, r = lane / kWords;
+    uint8_t* to = row0 + r * row_step + 4 * j;
+    // a lane's rows are an even number of rows apart, so all of them start alike
+    const int mid = ELEM == 2 ? (int)(reinterpret_cast<uintptr_t>(to) & 2u) : 0;
+    const bool first = mid != 0 && j == 0 && left > 0;
+    left = min(left, 16 * U) - 4 * j - mid;  // bytes of this lane's word
+    const bool word = left >= 4, half = ELEM == 2 && !word && left >= 2;
+    to += mid;
+    row_step *= kRows;
+#pragma unroll
+    for (int b = 0; b < 32 / (kBatch * kRows); ++b) {
+        if (b * kBatch * kRows >= rows) break;
+        uint32_t w[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int q = r + (b * kBatch + i) * kRows;
+            w[i] = *reinterpret_cast<const uint32_t*>(stage + q * 64 + (((j >> 2) ^ ((q >> 1) & 3)) << 4) + (j & 3) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i, to += row_step) {
+            const bool mine = r + (b * kBatch + i) * kRows < rows;
+            uint32_t v = w[i];
+            if constexpr (ELEM == 2) {
+                v = __funnelshift_r(v, __shfl_down_sync(0xffffffffu, v, 1), 8 * mid);
+                if (mine && first) *reinterpret_cast<uint16_t*>(to - 2) = (uint16_t)w[i];
+                if (mine && half) *reinterpret_cast<uint16_t*>(to) = (uint16_t)v;
+            }
+            if (mine && word) *reinterpret_cast<uint32_t*>(to) = v;
+        }
+    }
+    __syncwarp();
+}
+
 // Stores a warp's 32 rows (lane: row) of U 16-byte pieces, U <= 4, so that the
 // lanes of an instruction write whole segments of a few rows: straight from the
 // registers every lane would write to a row of its own, 32 lines per
-// instruction. `to`: this lane's piece of its first row, bytes; step: bytes from
-// one of its rows to the next (32 / U rows on). `whole`: every row and piece is
-// real and aligned; otherwise `rows` rows and `left` bytes of each are.
-template <int U>
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4 (&v)[U], uint8_t* to, int64_t step,
-                                           bool whole, int rows, int64_t left, int elem, bool vec, int lane) {
+// instruction. `row0`: the first row's first piece; row_step: bytes from a row to
+// the next. `whole`: every row and piece is real; otherwise `rows` rows and `left`
+// bytes of each are. LOOSE: rows that do not start on 16 bytes.
+template <int U, bool LOOSE>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4 (&v)[U], uint8_t* row0, int64_t row_step,
+                                           bool whole, int rows, int left, int elem, int lane) {
     // 64-byte rows, pieces permuted so that eight lanes hit different banks
     const int key = (lane >> 1) & 3;
 #pragma unroll
     for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ key) << 4)) = v[u];
     __syncwarp();
     constexpr int kRows = 32 / U;  // rows per instruction
+    if constexpr (LOOSE) {
+        if (elem == 4) store_words<U, 4>(stage, row0, row_step, rows, left);
+        else store_words<U, 2>(stage, row0, row_step, rows, left);
+        return;
+    }
     uint4 w[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -199,6 +247,8 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint4 (&v)[U], 
         w[i] = *reinterpret_cast<const uint4*>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
     }
     __syncwarp();
+    uint8_t* to = row0 + lane / U * row_step + lane % U * 16;
+    const int64_t step = kRows * row_step;
     if (whole) {
 #pragma unroll
         for (int i = 0; i < U; ++i, to += step) *reinterpret_cast<uint4*>(to) = w[i];
@@ -208,7 +258,7 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint4 (&v)[U], 
 #pragma unroll
     for (int i = 0; i < U; ++i, to += step) {
         if (i * kRows + lane / U >= rows || left <= 0) continue;
-        if (vec && left >= 16) {
+        if (left >= 16) {
             *reinterpret_cast<uint4*>(to) = w[i];
             continue;
         }
@@ -238,15 +288,13 @@ template <int DT> __device__ __forceinline__ uint32_t pack2(float2 v) {
 }
 
 // CW columns of the warp's rows, from `row0` (first row, first column) on.
-template <int DT, int CW>
+template <int DT, int CW, bool LOOSE>
 __device__ __forceinline__ void store_columns(uint8_t* stage, const float2 (&acc)[CW / 2], uint8_t* row0,
-                                              int64_t row_step, int rows, int cols, bool vec, int lane) {
+                                              int64_t row_step, int rows, int cols, int lane) {
     constexpr int kElem = DT == MR_DTYPE_F32 ? 4 : 2;
     constexpr int kMost = 64 / kElem;                // columns per 64-byte segment
     constexpr int W = CW < kMost ? CW : kMost, U = W * kElem / 16;
-    const bool whole = vec && rows == 32 && cols >= CW;
-    uint8_t* to = row0 + lane / U * row_step + lane % U * 16;
-    const int64_t step = 32 / U * row_step;
+    const bool whole = rows == 32 && cols >= CW;
 #pragma unroll
     for (int c = 0; c < CW; c += W) {
         uint4 v[U];
@@ -264,7 +312,7 @@ __device__ __forceinline__ void store_columns(uint8_t* stage, const float2 (&acc
             }
             v[u] = make_uint4(x[0], x[1], x[2], x[3]);
         }
-        store_rows<U>(stage, v, to + kElem * c, step, whole, rows, kElem * (int64_t)(cols - c), kElem, vec, lane);
+        store_rows<U, LOOSE>(stage, v, row0 + kElem * c, row_step, whole, rows, kElem * (cols - c), kElem, lane);
     }
 }
 
@@ -301,11 +349,11 @@ __device__ __forceinline__ void send_columns(uint8_t* stage, const float2 (&acc)
     }
 }
 
-template <int BN, bool SWIGLU, bool PAIR>
+template <int BN, bool SWIGLU, bool PAIR, bool LOOSE>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                           const __grid_constant__ CUtensorMap map_y, const GroupArgs a) {
-    using C = Cfg<BN, SWIGLU, PAIR>;
+    using C = Cfg<BN, SWIGLU, PAIR, LOOSE>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[C::kStages], s_empty[C::kStages];
     __shared__ __align__(8) uint64_t t_full[C::kBufs * C::kHalves], t_empty[C::kBufs * C::kHalves];
@@ -557,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     w[j] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
-                store_rows<4>(stage, w, a.hq + (r + lane / 4) * a.hq_stride + n + lane % 4 * 16, 8 * a.hq_stride,
-                              wrows == 32, wrows, 64, 4, true, lane);
+                store_rows<4, false>(stage, w, a.hq + r * a.hq_stride + n, a.hq_stride,
+                              wrows == 32, wrows, 64, 4, lane);
             } else if (wrows > 0 && MR_IN_RANGE(r + wrows - 1, a.rows, 901)) {
                 const int elem = a.y_dtype == MR_DTYPE_F32 ? 4 : 2;
                 const int n = n0 + group * C::kChunk;
@@ -566,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t step = a.y_stride * elem;
                 bool sent = false;
                 if constexpr (C::kSend) {
-                    if (a.y_map && wrows == 32) {
+                    if (wrows == 32) {
                         sent = true;
                         if (n < a.N) {
                             if (a.y_dtype == MR_DTYPE_BF16)
@@ -576,18 +624,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else
                                 send_columns<MR_DTYPE_F32, C::kChunk>(stage, acc[0], &map_y, (int)r, n, a.N - n, lane);
                         }
-                    } else if (a.y_map) {
+                    } else {
                         if (lane == 0) tma_store_read();
                         __syncwarp();
                     }
                 }
                 if (!sent && n < a.N) {
                     if (a.y_dtype == MR_DTYPE_BF16)
-                        store_columns<MR_DTYPE_BF16, C::kChunk>(stage, acc[0], to, step, wrows, a.N - n, a.y_vec, lane);
+                        store_columns<MR_DTYPE_BF16, C::kChunk, LOOSE>(stage, acc[0], to, step, wrows, a.N - n, lane);
                     else if (a.y_dtype == MR_DTYPE_F16)
-                        store_columns<MR_DTYPE_F16, C::kChunk>(stage, acc[0], to, step, wrows, a.N - n, a.y_vec, lane);
+                        store_columns<MR_DTYPE_F16, C::kChunk, LOOSE>(stage, acc[0], to, step, wrows, a.N - n, lane);
                     else
-                        store_columns<MR_DTYPE_F32, C::kChunk>(stage, acc[0], to, step, wrows, a.N - n, a.y_vec, lane);
+                        store_columns<MR_DTYPE_F32, C::kChunk, LOOSE>(stage, acc[0], to, step, wrows, a.N - n, lane);
                 }
             }
             ++done;
@@ -617,11 +665,11 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <int BN, bool SWIGLU, bool PAIR>
+template <int BN, bool SWIGLU, bool PAIR, bool LOOSE>
 cudaError_t launch_grouped(const CUtensorMap (&m)[3], const GroupArgs& a, int64_t tiles,
                            cudaStream_t s) {
-    auto kernel = grouped_matmul_kernel<BN, SWIGLU, PAIR>;
-    constexpr int smem = Cfg<BN, SWIGLU, PAIR>::kSmem;
+    auto kernel = grouped_matmul_kernel<BN, SWIGLU, PAIR, LOOSE>;
+    constexpr int smem = Cfg<BN, SWIGLU, PAIR, LOOSE>::kSmem;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
@@ -653,6 +701,16 @@ cudaError_t launch_grouped(const CUtensorMap (&m)[3], const GroupArgs& a, int64_
     }
     cfg.gridDim = dim3((unsigned)(tiles < n ? tiles : n) * (PAIR ? 2 : 1));
     return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], a);
+}
+
+template <bool LOOSE>
+cudaError_t launch_plain(const CUtensorMap (&m)[3], const GroupArgs& a, bool pair, int bn, int64_t tiles,
+                         cudaStream_t s) {
+    if (pair) return launch_grouped<256, false, true, LOOSE>(m, a, tiles, s);
+    if (bn == 256) return launch_grouped<256, false, false, LOOSE>(m, a, tiles, s);
+    if (bn == 128) return launch_grouped<128, false, false, LOOSE>(m, a, tiles, s);
+    if (bn == 64) return launch_grouped<64, false, false, LOOSE>(m, a, tiles, s);
+    return launch_grouped<32, false, false, LOOSE>(m, a, tiles, s);
 }
 
 // One product over the groups. x: e4m3 rows, w: e4m3 [experts][N][K]; the first
@@ -695,8 +753,7 @@ mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
         !make_tensor_map(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, 3, wd, ws, wb))
         return MR_ERR_CUDA;
     m[2] = m[0];  // not read
-    a.y_map = pair && !p.swiglu && a.y_vec;
-    if (a.y_map) {
+    if (pair && !p.swiglu && !a.y_loose) {
         const bool wide = a.y_dtype == MR_DTYPE_F32;
         const int elem = wide ? 4 : 2;
         const uint64_t yd[2] = {(uint64_t)a.N, (uint64_t)a.rows}, ys[1] = {(uint64_t)a.y_stride * elem};
@@ -706,13 +763,9 @@ mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
             return MR_ERR_CUDA;
     }
     cudaError_t e;
-    if (pair) e = p.swiglu ? launch_grouped<256, true, true>(m, a, tiles, s)
-                           : launch_grouped<256, false, true>(m, a, tiles, s);
-    else if (p.swiglu) e = launch_grouped<256, true, false>(m, a, tiles, s);
-    else if (bn == 256) e = launch_grouped<256, false, false>(m, a, tiles, s);
-    else if (bn == 128) e = launch_grouped<128, false, false>(m, a, tiles, s);
-    else if (bn == 64) e = launch_grouped<64, false, false>(m, a, tiles, s);
-    else e = launch_grouped<32, false, false>(m, a, tiles, s);
+    if (p.swiglu) e = pair ? launch_grouped<256, true, true, false>(m, a, tiles, s)
+                           : launch_grouped<256, true, false, false>(m, a, tiles, s);
+    else e = a.y_loose ? launch_plain<true>(m, a, pair, bn, tiles, s) : launch_plain<false>(m, a, pair, bn, tiles, s);
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
 
@@ -846,7 +899,7 @@ extern "C" mr_status moe_grouped_matmul(const void* x, int32_t xDtype, int64_t x
     a.y = y;
     a.y_stride = yStride;
     a.y_dtype = yDtype;
-    a.y_vec = aligned16(y) && (yStride * elem_bytes(yDtype)) % 16 == 0;
+    a.y_loose = !aligned16(y) || (yStride * elem_bytes(yDtype)) % 16 != 0;
     if (a.G == 0) return MR_OK;
     return run_product(p, a, s);
 }
@@ -939,6 +992,6 @@ extern "C" mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStri
     a.y = y;
     a.y_stride = yStride;
     a.y_dtype = yDtype;
-    a.y_vec = aligned16(y) && (yStride * elem_bytes(yDtype)) % 16 == 0;
+    a.y_loose = !aligned16(y) || (yStride * elem_bytes(yDtype)) % 16 != 0;
     return run_product(p, a, s);
 }

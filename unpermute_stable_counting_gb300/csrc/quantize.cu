@@ -23,9 +23,37 @@ template <int DT> struct Piece {
     static constexpr int kPieces = 16 / kValues;
     static constexpr int kStep = 8 * kValues;                   // values from piece to piece
 
-    static __device__ __forceinline__ uint4 load(const void* row, int64_t col, int64_t K, bool vec) {
-        if (vec && col + kValues <= K)
-            return ld_stream_v4(reinterpret_cast<const char*>(row) + col * (DT == MR_DTYPE_F32 ? 4 : 2));
+    // A whole piece that starts anywhere: the one or two aligned 16-byte words that hold it, from `q` on
+    // and `off` bytes before it, shifted into place.
+    static __device__ __forceinline__ uint4 load_shifted(const char* q, uint32_t off) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(q));
+        const uint4 b = off ? __ldg(reinterpret_cast<const uint4*>(q + 16)) : a;
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (off & 8u) {
+#pragma unroll
+            for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+        }
+        if (off & 4u) {
+#pragma unroll
+            for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+        }
+        if (DT != MR_DTYPE_F32) {
+            const uint32_t bits = (off & 2u) * 8u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], bits);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // lo, hi: the bytes of x are in [lo, hi)
+    static __device__ __forceinline__ uint4 load(const void* row, int64_t col, int64_t K, bool vec, const char* lo,
+                                                 const char* hi) {
+        if (col + kValues <= K) {
+            const char* p = reinterpret_cast<const char*>(row) + col * (DT == MR_DTYPE_F32 ? 4 : 2);
+            if (vec) return ld_stream_v4(p);
+            const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+            const char* q = p - off;
+            if (q >= lo && q + (off ? 32 : 16) <= hi) return load_shifted(q, off);
+        }
         uint32_t u[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int j = 0; j < kValues; ++j) {
@@ -55,6 +83,7 @@ template <int DT> struct Piece {
 
 struct QuantArgs {
     const void* x;
+    const char* x_end;  // past its last row's last value
     int64_t rows, K, x_stride;
     const int64_t* num_rows;
     uint8_t* q;
@@ -90,7 +119,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
         col[n] = (i - row[n] * a.blocks) * kScaleBlock + sub * P::kValues;
         const char* src = reinterpret_cast<const char*>(a.x) + row[n] * a.x_stride * kElem;
 #pragma unroll
-        for (int p = 0; p < P::kPieces; ++p) raw[n][p] = P::load(src, col[n] + p * P::kStep, a.K, a.vec_in);
+        for (int p = 0; p < P::kPieces; ++p)
+            raw[n][p] = P::load(src, col[n] + p * P::kStep, a.K, a.vec_in, reinterpret_cast<const char*>(a.x), a.x_end);
     }
 #pragma unroll
     for (int n = 0; n < kItems; ++n) {
@@ -175,6 +205,7 @@ cudaError_t enqueue_quantize(const void* x, int dt, int64_t rows, int64_t K, int
     const int elem = dt == MR_DTYPE_F32 ? 4 : 2;
     QuantArgs a;
     a.x = x;
+    a.x_end = reinterpret_cast<const char*>(x) + ((rows - 1) * xStride + K) * elem;
     a.rows = rows;
     a.K = K;
     a.x_stride = xStride;
