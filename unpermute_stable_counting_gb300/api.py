@@ -434,8 +434,12 @@ def _workspace(workspace, size, index):
 def _wide_rows(lead, cols, index):
     """e4m3 [*lead, cols] whose rows start on 16 bytes."""
     wide = -(-cols // 16) * 16
-    t = torch.empty((*lead, wide), dtype=_E4M3, device=_device(index))
-    return t if wide == cols else t[..., :cols]
+    if wide == cols:
+        return torch.empty((*lead, cols), dtype=_E4M3, device=_device(index))
+    strides = [1]  # one tensor, not a slice of a wider one: that costs a small call 4 us more
+    for n in (wide, *lead[:0:-1]):
+        strides.append(strides[-1] * max(n, 1))
+    return torch.empty_strided((*lead, cols), strides[::-1], dtype=_E4M3, device=_device(index))
 
 
 def quantize_outputs(shape, device, block_rows: int = 1) -> dict:

@@ -20,14 +20,24 @@ __device__ __forceinline__ float max_abs(float m, float v) {
 // whole lines).
 template <int DT> struct Piece {
     static constexpr int kValues = DT == MR_DTYPE_F32 ? 4 : 8;  // of a piece
+    static constexpr int kElem = 16 / kValues;
     static constexpr int kPieces = 16 / kValues;
     static constexpr int kStep = 8 * kValues;                   // values from piece to piece
 
-    // A whole piece that starts anywhere: the one or two aligned 16-byte words that hold it, from `q` on
-    // and `off` bytes before it, shifted into place.
-    static __device__ __forceinline__ uint4 load_shifted(const char* q, uint32_t off) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(q));
-        const uint4 b = off ? __ldg(reinterpret_cast<const uint4*>(q + 16)) : a;
+    // A piece of a row that starts on 16 bytes, or its values one by one.
+    static __device__ __forceinline__ uint4 load(const char* row, uint32_t col, int64_t K, bool vec) {
+        if (vec && col + kValues <= K) return ld_stream_v4(row + col * kElem);
+        uint32_t u[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < kValues; ++j) {
+            if (col + j >= K) break;
+            if (DT == MR_DTYPE_F32) u[j & 3] = reinterpret_cast<const uint32_t*>(row)[col + j];
+            else u[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[col + j] << (16 * (j & 1));
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    // 16 bytes that start `off` bytes into two aligned words of 16: words by selection, halves by a shift.
+    static __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_t off) {
         uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         if (off & 8u) {
 #pragma unroll
@@ -44,24 +54,32 @@ template <int DT> struct Piece {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // lo, hi: the bytes of x are in [lo, hi)
-    static __device__ __forceinline__ uint4 load(const void* row, int64_t col, int64_t K, bool vec, const char* lo,
-                                                 const char* hi) {
-        if (col + kValues <= K) {
-            const char* p = reinterpret_cast<const char*>(row) + col * (DT == MR_DTYPE_F32 ? 4 : 2);
-            if (vec) return ld_stream_v4(p);
-            const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
-            const char* q = p - off;
-            if (q >= lo && q + (off ? 32 : 16) <= hi) return load_shifted(q, off);
-        }
-        uint32_t u[4] = {0u, 0u, 0u, 0u};
+    // The pieces of a row that starts anywhere, from the aligned words that hold them; inside: the 16 bytes
+    // on either side of the row belong to x too, otherwise words outside [lo, hi) are left alone.
+    static __device__ __forceinline__ void load_loose(uint4 (&v)[kPieces], const char* row, uint32_t col, int64_t K,
+                                                      bool inside, const char* lo, const char* hi) {
+        const char* p = row + col * kElem;
+        const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);  // the same for all pieces
+        const char* q = p - off;
+        const uint32_t next = off ? 16 : 0;
+        if (inside && col + (kPieces - 1) * kStep + kValues <= K) {
+            uint4 b[kPieces];
 #pragma unroll
-        for (int j = 0; j < kValues; ++j) {
-            if (col + j >= K) break;
-            if (DT == MR_DTYPE_F32) u[j & 3] = reinterpret_cast<const uint32_t*>(row)[col + j];
-            else u[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[col + j] << (16 * (j & 1));
+            for (int i = 0; i < kPieces; ++i) {
+                v[i] = __ldg(reinterpret_cast<const uint4*>(q + i * 128));
+                b[i] = __ldg(reinterpret_cast<const uint4*>(q + i * 128 + next));
+            }
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) v[i] = shifted(v[i], b[i], off);
+            return;
         }
-        return make_uint4(u[0], u[1], u[2], u[3]);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const char* w = q + i * 128;
+            if (col + i * kStep + kValues <= K && w >= lo && w + next + 16 <= hi)
+                v[i] = shifted(__ldg(reinterpret_cast<const uint4*>(w)), __ldg(reinterpret_cast<const uint4*>(w + next)), off);
+            else v[i] = load(row, col + i * kStep, K, false);
+        }
     }
     static __device__ __forceinline__ void widen(const uint4& w, float* v) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -92,18 +110,19 @@ struct QuantArgs {
     int64_t row_step, block_step;
     uint32_t blocks;        // ceil(K / 128)
     uint32_t magic, shift;  // i / blocks = umulhi(i, magic) >> shift for i < 2^31 (magic 0: blocks is 1)
-    int vec_in;             // rows readable as 16-byte vectors
     int vec_out;            // q rows start on 16 bytes
 };
 
 // kItems blocks per 8 lanes, all loads before the first use. The instructions
 // bound this kernel before HBM does: about 6 per value here; with 8 values per lane
 // and 64-bit index arithmetic it was 19, and 32768 x 4096 bf16 rows took 84 us.
-template <int DT, int kItems>
+// LOOSE: rows that do not start on 16 bytes, by aligned words shifted into place
+// (27285 x 5005 bf16: 104 us, fp32 136; rows of 5008 take 87 and 120; with bounds
+// checks and a load-and-shift per piece it took 131 and 228).
+template <int DT, int kItems, bool LOOSE>
 __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     pdl_enter();
     using P = Piece<DT>;
-    constexpr int kElem = DT == MR_DTYPE_F32 ? 4 : 2;
     int64_t rows = a.rows;
     if (a.num_rows) rows = max((int64_t)0, min(rows, *a.num_rows));
     const uint32_t total = (uint32_t)(rows * a.blocks);
@@ -117,10 +136,14 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
         const uint32_t i = min(first + n * 32, total - 1);  // past the end: the last block again, not stored
         row[n] = a.magic ? __umulhi(i, a.magic) >> a.shift : i;
         col[n] = (i - row[n] * a.blocks) * kScaleBlock + sub * P::kValues;
-        const char* src = reinterpret_cast<const char*>(a.x) + row[n] * a.x_stride * kElem;
+        const char* src = reinterpret_cast<const char*>(a.x) + row[n] * a.x_stride * P::kElem;
+        if constexpr (LOOSE) {
+            const bool inside = a.x_stride >= 8 && row[n] - 1u < (uint32_t)a.rows - 2u;
+            P::load_loose(raw[n], src, col[n], a.K, inside, reinterpret_cast<const char*>(a.x), a.x_end);
+        } else {
 #pragma unroll
-        for (int p = 0; p < P::kPieces; ++p)
-            raw[n][p] = P::load(src, col[n] + p * P::kStep, a.K, a.vec_in, reinterpret_cast<const char*>(a.x), a.x_end);
+            for (int p = 0; p < P::kPieces; ++p) raw[n][p] = P::load(src, col[n] + p * P::kStep, a.K, true);
+        }
     }
 #pragma unroll
     for (int n = 0; n < kItems; ++n) {
@@ -158,13 +181,19 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     }
 }
 
-template <int DT>
+template <int DT, bool LOOSE>
 cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s) {
     // two blocks per 8 lanes once that still fills the SMs twice over
     const int64_t total = a.rows * a.blocks;
     if (total >= (int64_t)device_sm_count() * 8 * 64 * 2)
-        return launch_pdl(quantize_kernel<DT, 2>, dim3((unsigned)((total + 63) / 64)), dim3(256), 0, s, a);
-    return launch_pdl(quantize_kernel<DT, 1>, dim3((unsigned)((total + 31) / 32)), dim3(256), 0, s, a);
+        return launch_pdl(quantize_kernel<DT, 2, LOOSE>, dim3((unsigned)((total + 63) / 64)), dim3(256), 0, s, a);
+    return launch_pdl(quantize_kernel<DT, 1, LOOSE>, dim3((unsigned)((total + 31) / 32)), dim3(256), 0, s, a);
+}
+
+template <bool LOOSE> cudaError_t launch_quantize(const QuantArgs& a, int dt, cudaStream_t s) {
+    return dt == MR_DTYPE_F32   ? launch_quantize<MR_DTYPE_F32, LOOSE>(a, s)
+           : dt == MR_DTYPE_F16 ? launch_quantize<MR_DTYPE_F16, LOOSE>(a, s)
+                                : launch_quantize<MR_DTYPE_BF16, LOOSE>(a, s);
 }
 
 // 128 x 128 blocks (weights, quantized once when a model is loaded): one block
@@ -216,16 +245,14 @@ cudaError_t enqueue_quantize(const void* x, int dt, int64_t rows, int64_t K, int
     a.row_step = rowStep;
     a.block_step = blockStep;
     a.blocks = (uint32_t)((K + kScaleBlock - 1) / kScaleBlock);
-    a.vec_in = (reinterpret_cast<uintptr_t>(x) % 16 == 0) && (xStride * elem) % 16 == 0;
     a.vec_out = (reinterpret_cast<uintptr_t>(q) % 16 == 0) && qStride % 16 == 0;
     // ceil(2^(31 + l) / blocks) for 2^(l - 1) < blocks <= 2^l: below 2^32, and exact for i < 2^31
     int l = 0;
     while ((1u << l) < a.blocks) ++l;
     a.magic = l ? (uint32_t)(((1ull << (31 + l)) + a.blocks - 1) / a.blocks) : 0u;
     a.shift = l ? l - 1 : 0;
-    return dt == MR_DTYPE_F32   ? launch_quantize<MR_DTYPE_F32>(a, stream)
-           : dt == MR_DTYPE_F16 ? launch_quantize<MR_DTYPE_F16>(a, stream)
-                                : launch_quantize<MR_DTYPE_BF16>(a, stream);
+    const bool loose = reinterpret_cast<uintptr_t>(x) % 16 != 0 || (xStride * elem) % 16 != 0;
+    return loose ? launch_quantize<true>(a, dt, stream) : launch_quantize<false>(a, dt, stream);
 }
 
 }  // namespace mr
