@@ -313,7 +313,7 @@ def test_quantize_rows_that_start_anywhere(lead, dtype):
 
 @pytest.mark.parametrize("out", [BF16, F16, F32])
 @pytest.mark.parametrize("N,lead,step", [(131, 1, 2), (515, 0, 0), (514, 3, 1), (96, 1, 1), (33, 2, 3), (1, 1, 1)])
-@pytest.mark.parametrize("pairs", [[(0, 33), (1, 1), (2, 100)], [(1, 700)]])
+@pytest.mark.parametrize("pairs", [[(0, 33), (1, 1), (2, 100)], [(1, 700)], [(2, 417), (0, 343)]])
 def test_results_that_start_anywhere(N, lead, step, out, pairs):
     """Rows of results that share their words with what lies beside them, which stays as it is."""
     g = gen(42)
