@@ -163,13 +163,13 @@ template <int TM> struct Walk {
 // x 3705 x 5396 fp32 out: 106 us without, 120 with it).
 template <int BN, bool SWIGLU, bool PAIR, bool LOOSE> struct Cfg {
     static constexpr int kLoadN = PAIR ? BN / 2 : BN;                // weight columns this block loads
-    static constexpr int kStages = PAIR ? (SWIGLU || LOOSE ? 6 : 5) : BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kStages = PAIR ? (SWIGLU || LOOSE ? 6 : 5) : BN == 256 ? 4 : 6;
     static constexpr int kBufs = BN == 256 ? 2 : 4;                  // tensor memory buffers
     static constexpr int kHalves = BN == 256 ? 2 : 1;                // column halves with barriers of their own
     static constexpr int kHalf = BN / kHalves;
     static constexpr int kChunks = SWIGLU ? 2 : 1;                   // column chunks per warpgroup
     static constexpr int kChunk = BN / 2 / kChunks;                  // columns of a chunk
-    static constexpr int kLoad = kChunk < 16 ? kChunk : 16;          // columns per tensor memory load
+    static constexpr int kLoad = 16;                                 // columns per tensor memory load
     static constexpr int kLoads = kChunks * kChunk / kLoad;
     static constexpr int kStageBytes = (kTileM + kLoadN) * kTileK;
     // a summing warp's rows on their way out: a pair's results leave by 8 KB (send_columns), others
@@ -708,9 +708,7 @@ cudaError_t launch_plain(const CUtensorMap (&m)[3], const GroupArgs& a, bool pai
                          cudaStream_t s) {
     if (pair) return launch_grouped<256, false, true, LOOSE>(m, a, tiles, s);
     if (bn == 256) return launch_grouped<256, false, false, LOOSE>(m, a, tiles, s);
-    if (bn == 128) return launch_grouped<128, false, false, LOOSE>(m, a, tiles, s);
-    if (bn == 64) return launch_grouped<64, false, false, LOOSE>(m, a, tiles, s);
-    return launch_grouped<32, false, false, LOOSE>(m, a, tiles, s);
+    return launch_grouped<128, false, false, LOOSE>(m, a, tiles, s);
 }
 
 // One product over the groups. x: e4m3 rows, w: e4m3 [experts][N][K]; the first
@@ -725,21 +723,22 @@ struct Product {
 };
 
 mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
-    // Pairs of blocks (tiles of 256 rows) run 1.15 to 1.17 times as fast as single ones on full tiles
-    // (16384 rows x 7168 x 7168: 579 against 679 us; 64 groups of 512: 226 against 250 us), but
-    // round a group up to twice as many rows. One group: exactly. More: their sizes are not known
-    // here; a group of average size wastes about half a tile, which pays from some 360 rows on (64
-    // ragged groups of 512 on average: 871 against 907 us for the network).
-    const bool pair = a.G == 1 ? 100 * (int64_t)ceil_div(a.rows, 256) * 256 <= 115 * (int64_t)ceil_div(a.rows, 128) * 128
-                               : (int64_t)a.rows >= 360 * (int64_t)a.G;
-    const int tile_m = pair ? 2 * kTileM : kTileM;
-    const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G, a.rows);
+    // The tile whose rounds over the SMs cost least. A step of a tile of 128 x 128, of 128 x 256 and of a
+    // pair's 256 x 256 takes about 5 : 8 : 7 (in one round, of 56 steps: 25, 37 and 33 us; 64 columns
+    // take as long as 128, so there is no narrower tile). 512 rows x 7168 x 4096: 25 us in tiles of 128
+    // columns, 33 in pairs; 2048 x 4096 x 4096: 39 in pairs, 49 in tiles of 128, 43 of 256. The
+    // groups' sizes are not known here: half a tile of each is taken to be empty.
     const int sms = device_sm_count();
-    int bn = 256;
-    if (!p.swiglu && !pair) {
-        // the widest tile that still gives every SM one (narrower ones read the rows more often)
-        while (bn > 32 && m_tiles * ceil_div(a.N, bn) < sms) bn /= 2;
-    }
+    auto cost = [&](int rows, int cols, int units, int step) {
+        const int64_t down = a.G == 1 ? ceil_div(a.rows, rows) : std::max(std::min(a.G, a.rows), a.rows / rows + a.G / 2);
+        return (down * ceil_div(a.N, cols) + units - 1) / units * step;
+    };
+    const int64_t wide = cost(kTileM, p.swiglu ? 128 : 256, sms, 8);
+    const int64_t narrow = p.swiglu ? INT64_MAX : cost(kTileM, 128, sms, 5);
+    const bool pair = cost(2 * kTileM, p.swiglu ? 128 : 256, sms / 2, 7) <= std::min(wide, narrow);
+    const int bn = pair || wide <= narrow ? 256 : 128;
+    const int tile_m = pair ? 2 * kTileM : kTileM;
+    const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G - 1, a.rows);  // or fewer
     a.n_tiles = p.swiglu ? ceil_div(a.N, 128) : ceil_div(a.N, bn);
     const int64_t tiles = m_tiles * a.n_tiles;
     if (tiles > INT32_MAX) return MR_ERR_PARAM_INVALID;
