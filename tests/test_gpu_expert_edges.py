@@ -1,0 +1,71 @@
+"""The expert operators at the edges of what they take: layouts, streams, sizes
+and values, against the definitions in 64 bits. Tolerances: see _expert_util."""
+import ctypes
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import unpermute_stable_counting_gb300 as usc  # noqa: E402
+
+import _expert_util as eu  # noqa: E402
+
+BF16, F16, F32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+@pytest.fixture(autouse=True)
+def _no_wait_ran_out():
+    from unpermute_stable_counting_gb300 import _native
+    yield
+    n = ctypes.c_uint32(0)
+    assert _native.lib().mr_waits_out(ctypes.byref(n), 1) == 0
+    assert n.value == 0
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def as_bytes(t):
+    return t.contiguous().view(torch.uint8)
+
+
+# ---------------------------------------------------------------------------
+# moe_quantize
+# ---------------------------------------------------------------------------
+
+def quantized_blocks(x):
+    """(values, scales) of float64 weights [..., n, k] in 128 x 128 blocks."""
+    n, k = x.shape[-2:]
+    t = torch.nn.functional.pad(x, (0, -k % 128, 0, -n % 128)).unflatten(-1, (-1, 128)).unflatten(-3, (-1, 128))
+    s = eu.scale_of(t.abs().amax((-3, -1)))
+    return eu.e4m3(x / s.repeat_interleave(128, -2)[..., :n, :].repeat_interleave(128, -1)[..., :k]), s
+
+
+@pytest.mark.parametrize("cut", [lambda w: w[:, ::2], lambda w: w[:, 1:2], lambda w: w[1:2, ::2], lambda w: w[:, :, 3:90],
+                                 lambda w: w[::2, 1:2, :130, 8:]])
+def test_quantize_weights_of_four_dimensions_in_part(cut):
+    """Matrices some way apart, of x and of the values that are written."""
+    w = torch.randn(4, 2, 140, 200, generator=gen(3)).to(BF16)
+    x = cut(w)
+    buf = torch.full((4, 2, 140, 208), 0x55, dtype=torch.uint8, device="cuda")
+    values = cut(buf.view(E4M3))[..., :x.shape[-1]]
+    q, s = quantized_blocks(x.double())
+    out = dict(values=values, scales=torch.empty(s.shape, device="cuda"))
+    usc.moe_quantize(cut(w.cuda()), block_rows=128, out=out)
+    assert torch.equal(out["scales"].cpu().double(), s) and torch.equal(values.cpu().double(), q)
+    left = torch.ones(4, 2, 140, 208, dtype=torch.bool)
+    cut(left)[..., :x.shape[-1]] = False
+    assert (buf.cpu()[left] == 0x55).all()
+    r = usc.moe_quantize(cut(w.cuda()), block_rows=128)
+    assert torch.equal(r["scales"].cpu().double(), s) and torch.equal(r["values"].cpu().double(), q)

@@ -384,9 +384,13 @@ def _row_stride(shape, strides):
 def _matrix_strides(name, shape, strides, size=1):
     """{row, matrix} byte strides of weights [..., rows, cols] with evenly spaced matrices."""
     row = _row_stride(shape, strides)
-    if len(shape) == 4 and shape[0] > 1 and strides[0] != shape[1] * strides[1]:
-        raise ValueError(f"{name} must have evenly spaced matrices")
-    matrix = strides[-3] if shape[-3] > 1 else shape[-2] * row
+    matrix = shape[-2] * row  # of a single matrix, whose stride says nothing
+    if shape[-3] > 1:
+        matrix = strides[-3]
+        if len(shape) == 4 and shape[0] > 1 and strides[0] != shape[1] * matrix:
+            raise ValueError(f"{name} must have evenly spaced matrices")
+    elif len(shape) == 4 and shape[0] > 1:
+        matrix = strides[0]
     return _Pair(row * size, matrix * size)
 
 
