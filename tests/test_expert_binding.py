@@ -1,6 +1,8 @@
 """What the Python side of the operators hands to the library: addresses, strides
 and streams, without a GPU (tensors that say they are on one, and a library that
 only records its calls)."""
+import contextlib
+import inspect
 import types
 
 import pytest
@@ -18,6 +20,9 @@ class OnGpu(torch.Tensor):
 
     def get_device(self):
         return self.index
+
+    def record_stream(self, stream):
+        self.used_on = getattr(self, "used_on", []) + [stream.name]
 
 
 def gpu(t, index=0):
@@ -42,13 +47,48 @@ class Calls:
         return self.made[0]
 
 
+class Streams:
+    """A device's current stream, and the streams that memory was asked for on."""
+    def __init__(self):
+        self.current, self.asked = self.make("main", 7), []
+
+    def make(self, name, handle):
+        return types.SimpleNamespace(name=name, cuda_stream=handle)
+
+    @contextlib.contextmanager
+    def use(self, stream):
+        before, self.current = self.current, stream
+        yield
+        self.current = before
+
+    def counted(self, allocate):
+        def call(*args, **kw):
+            self.asked.append(self.current.name)
+            return gpu(allocate(*args, **kw))
+        return call
+
+
 @pytest.fixture
-def calls(monkeypatch):
+def streams(monkeypatch):
+    s = Streams()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: s.current)
+    monkeypatch.setattr(torch.cuda, "stream", s.use)
+    monkeypatch.setattr(api, "_as_stream", lambda stream: stream, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: s.current.cuda_stream, raising=False)
+    return s
+
+
+@pytest.fixture
+def calls(monkeypatch, streams):
     c = Calls()
     monkeypatch.setattr(api, "lib", lambda: c)
     monkeypatch.setattr(api, "_device", lambda index: torch.device("cpu"))
-    monkeypatch.setattr(api, "_raw_stream", lambda stream, index: 0)
-    return c
+    sizes = (api.grouped_matmul_workspace_size, api.expert_ffn_workspace_size, api.layer_workspace_size)
+    for f in sizes:
+        f.cache_clear()
+    yield c
+    for f in sizes:
+        f.cache_clear()
 
 
 def quantized_matrices(c, x, values, scales):
@@ -84,3 +124,72 @@ def test_weights_that_are_not_evenly_spaced_are_refused(calls):
     with pytest.raises(ValueError):
         api.moe_quantize(x, block_rows=128, out=out)
     assert not calls.made
+
+
+# ---------------------------------------------------------------------------
+# Calls for another stream than the current one
+# ---------------------------------------------------------------------------
+
+def zeros(*shape, dtype=torch.float32):
+    return gpu(torch.zeros(*shape, dtype=torch.uint8 if dtype is E4M3 else dtype).view(dtype))
+
+
+def an_expert_call(name):
+    BF16 = torch.bfloat16
+    x, w, ws = zeros(4, 128, dtype=BF16), zeros(2, 64, 128, dtype=E4M3), zeros(2, 1, 1)
+    w13, s13, w2, s2 = zeros(2, 2, 64, 128, dtype=E4M3), zeros(2, 2, 1, 1), zeros(2, 128, 64, dtype=E4M3), zeros(2, 1, 1)
+    return dict(moe_quantize=((x,), {}), moe_grouped_matmul=((x, w, ws), {}), moe_expert_ffn=((x, w13, s13, w2, s2), {}),
+                moe_layer=((x, zeros(2, 128, dtype=BF16), w13, w2), dict(topk=1, w13_scales=s13, w2_scales=s2)))[name]
+
+
+def a_call(name):
+    i32 = torch.int32
+    x, m = zeros(4, 16, dtype=torch.float16), zeros(4, 2, dtype=torch.int8)
+    if name == "moe_permute":
+        return (x, m), dict(topk=1)
+    if name == "moe_unpermute":
+        return (x, zeros(4, dtype=i32), m, zeros(4, 2)), {}
+    if name == "moe_update_expert":
+        return (zeros(4, 2, dtype=i32), zeros(2, 3, dtype=i32)), dict(world_size=1)
+    shape = dict(expert_num=2, max_out_shape=(1, 2, 2, 16), token_dtype=api.DT_F16)
+    if name == "ffnwb_batching":
+        return (zeros(4, dtype=i32), x, zeros(1, dtype=i32), zeros(1, dtype=i32)), shape
+    if name == "ffnwb_batching_context":
+        return (zeros(1024, dtype=torch.int8),), shape
+    return an_expert_call(name)
+
+
+ENTRIES = ["ffnwb_batching", "ffnwb_batching_context", "moe_permute", "moe_unpermute", "moe_update_expert", "moe_quantize",
+           "moe_grouped_matmul", "moe_expert_ffn", "moe_layer"]
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_memory_of_a_call_for_another_stream_is_asked_for_on_that_stream(calls, streams, monkeypatch, name):
+    """On the current stream it could be memory that a kernel in flight there still uses."""
+    args, kw = a_call(name)
+    f = getattr(api, name)
+    for maker in ("empty", "zeros", "empty_strided"):
+        monkeypatch.setattr(torch, maker, streams.counted(getattr(torch, maker)))
+    out = f(*args, **kw)
+    assert streams.asked and set(streams.asked) == {"main"}
+    assert not any(hasattr(t, "used_on") for t in args)
+    launches = [c for c in calls.made if not c.name.endswith("_size")]
+    assert len(launches) == 1 and getattr(launches[0].args[-1], "value", launches[0].args[-1]) == 7
+    streams.asked.clear(), calls.made.clear()
+    out = f(*args, **kw, stream=streams.make("side", 9))
+    assert streams.asked and set(streams.asked) == {"side"}
+    launches = [c for c in calls.made if not c.name.endswith("_size")]
+    assert len(launches) == 1 and getattr(launches[0].args[-1], "value", launches[0].args[-1]) == 9
+    # what the caller gave is in use on the side stream, what the call made may be on the caller's
+    assert all(t.used_on == ["side"] for t in args)
+    assert all(t.used_on == ["main"] for t in out.values() if t is not None)
+    assert "stream" in inspect.signature(f).parameters and streams.current.name == "main"
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_the_current_stream_by_name(calls, streams, monkeypatch, name):
+    args, kw = a_call(name)
+    for maker in ("empty", "zeros", "empty_strided"):
+        monkeypatch.setattr(torch, maker, streams.counted(getattr(torch, maker)))
+    getattr(api, name)(*args, **kw, stream=streams.current)
+    assert not any(hasattr(t, "used_on") for t in args)

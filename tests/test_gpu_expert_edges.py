@@ -69,3 +69,54 @@ def test_quantize_weights_of_four_dimensions_in_part(cut):
     assert (buf.cpu()[left] == 0x55).all()
     r = usc.moe_quantize(cut(w.cuda()), block_rows=128)
     assert torch.equal(r["scales"].cpu().double(), s) and torch.equal(r["values"].cpu().double(), q)
+
+
+# ---------------------------------------------------------------------------
+# Streams
+# ---------------------------------------------------------------------------
+
+def rows(n, k, dtype, g):
+    x = torch.randn(n, k, generator=g)
+    x[:, torch.randint(0, k, (max(1, k // 100),), generator=g)] *= 10
+    return x.to(dtype)
+
+
+def weights(lead, n, k, g):
+    w = (torch.randn(*lead, n, k, generator=g) * 100).clamp(-448, 448).to(E4M3)
+    s = torch.exp(0.4 * torch.randn(*lead, eu.blocks(n), eu.blocks(k), generator=g)) / (100 * k**0.5)
+    return w, s
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_call_on_another_stream_beside_one_whose_memory_was_just_freed(raw):
+    """The first call's workspace and result are freed on the host with its kernels still queued on the
+    current stream: the second call, on a side stream, must not be given them."""
+    g = gen(78)
+    H, inter, n = 512, 256, 900
+    w13, s13 = (t.cuda() for t in weights((2, 2), inter, H, g))
+    w2, s2 = (t.cuda() for t in weights((2,), H, inter, g))
+    xs = [rows(n, H, BF16, g).cuda() for _ in range(2)]
+    lists = [torch.tensor([[0, 400], [1, 500]]).cuda(), torch.tensor([[1, 300], [0, 600]]).cuda()]
+    net = lambda i, **kw: usc.moe_expert_ffn(xs[i], w13, s13, w2, s2, lists[i], **kw)["y"]
+    want = [net(0), net(1)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    first, second = [], []
+    for _ in range(8):
+        torch.cuda._sleep(2_000_000)
+        first.append(net(0)), net(0)           # the second one's result is dropped at once
+        second.append(net(1, stream=side.cuda_stream if raw else side))
+    torch.cuda.synchronize()
+    assert all(torch.equal(as_bytes(y), as_bytes(want[0])) for y in first)
+    assert all(torch.equal(as_bytes(y), as_bytes(want[1])) for y in second)
+
+
+def test_the_default_stream_by_its_handle():
+    x = rows(40, 300, BF16, gen(79)).cuda()
+    want = usc.moe_quantize(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = usc.moe_quantize(x, stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(as_bytes(want[k]), as_bytes(got[k])) for k in want)

@@ -4,11 +4,13 @@ Argument marshalling only: shapes, dtypes and device pointers of torch CUDA
 tensors go to the library; every step of every operation runs in the
 library's CUDA kernels. PyTorch supplies device memory (outputs and the
 workspace, when the caller does not pass them) and the current stream.
+A call with stream= runs as a whole with that stream current.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 
 import torch
 
@@ -50,12 +52,47 @@ def _require_cuda(name, t, dtype=None, strided=False):
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
 
 
-def _stream(stream, device):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device):
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _as_stream(stream):
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream
+    handle = int(stream)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def _cuda_tensors(values):
+    return [t for t in values if isinstance(t, torch.Tensor) and t.is_cuda]
+
+
+def _on_stream(f):
+    """f with an argument more: stream, a torch.cuda.Stream or a cudaStream_t (None: the
+    current stream). f runs with that stream current, so that the memory it allocates
+    comes from that stream's pool. Memory of the current stream's pool may have been freed
+    on the host with its last kernel still in flight, and nothing orders the other stream
+    behind that kernel. Tensors that the caller gave are kept until the stream is done with
+    them, and tensors that the call made until the caller's stream is."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        here, stream = torch.cuda.current_stream(), _as_stream(stream)
+        if stream == here:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            result = f(*args, **kw)
+        for t in _cuda_tensors((*args, *kw.values(), *(kw.get("out") or {}).values())):
+            t.record_stream(stream)
+        for t in _cuda_tensors(result.values()):
+            t.record_stream(here)
+        return result
+
+    signature = inspect.signature(f)
+    argument = inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)
+    call.__signature__ = signature.replace(parameters=[*signature.parameters.values(), argument])
+    return call
 
 
 # ---------------------------------------------------------------------------
@@ -86,11 +123,12 @@ def batching_outputs(Y: int, H: int, expert_num: int, token_dtype: int, device,
         sortedIndices=torch.empty(Y, **i32) if with_sorted_indices else None)
 
 
+@_on_stream
 def ffnwb_batching(expert_ids, token_data, session_ids, micro_batch_ids, *, expert_num: int,
                    max_out_shape, token_dtype: int, layer_num: int = 1, layer_id: int = 0,
                    token_ids=None, scales=None, scale_stride: int = 4, token_row_stride=None,
                    need_schedule: int = 0, with_sorted_indices: bool = False, out: dict | None = None,
-                   workspace=None, stream=None, full_tail: bool = False) -> dict:
+                   workspace=None, full_tail: bool = False) -> dict:
     """Run the batching on the current CUDA stream.
 
     token_data: CUDA tensor whose first dimension is the Y slots; row s starts
@@ -119,7 +157,7 @@ def ffnwb_batching(expert_ids, token_data, session_ids, micro_batch_ids, *, expe
             _ptr(out["y"]), _ptr(out["groupList"]), _ptr(out["sessionIds"]),
             _ptr(out["microBatchIds"]), _ptr(out["tokenIds"]), _ptr(out["expertOffsets"]),
             _ptr(out.get("dynamicScale")), _ptr(out["actualTokenNum"]), _ptr(out.get("sortedIndices"))]
-    tail = [_ptr(workspace), int(workspace.numel()), _stream(stream, dev)]
+    tail = [_ptr(workspace), int(workspace.numel()), _stream(dev)]
     if full_tail:
         st = lib().ffnwb_batching_ex(*args, MR_BATCHING_FULL_TAIL, *tail)
     else:
@@ -137,10 +175,11 @@ def batching_context_workspace_size(expert_num: int, max_out_shape, token_dtype:
     return int(ws.value)
 
 
+@_on_stream
 def ffnwb_batching_context(schedule_context, *, expert_num: int, max_out_shape, token_dtype: int,
                            layer_num: int = 1, need_schedule: int = 0,
                            wait_timeout_us: int = 1_000_000, out: dict | None = None,
-                           workspace=None, stream=None, full_tail: bool = False) -> dict:
+                           workspace=None, full_tail: bool = False) -> dict:
     """Batching from a ScheduleContext (a CUDA tensor of its 1024 bytes) on the
     current stream. Returns the batching outputs plus scheduleStatus (int32 [1]):
     blocks not ready with need_schedule = 1, or -1 for a context that does not fit.
@@ -163,7 +202,7 @@ def ffnwb_batching_context(schedule_context, *, expert_num: int, max_out_shape, 
             _ptr(out["groupList"]), _ptr(out["sessionIds"]), _ptr(out["microBatchIds"]),
             _ptr(out["tokenIds"]), _ptr(out["expertOffsets"]), _ptr(out.get("dynamicScale")),
             _ptr(out["actualTokenNum"]), _ptr(out["scheduleStatus"])]
-    tail = [_ptr(workspace), int(workspace.numel()), _stream(stream, dev)]
+    tail = [_ptr(workspace), int(workspace.numel()), _stream(dev)]
     if full_tail:
         st = lib().ffnwb_batching_context_ex(*args, MR_BATCHING_FULL_TAIL, *tail)
     else:
@@ -216,9 +255,10 @@ def unpermute_outputs(T: int, H: int, n: int, token_dtype: int, probs_dtype: int
                       if probs_dtype is not None else None))
 
 
+@_on_stream
 def moe_unpermute(permuted_tokens, sorted_indices, routing_map=None, probs=None, *,
                   padded_mode: bool = False, restore_shape=None, out: dict | None = None,
-                  workspace=None, stream=None) -> dict:
+                  workspace=None) -> dict:
     """Run the unpermute on the current CUDA stream. Returns unpermutedTokens,
     outIndex, permuteTokenId and permuteProbs (None without probs)."""
     _require_cuda("permuted_tokens", permuted_tokens)
@@ -239,7 +279,7 @@ def moe_unpermute(permuted_tokens, sorted_indices, routing_map=None, probs=None,
         _ptr(permuted_tokens), _ptr(sorted_indices), _ptr(routing_map), _ptr(probs), rows, H, tdt,
         n, pdt, T, Eu, int(bool(padded_mode)), rs, _ptr(out["unpermutedTokens"]),
         _ptr(out["outIndex"]), _ptr(out["permuteTokenId"]), _ptr(out.get("permuteProbs")),
-        _ptr(workspace), int(workspace.numel()), _stream(stream, dev))
+        _ptr(workspace), int(workspace.numel()), _stream(dev))
     _check(st, "moe_unpermute")
     return out
 
@@ -253,8 +293,9 @@ def permute_workspace_size(T: int, H: int, token_dtype: int, Eu: int, topk: int 
     return int(ws.value)
 
 
+@_on_stream
 def moe_permute(tokens, routing_map, *, topk: int = 0, padded_mode: bool = False, capacity: int = 0,
-                out: dict | None = None, workspace=None, stream=None) -> dict:
+                out: dict | None = None, workspace=None) -> dict:
     """Permute tokens [T, H] by routing_map [T, Eu] on the current stream.
     Returns permutedTokens, sortedIndices and permutedRows (int32 [1])."""
     _require_cuda("tokens", tokens)
@@ -276,7 +317,7 @@ def moe_permute(tokens, routing_map, *, topk: int = 0, padded_mode: bool = False
     st = lib().moe_permute(_ptr(tokens), _ptr(routing_map), T, H, tdt, Eu, int(topk),
                            int(bool(padded_mode)), int(capacity), _ptr(out["permutedTokens"]),
                            _ptr(out["sortedIndices"]), _ptr(out.get("permutedRows")),
-                           _ptr(workspace), int(workspace.numel()), _stream(stream, dev))
+                           _ptr(workspace), int(workspace.numel()), _stream(dev))
     _check(st, "moe_permute")
     return out
 
@@ -284,9 +325,10 @@ def moe_permute(tokens, routing_map, *, topk: int = 0, padded_mode: bool = False
 _ID_TO_DT = {torch.int32: 4, torch.int64: 5}
 
 
+@_on_stream
 def moe_update_expert(expert_ids, eplb_table, *, local_rank: int = 0, world_size: int,
                       balance_mode: int = 0, scales=None, threshold=None, active=None,
-                      out: dict | None = None, stream=None) -> dict:
+                      out: dict | None = None) -> dict:
     """Map expert_ids [BS, K] (int32/int64) to physical instances through
     eplb_table [E, F] int32 and, with scales [BS, K] and threshold [K] (or
     [1, K]), prune them. Strided views are passed by their strides (no copy).
@@ -320,7 +362,7 @@ def moe_update_expert(expert_ids, eplb_table, *, local_rank: int = 0, world_size
     st = lib().moe_update_expert(_ptr(expert_ids), _ID_TO_DT[expert_ids.dtype], _ptr(eplb_table),
                                  _ptr(scales), sdt, _ptr(threshold), _ptr(active), BS, K, E, F,
                                  int(local_rank), int(world_size), int(balance_mode),
-                                 int64_array(strides), _ptr(bal), _ptr(msk), _stream(stream, dev))
+                                 int64_array(strides), _ptr(bal), _ptr(msk), _stream(dev))
     _check(st, "moe_update_expert")
     return out
 
@@ -351,10 +393,8 @@ def _device(index):
     return torch.device("cuda", index)
 
 
-def _raw_stream(stream, index):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _float_dt(name, t, table=_TORCH_TO_DT):
@@ -415,17 +455,6 @@ def _same_device(name, t, index):
         raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
-def _used_on(stream, *tensors):
-    """Tensors that a call allocated for work on another stream than the current
-    one: their memory is not reused before that work is done."""
-    if stream is None:
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        t.record_stream(stream)
-
-
 def _workspace(workspace, size, index):
     if workspace is None:
         return torch.empty(max(size, 1), dtype=torch.uint8, device=_device(index))
@@ -457,7 +486,8 @@ def quantize_outputs(shape, device, block_rows: int = 1) -> dict:
                                    dtype=torch.float32, device=_device(index)))
 
 
-def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = None, stream=None) -> dict:
+@_on_stream
+def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = None) -> dict:
     """Quantize x (f16/bf16/f32) to e4m3 blocks on the current stream. Returns
     values and scales.
 
@@ -481,10 +511,9 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
         if block_rows == 1:
             st = lib().moe_quantize(x.data_ptr(), dt, 1, rows, cols, _Pair(0, _row_stride(shape, strides)), 1, num_rows,
                                     values.data_ptr(), _Pair(0, -(-cols // 16) * 16), scales.data_ptr(), None,
-                                    _raw_stream(stream, index))
+                                    _raw_stream(index))
             if st:
                 _check(st, "moe_quantize")
-            _used_on(stream, values, scales)
             return out
     else:
         values, scales = out["values"], out["scales"]
@@ -512,9 +541,8 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
             xs[0], xs[1] = xs[1], xs[0]
             vs[0], vs[1] = vs[1], vs[0]
     st = lib().moe_quantize(x.data_ptr(), dt, max(1, batch), rows, cols, xs, block_rows,
-                            num_rows, values.data_ptr(), vs, saddr, ss, _raw_stream(stream, index))
+                            num_rows, values.data_ptr(), vs, saddr, ss, _raw_stream(index))
     _check(st, "moe_quantize")
-    _used_on(stream, values, scales)
     return out
 
 
@@ -579,9 +607,10 @@ def _out_rows(out, rows, cols, dtype, index):
     return out, y.data_ptr(), _float_dt("y", y), _row_stride(shape, strides)
 
 
+@_on_stream
 def moe_grouped_matmul(x, weights, weight_scales, group_list=None, *, x_scales=None, num_rows=None,
                        expert_base: int = 0, out_dtype=torch.bfloat16, out: dict | None = None,
-                       workspace=None, stream=None) -> dict:
+                       workspace=None) -> dict:
     """Product of each group's rows with its expert's e4m3 weights [experts,
     out_cols, cols] on the current stream. Returns y [rows, out_cols].
 
@@ -601,10 +630,8 @@ def moe_grouped_matmul(x, weights, weight_scales, group_list=None, *, x_scales=N
         wsp, size = workspace.data_ptr(), workspace.numel()
     st = lib().moe_grouped_matmul(x.data_ptr(), dt, xst, xsa, xss, wa, wst, wsa, ga, groups,
                                   _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, N, K, ya,
-                                  ydt, yst, wsp, size, _raw_stream(stream, index))
+                                  ydt, yst, wsp, size, _raw_stream(index))
     _check(st, "moe_grouped_matmul")
-    if stream is not None:
-        _used_on(stream, out["y"], *([] if workspace is None else [workspace]))
     return out
 
 
@@ -616,9 +643,9 @@ def expert_ffn_workspace_size(rows: int, hidden: int, inter: int) -> int:
     return int(ws.value)
 
 
+@_on_stream
 def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scales=None, num_rows=None,
-                   expert_base: int = 0, out_dtype=None, out: dict | None = None, workspace=None,
-                   stream=None) -> dict:
+                   expert_base: int = 0, out_dtype=None, out: dict | None = None, workspace=None) -> dict:
     """The experts' network, y = quantized(silu(x W1^T) * (x W3^T)) W2^T, for
     each group's rows on the current stream. Returns y [rows, hidden].
 
@@ -637,9 +664,8 @@ def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scal
     workspace = _workspace(workspace, expert_ffn_workspace_size(rows, H, inter), index)
     st = lib().moe_expert_ffn(x.data_ptr(), dt, xst, xsa, xss, a13, st13, s13, a2, st2, s2, ga, groups,
                               _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, H, inter, ya,
-                              ydt, yst, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, index))
+                              ydt, yst, workspace.data_ptr(), workspace.numel(), _raw_stream(index))
     _check(st, "moe_expert_ffn")
-    _used_on(stream, out["y"], workspace)
     return out
 
 
@@ -654,9 +680,10 @@ def layer_workspace_size(tokens: int, hidden: int, inter: int, experts: int, top
     return int(ws.value)
 
 
+@_on_stream
 def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None, score: str = "softmax",
               renormalize: bool = True, routed_scale: float = 1.0, select_bias=None, out: dict | None = None,
-              workspace=None, stream=None) -> dict:
+              workspace=None) -> dict:
     """A whole mixture-of-experts layer for up to 64 tokens, in one launch on the
     current stream. Returns y [tokens, hidden], expertIds and expertWeights
     [tokens, topk].
@@ -716,10 +743,8 @@ def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None,
     st = lib().moe_layer(x.data_ptr(), xdt, _row_stride((T, H), xstrides), router.data_ptr(), rdt,
                          _row_stride(rshape, rstrides), bias, a13, wdt, st13, s13, a2, st2, s2, T, H, inter, E, topk,
                          flags, routed_scale, y.data_ptr(), _row_stride(yshape, ystrides), ids, weights,
-                         workspace.data_ptr(), workspace.numel(), _raw_stream(stream, index))
+                         workspace.data_ptr(), workspace.numel(), _raw_stream(index))
     _check(st, "moe_layer")
-    if stream is not None:
-        _used_on(stream, workspace, *out.values())
     return out
 
 
