@@ -82,6 +82,7 @@ def streams(monkeypatch):
 def calls(monkeypatch, streams):
     c = Calls()
     monkeypatch.setattr(api, "lib", lambda: c)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(api, "_device", lambda index: torch.device("cpu"))
     sizes = (api.grouped_matmul_workspace_size, api.expert_ffn_workspace_size, api.layer_workspace_size)
     for f in sizes:
@@ -193,3 +194,25 @@ def test_the_current_stream_by_name(calls, streams, monkeypatch, name):
         monkeypatch.setattr(torch, maker, streams.counted(getattr(torch, maker)))
     getattr(api, name)(*args, **kw, stream=streams.current)
     assert not any(hasattr(t, "used_on") for t in args)
+
+
+# ---------------------------------------------------------------------------
+# Tensors of another device than the current one
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_tensors_of_another_device_are_refused(calls, streams, monkeypatch, name):
+    """The library would launch on the current device, with the other one's addresses."""
+    args, kw = a_call(name)
+    for t in (*args, *kw.values()):
+        if isinstance(t, torch.Tensor):
+            t.index = 1
+    for maker in ("empty", "zeros", "empty_strided"):
+        monkeypatch.setattr(torch, maker, streams.counted(getattr(torch, maker)))
+    with pytest.raises(ValueError, match="current device"):
+        getattr(api, name)(*args, **kw)
+    assert not calls.made and not streams.asked
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for maker in ("empty", "zeros", "empty_strided"):
+        monkeypatch.setattr(torch, maker, lambda *a, f=getattr(torch, maker), **k: gpu(f(*a, **k), 1))
+    getattr(api, name)(*args, **kw)

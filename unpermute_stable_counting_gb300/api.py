@@ -41,11 +41,19 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _on_current_device(name, index):
+    """The library launches on the current device, whose streams the handles name."""
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{index}, which is not the current device "
+                         f"(cuda:{torch._C._cuda_getDevice()})")
+
+
 def _require_cuda(name, t, dtype=None, strided=False):
     if t is None:
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    _on_current_device(name, t.get_device())
     if not strided and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
@@ -501,6 +509,7 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
     if not 2 <= dims <= 4:
         raise ValueError("x must have 2 to 4 dimensions")
     dt, index = _float_dt("x", x), x.get_device()
+    _on_current_device("x", index)
     rows, cols = shape[-2], shape[-1]
     sshape = (*shape[:-2], rows if block_rows == 1 else _blocks(rows), _blocks(cols))
     num_rows = _vector("num_rows", num_rows, torch.int64, index)
@@ -558,6 +567,7 @@ def _expert_rows(x, x_scales, group_list):
     """Checks of the rows and groups that both products take."""
     shape, strides = _rows_of("x", x, 2)
     dt, index = _float_dt("x", x, _FLOAT_OR_E4M3), x.get_device()
+    _on_current_device("x", index)
     sa = ss = None
     if dt == DT_E4M3:
         if x_scales is None:
@@ -699,6 +709,7 @@ def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None,
     (T, H), xstrides = _rows_of("x", x, 2)
     rshape, rstrides = _rows_of("router", router, 2)
     xdt, rdt, index = _float_dt("x", x), _float_dt("router", router), x.get_device()
+    _on_current_device("x", index)
     E = rshape[0]
     if rshape[1] != H or w13.dim() != 4 or w13.shape[1] != 2:
         raise ValueError("router must be [experts, hidden], w13 [experts, 2, inter, hidden]")
