@@ -84,7 +84,7 @@ def calls(monkeypatch, streams):
     monkeypatch.setattr(api, "lib", lambda: c)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(api, "_device", lambda index: torch.device("cpu"))
-    sizes = (api.grouped_matmul_workspace_size, api.expert_ffn_workspace_size, api.layer_workspace_size)
+    sizes = [f for f in vars(api).values() if hasattr(f, "cache_clear") and "workspace" in f.__name__]
     for f in sizes:
         f.cache_clear()
     yield c
@@ -216,3 +216,16 @@ def test_tensors_of_another_device_are_refused(calls, streams, monkeypatch, name
     for maker in ("empty", "zeros", "empty_strided"):
         monkeypatch.setattr(torch, maker, lambda *a, f=getattr(torch, maker), **k: gpu(f(*a, **k), 1))
     getattr(api, name)(*args, **kw)
+
+
+def test_the_layer_s_workspace_is_that_of_the_device(calls, monkeypatch):
+    """The same sizes on a device with another number of SMs need another workspace."""
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    for index, size in ((0, 1000), (1, 3000), (0, 1000)):
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: index)
+
+        def answer(*args):
+            args[-1]._obj.value = size
+            return 0
+        monkeypatch.setattr(calls, "moe_layer_get_workspace_size", answer, raising=False)
+        assert api.layer_workspace_size(4, 128, 64, 8, 2, api.DT_E4M3) == size

@@ -392,7 +392,8 @@ def _blocks(n: int) -> int:
 # The expert products are called per layer of a decode step: what a call costs on
 # the host is part of its latency. So their checks read each tensor's attributes
 # once, pointers go to ctypes as plain ints, pairs of strides as arrays of one
-# type, and workspace sizes (pure functions of the sizes) are kept.
+# type, and workspace sizes (functions of the sizes, the layer's also of the device)
+# are kept.
 _Pair = ctypes.c_int64 * 2
 
 
@@ -682,8 +683,14 @@ def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scal
 MR_LAYER_SIGMOID, MR_LAYER_KEEP_WEIGHTS = 1, 2
 
 
-@functools.lru_cache(maxsize=1024)
 def layer_workspace_size(tokens: int, hidden: int, inter: int, experts: int, topk: int, weight_dtype: int) -> int:
+    index = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _layer_workspace_size(index, tokens, hidden, inter, experts, topk, weight_dtype)
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_workspace_size(index, tokens, hidden, inter, experts, topk, weight_dtype):
+    """Of the current device, whose index is `index`: the shares of the second product go by its SMs."""
     ws = ctypes.c_uint64(0)
     _check(lib().moe_layer_get_workspace_size(tokens, hidden, inter, experts, topk, weight_dtype, ctypes.byref(ws)),
            "moe_layer_get_workspace_size")
@@ -736,7 +743,7 @@ def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None,
         a13, a2, s13, s2 = w13.data_ptr(), w2.data_ptr(), None, None
     bias = _vector("select_bias", select_bias, torch.float32, index, (E,))
     # (the size call refuses what the layer does not take before anything is allocated)
-    size = layer_workspace_size(T, H, inter, E, topk, wdt)
+    size = _layer_workspace_size(index, T, H, inter, E, topk, wdt)
     if out is None:
         dev = _device(index)
         out = dict(y=torch.empty((T, H), dtype=x.dtype, device=dev),
