@@ -229,3 +229,33 @@ def test_the_layer_s_workspace_is_that_of_the_device(calls, monkeypatch):
             return 0
         monkeypatch.setattr(calls, "moe_layer_get_workspace_size", answer, raising=False)
         assert api.layer_workspace_size(4, 128, 64, 8, 2, api.DT_E4M3) == size
+
+
+# ---------------------------------------------------------------------------
+# Memory that holds less than it shows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["moe_grouped_matmul", "moe_expert_ffn", "moe_layer"])
+def test_an_expanded_workspace_is_refused(calls, streams, monkeypatch, name):
+    args, kw = an_expert_call(name)
+    with pytest.raises(ValueError, match="contiguous"):
+        getattr(api, name)(*args, **kw, workspace=zeros(1, dtype=torch.uint8).expand(1 << 20), out=OUT(name))
+    assert all(c.name.endswith("_size") for c in calls.made)
+    getattr(api, name)(*args, **kw, workspace=zeros(1 << 20, dtype=torch.uint8)[256:], out=OUT(name))
+
+
+def OUT(name):
+    y = zeros(4, 64 if name == "moe_grouped_matmul" else 128, dtype=torch.bfloat16)
+    return dict(y=y, expertIds=zeros(4, 1, dtype=torch.int32), expertWeights=zeros(4, 1))
+
+
+@pytest.mark.parametrize("scales", [lambda: zeros(1, 1).expand(5, 3), lambda: zeros(1, 3).expand(5, 3),
+                                    lambda: zeros(5, 1).expand(5, 3)])
+def test_expanded_scales_are_not_written(calls, scales):
+    x, values = zeros(5, 300, dtype=torch.bfloat16), zeros(5, 304, dtype=E4M3)[:, :300]
+    with pytest.raises(ValueError, match="scales"):
+        api.moe_quantize(x, out=dict(values=values, scales=scales()))
+    assert not calls.made
+    api.moe_quantize(x, out=dict(values=values, scales=zeros(3, 5).T))
+    api.moe_quantize(x[:1], out=dict(values=values[:1], scales=zeros(3).as_strided((1, 3), (0, 1))))
+    assert [tuple(c.args[11]) for c in calls.made] == [(1, 5), (1, 1)]

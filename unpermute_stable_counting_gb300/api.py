@@ -469,6 +469,8 @@ def _workspace(workspace, size, index):
         return torch.empty(max(size, 1), dtype=torch.uint8, device=_device(index))
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.dtype != torch.uint8:
         raise TypeError("workspace must be a CUDA tensor of uint8")
+    if not workspace.is_contiguous():  # its length in bytes is passed on, whatever lies behind it
+        raise ValueError("workspace must be contiguous")
     _same_device("workspace", workspace, index)
     return workspace
 
@@ -536,6 +538,9 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
         if not scales.is_cuda or scales.dtype != torch.float32 or scales.shape != sshape:
             raise ValueError(f"scales must be float32 {list(sshape)}")
         _same_device("scales", scales, index)
+        for n, step in zip(sshape, scales.stride()):
+            if n > 1 and step < 1:  # an expanded tensor has fewer elements than it shows
+                raise ValueError("scales must have an element of their own for each scale")
         s0, s1 = scales.stride()
         ss = _Pair(max(1, s0), max(1, s1))
         saddr = scales.data_ptr()
