@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 template <int BN, bool SWIGLU, bool PAIR, bool LOOSE>
 cudaError_t launch_grouped(const CUtensorMap (&m)[3], const GroupArgs& a, int64_t tiles,
@@ -866,9 +866,10 @@ extern "C" mr_status moe_grouped_matmul(const void* x, int32_t xDtype, int64_t x
     if (!eight && !workspace) return MR_ERR_PARAM_NULLPTR;
     if (!eight && workspaceSize < ws.bytes) return MR_ERR_WORKSPACE;
     if (!aligned16(weights) || (eight && !aligned16(x)) || (numGroups > 0 && !aligned16(groupList)) ||
-        (!eight && reinterpret_cast<uintptr_t>(workspace) % 256))
+        (!eight && !aligned(workspace, 256)))
         return MR_ERR_PARAM_INVALID;
-    if (reinterpret_cast<uintptr_t>(x) % elem_bytes(xDtype) || reinterpret_cast<uintptr_t>(y) % elem_bytes(yDtype))
+    if (!aligned(x, elem_bytes(xDtype)) || !aligned(y, elem_bytes(yDtype)) || !aligned(xScales, 4) ||
+        !aligned(weightScales, 4) || !aligned(numRows, 8))
         return MR_ERR_PARAM_INVALID;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     Product p{x, xStride, rows, weights, wr, wm, cols, false};
@@ -941,9 +942,10 @@ extern "C" mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStri
     const Quantized wx(rows, hidden), wh(rows, inter);
     if (workspaceSize < wx.bytes + wh.bytes) return MR_ERR_WORKSPACE;
     if (!aligned16(w13) || !aligned16(w2) || (eight && !aligned16(x)) || (numGroups > 0 && !aligned16(groupList)) ||
-        reinterpret_cast<uintptr_t>(workspace) % 256)
+        !aligned(workspace, 256))
         return MR_ERR_PARAM_INVALID;
-    if (reinterpret_cast<uintptr_t>(x) % elem_bytes(xDtype) || reinterpret_cast<uintptr_t>(y) % elem_bytes(yDtype))
+    if (!aligned(x, elem_bytes(xDtype)) || !aligned(y, elem_bytes(yDtype)) || !aligned(xScales, 4) ||
+        !aligned(w13Scales, 4) || !aligned(w2Scales, 4) || !aligned(numRows, 8))
         return MR_ERR_PARAM_INVALID;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     char* base = reinterpret_cast<char*>(workspace);

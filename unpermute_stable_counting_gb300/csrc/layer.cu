@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 bool float_dtype(int32_t dt) { return dt == MR_DTYPE_F16 || dt == MR_DTYPE_BF16 || dt == MR_DTYPE_F32; }
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 // Workspace regions, 256-byte aligned.
 struct LayerPlan {
@@ -1035,10 +1035,10 @@ extern "C" mr_status moe_layer(const void* x, int32_t xDtype, int64_t xStride, c
     if (eight != (w13Scales != nullptr) || eight != (w2Scales != nullptr)) return MR_ERR_PARAM_NULLPTR;
     const LayerPlan p(tokens, hidden, inter, experts, topK, eight);
     if (workspaceSize < p.bytes) return MR_ERR_WORKSPACE;
-    if (!aligned16(w13) || !aligned16(w2) || reinterpret_cast<uintptr_t>(workspace) % 256) return MR_ERR_PARAM_INVALID;
+    if (!aligned16(w13) || !aligned16(w2) || !aligned(workspace, 256)) return MR_ERR_PARAM_INVALID;
     const uintptr_t xe = xDtype == MR_DTYPE_F32 ? 4 : 2, re = routerDtype == MR_DTYPE_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(x) % xe || reinterpret_cast<uintptr_t>(y) % xe ||
-        reinterpret_cast<uintptr_t>(router) % re)
+    if (!aligned(x, xe) || !aligned(y, xe) || !aligned(router, re) || !aligned(selectBias, 4) ||
+        !aligned(w13Scales, 4) || !aligned(w2Scales, 4) || !aligned(expertIds, 4) || !aligned(expertWeights, 4))
         return MR_ERR_PARAM_INVALID;
 
     const int grid = device_sm_count();

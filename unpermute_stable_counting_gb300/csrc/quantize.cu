@@ -285,7 +285,7 @@ extern "C" mr_status moe_quantize(const void* x, int32_t dtype, int64_t batch, i
     if (rows == 0) return MR_OK;
     if (!x || !values || !scales) return MR_ERR_PARAM_NULLPTR;
     const uintptr_t elem = dtype == MR_DTYPE_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(x) % elem || reinterpret_cast<uintptr_t>(scales) % 4) return MR_ERR_PARAM_INVALID;
+    if (!aligned(x, elem) || !aligned(scales, 4) || !aligned(numRows, 8)) return MR_ERR_PARAM_INVALID;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (blockRows == 1) {
         MR_TRY_CUDA(enqueue_quantize(x, dtype, rows, cols, xr, numRows, values, vr, scales, sr, sb, s));

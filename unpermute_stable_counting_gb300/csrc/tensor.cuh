@@ -376,6 +376,9 @@ __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __e
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+// Whether an address is a multiple of n bytes (NULL is).
+inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
 // A tiled tensor map of `rank` dimensions (innermost first) with the swizzle of
 // its rows' width (128 or 64 bytes); strides[i] is the byte stride of dimension
 // i + 1. False if the driver refuses it.
