@@ -120,3 +120,29 @@ def test_the_default_stream_by_its_handle():
         got = usc.moe_quantize(x, stream=0)
     torch.cuda.synchronize()
     assert all(torch.equal(as_bytes(want[k]), as_bytes(got[k])) for k in want)
+
+
+# ---------------------------------------------------------------------------
+# moe_grouped_matmul
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("second", [1, 31])
+def test_counts_past_the_rows_at_the_largest_number_of_rows(second):
+    """2^30 rows and counts that add up to more than 2^31, in one window of 32 groups and over two."""
+    n = 1 << 30
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    x = torch.full((n, 16), 0x38, dtype=torch.uint8, device="cuda").view(E4M3)     # ones
+    w = torch.ones(2, 1, 16).to(E4M3)
+    w[1] = 2.0
+    lst = torch.zeros(second + 2, 2, dtype=torch.int64)
+    lst[0, 1], lst[second], lst[second + 1] = n - 3, torch.tensor([1, n]), torch.tensor([0, 7])
+    y = torch.zeros(n, 1, dtype=BF16, device="cuda")
+    usc.moe_grouped_matmul(x, w.cuda(), torch.ones(2, 1, 1, device="cuda"), lst.cuda(),
+                           x_scales=torch.ones(1, 1, device="cuda").expand(n, 1), out=dict(y=y))
+    assert (y[:n - 3] == 16).all() and (y[n - 3:] == 32).all()
+    # both counts are all of the rows: nothing is left for the others
+    lst[0, 1] = n
+    usc.moe_grouped_matmul(x, w.cuda(), torch.ones(2, 1, 1, device="cuda"), lst.cuda(),
+                           x_scales=torch.ones(1, 1, device="cuda").expand(n, 1), out=dict(y=y))
+    assert (y == 16).all()

@@ -67,7 +67,7 @@ struct Tile {
 // with the same t, ascending over the calls.
 template <int TM> struct Walk {
     int first, base_tile, total;      // window of 32 groups; tiles before it, tiles in it
-    int base_row, window_rows;        // rows before it, rows in it
+    uint32_t base_row, window_rows;   // rows before it, rows in it
     int expert, count, row0, tiles;   // this lane's group
     int end;                          // inclusive sum of tiles over the window
 
@@ -84,17 +84,19 @@ template <int TM> struct Walk {
                 c = a.rows;
             }
         }
-        // rows up to and with this group, at most a.rows (sums of two such values fit 32 bits)
-        int sum = c;
+        // rows up to and with this group, at most a.rows <= 2^30: the sum of two is 2^31, which an
+        // unsigned number holds and a signed one does not
+        const uint32_t most = (uint32_t)a.rows;
+        uint32_t sum = (uint32_t)c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum = min(sum + up, a.rows);
+            const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum = min(sum + up, most);
         }
-        int before = __shfl_up_sync(0xffffffffu, sum, 1);
-        if (lane == 0) before = 0;
+        uint32_t before = __shfl_up_sync(0xffffffffu, sum, 1);
+        if (lane == 0) before = 0u;
         window_rows = __shfl_sync(0xffffffffu, sum, 31);
-        row0 = min(base_row + before, a.rows);
+        row0 = (int)min(base_row + before, most);
         count = min(c, a.rows - row0);
         const bool ok = e >= 0 && e < a.experts;
         expert = ok ? (int)e : 0;
@@ -126,14 +128,15 @@ template <int TM> struct Walk {
         return g;
     }
     __device__ __forceinline__ void begin(const GroupArgs& a, int lane) {
-        first = base_tile = base_row = 0;
+        first = base_tile = 0;
+        base_row = 0u;
         load(a, lane);
     }
     __device__ __forceinline__ bool next(const GroupArgs& a, int lane, int t, int bn, Tile& out) {
         while (t >= base_tile + total) {
             if (first + 32 >= a.G) return false;
             base_tile += total;
-            base_row = min(base_row + window_rows, a.rows);
+            base_row = min(base_row + window_rows, (uint32_t)a.rows);
             first = skip(a, lane, first + 32);
             load(a, lane);
         }
