@@ -32,6 +32,12 @@ STAMP_PATH = LIB_PATH + ".sha256"
 CHECKED_FLAGS = ["-DMR_CHECKED"]
 CHECKED_BUILD_DIR = os.path.join(CSRC, "_build_checked")
 CHECKED_LIB_PATH = os.path.join(PKG, "libmoe_reorder_checked.so")
+# the same on few SMs (-DMR_SM_COUNT): the launches take the device for one of FEW_SMS SMs, so that
+# each block of a persistent kernel has several tiles at the tests' sizes
+FEW_SMS = 60
+FEW_SMS_FLAGS = CHECKED_FLAGS + [f"-DMR_SM_COUNT={FEW_SMS}"]
+FEW_SMS_BUILD_DIR = os.path.join(CHECKED_BUILD_DIR, "few_sms")
+FEW_SMS_LIB_PATH = os.path.join(PKG, "libmoe_reorder_checked_few_sms.so")
 HEADER = os.path.join(ROOT, "include", "moe_reorder.h")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -79,14 +85,16 @@ def current_digest(extra_flags=None) -> str:
                          platform.machine())
 
 
-def _paths(checked: bool):
+def _paths(checked: bool, few_sms: bool = False):
+    if few_sms:
+        return FEW_SMS_LIB_PATH, FEW_SMS_LIB_PATH + ".sha256", FEW_SMS_BUILD_DIR, FEW_SMS_FLAGS
     if checked:
         return CHECKED_LIB_PATH, CHECKED_LIB_PATH + ".sha256", CHECKED_BUILD_DIR, CHECKED_FLAGS
     return LIB_PATH, STAMP_PATH, BUILD_DIR, []
 
 
-def needs_build(extra_flags=None, checked: bool = False) -> bool:
-    lib_path, stamp, _, cflags = _paths(checked)
+def needs_build(extra_flags=None, checked: bool = False, few_sms: bool = False) -> bool:
+    lib_path, stamp, _, cflags = _paths(checked, few_sms)
     if not os.path.exists(lib_path) or not os.path.exists(stamp):
         return True
     with open(stamp) as f:
@@ -105,23 +113,25 @@ def _build_lock():
             fcntl.flock(f, fcntl.LOCK_UN)
 
 
-def build_library(force: bool = False, extra_flags: list[str] | None = None, checked: bool = False) -> str:
+def build_library(force: bool = False, extra_flags: list[str] | None = None, checked: bool = False,
+                  few_sms: bool = False) -> str:
     """Build (or reuse) the library; checked=True builds the bounds-checked
-    variant (-DMR_CHECKED) into its own objects and library file."""
-    lib_path, _, _, cflags = _paths(checked)
+    variant (-DMR_CHECKED), few_sms=True the bounds-checked variant for FEW_SMS
+    SMs, each into its own objects and library file."""
+    lib_path, _, _, cflags = _paths(checked, few_sms)
     flags = cflags + list(extra_flags or [])
-    if not force and not needs_build(extra_flags, checked):
+    if not force and not needs_build(extra_flags, checked, few_sms):
         print(f"{os.path.basename(lib_path)}: reused (sources unchanged, digest "
               f"{current_digest(flags)[:16]})", file=sys.stderr)
         return lib_path
     with _build_lock():
-        if not force and not needs_build(extra_flags, checked):
+        if not force and not needs_build(extra_flags, checked, few_sms):
             return lib_path
-        return _build_locked(extra_flags, checked)
+        return _build_locked(extra_flags, checked, few_sms)
 
 
-def _build_locked(extra_flags: list[str] | None, checked: bool = False) -> str:
-    lib_path, stamp, build_dir, cflags = _paths(checked)
+def _build_locked(extra_flags: list[str] | None, checked: bool = False, few_sms: bool = False) -> str:
+    lib_path, stamp, build_dir, cflags = _paths(checked, few_sms)
     os.makedirs(build_dir, exist_ok=True)
     nvcc = _nvcc()
     flags = NVCC_FLAGS + cflags + list(extra_flags or [])

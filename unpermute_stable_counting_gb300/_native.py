@@ -3,7 +3,7 @@
 Loading fails loudly when libmoe_reorder.so is missing: there is no CPU or
 PyTorch fallback for any operation of this package. With USC_CHECKED=1 in the
 environment the bounds-checked build (libmoe_reorder_checked.so, built with
--DMR_CHECKED) is loaded instead.
+-DMR_CHECKED) is loaded instead, with USC_FEW_SMS=1 beside it that for few SMs.
 """
 from __future__ import annotations
 
@@ -64,6 +64,11 @@ SIGNATURES = {
 def checked_requested() -> bool:
     return os.environ.get("USC_CHECKED", "") == "1"
 
+
+def few_sms_requested() -> bool:
+    return checked_requested() and os.environ.get("USC_FEW_SMS", "") == "1"
+
+
 _lib = None
 
 
@@ -75,7 +80,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     """The loaded library (loaded once)."""
     global _lib
     if _lib is None:
-        p = path or (_build.CHECKED_LIB_PATH if checked_requested() else _build.LIB_PATH)
+        p = path or (_build.FEW_SMS_LIB_PATH if few_sms_requested()
+                     else _build.CHECKED_LIB_PATH if checked_requested() else _build.LIB_PATH)
         if not os.path.exists(p):
             raise LibraryMissing(
                 f"{p} is not built; run unpermute_stable_counting_gb300._build.build_library() "

@@ -699,6 +699,7 @@ cudaError_t launch_grouped(const CUtensorMap (&m)[3], const GroupArgs& a, int64_
             cfg.gridDim = dim3(n / 2 * 2);
             if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
             if (n < 1) return cudaErrorInvalidConfiguration;
+            n = std::min(n, device_sm_count() / 2);
         }
         resident[dev].store(n, std::memory_order_release);
     }

@@ -849,11 +849,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // 2
     // Up to a token per warp every block chooses all tokens' experts for itself, which saves a
-    // barrier (1.3 us); more tokens are a block's each.
+    // barrier (1.3 us); more tokens are a block's each (several, if there are fewer blocks than tokens).
     const bool shared_choice = a.T > kWarps;
     const int token = shared_choice ? (warp == 0 ? (int)blockIdx.x : a.T) : warp;
     Choice& choice = *reinterpret_cast<Choice*>(ring);
-    if (token < a.T) choose(a, choice, token, shared_choice || blockIdx.x == 0);
+    for (int t = token; t < a.T; t += shared_choice ? (int)gridDim.x : kWarps)
+        choose(a, choice, t, shared_choice || blockIdx.x == 0);
     if (shared_choice) grid.sync();
     else __syncthreads();
     int most = 0;
