@@ -13,6 +13,7 @@ if not torch.cuda.is_available():
 import unpermute_stable_counting_gb300 as usc  # noqa: E402
 
 import _expert_util as eu  # noqa: E402
+import test_gpu_layer as layer  # noqa: E402
 
 BF16, F16, F32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
 
@@ -146,3 +147,30 @@ def test_counts_past_the_rows_at_the_largest_number_of_rows(second):
     usc.moe_grouped_matmul(x, w.cuda(), torch.ones(2, 1, 1, device="cuda"), lst.cuda(),
                            x_scales=torch.ones(1, 1, device="cuda").expand(n, 1), out=dict(y=y))
     assert (y == 16).all()
+
+
+# ---------------------------------------------------------------------------
+# moe_layer
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("infinite", [True, False])
+def test_bf16_values_of_h_past_the_range(infinite, sign):
+    """An infinite h is one in its high part alone: y is infinite, not NaN. fp32's highest finite values,
+    which round to an infinite bf16, stay finite."""
+    c = layer.make(3, 4, 128, 32, BF16, BF16, 24)
+    for k in ("x", "router", "w13", "w2"):
+        c[k][:] = 0.0
+    c["x"][1, :2] = 2.0**60
+    c["w13"][:, 0, 5, 0] = 1.0                   # g = 2^60 = silu(g)
+    if infinite:
+        c["w13"][:, 1, 5, 0] = sign * 2.0**40    # h = 2^160
+    else:                                        # u = 2^60 (256 - 2^-3): h = 2^128 (1 - 2^-11)
+        c["w13"][:, 1, 5, 0], c["w13"][:, 1, 5, 1] = sign * 255.0, sign * 0.875
+    c["w2"][:, :, 5] = 0.5
+    y = layer.run(c, 2)["y"].double().cpu()
+    assert (y[[0, 2]] == 0).all()
+    if infinite:
+        assert (y[1] == sign * float("inf")).all()
+    else:                                        # half of h, to the nearest bf16 value
+        assert ((y[1] - sign * 2.0**127).abs() <= 2.0**127 * 2.0**-8).all()

@@ -550,9 +550,13 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
                     uint16_t* p = reinterpret_cast<uint16_t*>(a.hs + (int64_t)slot * a.hs_stride) + i;
                     uint16_t* q = reinterpret_cast<uint16_t*>(a.hs + (int64_t)(a.slots + slot) * a.hs_stride) + i;
                     if (a.bf16) {
-                        const uint16_t hi = Elem<MR_DTYPE_BF16>::from_f32(h);
+                        // the highest finite values round to an infinity: the high part is then the
+                        // largest bf16 value, and what is above it the low part; an infinite h has none
+                        uint16_t hi = Elem<MR_DTYPE_BF16>::from_f32(h);
+                        const bool inf = abs_bits(h) == 0x7F800000u;
+                        if ((hi & 0x7FFFu) == 0x7F80u && !inf) --hi;
                         *p = hi;
-                        *q = Elem<MR_DTYPE_BF16>::from_f32(h - Elem<MR_DTYPE_BF16>::to_f32(hi));
+                        *q = inf ? 0 : Elem<MR_DTYPE_BF16>::from_f32(h - Elem<MR_DTYPE_BF16>::to_f32(hi));
                     } else {
                         const uint16_t hi = Elem<MR_DTYPE_F16>::from_f32(h);
                         *p = hi;
