@@ -606,7 +606,7 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
  *   e4m3 weights: ffn_e is moe_expert_ffn's, its quantizations of x and h
  *   included. 16-bit weights: silu(x W1^T) * (x W3^T) W2^T with fp32 sums, h
  *   held to at least 16 bits of precision in two 16-bit parts (with F16 an h
- *   past its range is an infinity).
+ *   below 2^-20 to 2^-36, and an h past F16's range is an infinity).
  *
  *   x             [tokens, hidden] of xDtype (F16, BF16, F32; with 16-bit
  *                 weights, theirs), row stride xStride elements.

@@ -174,3 +174,29 @@ def test_bf16_values_of_h_past_the_range(infinite, sign):
         assert (y[1] == sign * float("inf")).all()
     else:                                        # half of h, to the nearest bf16 value
         assert ((y[1] - sign * 2.0**127).abs() <= 2.0**127 * 2.0**-8).all()
+
+
+def test_f16_keeps_16_bits_of_a_small_h():
+    """h of about 3e-5, of which f16 alone holds 9 bits: what cancels in y is known to 16 bits of h."""
+    g = gen(25)
+    T, E, H, I = 6, 2, 8, 32
+    near = lambda *s: 1.0 + 0.02 * torch.rand(*s, generator=g)
+    w13 = near(E, 2, I, H)
+    w13[:, 1] *= 0.0625
+    w2 = 400.0 * near(E, H, I)
+    w2[:, :, 1::2] *= -1.0
+    c = dict(x=(4e-3 * near(T, H)).to(F16), router=torch.zeros(E, H).to(F16), w13=w13.to(F16), w2=w2.to(F16), s13=None, s2=None)
+    r = layer.run(c, 2)
+    x, W13, W2 = c["x"].double(), c["w13"].double(), c["w2"].double()
+    y, b = torch.zeros(T, H, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
+    for e in range(E):
+        ye, be = eu.net(x, W13[e, 0], W13[e, 1], W2[e], rounded=False)
+        a, u = x @ W13[e, 0].T, x @ W13[e, 1].T
+        h = a * torch.sigmoid(a) * u
+        assert (h > 2.0**-20).all() and (h < 2.0**-14).all()
+        be = be + (h * 2.0**-16) @ W2[e].abs().T
+        y += 0.5 * ye
+        b += 0.5 * (be + 4 * 2.0**-23 * (ye.abs() + be))
+    eu.assert_close(r["y"], y, b)
+    # the bound means something: f16's own 2^-25 per value of h would be outside of it
+    assert (b < 2.0**-25 * 400 * I**0.5).all()

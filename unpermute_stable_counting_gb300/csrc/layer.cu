@@ -48,6 +48,7 @@ constexpr int kMaxTokens = MR_MAX_LAYER_TOKENS, kMaxExperts = MR_MAX_LAYER_EXPER
 constexpr int kLine = 128;            // bytes of a row per stage (the swizzle's width)
 constexpr int kMaxStages = 24, kMaxSplits = 8;
 constexpr int kBufs = 4, kBufCols = 128;  // tensor memory
+constexpr float kLowUp = 2048.0f;     // f16 weights: what the low parts of h are multiplied by
 static_assert(kMaxTokens == 64, "a token set is a 64-bit mask");
 
 struct LayerArgs {
@@ -545,8 +546,8 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
                 if (EIGHT) {
                     a.hf[(int64_t)slot * a.h_cols + i] = h;
                 } else {
-                    // the value in two 16-bit parts: the second product loses nothing of the 32 bits but
-                    // their last few
+                    // the value in two 16-bit parts: 16 bits of it (bf16), 22 (f16; 16 down to 2^-20, and
+                    // below that all but 2^-36)
                     uint16_t* p = reinterpret_cast<uint16_t*>(a.hs + (int64_t)slot * a.hs_stride) + i;
                     uint16_t* q = reinterpret_cast<uint16_t*>(a.hs + (int64_t)(a.slots + slot) * a.hs_stride) + i;
                     if (a.bf16) {
@@ -560,9 +561,11 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
                     } else {
                         const uint16_t hi = Elem<MR_DTYPE_F16>::from_f32(h);
                         *p = hi;
-                        // past f16's range the high part is an infinity, and the whole value
-                        *q = (hi & 0x7FFFu) == 0x7C00u ? 0
-                                                       : Elem<MR_DTYPE_F16>::from_f32(h - Elem<MR_DTYPE_F16>::to_f32(hi));
+                        // past f16's range the high part is an infinity, and the whole value; the low part
+                        // is held times 2^11, which keeps it out of f16's subnormal numbers
+                        *q = (hi & 0x7FFFu) == 0x7C00u
+                                 ? 0
+                                 : Elem<MR_DTYPE_F16>::from_f32((h - Elem<MR_DTYPE_F16>::to_f32(hi)) * kLowUp);
                     }
                 }
             }
@@ -763,7 +766,8 @@ __device__ __forceinline__ void step_y(const LayerArgs& a, const Tables& tb, con
                 if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[buf]));
                 ++use;
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) y[c] = __uint_as_float(hi[c]) + __uint_as_float(lo[c]);
+                for (int c = 0; c < COLS; ++c)
+                    y[c] = fmaf(__uint_as_float(lo[c]), a.bf16 ? 1.0f : 1.0f / kLowUp, __uint_as_float(hi[c]));
             }
             if (row < a.rows2) {
 #pragma unroll
