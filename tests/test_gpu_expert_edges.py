@@ -200,3 +200,44 @@ def test_f16_keeps_16_bits_of_a_small_h():
     eu.assert_close(r["y"], y, b)
     # the bound means something: f16's own 2^-25 per value of h would be outside of it
     assert (b < 2.0**-25 * 400 * I**0.5).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_scores_below_fp32_s_range_still_weigh(score):
+    """Scores whose sum fp32 does not hold, chosen by a bias: their ratios are those of the definition."""
+    c = layer.make(5, 8, 128, 32, BF16, BF16, 26)
+    c["x"][:] = 0.0
+    c["x"][:, 0] = 1.0
+    c["router"][:] = 0.0
+    c["router"][:, 0] = torch.tensor([300.0 if score == "softmax" else 3.0, -96.0, -95.0, -95.5, -97.0, -170.0, -94.0, -99.0])
+    bias = torch.tensor([0.0, 9.0, 8.0, 7.0, 6.0, 5.0, -1.0, -1.0])
+    r = layer.run(c, 5, score=score, select_bias=bias.cuda(), routed_scale=2.5)
+    assert torch.equal(r["expertIds"].cpu(), torch.tensor([1, 2, 3, 4, 5], dtype=torch.int32).expand(5, 5))
+    assert ((r["expertWeights"].sum(1) - 2.5).abs() < 1e-5).all()
+    layer.check(c, 5, r, score=score, routed_scale=2.5, bias=bias)
+
+
+def test_a_taken_score_that_is_nan_leaves_no_weight():
+    """The sum of the taken scores is NaN, and so is every weight of the token; other tokens keep theirs."""
+    c = layer.make(3, 4, 128, 32, BF16, BF16, 27)
+    c["router"][:, 5] = 0.0
+    c["router"][2, 5] = float("nan")             # every token's logit of expert 2
+    r = layer.run(c, 4, score="sigmoid")
+    assert r["expertWeights"].isnan().all() and (r["expertIds"][:, 3] == 2).all() and r["y"].isnan().all()
+    r = layer.run(c, 3, score="sigmoid")         # not taken
+    assert ((r["expertWeights"].sum(1) - 1).abs() < 1e-5).all() and r["y"].isfinite().all()
+    c["router"][2, 5] = 0.0
+    c["x"][1, 9] = float("nan")                  # every logit of token 1
+    r = layer.run(c, 2, score="sigmoid")
+    assert r["expertWeights"][1].isnan().all() and r["expertWeights"][[0, 2]].isfinite().all()
+
+
+def test_scores_that_are_all_zero_have_no_ratios():
+    c = layer.make(2, 4, 128, 32, BF16, BF16, 28)
+    c["x"][:] = 0.0
+    c["x"][:, 0] = 1.0
+    c["router"][:] = 0.0
+    c["router"][:, 0] = float("-inf")
+    r = layer.run(c, 2, score="sigmoid")
+    assert r["expertWeights"].isnan().all() and torch.equal(r["expertIds"].cpu(), torch.tensor([[0, 1]] * 2, dtype=torch.int32))
+    assert (layer.run(c, 2, score="sigmoid", renormalize=False)["expertWeights"] == 0).all()

@@ -48,6 +48,7 @@ constexpr int kMaxTokens = MR_MAX_LAYER_TOKENS, kMaxExperts = MR_MAX_LAYER_EXPER
 constexpr int kLine = 128;            // bytes of a row per stage (the swizzle's width)
 constexpr int kMaxStages = 24, kMaxSplits = 8;
 constexpr int kBufs = 4, kBufCols = 128;  // tensor memory
+constexpr float kLowScores = 7.8886091e-31f;  // 2^-100: sums of scores below it are taken anew
 constexpr float kLowUp = 2048.0f;     // f16 weights: what the low parts of h are multiplied by
 static_assert(kMaxTokens == 64, "a token set is a 64-bit mask");
 
@@ -287,12 +288,23 @@ __device__ __forceinline__ void choose(const LayerArgs& a, Choice& c, int t, boo
         if ((e & 31) == lane) key[e] = 0u;
         if (lane == r) mine = e;
     }
-    const float s = lane < a.K ? score(__ldcg(logits + mine)) : 0.0f;
-    float total = s;
+    const float l = lane < a.K ? __ldcg(logits + mine) : -INFINITY;
+    float s = lane < a.K ? score(l) : 0.0f, total = s;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (!a.keep && total < kLowScores) {
+        // (chosen by a bias, or all of a token's sigmoids) fp32 loses digits of such scores, or all of
+        // them: their ratios, those of exp(l) for a softmax and for sigmoids this small, are taken
+        // with the largest one's exponent off
+        float high = l;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+        total = s = lane < a.K ? expf(l - high) : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
     if (lane < a.K) {
-        const float w = (a.keep ? s : s / fmaxf(total, 1.17549435e-38f)) * a.scale;
+        const float w = (a.keep ? s : s / total) * a.scale;
         c.expert[t][lane] = (uint16_t)mine;
         c.weight[t][lane] = w;
         if (write) {
