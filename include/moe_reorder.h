@@ -681,7 +681,8 @@ mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, int32_t res
 /*
  * mr_waits_out -- blocks of the expert products that gave up a wait.
  *   Those kernels wait on copies and matrix instructions of their own block;
- *   every such wait ends after two seconds at the latest. A block whose wait
+ *   every such wait ends after two seconds of the kernel's running at the latest
+ *   (time in which the context is suspended does not count). A block whose wait
  *   ran out leaves its remaining tiles unwritten and is counted here. The count
  *   stays 0 on a working device. This call synchronises with the device, writes
  *   the count since the last reset to *count (host pointer), and with

@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "wait_clock.cuh"
 
 namespace mr {
 
@@ -72,24 +73,21 @@ __device__ __forceinline__ uint64_t global_ns() {
     return t;
 }
 
-// Every wait of these kernels ends: a wait that has not come through in
-// kWaitNs raises the block's abort flag (so the block's other waits end too)
-// and returns false; the block then leaves its loops, waits (bounded) for its
-// own copies and matrix instructions in flight, frees its tensor memory, adds
-// one to the library's count of waits that ran out, and returns.
-// In a cluster of two blocks (PAIR) the flag is raised in both.
-constexpr uint64_t kWaitNs = 2000000000ull;
+// Every wait of these kernels ends: a wait that has not come through in two
+// seconds (of the kernel's running, see WaitClock) raises the block's abort flag
+// (so the block's other waits end too) and returns false; the block then leaves
+// its loops, waits (bounded) for its own copies and matrix instructions in flight,
+// frees its tensor memory, adds one to the library's count of waits that ran out,
+// and returns. In a cluster of two blocks (PAIR) the flag is raised in both.
 template <bool PAIR = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
     if (mbar_try(bar, parity)) return true;
-    uint64_t start = 0;
+    WaitClock clock;
     for (uint32_t i = 1;; ++i) {
         if (mbar_try(bar, parity)) return true;
         if ((i & 63u) == 0u) {
             if (*abort != 0u) return false;
-            const uint64_t now = global_ns();
-            if (start == 0) start = now;
-            if (now - start > kWaitNs) {
+            if (clock.out(global_ns())) {
                 *abort = 1u;
                 if (PAIR) st_cluster(map_cluster(smem_u32((const void*)abort), cluster_rank() ^ 1u), 1u);
                 return false;
