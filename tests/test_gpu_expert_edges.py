@@ -241,3 +241,19 @@ def test_scores_that_are_all_zero_have_no_ratios():
     r = layer.run(c, 2, score="sigmoid")
     assert r["expertWeights"].isnan().all() and torch.equal(r["expertIds"].cpu(), torch.tensor([[0, 1]] * 2, dtype=torch.int32))
     assert (layer.run(c, 2, score="sigmoid", renormalize=False)["expertWeights"] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# The count of waits that ran out
+# ---------------------------------------------------------------------------
+
+def test_the_count_of_waits_waits_for_every_stream():
+    """Also for streams that the legacy default stream is not ordered with, as PyTorch's are."""
+    from unpermute_stable_counting_gb300 import _native
+    side, done, n = torch.cuda.Stream(), torch.cuda.Event(), ctypes.c_uint32(9)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)           # about 0.2 s
+        done.record()
+    assert _native.lib().mr_waits_out(ctypes.byref(n), 0) == 0 and n.value == 0
+    assert done.query()

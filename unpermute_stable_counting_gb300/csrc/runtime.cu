@@ -129,6 +129,8 @@ extern "C" mr_status mr_waits_out(uint32_t* count, int32_t reset) {
     if (!count) return MR_ERR_PARAM_NULLPTR;
     cudaError_t (*readers[])(unsigned*, bool) = {mr::waits_out_grouped_matmul, mr::waits_out_layer};
     *count = 0u;
+    // the copies below are in the legacy default stream's order, which streams that do not block it are not in
+    MR_TRY_CUDA(cudaDeviceSynchronize());
     for (auto rd : readers) {
         unsigned n = 0u;
         MR_TRY_CUDA(rd(&n, reset != 0));
