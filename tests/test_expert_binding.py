@@ -259,3 +259,20 @@ def test_expanded_scales_are_not_written(calls, scales):
     api.moe_quantize(x, out=dict(values=values, scales=zeros(3, 5).T))
     api.moe_quantize(x[:1], out=dict(values=values[:1], scales=zeros(3).as_strided((1, 3), (0, 1))))
     assert [tuple(c.args[11]) for c in calls.made] == [(1, 5), (1, 1)]
+
+
+# ---------------------------------------------------------------------------
+# Waits that ran out
+# ---------------------------------------------------------------------------
+
+def test_the_count_of_waits_that_ran_out(calls):
+    """A call whose blocks gave up a wait returns like any other: the count is how a user learns of it."""
+    import unpermute_stable_counting_gb300 as usc
+    assert "waits_out" in usc.__all__
+
+    def answer(count, reset):
+        resets.append(reset)
+        count._obj.value = 3
+        return 0
+    resets, calls.mr_waits_out = [], answer
+    assert usc.waits_out() == 3 and usc.waits_out(reset=True) == 3 and resets == [0, 1]

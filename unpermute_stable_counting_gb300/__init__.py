@@ -25,11 +25,11 @@ from .api import (DT_BF16, DT_E4M3, DT_F16, DT_F32, DT_INT8, MoeReorderError, ba
                   ffnwb_batching_context, grouped_matmul_workspace_size, layer_workspace_size, moe_expert_ffn,
                   moe_grouped_matmul, moe_layer, moe_permute, moe_quantize, moe_unpermute, moe_update_expert,
                   permute_workspace_size, profile_set_events, quantize_outputs, unpermute_outputs,
-                  unpermute_workspace_size)
+                  unpermute_workspace_size, waits_out)
 
 __all__ = ["ffnwb_batching", "ffnwb_batching_context", "moe_unpermute", "moe_permute", "moe_update_expert",
            "moe_quantize", "moe_grouped_matmul", "moe_expert_ffn", "moe_layer", "quantize_outputs",
            "grouped_matmul_workspace_size", "expert_ffn_workspace_size", "layer_workspace_size", "permute_workspace_size",
            "batching_context_workspace_size", "batching_workspace_size",
            "unpermute_workspace_size", "batching_outputs", "unpermute_outputs",
-           "profile_set_events", "MoeReorderError", "DT_F16", "DT_BF16", "DT_INT8", "DT_F32", "DT_E4M3"]
+           "profile_set_events", "waits_out", "MoeReorderError", "DT_F16", "DT_BF16", "DT_INT8", "DT_F32", "DT_E4M3"]

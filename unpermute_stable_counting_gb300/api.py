@@ -771,6 +771,14 @@ def moe_layer(x, router, w13, w2, *, topk: int, w13_scales=None, w2_scales=None,
     return out
 
 
+def waits_out(reset: bool = False) -> int:
+    """Blocks of the expert operators on the current device that gave up a wait, and so left
+    results unwritten, since the last reset: 0 on a working device. Waits for the device."""
+    n = ctypes.c_uint32(0)
+    _check(lib().mr_waits_out(ctypes.byref(n), 1 if reset else 0), "mr_waits_out")
+    return int(n.value)
+
+
 def profile_set_events(events) -> None:
     """Attach cudaEvents (torch.cuda.Event, created with enable_timing) to the
     library's phase markers for this thread; None to detach."""
