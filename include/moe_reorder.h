@@ -494,7 +494,8 @@ mr_status moe_update_expert(const void* expertIds, int32_t idDtype, const int32_
  * Operands of the matrix instructions (e4m3 rows given to moe_grouped_matmul
  * or moe_expert_ffn, and all weights) start on 16 bytes and have row strides
  * that are multiples of 16 bytes; a length that is not is padded by the stride,
- * and the padding is never read as values. Every other tensor may start
+ * and the padding is never read as values (the stride of a single row or matrix
+ * is not used). Every other tensor may start
  * anywhere its element type may, with any row stride.
  */
 

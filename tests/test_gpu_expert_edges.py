@@ -149,6 +149,55 @@ def test_counts_past_the_rows_at_the_largest_number_of_rows(second):
     assert (y == 16).all()
 
 
+def eight(n, k, g):
+    q = (torch.randn(n, k, generator=g) * 100).clamp(-448, 448).to(E4M3)
+    s = torch.exp(0.5 * torch.randn(n, eu.blocks(k), generator=g)) * 0.01
+    return q, s, q.double() * eu.spread(s.double(), k)
+
+
+def apart(t, unit=16):
+    """A device copy whose last dimension is contiguous and whose matrices (or rows) start on 16 bytes."""
+    lead, n = t.shape[0], t[0].numel()
+    buf = torch.zeros(lead, -(-n // unit) * unit, dtype=t.dtype, device="cuda")
+    v = buf.as_strided(t.shape, (buf.stride(0), *t.stride()[1:]))
+    v.copy_(t.cuda())
+    return v
+
+
+@pytest.mark.parametrize("k", [500, 1, 129])
+@pytest.mark.parametrize("n,N,E", [(1, 1, 1), (1, 1, 3), (1, 48, 1), (5, 1, 2)])
+def test_single_rows_of_any_length(n, N, E, k):
+    """A single e4m3 row (of x, or of each expert's weights) has no stride that 16 would have to divide."""
+    g = gen(31 + k)
+    q, s, x = eight(n, k, g)
+    w, ws = weights((E,), N, k, g)
+    xd = q.cuda() if n == 1 else apart(q)
+    wd = w.cuda() if N == E == 1 else apart(w) if N == 1 else apart(w[0])[None]
+    lst = torch.tensor([[E - 1, n]]).cuda()
+    y = usc.moe_grouped_matmul(xd, wd, ws.cuda(), lst, x_scales=s.cuda(), out_dtype=F32)["y"]
+    eu.assert_close(y, *eu.product(x, eu.weight(w, ws)[E - 1]))
+
+
+def test_single_rows_through_the_network_and_the_layer():
+    g = gen(32)
+    H, inter = 137, 1                            # W1 and W3 have one row, which need not be padded
+    w13, s13 = weights((2, 2), inter, H, g)
+    w2, s2 = weights((2,), H, inter, g)
+    q, s, x = eight(1, H, g)
+    w13d = apart(w13.flatten(0, 1)).unflatten(0, (2, 2))
+    w2d = apart(w2.flatten(0, 1)).unflatten(0, (2, H))
+    assert w13d.stride()[-2] == H and w2d.stride()[-2] == 16
+    y = usc.moe_expert_ffn(q.cuda(), w13d, s13.cuda(), w2d, s2.cuda(), torch.tensor([[1, 1]]).cuda(), x_scales=s.cuda(),
+                           out_dtype=F32)["y"]
+    W13, W2 = eu.weight(w13, s13), eu.weight(w2, s2)
+    eu.assert_close(y, *eu.net(x, W13[1, 0], W13[1, 1], W2[1]))
+    c = layer.make(3, 2, H, inter, BF16, E4M3, 33)
+    r = usc.moe_layer(c["x"].cuda(), c["router"].cuda(), apart(c["w13"].flatten(0, 1)).unflatten(0, (2, 2)),
+                      apart(c["w2"].flatten(0, 1)).unflatten(0, (2, H)), topk=2, w13_scales=c["s13"].cuda(),
+                      w2_scales=c["s2"].cuda())
+    layer.check(c, 2, r)
+
+
 # ---------------------------------------------------------------------------
 # moe_layer
 # ---------------------------------------------------------------------------

@@ -855,9 +855,12 @@ extern "C" mr_status moe_grouped_matmul(const void* x, int32_t xDtype, int64_t x
     if (!common_sizes(rows, experts, numGroups, outCols, cols)) return MR_ERR_PARAM_INVALID;
     if (!groupList && numGroups > 0) return MR_ERR_PARAM_NULLPTR;
     const int64_t top = INT64_C(1) << 40;
+    if (eight) xStride = stride_of(rows, xStride, cols);
     if (xStride < cols || xStride > top || yStride < outCols || yStride > top) return MR_ERR_PARAM_INVALID;
     int64_t wr = cols, wm = outCols * cols;
     if (weightStrides) wr = weightStrides[0], wm = weightStrides[1];
+    wr = stride_of(outCols, wr, cols);
+    wm = stride_of(experts, wm, outCols * wr);
     if (wr < cols || wr % 16 || wm % 16 || wr > top || wm > top || (experts > 1 && wm < (outCols - 1) * wr + cols))
         return MR_ERR_PARAM_INVALID;
     int64_t sr = blocks_of(cols), sb = 1;
@@ -928,10 +931,14 @@ extern "C" mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStri
     if (!common_sizes(rows, experts, numGroups, hidden, inter)) return MR_ERR_PARAM_INVALID;
     if (!groupList && numGroups > 0) return MR_ERR_PARAM_NULLPTR;
     const int64_t top = INT64_C(1) << 40;
+    if (eight) xStride = stride_of(rows, xStride, hidden);
     if (xStride < hidden || xStride > top || yStride < hidden || yStride > top) return MR_ERR_PARAM_INVALID;
     int64_t ar = hidden, am = inter * hidden, br = inter, bm = hidden * inter;
     if (w13Strides) ar = w13Strides[0], am = w13Strides[1];
     if (w2Strides) br = w2Strides[0], bm = w2Strides[1];
+    ar = stride_of(inter, ar, hidden);
+    br = stride_of(hidden, br, inter);
+    bm = stride_of(experts, bm, hidden * br);
     if (ar < hidden || ar % 16 || am % 16 || ar > top || am > top || am < (inter - 1) * ar + hidden)
         return MR_ERR_PARAM_INVALID;
     if (br < inter || br % 16 || bm % 16 || br > top || bm > top || (experts > 1 && bm < (hidden - 1) * br + inter))

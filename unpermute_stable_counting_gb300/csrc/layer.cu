@@ -1046,6 +1046,9 @@ extern "C" mr_status moe_layer(const void* x, int32_t xDtype, int64_t xStride, c
     int64_t ar = hidden * el, am = inter * ar, br = inter * el, bm = hidden * br;
     if (w13Strides) ar = w13Strides[0], am = w13Strides[1];
     if (w2Strides) br = w2Strides[0], bm = w2Strides[1];
+    ar = stride_of(inter, ar, hidden * el);
+    br = stride_of(hidden, br, inter * el);
+    bm = stride_of(experts, bm, hidden * br);
     if (ar < hidden * el || ar % 16 || am % 16 || ar > top || am > top || am < (inter - 1) * ar + hidden * el)
         return MR_ERR_PARAM_INVALID;
     if (br < inter * el || br % 16 || bm % 16 || br > top || bm > top ||

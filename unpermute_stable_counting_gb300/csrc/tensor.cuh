@@ -377,6 +377,12 @@ __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __e
 // Whether an address is a multiple of n bytes (NULL is).
 inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// The byte stride of n rows (or matrices) of `least` bytes. That of a single one says nothing:
+// one that a tensor map takes.
+inline int64_t stride_of(int64_t n, int64_t stride, int64_t least) {
+    return n > 1 ? stride : (int64_t)align_up((uint64_t)least, 16);
+}
+
 // A tiled tensor map of `rank` dimensions (innermost first) with the swizzle of
 // its rows' width (128 or 64 bytes); strides[i] is the byte stride of dimension
 // i + 1. False if the driver refuses it.
