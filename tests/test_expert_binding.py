@@ -276,3 +276,13 @@ def test_the_count_of_waits_that_ran_out(calls):
         return 0
     resets, calls.mr_waits_out = [], answer
     assert usc.waits_out() == 3 and usc.waits_out(reset=True) == 3 and resets == [0, 1]
+
+
+@pytest.mark.parametrize("lead", [(0,), (0, 2), (3, 0)])
+def test_no_weights_to_quantize(calls, lead):
+    """A shard without experts."""
+    x = zeros(*lead, 130, 64, dtype=torch.bfloat16)
+    out = dict(values=zeros(*lead, 130, 64, dtype=E4M3), scales=zeros(*lead, 2, 1))
+    assert api.moe_quantize(x, block_rows=128, out=out) is out and not calls.made
+    r = api.moe_quantize(x[..., :0, :], block_rows=128, out=dict(values=out["values"][..., :0, :], scales=zeros(*lead, 0, 1)))
+    assert r["values"].shape == (*lead, 0, 64)

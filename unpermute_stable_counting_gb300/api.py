@@ -548,6 +548,8 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
         batch = 1
     else:
         saddr = _vector("scales", scales, torch.float32, index, sshape)
+        if x.numel() == 0 and rows and cols:  # no matrices
+            return out
         batch = x.numel() // max(1, rows * cols)
         if dims == 2:
             xs, vs = _Pair(0, _row_stride(shape, strides)), _Pair(0, _row_stride(vshape, vstrides))
