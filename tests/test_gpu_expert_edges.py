@@ -198,6 +198,20 @@ def test_single_rows_through_the_network_and_the_layer():
     layer.check(c, 2, r)
 
 
+@pytest.mark.parametrize("out", [BF16, F16, F32])
+@pytest.mark.parametrize("N", [4092, 4090, 4089, 3970])
+def test_rows_of_results_that_end_inside_16_bytes(N, out):
+    """Rows that start on 16 bytes, N values in a row of 4096: what lies beside them stays as it is."""
+    g = gen(N)
+    n, k = 1000, 136
+    q, s, x = eight(n, k, g)
+    w, ws = weights((1,), N, k, g)
+    buf = torch.full((n, 4096), 77.0, dtype=out, device="cuda")
+    usc.moe_grouped_matmul(apart(q), apart(w[0])[None], ws.cuda(), x_scales=s.cuda(), out=dict(y=buf[:, :N]))
+    eu.assert_close(buf[:, :N], *eu.product(x, eu.weight(w, ws)[0]))
+    assert (buf[:, N:] == 77).all()
+
+
 # ---------------------------------------------------------------------------
 # moe_layer
 # ---------------------------------------------------------------------------

@@ -319,7 +319,7 @@ __device__ __forceinline__ void store_columns(uint8_t* stage, const float2 (&acc
     }
 }
 
-// The same for 32 real rows and a map of y: the columns go to shared memory as
+// The same for 32 real rows and a map of y (whose columns that are real end on 16 bytes): the columns go to shared memory as
 // tiles of 128-byte rows in the map's swizzle, two of them at a time (all of a
 // warp's 16-bit columns, half of its fp32 ones), and from there by asynchronous
 // copies beside the next tile's sums. (Stores from registers took 3400 cycles of a
@@ -617,7 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t step = a.y_stride * elem;
                 bool sent = false;
                 if constexpr (C::kSend) {
-                    if (wrows == 32) {
+                    // A copy's last 16 bytes of a row are written whole: where the row ends inside them,
+                    // what follows it is not the call's, and the warp with its end stores the values.
+                    const bool cut = n + C::kChunk > a.N && (a.N * elem & 15) != 0;
+                    if (wrows == 32 && !cut) {
                         sent = true;
                         if (n < a.N) {
                             if (a.y_dtype == MR_DTYPE_BF16)
