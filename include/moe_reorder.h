@@ -680,6 +680,17 @@ mr_status mr_profile_set_events(void* const* events, int32_t count);
 mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, int32_t reset);
 
 /*
+ * mr_expert_tile -- how moe_grouped_matmul (network 0), or the first product of
+ *   moe_expert_ffn (network 1, outCols: inter), cuts its result on the current
+ *   device, so that a test can tell which kernel its sizes reach. rows, numGroups
+ *   and outCols as in the call; tile (host int32 [3]) receives a tile's rows and
+ *   columns (256 rows: a pair of blocks) and the tiles in work at once: with more
+ *   of them a block takes several. Nothing is launched.
+ *   Returns MR_OK, MR_ERR_PARAM_NULLPTR or MR_ERR_PARAM_INVALID.
+ */
+mr_status mr_expert_tile(int64_t rows, int64_t numGroups, int64_t outCols, int32_t network, int32_t* tile);
+
+/*
  * mr_waits_out -- blocks of the expert products that gave up a wait.
  *   Those kernels wait on copies and matrix instructions of their own block;
  *   every such wait ends after two seconds of the kernel's running at the latest

@@ -31,3 +31,16 @@ def ffn_rows_in_use(L, num):
 def test_addresses_that_their_type_cannot_have(L, call, kw):
     """Scales, counts, ids: a kernel would read (or write) them at an address that faults."""
     assert call(L, **kw) == INVALID
+
+
+def test_the_tile_of_a_product(L):
+    t = (ctypes.c_int32 * 3)()
+    assert L.mr_expert_tile(16384, -1, 7168, 0, t) == OK and tuple(t[:2]) == (256, 256) and t[2] > 0
+    assert L.mr_expert_tile(1, 1, 16, 0, t) == OK and tuple(t[:2]) == (128, 128)
+    assert L.mr_expert_tile(32768, 64, 2048, 1, t) == OK and tuple(t[:2]) == (256, 128)
+    assert L.mr_expert_tile(4, 1, 16, 0, None) == _NULLPTR
+    for bad in ((0, 1, 16), (4, 0, 16), (4, -2, 16), (4, 1, 0), ((1 << 30) + 1, 1, 16)):
+        assert L.mr_expert_tile(*bad, 0, t) == INVALID
+
+
+_NULLPTR = 161001

@@ -17,14 +17,27 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SUITES = ["test_gpu_layer.py", "test_gpu_expert_products.py", "test_gpu_expert_edges.py"]
 
 
+def run_suites(suites, **env):
+    r = subprocess.run([sys.executable, "-m", "pytest", "-m", "gpu", "-x", "-q", "-p", "no:cacheprovider"]
+                       + [os.path.join("tests", f) for f in suites], cwd=ROOT,
+                       env=dict(os.environ, **env), capture_output=True, text=True, timeout=1500)
+    tail = r.stdout[-4000:] + r.stderr[-2000:]
+    assert r.returncode == 0 and " passed" in r.stdout and " failed" not in r.stdout, tail
+
+
 def test_expert_suites_on_few_sms():
     from unpermute_stable_counting_gb300 import _build, _native
     if _native.checked_requested():
         pytest.skip("this process runs against another build")
     assert _build.FEW_SMS < 64                   # the most tokens of a layer
     _build.build_library(few_sms=True)
-    r = subprocess.run([sys.executable, "-m", "pytest", "-m", "gpu", "-x", "-q", "-p", "no:cacheprovider"]
-                       + [os.path.join("tests", f) for f in SUITES], cwd=ROOT,
-                       env=dict(os.environ, USC_CHECKED="1", USC_FEW_SMS="1"), capture_output=True, text=True, timeout=1500)
-    tail = r.stdout[-4000:] + r.stderr[-2000:]
-    assert r.returncode == 0 and " passed" in r.stdout and " failed" not in r.stdout, tail
+    run_suites(SUITES, USC_CHECKED="1", USC_FEW_SMS="1")
+
+
+def test_several_tiles_on_the_checked_build():
+    """(Their sizes go by the device's own SMs.)"""
+    from unpermute_stable_counting_gb300 import _build, _native
+    if _native.checked_requested():
+        pytest.skip("this process runs against another build")
+    _build.build_library(checked=True)
+    run_suites(["test_gpu_expert_tiles.py"], USC_CHECKED="1")

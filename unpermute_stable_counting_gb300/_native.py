@@ -53,6 +53,7 @@ SIGNATURES = {
     "moe_layer_get_workspace_size": (_I32, [_I64, _I64, _I64, _I64, _I64, _I32, _PU64]),
     "moe_layer": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _P, _P, _I32, _PI64, _P, _P, _PI64, _P, _I64, _I64, _I64,
                          _I64, _I64, _U32, ctypes.c_float, _P, _I64, _P, _P, _P, _U64, _P]),
+    "mr_expert_tile": (_I32, [_I64, _I64, _I64, _I32, ctypes.POINTER(_I32)]),
     "mr_waits_out": (_I32, [ctypes.POINTER(_U32), _I32]),
     "mr_status_string": (ctypes.c_char_p, [_I32]),
     "mr_version": (_I32, []),

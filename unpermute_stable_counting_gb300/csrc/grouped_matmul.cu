@@ -729,24 +729,38 @@ struct Product {
     bool swiglu;
 };
 
-mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
-    // The tile whose rounds over the SMs cost least. A step of a tile of 128 x 128, of 128 x 256 and of a
-    // pair's 256 x 256 takes about 5 : 8 : 7 (in one round, of 56 steps: 25, 37 and 33 us; 64 columns
-    // take as long as 128, so there is no narrower tile). 512 rows x 7168 x 4096: 25 us in tiles of 128
-    // columns, 33 in pairs; 2048 x 4096 x 4096: 39 in pairs, 49 in tiles of 128, 43 of 256. The
-    // groups' sizes are not known here: half a tile of each is taken to be empty.
+// The tile whose rounds over the SMs cost least. A step of a tile of 128 x 128, of 128 x 256 and of a
+// pair's 256 x 256 takes about 5 : 8 : 7 (in one round, of 56 steps: 25, 37 and 33 us; 64 columns
+// take as long as 128, so there is no narrower tile). 512 rows x 7168 x 4096: 25 us in tiles of 128
+// columns, 33 in pairs; 2048 x 4096 x 4096: 39 in pairs, 49 in tiles of 128, 43 of 256. The
+// groups' sizes are not known here: half a tile of each is taken to be empty.
+struct TileChoice {
+    bool pair;
+    int bn;         // instruction columns of a tile (the network's: of both factors)
+    int rows, cols;  // of the result
+    int at_once;    // tiles
+};
+TileChoice choose_tile(int64_t all_rows, int64_t G, int64_t N, bool swiglu) {
     const int sms = device_sm_count();
     auto cost = [&](int rows, int cols, int units, int step) {
-        const int64_t down = a.G == 1 ? ceil_div(a.rows, rows) : std::max(std::min(a.G, a.rows), a.rows / rows + a.G / 2);
-        return (down * ceil_div(a.N, cols) + units - 1) / units * step;
+        const int64_t down =
+            G == 1 ? ceil_div(all_rows, rows) : std::max(std::min(G, all_rows), all_rows / rows + G / 2);
+        return (down * ceil_div(N, cols) + units - 1) / units * step;
     };
-    const int64_t wide = cost(kTileM, p.swiglu ? 128 : 256, sms, 8);
-    const int64_t narrow = p.swiglu ? INT64_MAX : cost(kTileM, 128, sms, 5);
-    const bool pair = cost(2 * kTileM, p.swiglu ? 128 : 256, sms / 2, 7) <= std::min(wide, narrow);
-    const int bn = pair || wide <= narrow ? 256 : 128;
-    const int tile_m = pair ? 2 * kTileM : kTileM;
+    const int cols = swiglu ? 128 : 256;
+    const int64_t wide = cost(kTileM, cols, sms, 8);
+    const int64_t narrow = swiglu ? INT64_MAX : cost(kTileM, 128, sms, 5);
+    if (cost(2 * kTileM, cols, sms / 2, 7) <= std::min(wide, narrow)) return {true, 256, 2 * kTileM, cols, sms / 2};
+    if (wide <= narrow) return {false, 256, kTileM, cols, sms};
+    return {false, 128, kTileM, 128, sms};
+}
+
+mr_status run_product(const Product& p, GroupArgs a, cudaStream_t s) {
+    const TileChoice tile = choose_tile(a.rows, a.G, a.N, p.swiglu);
+    const bool pair = tile.pair;
+    const int bn = tile.bn, tile_m = tile.rows;
     const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G - 1, a.rows);  // or fewer
-    a.n_tiles = p.swiglu ? ceil_div(a.N, 128) : ceil_div(a.N, bn);
+    a.n_tiles = ceil_div(a.N, tile.cols);
     const int64_t tiles = m_tiles * a.n_tiles;
     if (tiles > INT32_MAX) return MR_ERR_PARAM_INVALID;
     CUtensorMap m[3];
@@ -836,6 +850,16 @@ bool make_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes,
 }  // namespace mr
 
 using namespace mr;
+
+extern "C" mr_status mr_expert_tile(int64_t rows, int64_t numGroups, int64_t outCols, int32_t network, int32_t* tile) {
+    if (!common_sizes(rows, 1, numGroups, outCols, 1) || rows == 0 || numGroups == 0) return MR_ERR_PARAM_INVALID;
+    if (!tile) return MR_ERR_PARAM_NULLPTR;
+    const TileChoice t = choose_tile(rows, numGroups < 0 ? 1 : numGroups, outCols, network != 0);
+    tile[0] = t.rows;
+    tile[1] = t.cols;
+    tile[2] = t.at_once;
+    return MR_OK;
+}
 
 extern "C" mr_status moe_grouped_matmul_get_workspace_size(int64_t rows, int64_t cols, int32_t xDtype,
                                                            uint64_t* workspaceSize) {
