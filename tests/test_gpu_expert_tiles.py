@@ -135,3 +135,20 @@ def test_several_tiles_of_the_network(tile, H, inter, second):
     for _ in range(3):
         again = usc.moe_expert_ffn(x.cuda(), w13, s13, w2, s2, lst)["y"]
         assert torch.equal(y.view(torch.uint8), again.view(torch.uint8))
+
+
+@pytest.mark.parametrize("T,E,topk,I", [(16, 40, 8, 520), (32, 40, 8, 1000), (64, 48, 8, 424), (64, 20, 5, 2056)])
+@pytest.mark.parametrize("wdt", [E4M3, BF16, F16])
+def test_several_tiles_of_the_layer(T, E, topk, I, wdt):
+    """moe_layer's second step takes 16 groups of 8 rows of W1 and W3 at a time: here a block has more, so
+    that blocks of 128 values of h are completed over several tiles, of one block and of neighbours."""
+    import test_gpu_layer as layer
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    c = layer.make(T, E, 200, I, BF16 if wdt is E4M3 else wdt, wdt, T + I)
+    r = layer.run(c, topk)
+    taken = r["expertIds"].unique().numel()
+    assert taken * -(-I // 8) > 16 * sms, f"{taken} experts taken"
+    layer.check(c, topk, r)
+    for _ in range(3):
+        again = layer.run(c, topk)
+        assert all(torch.equal(r[k], again[k]) for k in r)
