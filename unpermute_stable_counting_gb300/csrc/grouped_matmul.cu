@@ -512,7 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tile = info[n & 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
-            xp = a.x_scales + (int64_t)(tile.row0 + max(0, min((int)rank * kTileM + row, tile.rows - 1))) * a.xs_row;
+            int srow = tile.row0 + max(0, min((int)rank * kTileM + row, tile.rows - 1));
+            if (tile.rows > 0 && !MR_IN_RANGE(srow, a.rows, 902)) srow = 0;
+            if (!MR_IN_RANGE(tile.expert, a.experts, 903)) tile.expert = 0;
+            xp = a.x_scales + (int64_t)srow * a.xs_row;
             const int nb = min(SWIGLU ? tile.n0 / 2 / kScaleBlock : tile.n0 / kScaleBlock + half, a.scale_rows - 1);
             wp = a.w_scales + ((int64_t)(SWIGLU ? tile.expert * 2 : tile.expert) * a.scale_rows + nb) * a.KB;
             xs[0] = *xp;
@@ -596,7 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s, inv;
                 block_scale(m, &s, &inv);
                 const int n = n0 / 2 + group * 64;
-                if (group == 0 && lane < wrows) a.hs[(n0 / 2 / kScaleBlock) * a.hs_block + r + lane] = s;
+                const bool mine = wrows <= 0 || (MR_IN_RANGE(r + wrows - 1, a.rows, 904) &&
+                                                 MR_IN_RANGE(n + 63, a.hq_stride, 905));
+                if (mine && group == 0 && lane < wrows) a.hs[(n0 / 2 / kScaleBlock) * a.hs_block + r + lane] = s;
                 uint4 w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w[j] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
                 store_rows<4, false>(stage, w, a.hq + r * a.hq_stride + n, a.hq_stride,
-                              wrows == 32, wrows, 64, 4, lane);
+                              mine && wrows == 32, mine ? wrows : 0, 64, 4, lane);
             } else if (wrows > 0 && MR_IN_RANGE(r + wrows - 1, a.rows, 901)) {
                 const int elem = a.y_dtype == MR_DTYPE_F32 ? 4 : 2;
                 const int n = n0 + group * C::kChunk;

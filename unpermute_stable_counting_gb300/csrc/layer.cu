@@ -338,6 +338,7 @@ __device__ __forceinline__ int make_tables(const LayerArgs& a, Tables& tb, Choic
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
             const int i = threadIdx.x + j * kThreads;
+            if ((i >> 4) < a.T && (i & 15) < a.K && !MR_IN_RANGE(ex[j], a.E, 951)) ex[j] = 0;
             if (i < kMaxTokens * 16) c.expert[i >> 4][i & 15] = (uint16_t)ex[j], c.weight[i >> 4][i & 15] = w[j];
         }
     }
@@ -367,7 +368,7 @@ __device__ __forceinline__ int make_tables(const LayerArgs& a, Tables& tb, Choic
     for (int e = e0; e < e1; ++e) {
         const int n = __popcll(tb.mask[e]);
         tb.start[e] = (uint16_t)(before & 0xFFFFu);
-        if (n) tb.active[before >> 16] = (uint16_t)e;
+        if (n && MR_IN_RANGE(before >> 16, a.T * a.K, 952)) tb.active[before >> 16] = (uint16_t)e;
         before += (n ? 0x10000u : 0u) + n;
     }
     __syncthreads();
@@ -376,6 +377,7 @@ __device__ __forceinline__ int make_tables(const LayerArgs& a, Tables& tb, Choic
         const int t = i >> 4, r = i & 15;
         if (r >= a.K) continue;
         const int e = c.expert[t][r], slot = tb.start[e] + rank_of(tb.mask[e], t);
+        if (!MR_IN_RANGE(slot, a.T * a.K, 953)) continue;
         tb.weight[slot] = c.weight[t][r];
         tb.token[slot] = (uint8_t)t;
     }
@@ -590,13 +592,15 @@ __device__ __forceinline__ void step_h(const LayerArgs& a, const Tables& tb, con
                     const int ex = tb.active[j], whole = min(16, per - b * 16);
                     named_barrier(1, 256);  // the tile's rows are stored; *flag is free
                     if (threadIdx.x == 128) {
-                        *flag = atomicAdd(&a.count[ex * ib + b], (unsigned)run) + run == (unsigned)whole;
+                        *flag = MR_IN_RANGE(ex, a.E, 954) && MR_IN_RANGE(b, ib, 955) &&
+                                atomicAdd(&a.count[ex * ib + b], (unsigned)run) + run == (unsigned)whole;
                         __threadfence();
                     }
                     named_barrier(1, 256);
                     if (*flag) {
                         const int tokens = __popcll(tb.mask[ex]), s0 = tb.start[ex];
                         for (int s = warp - 4; s < tokens; s += 8) {
+                            if (!MR_IN_RANGE(s0 + s, a.T * a.K, 956)) break;
                             const int64_t at = (int64_t)(s0 + s) * a.h_cols + b * kScaleBlock + lane * 4;
                             const float4 v = __ldcg(reinterpret_cast<const float4*>(a.hf + at));
                             // columns past I hold nothing
@@ -786,6 +790,7 @@ __device__ __forceinline__ void step_y(const LayerArgs& a, const Tables& tb, con
                 for (int c = 0; c < COLS; ++c) {
                     if (half * COLS + c >= tokens) break;
                     const int slot = s0 + half * COLS + c;
+                    if (!MR_IN_RANGE(slot, a.T * a.K, 957) || !MR_IN_RANGE(tb.token[slot], a.T, 958)) break;
                     float* p = mine + tb.token[slot] * a.rows2;
                     *p = fmaf(tb.weight[slot], y[c], *p);
                 }

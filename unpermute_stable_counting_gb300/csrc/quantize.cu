@@ -136,6 +136,9 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
         const uint32_t i = min(first + n * 32, total - 1);  // past the end: the last block again, not stored
         row[n] = a.magic ? __umulhi(i, a.magic) >> a.shift : i;
         col[n] = (i - row[n] * a.blocks) * kScaleBlock + sub * P::kValues;
+        // (a row or block out of range: the first one again)
+        if (!MR_IN_RANGE(row[n], rows, 971) || !MR_IN_RANGE(col[n] / kScaleBlock, a.blocks, 972))
+            row[n] = 0u, col[n] = sub * P::kValues;
         const char* src = reinterpret_cast<const char*>(a.x) + row[n] * a.x_stride * P::kElem;
         if constexpr (LOOSE) {
             const bool inside = a.x_stride >= 8 && row[n] - 1u < (uint32_t)a.rows - 2u;
@@ -210,6 +213,7 @@ __global__ void __launch_bounds__(256)
     const int64_t e = rest / row_blocks;
     const int64_t r0 = (int64_t)rb * kScaleBlock, c = (int64_t)b * kScaleBlock + (threadIdx.x & 127);
     const int64_t r1 = min(r0 + kScaleBlock, rows);
+    if (!MR_IN_RANGE(r0, rows, 973) || !MR_IN_RANGE((int64_t)b * kScaleBlock, K, 974)) return;
     uint32_t m = 0u;
     if (c < K)
         for (int64_t r = r0 + (threadIdx.x >> 7); r < r1; r += 2)
@@ -254,6 +258,8 @@ cudaError_t enqueue_quantize(const void* x, int dt, int64_t rows, int64_t K, int
     const bool loose = reinterpret_cast<uintptr_t>(x) % 16 != 0 || (xStride * elem) % 16 != 0;
     return loose ? launch_quantize<true>(a, dt, stream) : launch_quantize<false>(a, dt, stream);
 }
+
+MR_CHECK_ACCESSOR(quantize)
 
 }  // namespace mr
 
