@@ -72,6 +72,29 @@ def test_quantize_weights_of_four_dimensions_in_part(cut):
     assert torch.equal(r["scales"].cpu().double(), s) and torch.equal(r["values"].cpu().double(), q)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("lead", [0, 3])
+def test_quantize_many_rows(lead, dtype):
+    """Enough blocks that each 8 lanes take two of them; rows that start on 16 bytes, and anywhere."""
+    n, k, used = 40_001, 513, 39_990             # 5 blocks a row, the last of one value
+    g = torch.Generator(device="cuda").manual_seed(4)
+    buf = torch.full((lead + n * 520,), float("nan"), dtype=dtype, device="cuda")
+    x = buf[lead:].view(n, 520)[:, :k] if lead == 0 else buf[lead:lead + n * 517].view(n, 517)[:, :k]
+    x.copy_(torch.randn(n, k, device="cuda", generator=g) * torch.exp(3 * torch.randn(n, 1, device="cuda", generator=g)))
+    out = usc.quantize_outputs((n, k), "cuda")
+    out["values"].view(torch.uint8).fill_(0x55), out["scales"].fill_(-1.0)
+    usc.moe_quantize(x, num_rows=torch.tensor([used], device="cuda"), out=out)
+    q, s = eu.quantize(x[:used].double())
+    for got, want in ((out["values"][:used].double(), q), (out["scales"][:used].double(), s)):
+        bad = want.isnan()                       # f16: blocks with an infinity
+        assert torch.equal(got.isnan(), bad) and torch.equal(got[~bad], want[~bad])
+    assert (out["values"][used:].view(torch.uint8) == 0x55).all() and (out["scales"][used:] == -1).all()
+    for rows_in_use, first in ((-5, 0), (n + 7, n)):
+        out["scales"].fill_(-1.0)
+        usc.moe_quantize(x, num_rows=torch.tensor([rows_in_use], device="cuda"), out=out)
+        assert (out["scales"][first:] == -1).all() and (out["scales"][:first] != -1).all()
+
+
 # ---------------------------------------------------------------------------
 # Streams
 # ---------------------------------------------------------------------------
@@ -304,6 +327,16 @@ def test_scores_that_are_all_zero_have_no_ratios():
     r = layer.run(c, 2, score="sigmoid")
     assert r["expertWeights"].isnan().all() and torch.equal(r["expertIds"].cpu(), torch.tensor([[0, 1]] * 2, dtype=torch.int32))
     assert (layer.run(c, 2, score="sigmoid", renormalize=False)["expertWeights"] == 0).all()
+
+
+@pytest.mark.parametrize("T,E,topk,H,I", [(64, 4, 2, 16384, 40), (64, 4, 2, 72, 16384), (64, 1024, 16, 136, 24),
+                                          (13, 16, 16, 9800, 136)])
+@pytest.mark.parametrize("wdt", [E4M3, BF16])
+def test_the_largest_sizes_of_a_layer(T, E, topk, H, I, wdt):
+    c = layer.make(T, E, H, I, BF16, wdt, T + E + H + I)
+    if T == 64 and H == 16384 and torch.cuda.get_device_properties(0).multi_processor_count < 128:
+        pytest.skip("needs 128 SMs")
+    layer.check(c, topk, layer.run(c, topk))
 
 
 # ---------------------------------------------------------------------------
