@@ -353,3 +353,25 @@ def test_the_count_of_waits_waits_for_every_stream():
         done.record()
     assert _native.lib().mr_waits_out(ctypes.byref(n), 0) == 0 and n.value == 0
     assert done.query()
+
+
+# ---------------------------------------------------------------------------
+# The example
+# ---------------------------------------------------------------------------
+
+def test_the_example_runs_the_routed_rows_alone(monkeypatch):
+    """Groups of as many rows as were routed; a capacity that holds every token gives the same result."""
+    import os
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    monkeypatch.setattr(sys, "path", [os.path.join(root, "examples"), *sys.path])
+    import moe_step
+    T, E, topk, H = 100, 16, 3, 256
+    wt = moe_step.make_weights(E, H, 128, seed=5)
+    x = torch.randn(T, H, generator=gen(6)).to(BF16).cuda()
+    seen, ffn = [], usc.moe_expert_ffn
+    monkeypatch.setattr(moe_step.usc, "moe_expert_ffn", lambda r, *a, **k: (seen.append(r.shape[0]), ffn(r, *a, **k))[1])
+    y, z = moe_step.routed_step(x, wt, topk), moe_step.routed_step(x, wt, topk, capacity=T)
+    assert seen == [T * topk, T * E]
+    # the padded way rounds each expert's rows to bf16 (2^-8 of each term), both round the result
+    assert ((y - z).float().norm() / y.float().norm()) < 2.0**-7 and (y - z).abs().amax() <= y.abs().amax() * 2.0**-5
