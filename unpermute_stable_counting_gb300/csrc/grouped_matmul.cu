@@ -22,11 +22,12 @@
 // What bounds it: with many rows the sums. A step of a pair's tile is 512 cycles of
 // the tensor cores, and 128 columns of loads from tensor memory and fp32 additions
 // for each of two warps per scheduler take about 690; the tensor pipe is active
-// 66 % of the time (4096 x 7168 x 7168). Sums of more warps with fewer columns, loads
+// 65 % of the time (4096 x 7168 x 7168). Sums of more warps with fewer columns, loads
 // of 32 columns and a step unrolled twice were all slower: they spill. Without the
 // additions the same kernel takes 516 us for 16384 x 7168 x 7168 (with them 572 us
 // = 2.94 PFLOP/s). With few rows per group the weights' way from HBM: 576 rows over
-// 64 experts, 7168 -> 4096, 285 us = 0.98 of the measured copy rate.
+// 64 experts, 7168 -> 4096, 275 to 287 us (from GPU to GPU), 0.97 to 1.01 of the
+// measured copy rate.
 #include "tensor.cuh"
 
 #include <algorithm>
@@ -738,7 +739,10 @@ struct Product {
 // pair's 256 x 256 takes about 5 : 8 : 7 (in one round, of 56 steps: 25, 37 and 33 us; 64 columns
 // take as long as 128, so there is no narrower tile). 512 rows x 7168 x 4096: 25 us in tiles of 128
 // columns, 33 in pairs; 2048 x 4096 x 4096: 39 in pairs, 49 in tiles of 128, 43 of 256. The
-// groups' sizes are not known here: half a tile of each is taken to be empty.
+// groups' sizes are not known here: half a tile of each row of the list is taken to be empty. What
+// that costs full groups, and lists with many empty ones: four full groups of 256 rows went from 20 to
+// 25 us when this rule replaced one by rows; 32768 rows of 64 full groups, 4096 -> 2048, 223 us with a list of 64 and 262 to
+// 268 with one of 128 to 1024 rows, for which it takes single blocks.
 struct TileChoice {
     bool pair;
     int bn;         // instruction columns of a tile (the network's: of both factors)

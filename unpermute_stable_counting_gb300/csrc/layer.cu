@@ -27,7 +27,10 @@
 // bits: 235 MB in 39 us and 117 MB in 25 us with their starts and ends), and around
 // them about 12 us of latency: the launch, the logits, three to four barriers of 1.3 us, and
 // the choice, whose instructions come from L2. 76 us, 0.68 of the time that the copy
-// rate gives the bytes; 64 tokens, 64 experts of 7168 x 1024 in 16 bits: 480 us, 0.86.
+// rate gives the bytes; 64 tokens, 64 experts of 7168 x 1024 in 16 bits: 459 to 469 us
+// (from GPU to GPU), 0.88 to 0.90. 8-bit weights with more tokens, 64 experts of 7168 x
+// 2048: 8 tokens 344 us (0.79 of what their 42 experts' bytes take), 32 tokens 490 us
+// (0.85), 64 tokens 528 us (0.79; the kernel for 33 to 64 tokens spills 48 bytes a thread).
 #include "tensor.cuh"
 
 #include <cooperative_groups.h>

@@ -113,9 +113,10 @@ struct QuantArgs {
     int vec_out;            // q rows start on 16 bytes
 };
 
-// kItems blocks per 8 lanes, all loads before the first use. The instructions
-// bound this kernel before HBM does: about 6 per value here; with 8 values per lane
-// and 64-bit index arithmetic it was 19, and 32768 x 4096 bf16 rows took 84 us.
+// kItems blocks per 8 lanes, all loads before the first use. The instructions are
+// what to keep low: 10 per value here, which fill 62 % of the issue slots, and
+// 32768 x 4096 bf16 rows take 60 to 61 us, 0.98 of the copy rate; with 8 values per
+// lane and 64-bit index arithmetic there were 19, and it took 75.6 us.
 // LOOSE: rows that do not start on 16 bytes, by aligned words shifted into place
 // (27285 x 5005 bf16: 104 us, fp32 136; rows of 5008 take 87 and 120; with bounds
 // checks and a load-and-shift per piece it took 131 and 228).
@@ -200,7 +201,8 @@ template <bool LOOSE> cudaError_t launch_quantize(const QuantArgs& a, int dt, cu
 }
 
 // 128 x 128 blocks (weights, quantized once when a model is loaded): one block
-// of threads per block of values, read twice.
+// of threads per block of values, read twice, a value per thread and access. 128
+// matrices of 2048 x 4096 bf16 take 1105 us, 2.3 times their bytes at the copy rate.
 __global__ void __launch_bounds__(256)
     quantize_tile_kernel(const void* x, int dt, int64_t rows, int64_t K, int64_t x_stride,
                          int64_t x_batch, uint8_t* q, int64_t q_stride, int64_t q_batch, float* scales,
