@@ -333,9 +333,11 @@ def test_scores_that_are_all_zero_have_no_ratios():
                                           (13, 16, 16, 9800, 136)])
 @pytest.mark.parametrize("wdt", [E4M3, BF16])
 def test_the_largest_sizes_of_a_layer(T, E, topk, H, I, wdt):
+    from unpermute_stable_counting_gb300 import _build, _native
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if H > 128 * (_build.FEW_SMS if _native.few_sms_requested() else sms):
+        pytest.skip("a block takes at most 128 rows of y")
     c = layer.make(T, E, H, I, BF16, wdt, T + E + H + I)
-    if T == 64 and H == 16384 and torch.cuda.get_device_properties(0).multi_processor_count < 128:
-        pytest.skip("needs 128 SMs")
     layer.check(c, topk, layer.run(c, topk))
 
 
