@@ -235,6 +235,32 @@ def test_rows_of_results_that_end_inside_16_bytes(N, out):
     assert (buf[:, N:] == 77).all()
 
 
+def test_offsets_past_32_bits():
+    """Rows of x, of its 8-bit values and of y that lie past 2^31 elements, and weights past 2^32 bytes."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(35)
+    n, k, N = 560_000, 4096, 4100
+    x = torch.empty(n, k, dtype=BF16, device="cuda")
+    for i in range(0, n, 40_000):
+        x[i:i + 40_000] = torch.randn(40_000, k, device="cuda", generator=g).to(BF16)
+    w = torch.randint(0, 256, (258, N, k), dtype=torch.uint8, device="cuda", generator=g).bitwise_and_(0xB7).view(E4M3)
+    ws = torch.rand(258, eu.blocks(N), k // 128, device="cuda", generator=g) * 0.01
+    lst = torch.tensor([[257, n - 70_001], [1, 70_001]]).cuda()
+    q = usc.moe_quantize(x)
+    sel = torch.tensor([0, 1, 299_999, 524_287, 524_288, n - 1], device="cuda")
+    v, s = eu.quantize(x[sel].double())
+    assert torch.equal(q["values"][sel].double(), v) and torch.equal(q["scales"][sel].double(), s)
+    rows = v * eu.spread(s, k)
+    ref = [eu.product(rows[j:j + 1], eu.weight(w[e], ws[e])) for j, e in enumerate([257, 257, 257, 1, 1, 1])]
+    assert n - 70_001 <= 524_287
+    ref, bound = (torch.cat(t).cpu() for t in zip(*ref))
+    for xx, kw in ((x, {}), (q["values"], dict(x_scales=q["scales"]))):
+        y = usc.moe_grouped_matmul(xx, w, ws, lst, **kw)["y"]
+        eu.assert_close(y[sel], ref, bound)
+        del y
+
+
 # ---------------------------------------------------------------------------
 # moe_layer
 # ---------------------------------------------------------------------------
