@@ -527,6 +527,68 @@ mr_status moe_quantize(const void* x, int32_t dtype, int64_t batch, int64_t rows
                        void* stream);
 
 /*
+ * INT8 rows. The batching's INT8 mode and the products below it take rows as
+ * int8 values with one fp32 scale per row, and weights as int8 values with one
+ * scale per output channel (a row of the weight matrix). A value stands for its
+ * integer times its scale.
+ *
+ * moe_quantize_int8 -- rows (a token's scale) or weights (a channel's) to int8.
+ *   a = max(max |x|, 2^-96) over a row, s = a / 127, value = x * (127 / a)
+ *   rounded to nearest even (so at most 127 in magnitude); the two quotients and
+ *   the product are rounded to fp32 first. A row that holds an infinity or a NaN
+ *   gets s = NaN and values 0.
+ *
+ *   x            [batch, rows, cols] of dtype (F16, BF16, F32), device.
+ *   xStrides     host array {batch, row} of element strides, nullable
+ *                (contiguous); a row's elements are adjacent.
+ *   numRows      device int64 [1], nullable (batch 1 only): rows at or past it
+ *                are not written.
+ *   values       int8 [batch, rows, cols]; valueStrides as xStrides, in bytes.
+ *   scales       float32 [batch, rows]; scaleStrides = host {batch, row} element
+ *                strides, nullable. A scale may stand behind its row's values
+ *                (cols a multiple of 4, a row stride of cols + 4 bytes: the
+ *                batching's interleaved rows).
+ *   rows at most 2^30, cols at most 2^24, batch * rows below 2^31.
+ *   Returns MR_OK, MR_ERR_PARAM_NULLPTR, MR_ERR_PARAM_INVALID or MR_ERR_CUDA.
+ */
+mr_status moe_quantize_int8(const void* x, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                            const int64_t* xStrides, const int64_t* numRows, void* values,
+                            const int64_t* valueStrides, float* scales, const int64_t* scaleStrides,
+                            void* stream);
+
+/*
+ * moe_add_rms_norm -- the residual's addition, the root-mean-square norm, and its
+ * result in 16 (or 32) bits, in 8 bits, or both, in one pass.
+ *   h = x + residual, rounded to dtype (without residual: x)
+ *   r = 1 / sqrt(mean(h^2) + eps) over a row, rounded to fp32 once
+ *   y = (h * r) * weight, each product rounded to fp32
+ *   residualOut = h; y rounded to dtype; values and scales from y in fp32, as
+ *   moe_quantize_int8 makes them (MR_DTYPE_INT8) or as moe_quantize does
+ *   (MR_DTYPE_E4M3, a scale per 128 values). Squares below 2^-149 count as 0.
+ *
+ *   x, residual   [rows, cols] of dtype (F16, BF16, F32), row strides in
+ *                 elements; residual is nullable.
+ *   weight        [cols] of dtype or F32 (weightDtype).
+ *   eps           in [2^-100, 2^100].
+ *   numRows       device int64 [1], nullable: rows at or past it are not written.
+ *   residualOut   [rows, cols] of dtype, nullable (and NULL without residual). It
+ *                 may be residual or x itself, with the same row stride.
+ *   y             [rows, cols] of dtype, nullable.
+ *   quantDtype    MR_DTYPE_INT8, MR_DTYPE_E4M3, or -1 for no 8-bit result.
+ *   values        [rows, cols] of 8 bits, row stride in bytes.
+ *   scales        float32, INT8: [rows]; E4M3: [rows, ceil(cols/128)];
+ *                 scaleStrides = host {row, block} element strides, nullable.
+ *   rows at most 2^30, cols at most 2^24.
+ *   Returns MR_OK, MR_ERR_PARAM_NULLPTR, MR_ERR_PARAM_INVALID or MR_ERR_CUDA.
+ */
+mr_status moe_add_rms_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t xStride,
+                           const void* residual, int64_t residualStride, const void* weight,
+                           int32_t weightDtype, double eps, const int64_t* numRows, void* residualOut,
+                           int64_t residualOutStride, void* y, int64_t yStride, int32_t quantDtype,
+                           void* values, int64_t valueStride, float* scales, const int64_t* scaleStrides,
+                           void* stream);
+
+/*
  * moe_grouped_matmul_get_workspace_size / moe_grouped_matmul
  *   y[r, n] = sum_b xs[r, b] ws[e, n/128, b] sum_{k in block b} x[r, k] w[e, n, k]
  *   for the rows of each group. Sums over the blocks are fp32; the result is

@@ -44,6 +44,9 @@ SIGNATURES = {
     "moe_update_expert": (_I32, [_P, _I32, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
                                  _I64, _PI64, _P, _P, _P]),
     "moe_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _PI64, _I32, _P, _P, _PI64, _P, _PI64, _P]),
+    "moe_quantize_int8": (_I32, [_P, _I32, _I64, _I64, _I64, _PI64, _P, _P, _PI64, _P, _PI64, _P]),
+    "moe_add_rms_norm": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _I32, ctypes.c_double, _P, _P, _I64, _P, _I64,
+                                _I32, _P, _I64, _P, _PI64, _P]),
     "moe_grouped_matmul_get_workspace_size": (_I32, [_I64, _I64, _I32, _PU64]),
     "moe_grouped_matmul": (_I32, [_P, _I32, _I64, _P, _PI64, _P, _PI64, _P, _P, _I64, _P, _I64, _I64,
                                   _I64, _I64, _I64, _P, _I32, _I64, _P, _U64, _P]),

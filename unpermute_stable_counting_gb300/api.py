@@ -475,15 +475,15 @@ def _workspace(workspace, size, index):
     return workspace
 
 
-def _wide_rows(lead, cols, index):
-    """e4m3 [*lead, cols] whose rows start on 16 bytes."""
+def _wide_rows(lead, cols, index, dtype=_E4M3):
+    """8-bit [*lead, cols] whose rows start on 16 bytes."""
     wide = -(-cols // 16) * 16
     if wide == cols:
-        return torch.empty((*lead, cols), dtype=_E4M3, device=_device(index))
+        return torch.empty((*lead, cols), dtype=dtype, device=_device(index))
     strides = [1]  # one tensor, not a slice of a wider one: that costs a small call 4 us more
     for n in (wide, *lead[:0:-1]):
         strides.append(strides[-1] * max(n, 1))
-    return torch.empty_strided((*lead, cols), strides[::-1], dtype=_E4M3, device=_device(index))
+    return torch.empty_strided((*lead, cols), strides[::-1], dtype=dtype, device=_device(index))
 
 
 def quantize_outputs(shape, device, block_rows: int = 1) -> dict:
@@ -495,6 +495,18 @@ def quantize_outputs(shape, device, block_rows: int = 1) -> dict:
     return dict(values=_wide_rows((*lead, rows), cols, index),
                 scales=torch.empty((*lead, rows if block_rows == 1 else _blocks(rows), _blocks(cols)),
                                    dtype=torch.float32, device=_device(index)))
+
+
+def _block_scales(scales, shape, index):
+    """Address and strides of float32 [rows, blocks] to write."""
+    if not scales.is_cuda or scales.dtype != torch.float32 or scales.shape != shape:
+        raise ValueError(f"scales must be float32 {list(shape)}")
+    _same_device("scales", scales, index)
+    for n, step in zip(shape, scales.stride()):
+        if n > 1 and step < 1:  # an expanded tensor has fewer elements than it shows
+            raise ValueError("scales must have an element of their own for each scale")
+    s0, s1 = scales.stride()
+    return scales.data_ptr(), _Pair(max(1, s0), max(1, s1))
 
 
 @_on_stream
@@ -535,15 +547,7 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
     _same_device("values", values, index)
     ss = None
     if block_rows == 1:
-        if not scales.is_cuda or scales.dtype != torch.float32 or scales.shape != sshape:
-            raise ValueError(f"scales must be float32 {list(sshape)}")
-        _same_device("scales", scales, index)
-        for n, step in zip(sshape, scales.stride()):
-            if n > 1 and step < 1:  # an expanded tensor has fewer elements than it shows
-                raise ValueError("scales must have an element of their own for each scale")
-        s0, s1 = scales.stride()
-        ss = _Pair(max(1, s0), max(1, s1))
-        saddr = scales.data_ptr()
+        saddr, ss = _block_scales(scales, sshape, index)
         xs, vs = _Pair(0, _row_stride(shape, strides)), _Pair(0, _row_stride(vshape, vstrides))
         batch = 1
     else:
@@ -561,6 +565,154 @@ def moe_quantize(x, *, block_rows: int = 1, num_rows=None, out: dict | None = No
                             num_rows, values.data_ptr(), vs, saddr, ss, _raw_stream(index))
     _check(st, "moe_quantize")
     return out
+
+
+def _interleaved(rows, cols, index):
+    """int8 rows with their fp32 scale behind them, as the batching's INT8 mode takes them."""
+    if cols % 4:
+        raise ValueError("interleaved rows need a multiple of 4 columns")
+    both = torch.empty((rows, cols + 4), dtype=torch.int8, device=_device(index))
+    return dict(rows=both, values=both[:, :cols], scales=both.view(torch.float32)[:, cols // 4])
+
+
+def _scales_of_rows(scales, rows, index):
+    """Address and stride of float32 [rows], each scale with an element of its own."""
+    if not isinstance(scales, torch.Tensor) or not scales.is_cuda or scales.dtype != torch.float32:
+        raise TypeError("scales must be a CUDA tensor of float32")
+    if scales.shape != (rows,):
+        raise ValueError(f"scales must be float32 [{rows}]")
+    _same_device("scales", scales, index)
+    step = scales.stride(0)
+    if rows > 1 and step < 1:
+        raise ValueError("scales must have an element of their own for each scale")
+    return scales.data_ptr(), max(1, step)
+
+
+@_on_stream
+def moe_quantize_int8(x, *, num_rows=None, interleaved: bool = False, out: dict | None = None) -> dict:
+    """Quantize x [..., cols] (f16/bf16/f32, 2 to 4 dimensions) to int8 with a scale
+    per row, on the current stream: a token's, or of weights [..., out, in] an output
+    channel's. Returns values (whose rows start on 16 bytes) and scales [...].
+
+    interleaved (x of 2 dimensions, cols a multiple of 4): also rows [rows, cols + 4],
+    each row's values and then its scale, the batching's token_data; values and scales
+    are views of it. num_rows (int64 [1] on the device, x of 2 dimensions): rows at or
+    past it are not written."""
+    dims = x.dim()
+    if not 2 <= dims <= 4:
+        raise ValueError("x must have 2 to 4 dimensions")
+    shape, strides = _rows_of("x", x, dims)
+    dt, index = _float_dt("x", x), x.get_device()
+    _on_current_device("x", index)
+    rows, cols = shape[-2], shape[-1]
+    num_rows = _vector("num_rows", num_rows, torch.int64, index)
+    if interleaved and dims != 2:
+        raise ValueError("interleaved rows need x of 2 dimensions")
+    if out is None:
+        out = _interleaved(rows, cols, index) if interleaved else dict(
+            values=_wide_rows(shape[:-1], cols, index, torch.int8),
+            scales=torch.empty(shape[:-1], dtype=torch.float32, device=_device(index)))
+    values, scales = out["values"], out["scales"]
+    vshape, vstrides = _rows_of("values", values, dims)
+    if values.dtype != torch.int8 or vshape != shape:
+        raise ValueError("values must be int8 of x's shape")
+    _same_device("values", values, index)
+    if dims == 2:
+        batch = 1
+        xs, vs = _Pair(0, _row_stride(shape, strides)), _Pair(0, _row_stride(vshape, vstrides))
+        sa, step = _scales_of_rows(scales, rows, index)
+        ss = _Pair(0, step)
+    else:
+        sa, ss = _vector("scales", scales, torch.float32, index, shape[:-1]), None
+        if x.numel() == 0 and rows and cols:  # no matrices
+            return out
+        batch = max(1, x.numel() // max(1, rows * cols))
+        xs, vs = _matrix_strides("x", shape, strides), _matrix_strides("values", vshape, vstrides)
+        xs[0], xs[1] = xs[1], xs[0]
+        vs[0], vs[1] = vs[1], vs[0]
+    st = lib().moe_quantize_int8(x.data_ptr(), dt, batch, rows, cols, xs, num_rows, values.data_ptr(), vs, sa, ss,
+                                 _raw_stream(index))
+    if st:
+        _check(st, "moe_quantize_int8")
+    return out
+
+
+_QUANTIZED = {None: -1, "int8": DT_INT8, "e4m3": DT_E4M3}
+
+
+@_on_stream
+def moe_add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quantize: str | None = None,
+                     with_y: bool = True, interleaved: bool = False, num_rows=None, out: dict | None = None) -> dict:
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over rows [rows, cols]
+    (f16/bf16/f32), on the current stream. Returns residual (h, where a residual was
+    given), y (with_y), and with quantize values and scales made from y in fp32:
+    "int8" with a scale per row, or "e4m3" with a scale per 128 values, as the expert
+    products take them.
+
+    weight: [cols] of x's dtype or float32. interleaved: as moe_quantize_int8's, for
+    "int8". out["residual"] may be residual or x itself. num_rows (int64 [1] on the
+    device): rows at or past it are not written."""
+    if quantize not in _QUANTIZED:
+        raise ValueError("quantize must be None, int8 or e4m3")
+    if interleaved and quantize != "int8":
+        raise ValueError("interleaved rows are int8 rows")
+    shape, strides = _rows_of("x", x, 2)
+    dt, index = _float_dt("x", x), x.get_device()
+    _on_current_device("x", index)
+    rows, cols = shape
+    if weight.dtype not in (x.dtype, torch.float32):
+        raise TypeError("weight must have x's dtype or float32")
+    wa = _vector("weight", weight, weight.dtype, index, (cols,))
+    num_rows = _vector("num_rows", num_rows, torch.int64, index)
+    ra = rs = 0
+    if residual is not None:
+        ra, rs = _like_x("residual", residual, x, shape, index)
+    if out is None:
+        out = {}
+        if residual is not None:
+            out["residual"] = torch.empty((rows, cols), dtype=x.dtype, device=_device(index))
+        if with_y:
+            out["y"] = torch.empty((rows, cols), dtype=x.dtype, device=_device(index))
+        if interleaved:
+            out.update(_interleaved(rows, cols, index))
+        elif quantize is not None:
+            eight = quantize == "int8"
+            out["values"] = _wide_rows((rows,), cols, index, torch.int8 if eight else _E4M3)
+            out["scales"] = torch.empty((rows,) if eight else (rows, _blocks(cols)), dtype=torch.float32,
+                                        device=_device(index))
+    ha = hs = ya = ys = va = vst = sa = 0
+    ss = None
+    if residual is not None:
+        ha, hs = _like_x("residual", out["residual"], x, shape, index)
+    if with_y:
+        ya, ys = _like_x("y", out["y"], x, shape, index)
+    if quantize is not None:
+        values, scales = out["values"], out["scales"]
+        vshape, vstrides = _rows_of("values", values, 2)
+        if values.dtype != (torch.int8 if quantize == "int8" else _E4M3) or vshape != shape:
+            raise ValueError(f"values must be {quantize} of x's shape")
+        _same_device("values", values, index)
+        va, vst = values.data_ptr(), _row_stride(vshape, vstrides)
+        if quantize == "int8":
+            sa, step = _scales_of_rows(scales, rows, index)
+            ss = _Pair(step, 1)
+        else:
+            sa, ss = _block_scales(scales, (rows, _blocks(cols)), index)
+    st = lib().moe_add_rms_norm(x.data_ptr(), dt, rows, cols, _row_stride(shape, strides), ra, rs, wa,
+                                _TORCH_TO_DT[weight.dtype], eps, num_rows, ha, hs, ya, ys, _QUANTIZED[quantize], va, vst,
+                                sa, ss, _raw_stream(index))
+    if st:
+        _check(st, "moe_add_rms_norm")
+    return out
+
+
+def _like_x(name, t, x, shape, index):
+    """Address and row stride of a tensor of x's shape and dtype."""
+    tshape, strides = _rows_of(name, t, 2)
+    if t.dtype != x.dtype or tshape != shape:
+        raise ValueError(f"{name} must be of x's shape and dtype")
+    _same_device(name, t, index)
+    return t.data_ptr(), _row_stride(tshape, strides)
 
 
 @functools.lru_cache(maxsize=1024)

@@ -89,6 +89,9 @@ cudaError_t mr_check_words_batching(unsigned* out, bool reset);
 cudaError_t mr_check_words_context(unsigned* out, bool reset);
 cudaError_t mr_check_words_grouped_matmul(unsigned* out, bool reset);
 cudaError_t mr_check_words_layer(unsigned* out, bool reset);
+cudaError_t mr_check_words_norm_bf16(unsigned* out, bool reset);
+cudaError_t mr_check_words_norm_f16(unsigned* out, bool reset);
+cudaError_t mr_check_words_norm_f32(unsigned* out, bool reset);
 cudaError_t mr_check_words_permute(unsigned* out, bool reset);
 cudaError_t mr_check_words_quantize(unsigned* out, bool reset);
 cudaError_t mr_check_words_unpermute(unsigned* out, bool reset);
@@ -101,6 +104,8 @@ extern "C" mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, 
     if (!failures) return MR_ERR_PARAM_NULLPTR;
     cudaError_t (*readers[])(unsigned*, bool) = {mr::mr_check_words_batching, mr::mr_check_words_context,
                                                  mr::mr_check_words_grouped_matmul, mr::mr_check_words_layer,
+                                                 mr::mr_check_words_norm_bf16, mr::mr_check_words_norm_f16,
+                                                 mr::mr_check_words_norm_f32,
                                                  mr::mr_check_words_permute, mr::mr_check_words_quantize,
                                                  mr::mr_check_words_unpermute, mr::mr_check_words_update_expert};
     uint32_t total = 0u, first = 0u;
