@@ -656,6 +656,65 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
                          void* workspace, uint64_t workspaceSize, void* stream);
 
 /*
+ * moe_grouped_matmul_int8_get_workspace_size / moe_grouped_matmul_int8
+ *   y[r, n] = (sum_k x[r, k] w[e, n, k]) ws[e, n] xs[r]
+ *   for the rows of each group. Products of int8 values are exact and so are
+ *   their fp32 sums while they stay below 2^24; 16-bit rows multiply as they are.
+ *   The result is rounded once to yDtype (each scale's product once to fp32).
+ *
+ *   x             [rows, cols] of xDtype: INT8 with xScales (the batching's y and
+ *                 dynamicScale, or moe_quantize_int8's), or F16 or BF16, whose
+ *                 xScales is nullable; row stride xStride elements.
+ *   xScales       float32 [rows], xScaleStride elements apart.
+ *   weights       int8 [experts, outCols, cols]; weightStrides = host {row,
+ *                 matrix} byte strides, nullable (contiguous).
+ *   weightScales  float32 [experts, outCols].
+ *   numRows       device int64 [1], nullable: the rows in use (the batching's
+ *                 actualTokenNum), so that no others are read.
+ *   groupList, numGroups, expertBase, y and the limits are moe_grouped_matmul's.
+ *   x and weights start on 16 bytes and have row strides that are multiples of 16
+ *   bytes, as 8-bit operands of the other expert products; a length that is not is
+ *   padded by the stride, and the padding is never read as values.
+ *   workspace     256-byte aligned; not needed (NULL) for 16-bit rows.
+ *   Returns MR_OK, MR_ERR_PARAM_NULLPTR, MR_ERR_PARAM_INVALID,
+ *   MR_ERR_WORKSPACE or MR_ERR_CUDA.
+ */
+mr_status moe_grouped_matmul_int8_get_workspace_size(int64_t rows, int64_t cols, int32_t xDtype,
+                                                     uint64_t* workspaceSize);
+mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int64_t xStride, const float* xScales,
+                                  int64_t xScaleStride, const void* weights, const int64_t* weightStrides,
+                                  const float* weightScales, const int64_t* groupList, int64_t numGroups,
+                                  const int64_t* numRows, int64_t expertBase, int64_t rows, int64_t experts,
+                                  int64_t outCols, int64_t cols, void* y, int32_t yDtype, int64_t yStride,
+                                  void* workspace, uint64_t workspaceSize, void* stream);
+
+/*
+ * moe_expert_ffn_int8_get_workspace_size / moe_expert_ffn_int8
+ *   h = silu(x W1^T) * (x W3^T), rounded to bf16, y = h W2^T, for the rows of each
+ *   group. Two products as in moe_grouped_matmul_int8; h exists only in the
+ *   workspace. (The products run at the 16-bit rate whatever the rows hold: 8 bits
+ *   for h would cost a pass over its rows for their scales, and precision.)
+ *
+ *   w13           int8 [experts, 2, inter, hidden]: W1 then W3; w13Strides = host
+ *                 {row, matrix} byte strides, nullable.
+ *   w13Scales     float32 [experts, 2, inter].
+ *   w2            int8 [experts, hidden, inter]; w2Strides as w13Strides.
+ *   w2Scales      float32 [experts, hidden].
+ *   y             [rows, hidden] of yDtype.
+ *   The other arguments, limits and errors are moe_grouped_matmul_int8's; the
+ *   workspace is always needed.
+ */
+mr_status moe_expert_ffn_int8_get_workspace_size(int64_t rows, int64_t hidden, int64_t inter,
+                                                 int32_t xDtype, uint64_t* workspaceSize);
+mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t xStride, const float* xScales,
+                              int64_t xScaleStride, const void* w13, const int64_t* w13Strides,
+                              const float* w13Scales, const void* w2, const int64_t* w2Strides,
+                              const float* w2Scales, const int64_t* groupList, int64_t numGroups,
+                              const int64_t* numRows, int64_t expertBase, int64_t rows, int64_t experts,
+                              int64_t hidden, int64_t inter, void* y, int32_t yDtype, int64_t yStride,
+                              void* workspace, uint64_t workspaceSize, void* stream);
+
+/*
  * moe_layer_get_workspace_size / moe_layer
  *   A whole mixture-of-experts layer for up to 64 tokens (a decode step), in
  *   one launch:

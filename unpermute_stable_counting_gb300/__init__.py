@@ -21,17 +21,21 @@ Importing the package does not load the CUDA library; the first call does,
 and fails loudly if the library was not built.
 """
 from .api import (DT_BF16, DT_E4M3, DT_F16, DT_F32, DT_INT8, MoeReorderError, batching_context_workspace_size,
-                  batching_outputs, batching_workspace_size, expert_ffn_workspace_size, ffnwb_batching,
-                  ffnwb_batching_context, grouped_matmul_workspace_size, layer_workspace_size, moe_add_rms_norm,
-                  moe_expert_ffn, moe_grouped_matmul, moe_layer, moe_permute, moe_quantize, moe_quantize_int8,
-                  moe_unpermute, moe_update_expert,
-                  permute_workspace_size, profile_set_events, quantize_outputs, unpermute_outputs,
-                  unpermute_workspace_size, waits_out)
+                  batching_outputs, batching_workspace_size, expert_ffn_int8_workspace_size,
+                  expert_ffn_workspace_size, ffnwb_batching, ffnwb_batching_context,
+                  grouped_matmul_int8_workspace_size, grouped_matmul_workspace_size,
+                  layer_workspace_size, moe_add_rms_norm, moe_expert_ffn, moe_expert_ffn_int8,
+                  moe_grouped_matmul, moe_grouped_matmul_int8, moe_layer, moe_permute, moe_quantize,
+                  moe_quantize_int8, moe_unpermute, moe_update_expert, permute_workspace_size,
+                  profile_set_events, quantize_outputs, unpermute_outputs, unpermute_workspace_size,
+                  waits_out)
 
 __all__ = ["ffnwb_batching", "ffnwb_batching_context", "moe_unpermute", "moe_permute", "moe_update_expert",
-           "moe_quantize", "moe_quantize_int8", "moe_add_rms_norm", "moe_grouped_matmul", "moe_expert_ffn", "moe_layer",
-           "quantize_outputs",
-           "grouped_matmul_workspace_size", "expert_ffn_workspace_size", "layer_workspace_size", "permute_workspace_size",
-           "batching_context_workspace_size", "batching_workspace_size",
-           "unpermute_workspace_size", "batching_outputs", "unpermute_outputs",
-           "profile_set_events", "waits_out", "MoeReorderError", "DT_F16", "DT_BF16", "DT_INT8", "DT_F32", "DT_E4M3"]
+           "moe_quantize", "moe_quantize_int8", "moe_add_rms_norm", "moe_grouped_matmul",
+           "moe_expert_ffn", "moe_grouped_matmul_int8", "moe_expert_ffn_int8",
+           "grouped_matmul_int8_workspace_size", "expert_ffn_int8_workspace_size", "moe_layer",
+           "quantize_outputs", "grouped_matmul_workspace_size", "expert_ffn_workspace_size",
+           "layer_workspace_size", "permute_workspace_size", "batching_context_workspace_size",
+           "batching_workspace_size", "unpermute_workspace_size", "batching_outputs",
+           "unpermute_outputs", "profile_set_events", "waits_out", "MoeReorderError", "DT_F16",
+           "DT_BF16", "DT_INT8", "DT_F32", "DT_E4M3"]

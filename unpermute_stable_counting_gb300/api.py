@@ -839,6 +839,120 @@ def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scal
     return out
 
 
+_INT8_ROWS = {torch.int8: DT_INT8, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+
+
+@functools.lru_cache(maxsize=1024)
+def grouped_matmul_int8_workspace_size(rows: int, cols: int, x_dtype: int) -> int:
+    ws = ctypes.c_uint64(0)
+    _check(lib().moe_grouped_matmul_int8_get_workspace_size(rows, cols, x_dtype, ctypes.byref(ws)),
+           "moe_grouped_matmul_int8_get_workspace_size")
+    return int(ws.value)
+
+
+def _int8_rows(x, x_scales, group_list):
+    """Checks of the rows and groups that both products with int8 weights take."""
+    shape, strides = _rows_of("x", x, 2)
+    dt = _INT8_ROWS.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x dtype {x.dtype} is not int8/f16/bf16")
+    index = x.get_device()
+    _on_current_device("x", index)
+    sa = ss = 0
+    if x_scales is None:
+        if dt == DT_INT8:
+            raise ValueError("int8 rows need x_scales")
+    else:
+        if not isinstance(x_scales, torch.Tensor) or not x_scales.is_cuda or x_scales.dtype != torch.float32:
+            raise TypeError("x_scales must be a CUDA tensor of float32")
+        if x_scales.dim() != 1 or x_scales.shape[0] != shape[0]:
+            raise ValueError("x_scales must be [rows]")
+        _same_device("x_scales", x_scales, index)
+        sa, ss = x_scales.data_ptr(), x_scales.stride(0)
+    ga, groups = _vector("group_list", group_list, torch.int64, index), -1
+    if group_list is not None:
+        if group_list.dim() != 2 or group_list.shape[1] != 2:
+            raise ValueError("group_list must be [groups, 2]")
+        groups = group_list.shape[0]
+    return dt, index, shape, _row_stride(shape, strides), sa, ss, ga, groups
+
+
+def _int8_weights(name, w, scales, shape, index):
+    """Address and strides of int8 weights of `shape`, address of their scales."""
+    wshape, strides = _rows_of(name, w, len(shape))
+    if w.dtype != torch.int8:
+        raise TypeError(f"{name} must have dtype {torch.int8}, got {w.dtype}")
+    if wshape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(wshape)}")
+    _same_device(name, w, index)
+    if scales is None:
+        raise ValueError(f"{name} needs its scales")
+    sa = _vector(name + "_scales", scales, torch.float32, index, shape[:-1])
+    return w.data_ptr(), _matrix_strides(name, wshape, strides), sa
+
+
+@_on_stream
+def moe_grouped_matmul_int8(x, weights, weight_scales, group_list=None, *, x_scales=None, num_rows=None,
+                            expert_base: int = 0, out_dtype=torch.bfloat16, out: dict | None = None,
+                            workspace=None) -> dict:
+    """Product of each group's rows with its expert's int8 weights [experts,
+    out_cols, cols], whose scales are [experts, out_cols], on the current stream.
+    Returns y [rows, out_cols].
+
+    x: int8 rows with x_scales [rows] (the batching's y and dynamicScale), or f16
+    or bf16 rows, which multiply as they are (x_scales optional). The other
+    arguments are moe_grouped_matmul's."""
+    dt, index, (rows, K), xst, xsa, xss, ga, groups = _int8_rows(x, x_scales, group_list)
+    if weights.dim() != 3 or weights.shape[2] != K:
+        raise ValueError("weights must be [experts, out_cols, cols]")
+    E, N = weights.shape[0], weights.shape[1]
+    wa, wst, wsa = _int8_weights("weights", weights, weight_scales, (E, N, K), index)
+    out, ya, ydt, yst = _out_rows(out, rows, N, out_dtype, index)
+    wsp, size = None, 0
+    if dt == DT_INT8 or workspace is not None:
+        workspace = _workspace(workspace, grouped_matmul_int8_workspace_size(rows, K, dt), index)
+        wsp, size = workspace.data_ptr(), workspace.numel()
+    st = lib().moe_grouped_matmul_int8(x.data_ptr(), dt, xst, xsa, xss, wa, wst, wsa, ga, groups,
+                                       _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, N, K,
+                                       ya, ydt, yst, wsp, size, _raw_stream(index))
+    _check(st, "moe_grouped_matmul_int8")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def expert_ffn_int8_workspace_size(rows: int, hidden: int, inter: int, x_dtype: int) -> int:
+    ws = ctypes.c_uint64(0)
+    _check(lib().moe_expert_ffn_int8_get_workspace_size(rows, hidden, inter, x_dtype, ctypes.byref(ws)),
+           "moe_expert_ffn_int8_get_workspace_size")
+    return int(ws.value)
+
+
+@_on_stream
+def moe_expert_ffn_int8(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scales=None, num_rows=None,
+                        expert_base: int = 0, out_dtype=None, out: dict | None = None, workspace=None) -> dict:
+    """The experts' network with int8 weights, y = bf16(silu(x W1^T) * (x W3^T)) W2^T,
+    for each group's rows on the current stream. Returns y [rows, hidden].
+
+    w13: int8 [experts, 2, inter, hidden], its scales [experts, 2, inter]; w2: int8
+    [experts, hidden, inter], its scales [experts, hidden]. out_dtype: x's by default
+    (bf16 for int8 rows). The other arguments are moe_grouped_matmul_int8's."""
+    dt, index, (rows, H), xst, xsa, xss, ga, groups = _int8_rows(x, x_scales, group_list)
+    if w13.dim() != 4 or w13.shape[1] != 2 or w13.shape[3] != H:
+        raise ValueError("w13 must be [experts, 2, inter, hidden]")
+    E, inter = w13.shape[0], w13.shape[2]
+    a13, st13, s13 = _int8_weights("w13", w13, w13_scales, (E, 2, inter, H), index)
+    a2, st2, s2 = _int8_weights("w2", w2, w2_scales, (E, H, inter), index)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if dt == DT_INT8 else x.dtype
+    out, ya, ydt, yst = _out_rows(out, rows, H, out_dtype, index)
+    workspace = _workspace(workspace, expert_ffn_int8_workspace_size(rows, H, inter, dt), index)
+    st = lib().moe_expert_ffn_int8(x.data_ptr(), dt, xst, xsa, xss, a13, st13, s13, a2, st2, s2, ga, groups,
+                                   _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, H,
+                                   inter, ya, ydt, yst, workspace.data_ptr(), workspace.numel(), _raw_stream(index))
+    _check(st, "moe_expert_ffn_int8")
+    return out
+
+
 MR_LAYER_SIGMOID, MR_LAYER_KEEP_WEIGHTS = 1, 2
 
 

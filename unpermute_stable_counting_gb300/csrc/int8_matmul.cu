@@ -1,0 +1,749 @@
+// Grouped product of rows with 8-bit integer expert weights that have a scale per
+// output channel, and the experts' network built on it:
+//   y[r, n] = sx[r] sw[e, n] sum_k x[r, k] w[e, n, k]
+// for the rows r of each group (expert e, count) of a list on the device. Rows are
+// int8 with a scale each, or of 16 bits.
+//
+// The tensor cores of sm_103a have no 8-bit integer products. An int8 value is
+// exact in f16 and in bf16, a product of two in the fp32 accumulators, and so is a
+// sum while it stays below 2^24. So the products run at the 16-bit rate, and the
+// weights, which are the bulk of what is read, become 16 bits on their way to the
+// tensor cores: W is the operand with 128 rows (A), and its values go from shared
+// memory through registers to tensor memory, which costs shared memory neither the
+// store nor the instructions' reads. The rows of a group are the other operand (B):
+// an instruction has as many columns as the group has rows left, to the next 16.
+//   warp 0       TMA loads of the weights (and of int8 rows): a ring of 128 values of k
+//   warp 1       matrix instructions, 64 values of k a step
+//   warp 2       hands tiles to the warps below
+//   warp 3       TMA loads of 16-bit rows: a ring of 64 values of k
+//   warps 4-11   weights (and int8 rows) to 16 bits; each warpgroup has one half of a
+//                load's 128 values
+//   warps 12-19  results: scales, rounding, stores
+// One persistent block per SM takes tiles round robin; a pair of blocks shares a tile
+// of 256 channels, where each converts its own 128 and loads half of the rows.
+#include "groups.cuh"
+#include "tensor.cuh"
+
+#include <algorithm>
+#include <atomic>
+
+namespace mr {
+
+namespace {
+
+__device__ unsigned g_waits_out;  // blocks that left early, see mbar_wait
+
+constexpr int kThreads = 640, kConvertWarps = 8, kSumWarps = 8;
+constexpr int kWRows = 128, kWBytes = kWRows * 128;  // a load: 128 channels x 128 values
+
+struct Int8Args : Groups {
+    const float* x_scales;  // [r * xs_row], or NULL
+    int64_t xs_row;
+    const float* w_scales;  // [expert (, 2)][N]
+    int N, KB;              // channels (the network's first product: inter), loads of 128 values of k
+    void* y;
+    int64_t y_stride;
+    int y_dtype;
+};
+
+enum { kInt8 = 0, kF16 = 1, kBf16 = 2 };  // rows
+
+// XT: the rows' type. SWIGLU: the network's first product, whose gate and other
+// factor are two planes of instructions with sums side by side.
+template <int XT, bool SWIGLU, bool PAIR> struct Cfg {
+    static constexpr int kPlanes = SWIGLU ? 2 : 1;
+    static constexpr int kRows = PAIR ? (SWIGLU ? 128 : 256) : 64;  // rows of a tile
+    static constexpr int kLoadRows = PAIR ? kRows / 2 : kRows;      // of them, those this block loads
+    static constexpr int kGrain = PAIR ? 64 : 16;                   // columns of an instruction are a multiple of this
+    static constexpr int kSteps = PAIR ? (SWIGLU ? 4 : 6) : 4;      // steps of converted weights (and 16-bit rows) held
+    static constexpr int kSumBufs = PAIR ? 1 : 2;
+    static constexpr int kSumCols = kPlanes * kRows;
+    static constexpr int kACols = 256;                              // tensor memory: sums, then weights
+    static_assert(kSumCols * kSumBufs <= kACols && kSteps * 32 * kPlanes <= 256, "tensor memory");
+    static constexpr int kLoads = PAIR ? (SWIGLU ? 5 : 7) : XT == kInt8 ? (SWIGLU ? 4 : 7) : (SWIGLU ? 5 : 10);
+    static constexpr int kLoadBytes = kPlanes * kWBytes + (XT == kInt8 ? kLoadRows * 128 : 0);
+    static constexpr int kStepBytes = kLoadRows * 128;
+    static constexpr int kSmem = 1024 + kLoads * kLoadBytes + kSteps * kStepBytes;
+    static constexpr int kHalf = kRows / 2;                         // rows of a warpgroup of results
+};
+
+// Matrix instruction with A in tensor memory.
+template <bool PAIR>
+__device__ __forceinline__ void mma_16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
+        "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
+        "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four int8 to four 16-bit values, without a conversion instruction: a byte below an
+// exponent's byte is an offset value, and one subtraction, exact, takes the offset off.
+//   f16   0x64xx is 1024 + xx; xx = x + 128 by flipping the sign bit
+//   bf16  0x43xx is 128 + xx below 128 and 256 + 2 (xx - 128) above, 8 bits being all it
+//         has: x = (128 + low 7 bits) - (256 if x < 0, else 128)
+template <bool BF16> __device__ __forceinline__ void widen4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    if constexpr (BF16) {
+        const uint32_t p = __byte_perm(x, 0x43434343u, 0x5140), q = __byte_perm(x, 0x43434343u, 0x5342);
+        const uint32_t pa = p & 0xFF7FFF7Fu, pb = p & 0xFF80FF80u, qa = q & 0xFF7FFF7Fu, qb = q & 0xFF80FF80u;
+        const __nv_bfloat162 l = __hsub2(reinterpret_cast<const __nv_bfloat162&>(pa), reinterpret_cast<const __nv_bfloat162&>(pb));
+        const __nv_bfloat162 h = __hsub2(reinterpret_cast<const __nv_bfloat162&>(qa), reinterpret_cast<const __nv_bfloat162&>(qb));
+        lo = reinterpret_cast<const uint32_t&>(l);
+        hi = reinterpret_cast<const uint32_t&>(h);
+    } else {
+        x ^= 0x80808080u;
+        const uint32_t p = __byte_perm(x, 0x64646464u, 0x5140), q = __byte_perm(x, 0x64646464u, 0x5342), off = 0x64806480u;
+        const __half2 l = __hsub2(reinterpret_cast<const __half2&>(p), reinterpret_cast<const __half2&>(off));
+        const __half2 h = __hsub2(reinterpret_cast<const __half2&>(q), reinterpret_cast<const __half2&>(off));
+        lo = reinterpret_cast<const uint32_t&>(l);
+        hi = reinterpret_cast<const uint32_t&>(h);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(int dt, float a, float b) {
+    if (dt == MR_DTYPE_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return reinterpret_cast<const uint32_t&>(h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return reinterpret_cast<const uint32_t&>(h);
+}
+
+template <int XT, bool SWIGLU, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       const Int8Args a) {
+    using C = Cfg<XT, SWIGLU, PAIR>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t l_full[C::kLoads], l_empty[C::kLoads];                   // loads
+    __shared__ __align__(8) uint64_t x_full[C::kSteps], a_full[C::kSteps], a_empty[C::kSteps];  // steps
+    __shared__ __align__(8) uint64_t t_full[2], t_empty[2], i_full[2], i_empty[2];
+    __shared__ Tile info[2];
+    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ uint32_t tmem_base, abort_word;
+
+    uint8_t* loads = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    static_assert(C::kSmem + 1024 <= 232448, "shared memory of a block");
+    uint8_t* rows16 = loads + C::kLoads * C::kLoadBytes;
+    volatile uint32_t* abort = &abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kBlocks = PAIR ? 2 : 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kLoads; ++i)
+            mbar_init(smem_u32(&l_full[i]), 1), mbar_init(smem_u32(&l_empty[i]), kConvertWarps);
+        for (int i = 0; i < C::kSteps; ++i) {
+            mbar_init(smem_u32(&x_full[i]), 1);
+            mbar_init(smem_u32(&a_full[i]), kBlocks * kConvertWarps / 2);
+            mbar_init(smem_u32(&a_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&t_full[i]), 1);
+            mbar_init(smem_u32(&t_empty[i]), kBlocks * kSumWarps);
+            mbar_init(smem_u32(&i_full[i]), 1);
+            mbar_init(smem_u32(&i_empty[i]), kConvertWarps + kSumWarps);
+        }
+        mbar_init(smem_u32(&drain_bar), 1);
+        abort_word = 0u;
+        mbar_init_fence();
+        tma_prefetch(&map_x);
+        tma_prefetch(&map_w);
+    }
+    if (warp == 1) tmem_alloc<PAIR>(smem_u32(&tmem_base), 512);
+    tc_fence_before();
+    if (PAIR) cluster_sync();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const uint32_t rank = PAIR ? cluster_rank() : 0u;
+    const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+    pdl_enter();
+
+    Walk<C::kRows> walk;
+    Tile tile;
+    uint32_t it = 0;  // loads or steps that this warp has taken, over all of its tiles
+    bool ok = true;
+    // columns of a tile's instructions, and boxes of 32 rows that this block loads
+    auto columns = [&](int rows) { return (rows + C::kGrain - 1) / C::kGrain * C::kGrain; };
+    auto boxes_of = [&](int rows) { return (columns(rows) / kBlocks + 31) / 32; };
+
+    if (warp < 4) {
+        regs_dec<48>();
+        if (warp == 0) {
+            walk.begin(a, lane);
+            for (int t = first; ok && walk.next(a, lane, t, kWRows * kBlocks, tile); t += step) {
+                const int n0 = tile.n0 + (int)rank * kWRows;
+                const int boxes = XT == kInt8 ? boxes_of(tile.rows) : 0;
+                if (elect_one()) {
+                    for (int kb = 0; kb < a.KB; ++kb, ++it) {
+                        const uint32_t st = it % C::kLoads;
+                        ok = mbar_wait<PAIR>(smem_u32(&l_empty[st]), ((it / C::kLoads) & 1) ^ 1, abort);
+                        if (!ok) break;
+                        const uint32_t bar = smem_u32(&l_full[st]), dst = smem_u32(loads + st * C::kLoadBytes);
+                        mbar_expect(bar, (uint32_t)(C::kPlanes * kWBytes + boxes * 32 * 128));
+#pragma unroll
+                        for (int p = 0; p < C::kPlanes; ++p)
+                            tma_load_3d(dst + p * kWBytes, &map_w, bar, kb * 128, n0, tile.expert * C::kPlanes + p);
+                        if (XT == kInt8)
+                            for (int j = 0; j < boxes; ++j)
+                                tma_load_2d(dst + C::kPlanes * kWBytes + j * 32 * 128, &map_x, bar, kb * 128,
+                                            tile.row0 + 32 * j);
+                    }
+                }
+                __syncwarp();
+                it = __reduce_max_sync(0xffffffffu, it);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+        } else if (warp == 1) {
+            ok = rank == 0;
+            walk.begin(a, lane);
+            uint32_t n = 0;
+            for (int t = first; ok && walk.next(a, lane, t, kWRows * kBlocks, tile); t += step, ++n) {
+                const uint32_t buf = n % C::kSumBufs;
+                const uint32_t idesc = idesc_16(kWRows * kBlocks, columns(tile.rows), XT == kBf16);
+                if (elect_one()) {
+                    ok = mbar_wait<PAIR>(smem_u32(&t_empty[buf]), ((n / C::kSumBufs) & 1) ^ 1, abort);
+                    const uint32_t d = tmem + buf * C::kSumCols;
+                    for (int k = 0; ok && k < 2 * a.KB; ++k, ++it) {
+                        const uint32_t s = it % C::kSteps, parity = (it / C::kSteps) & 1;
+                        ok = mbar_wait<PAIR>(smem_u32(&a_full[s]), parity, abort);
+                        if (XT != kInt8) ok = ok && mbar_wait<PAIR>(smem_u32(&x_full[s]), parity, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t b = smem_desc(smem_u32(rows16 + s * C::kStepBytes));
+#pragma unroll
+                        for (int p = 0; p < C::kPlanes; ++p)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mma_16_tmem<PAIR>(d + p * C::kRows, tmem + C::kACols + (s * C::kPlanes + p) * 32 + 8 * j,
+                                                  b + 2 * j, idesc, k > 0 || j > 0);
+                        tc_commit<PAIR>(smem_u32(&a_empty[s]));
+                    }
+                    if (ok) tc_commit<PAIR>(smem_u32(&t_full[buf]));
+                }
+                __syncwarp();
+                it = __reduce_max_sync(0xffffffffu, it);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+        } else if (warp == 2) {
+            // tiles for the warps below; one of no rows ends them
+            walk.begin(a, lane);
+            uint32_t n = 0;
+            for (int t = first;; t += step, ++n) {
+                const bool more = walk.next(a, lane, t, kWRows * kBlocks, tile);
+                if (!mbar_wait<PAIR>(smem_u32(&i_empty[n & 1]), ((n >> 1) & 1) ^ 1, abort)) break;
+                if (lane == 0) {
+                    if (!more) tile = Tile{0, 0, 0, 0};
+                    info[n & 1] = tile;
+                    mbar_arrive(smem_u32(&i_full[n & 1]));
+                }
+                if (!more) break;
+            }
+        } else if (XT != kInt8) {
+            walk.begin(a, lane);
+            for (int t = first; ok && walk.next(a, lane, t, kWRows * kBlocks, tile); t += step) {
+                const int boxes = boxes_of(tile.rows);
+                const int row0 = tile.row0 + (int)rank * columns(tile.rows) / 2;
+                if (elect_one()) {
+                    for (int k = 0; k < 2 * a.KB; ++k, ++it) {
+                        const uint32_t s = it % C::kSteps;
+                        ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
+                        if (!ok) break;
+                        const uint32_t own = smem_u32(&x_full[s]), bar = PAIR ? map_cluster(own, 0) : own;
+                        const uint32_t dst = smem_u32(rows16 + s * C::kStepBytes);
+                        if (rank == 0) mbar_expect(own, (uint32_t)(kBlocks * boxes * 32 * 128));
+                        for (int j = 0; j < boxes; ++j)
+                            tma_load_2d<PAIR>(dst + j * 32 * 128, &map_x, bar, k * 64, row0 + 32 * j);
+                    }
+                }
+                __syncwarp();
+                it = __reduce_max_sync(0xffffffffu, it);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+        }
+    } else if (warp < 4 + kConvertWarps) {
+        regs_dec<80>();
+        const int half = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t to = tmem + ((uint32_t)quarter << 21) + C::kACols;  // 32 lanes << 16
+        for (uint32_t n = 0;; ++n) {
+            ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
+            if (!ok) break;
+            const int rows = info[n & 1].rows;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
+            if (rows == 0) break;
+            for (int kb = 0; kb < a.KB; ++kb, ++it) {
+                const uint32_t st = it % C::kLoads;
+                ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
+                if (!ok) break;
+                const uint8_t* src = loads + st * C::kLoadBytes;
+                uint4 w[C::kPlanes][4], x[XT == kInt8 ? C::kLoadRows / 32 : 1];
+#pragma unroll
+                for (int p = 0; p < C::kPlanes; ++p)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[p][j] = *reinterpret_cast<const uint4*>(src + p * kWBytes + row * 128 +
+                                                                  (((half * 4 + j) ^ (row & 7)) << 4));
+                if constexpr (XT == kInt8) {
+#pragma unroll
+                    for (int i = 0; i < C::kLoadRows / 32; ++i)
+                        if (32 * i < rows)
+                            x[i] = *reinterpret_cast<const uint4*>(src + C::kPlanes * kWBytes + (32 * i + lane) * 128 +
+                                                                   (((half * 4 + quarter) ^ (lane & 7)) << 4));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
+                const uint32_t k = 2 * it + half, s = k % C::kSteps;
+                ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((k / C::kSteps) & 1) ^ 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                if constexpr (XT == kInt8) {
+                    uint8_t* dst = rows16 + s * C::kStepBytes;
+#pragma unroll
+                    for (int i = 0; i < C::kLoadRows / 32; ++i) {
+                        if (32 * i >= rows) continue;
+                        uint4 u, v;
+                        widen4<false>(x[i].x, u.x, u.y);
+                        widen4<false>(x[i].y, u.z, u.w);
+                        widen4<false>(x[i].z, v.x, v.y);
+                        widen4<false>(x[i].w, v.z, v.w);
+                        uint8_t* line = dst + (32 * i + lane) * 128;
+                        *reinterpret_cast<uint4*>(line + (((2 * quarter) ^ (lane & 7)) << 4)) = u;
+                        *reinterpret_cast<uint4*>(line + (((2 * quarter + 1) ^ (lane & 7)) << 4)) = v;
+                    }
+                    smem_proxy_fence();
+                }
+#pragma unroll
+                for (int p = 0; p < C::kPlanes; ++p) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        widen4<XT == kBf16>(w[p][j].x, v[8 * j], v[8 * j + 1]);
+                        widen4<XT == kBf16>(w[p][j].y, v[8 * j + 2], v[8 * j + 3]);
+                        widen4<XT == kBf16>(w[p][j].z, v[8 * j + 4], v[8 * j + 5]);
+                        widen4<XT == kBf16>(w[p][j].w, v[8 * j + 6], v[8 * j + 7]);
+                    }
+                    tmem_st32(to + (s * C::kPlanes + p) * 32, v);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&a_full[s]), 0));
+                    else mbar_arrive(smem_u32(&a_full[s]));
+                }
+            }
+            if (!ok) break;
+        }
+    } else {
+        regs_inc<136>();
+        const int half = (warp - 4 - kConvertWarps) >> 2, quarter = warp & 3;
+        const uint32_t from = tmem + ((uint32_t)quarter << 21) + half * C::kHalf;
+        for (uint32_t n = 0;; ++n) {
+            ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
+            if (!ok) break;
+            tile = info[n & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
+            if (tile.rows == 0) break;
+            if (!MR_IN_RANGE(tile.expert, a.experts, 911)) tile.expert = 0;
+            const int col = tile.n0 + (int)rank * kWRows + quarter * 32 + lane;
+            const bool real = col < a.N;
+            const float* ws = a.w_scales + (int64_t)tile.expert * C::kPlanes * a.N + (real ? col : 0);
+            const float w0 = *ws, w1 = SWIGLU ? ws[a.N] : 0.0f;
+            const int mine = min(C::kHalf, tile.rows - half * C::kHalf);  // rows of this warp, may be none
+            int64_t row0 = (int64_t)tile.row0 + half * C::kHalf;
+            const bool inside = mine <= 0 || MR_IN_RANGE(row0 + mine - 1, a.rows, 912);
+            float xs[(C::kHalf + 31) / 32];  // lane i: those of rows i, 32 + i, ...
+#pragma unroll
+            for (int i = 0; i < (C::kHalf + 31) / 32; ++i)
+                xs[i] = a.x_scales && inside && 32 * i + lane < mine ? a.x_scales[(row0 + 32 * i + lane) * a.xs_row] : 1.0f;
+            const uint32_t buf = n % C::kSumBufs;
+            ok = mbar_wait<PAIR>(smem_u32(&t_full[buf]), (n / C::kSumBufs) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            constexpr int kLd = 16;
+            const bool wide = !SWIGLU && a.y_dtype == MR_DTYPE_F32;
+            const int elem = wide ? 4 : 2;
+            char* y = reinterpret_cast<char*>(a.y) + (row0 * a.y_stride + col) * elem;
+            const int64_t y_step = a.y_stride * elem;
+            uint32_t packed[C::kHalf / 2];
+#pragma unroll
+            for (int c = 0; c < C::kHalf; c += kLd) {
+                if (c >= mine) break;
+                uint32_t v[kLd], u[SWIGLU ? kLd : 1];
+                const uint32_t at = from + buf * C::kSumCols + c;
+                tmem_load(v, at);
+                if constexpr (SWIGLU) {
+                    tmem_load(u, at + C::kRows);
+                    tmem_ld_wait(u);
+                }
+                tmem_ld_wait(v);
+                float f[kLd];
+#pragma unroll
+                for (int j = 0; j < kLd; ++j) {
+                    const float s = __shfl_sync(0xffffffffu, xs[(c + j) / 32], (c + j) % 32);
+                    f[j] = __fmul_rn(__fmul_rn(__uint_as_float(v[j]), w0), s);
+                    if constexpr (SWIGLU) f[j] = silu(f[j]) * (__uint_as_float(u[j]) * w1 * s);
+                }
+                if (wide) {
+#pragma unroll
+                    for (int j = 0; j < kLd; ++j)
+                        if (real && inside && c + j < mine) *reinterpret_cast<float*>(y + (c + j) * y_step) = f[j];
+                }
+#pragma unroll
+                for (int j = 0; j < kLd; j += 2)
+                    packed[(c + j) / 2] = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], f[j + 1]);
+            }
+            // everything is in registers: hand the sums back before the stores
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&t_empty[buf]), 0));
+                else mbar_arrive(smem_u32(&t_empty[buf]));
+            }
+            if (!wide && real && inside) {
+#pragma unroll
+                for (int j = 0; j < C::kHalf; ++j) {
+                    if (j < mine) *reinterpret_cast<uint16_t*>(y) = (uint16_t)(packed[j / 2] >> (16 * (j & 1)));
+                    y += y_step;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (PAIR) cluster_sync();
+    if (abort_word) {  // let what is in flight land
+        if (warp == 0)
+            for (uint32_t k = it > C::kLoads ? it - C::kLoads : 0; k < it; ++k)
+                mbar_drain(smem_u32(&l_full[k % C::kLoads]), (k / C::kLoads) & 1);
+        if (XT != kInt8 && warp == 3 && rank == 0)
+            for (uint32_t k = it > C::kSteps ? it - C::kSteps : 0; k < it; ++k)
+                mbar_drain(smem_u32(&x_full[k % C::kSteps]), (k / C::kSteps) & 1);
+        if (warp == 1 && rank == 0) {
+            if (elect_one()) tc_commit<PAIR>(smem_u32(&drain_bar));
+            mbar_drain(smem_u32(&drain_bar), 0);
+        }
+        if (threadIdx.x == 0) atomicAdd(&g_waits_out, 1u);
+    }
+    tc_fence_before();
+    if (PAIR) cluster_sync();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free<PAIR>(tmem, 512);
+}
+
+// int8 rows to f16, whose sums the kernels above then take as they are: 16 values a thread.
+__global__ void __launch_bounds__(256)
+    widen_rows_kernel(const char* x, int64_t x_row, int64_t rows, int64_t K, const int64_t* num_rows, char* to,
+                      int64_t to_row, uint32_t chunks) {
+    pdl_enter();
+    if (num_rows) rows = max((int64_t)0, min(rows, *num_rows));
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / chunks, c = i - row * chunks;
+    if (row >= rows) return;
+    const char* p = x + row * x_row + c * 16;
+    uint4 w;
+    if (c * 16 + 16 <= K) {
+        w = ld_stream_v4(p);
+    } else {
+        uint32_t u[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (c * 16 + j < K) u[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
+        w = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    uint4 a, b;
+    widen4<false>(w.x, a.x, a.y);
+    widen4<false>(w.y, a.z, a.w);
+    widen4<false>(w.z, b.x, b.y);
+    widen4<false>(w.w, b.z, b.w);
+    uint4* q = reinterpret_cast<uint4*>(to + row * to_row + c * 32);
+    q[0] = a;
+    q[1] = b;
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+bool aligned16(const void* p) { return aligned(p, 16); }
+
+template <int XT, bool SWIGLU, bool PAIR>
+cudaError_t launch_int8(const CUtensorMap (&m)[2], const Int8Args& a, int64_t tiles, cudaStream_t s) {
+    auto kernel = int8_matmul_kernel<XT, SWIGLU, PAIR>;
+    constexpr int smem = Cfg<XT, SWIGLU, PAIR>::kSmem;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    // blocks (pairs) the device holds at once, found once per device
+    static std::atomic<int> resident[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    int n = resident[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return e;
+        n = device_sm_count();
+        if (PAIR) {
+            cfg.gridDim = dim3(n / 2 * 2);
+            if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+            if (n < 1) return cudaErrorInvalidConfiguration;
+            n = std::min(n, device_sm_count() / 2);
+        }
+        resident[dev].store(n, std::memory_order_release);
+    }
+    cfg.gridDim = dim3((unsigned)(tiles < n ? tiles : n) * (PAIR ? 2 : 1));
+    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], a);
+}
+
+// One product over the groups. x: rows of type xt; w: int8 [experts][N][K], or [experts][2][N][K]
+// for the network's first product (swiglu).
+struct Product {
+    const void* x;
+    int64_t x_stride;          // bytes
+    int xt;
+    const void* w;
+    int64_t w_row, w_matrix;   // byte strides of a row and of a matrix [N, K]
+    int64_t K;
+    bool swiglu;
+};
+
+bool use_pairs(int64_t rows, int64_t G) { return rows > 64 * std::min<int64_t>(G, rows); }
+
+mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
+    const int tile_m = pair ? (p.swiglu ? 128 : 256) : 64;
+    const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G - 1, a.rows);  // or fewer
+    a.n_tiles = ceil_div(a.N, pair ? 2 * kWRows : kWRows);
+    a.KB = ceil_div(p.K, 128);
+    const int64_t tiles = m_tiles * a.n_tiles;
+    if (tiles > INT32_MAX) return MR_ERR_PARAM_INVALID;
+    CUtensorMap m[2];
+    const bool eight = p.xt == kInt8;
+    const uint64_t xd[2] = {(uint64_t)p.K, (uint64_t)a.rows}, xs[1] = {(uint64_t)p.x_stride};
+    const uint32_t xb[2] = {eight ? 128u : 64u, 32};
+    const uint64_t wd[3] = {(uint64_t)p.K, (uint64_t)a.N, (uint64_t)a.experts * (p.swiglu ? 2 : 1)};
+    const uint64_t ws[2] = {(uint64_t)p.w_row, (uint64_t)p.w_matrix};
+    const uint32_t wb[3] = {128, (uint32_t)kWRows, 1};
+    if (!make_tensor_map(&m[0], eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, eight ? 1 : 2, p.x, 2,
+                         xd, xs, xb) ||
+        !make_tensor_map(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, 3, wd, ws, wb))
+        return MR_ERR_CUDA;
+    cudaError_t e;
+    if (pair) {
+        if (p.swiglu) e = p.xt == kBf16 ? launch_int8<kBf16, true, true>(m, a, tiles, s)
+                                        : launch_int8<kF16, true, true>(m, a, tiles, s);
+        else e = p.xt == kBf16 ? launch_int8<kBf16, false, true>(m, a, tiles, s)
+                               : launch_int8<kF16, false, true>(m, a, tiles, s);
+    } else if (p.swiglu) {
+        e = p.xt == kBf16  ? launch_int8<kBf16, true, false>(m, a, tiles, s)
+            : p.xt == kF16 ? launch_int8<kF16, true, false>(m, a, tiles, s)
+                           : launch_int8<kInt8, true, false>(m, a, tiles, s);
+    } else {
+        e = p.xt == kBf16  ? launch_int8<kBf16, false, false>(m, a, tiles, s)
+            : p.xt == kF16 ? launch_int8<kF16, false, false>(m, a, tiles, s)
+                           : launch_int8<kInt8, false, false>(m, a, tiles, s);
+    }
+    return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+}
+
+bool row_type(int32_t dt) { return dt == MR_DTYPE_INT8 || dt == MR_DTYPE_F16 || dt == MR_DTYPE_BF16; }
+bool out_type(int32_t dt) { return dt == MR_DTYPE_F16 || dt == MR_DTYPE_BF16 || dt == MR_DTYPE_F32; }
+
+bool common_sizes(int64_t rows, int64_t experts, int64_t numGroups, int64_t a, int64_t b) {
+    return rows >= 0 && rows <= MR_MAX_EXPERT_ROWS && experts >= 1 && experts <= MR_MAX_EXPERT_NUM &&
+           numGroups >= -1 && numGroups <= MR_MAX_EXPERT_ROWS && a >= 1 && a <= MR_MAX_EXPERT_COLS && b >= 1 &&
+           b <= MR_MAX_EXPERT_COLS;
+}
+
+// 16-bit rows [rows, cols] in the workspace.
+int64_t wide_stride(int64_t cols) { return (int64_t)align_up((uint64_t)cols, 64) * 2; }
+uint64_t wide_bytes(int64_t rows, int64_t cols) { return align_up((uint64_t)rows * wide_stride(cols), 256); }
+
+// x as the product takes it: int8 rows in front of a kernel of pairs become 16-bit rows in `room`.
+cudaError_t prepare_rows(Product& p, const Int8Args& a, bool pair, const int64_t* numRows, void* room, cudaStream_t s) {
+    if (!pair || p.xt != kInt8) return cudaSuccess;
+    const uint32_t chunks = (uint32_t)((p.K + 15) / 16);
+    const int64_t total = (int64_t)a.rows * chunks;
+    cudaError_t e = launch_pdl(widen_rows_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s,
+                               reinterpret_cast<const char*>(p.x), p.x_stride, (int64_t)a.rows, p.K, numRows,
+                               reinterpret_cast<char*>(room), wide_stride(p.K), chunks);
+    p.x = room;
+    p.x_stride = wide_stride(p.K);
+    p.xt = kF16;
+    return e;
+}
+
+// Checks that both products make of their weights; wr, wm: byte strides.
+bool weight_strides(const int64_t* strides, int64_t matrices, int64_t N, int64_t K, int64_t* wr, int64_t* wm) {
+    const int64_t top = INT64_C(1) << 40;
+    *wr = K, *wm = N * K;
+    if (strides) *wr = strides[0], *wm = strides[1];
+    *wr = stride_of(N, *wr, K);
+    *wm = stride_of(matrices, *wm, N * *wr);
+    return *wr >= K && *wr % 16 == 0 && *wm % 16 == 0 && *wr <= top && *wm <= top &&
+           (matrices == 1 || *wm >= (N - 1) * *wr + K);
+}
+
+}  // namespace
+
+MR_CHECK_ACCESSOR(int8_matmul)
+
+cudaError_t waits_out_int8_matmul(unsigned* out, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_waits_out, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0u;
+        e = cudaMemcpyToSymbol(g_waits_out, &zero, sizeof(zero));
+    }
+    return e;
+}
+
+}  // namespace mr
+
+using namespace mr;
+
+extern "C" mr_status moe_grouped_matmul_int8_get_workspace_size(int64_t rows, int64_t cols, int32_t xDtype,
+                                                                uint64_t* workspaceSize) {
+    if (!row_type(xDtype) || !common_sizes(rows, 1, 0, cols, 1)) return MR_ERR_PARAM_INVALID;
+    if (!workspaceSize) return MR_ERR_PARAM_NULLPTR;
+    *workspaceSize = xDtype == MR_DTYPE_INT8 ? wide_bytes(rows, cols) : 0;
+    return MR_OK;
+}
+
+extern "C" mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int64_t xStride, const float* xScales,
+                                             int64_t xScaleStride, const void* weights, const int64_t* weightStrides,
+                                             const float* weightScales, const int64_t* groupList, int64_t numGroups,
+                                             const int64_t* numRows, int64_t expertBase, int64_t rows, int64_t experts,
+                                             int64_t outCols, int64_t cols, void* y, int32_t yDtype, int64_t yStride,
+                                             void* workspace, uint64_t workspaceSize, void* stream) {
+    const bool eight = xDtype == MR_DTYPE_INT8;
+    const int64_t top = INT64_C(1) << 40, elem = eight ? 1 : 2;
+    if (!row_type(xDtype) || !out_type(yDtype)) return MR_ERR_PARAM_INVALID;
+    if (!common_sizes(rows, experts, numGroups, outCols, cols)) return MR_ERR_PARAM_INVALID;
+    if (!groupList && numGroups > 0) return MR_ERR_PARAM_NULLPTR;
+    if (xStride < 0 || xStride > top || yStride < outCols || yStride > top) return MR_ERR_PARAM_INVALID;
+    xStride = stride_of(rows, xStride * elem, cols * elem);
+    if (xStride < cols * elem || xStride % 16) return MR_ERR_PARAM_INVALID;
+    int64_t wr, wm;
+    if (!weight_strides(weightStrides, experts, outCols, cols, &wr, &wm)) return MR_ERR_PARAM_INVALID;
+    if (xScales && (xScaleStride < 0 || xScaleStride > top)) return MR_ERR_PARAM_INVALID;
+    if (rows == 0) return MR_OK;
+    if (!x || !weights || !weightScales || !y || (eight && (!xScales || !workspace))) return MR_ERR_PARAM_NULLPTR;
+    if (eight && workspaceSize < wide_bytes(rows, cols)) return MR_ERR_WORKSPACE;
+    if (!aligned16(weights) || !aligned16(x) || (numGroups > 0 && !aligned16(groupList)) ||
+        (eight && !aligned(workspace, 256)) || !aligned(y, yDtype == MR_DTYPE_F32 ? 4 : 2) || !aligned(xScales, 4) ||
+        !aligned(weightScales, 4) || !aligned(numRows, 8))
+        return MR_ERR_PARAM_INVALID;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Int8Args a{};
+    a.groups = numGroups < 0 ? nullptr : groupList;
+    a.G = numGroups < 0 ? 1 : (int)numGroups;
+    a.rows = (int)rows;
+    a.experts = (int)experts;
+    a.expert_base = expertBase;
+    if (a.G == 0) return MR_OK;
+    a.x_scales = xScales;
+    a.xs_row = xScaleStride;
+    a.w_scales = weightScales;
+    a.N = (int)outCols;
+    a.y = y;
+    a.y_stride = yStride;
+    a.y_dtype = yDtype;
+    Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, weights, wr, wm, cols, false};
+    const bool pair = use_pairs(rows, a.G);
+    MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, workspace, s));
+    return run_product(p, a, pair, s);
+}
+
+extern "C" mr_status moe_expert_ffn_int8_get_workspace_size(int64_t rows, int64_t hidden, int64_t inter,
+                                                            int32_t xDtype, uint64_t* workspaceSize) {
+    if (!row_type(xDtype) || !common_sizes(rows, 1, 0, hidden, inter)) return MR_ERR_PARAM_INVALID;
+    if (!workspaceSize) return MR_ERR_PARAM_NULLPTR;
+    *workspaceSize = (xDtype == MR_DTYPE_INT8 ? wide_bytes(rows, hidden) : 0) + wide_bytes(rows, inter);
+    return MR_OK;
+}
+
+extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t xStride, const float* xScales,
+                                         int64_t xScaleStride, const void* w13, const int64_t* w13Strides,
+                                         const float* w13Scales, const void* w2, const int64_t* w2Strides,
+                                         const float* w2Scales, const int64_t* groupList, int64_t numGroups,
+                                         const int64_t* numRows, int64_t expertBase, int64_t rows, int64_t experts,
+                                         int64_t hidden, int64_t inter, void* y, int32_t yDtype, int64_t yStride,
+                                         void* workspace, uint64_t workspaceSize, void* stream) {
+    const bool eight = xDtype == MR_DTYPE_INT8;
+    const int64_t top = INT64_C(1) << 40, elem = eight ? 1 : 2;
+    if (!row_type(xDtype) || !out_type(yDtype)) return MR_ERR_PARAM_INVALID;
+    if (!common_sizes(rows, experts, numGroups, hidden, inter)) return MR_ERR_PARAM_INVALID;
+    if (!groupList && numGroups > 0) return MR_ERR_PARAM_NULLPTR;
+    if (xStride < 0 || xStride > top || yStride < hidden || yStride > top) return MR_ERR_PARAM_INVALID;
+    xStride = stride_of(rows, xStride * elem, hidden * elem);
+    if (xStride < hidden * elem || xStride % 16) return MR_ERR_PARAM_INVALID;
+    int64_t ar, am, br, bm;
+    if (!weight_strides(w13Strides, 2 * experts, inter, hidden, &ar, &am) ||
+        !weight_strides(w2Strides, experts, hidden, inter, &br, &bm))
+        return MR_ERR_PARAM_INVALID;
+    if (xScales && (xScaleStride < 0 || xScaleStride > top)) return MR_ERR_PARAM_INVALID;
+    if (rows == 0) return MR_OK;
+    if (!x || !w13 || !w13Scales || !w2 || !w2Scales || !y || !workspace || (eight && !xScales))
+        return MR_ERR_PARAM_NULLPTR;
+    const uint64_t x_bytes = eight ? wide_bytes(rows, hidden) : 0;
+    if (workspaceSize < x_bytes + wide_bytes(rows, inter)) return MR_ERR_WORKSPACE;
+    if (!aligned16(w13) || !aligned16(w2) || !aligned16(x) || (numGroups > 0 && !aligned16(groupList)) ||
+        !aligned(workspace, 256) || !aligned(y, yDtype == MR_DTYPE_F32 ? 4 : 2) || !aligned(xScales, 4) ||
+        !aligned(w13Scales, 4) || !aligned(w2Scales, 4) || !aligned(numRows, 8))
+        return MR_ERR_PARAM_INVALID;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Int8Args a{};
+    a.groups = numGroups < 0 ? nullptr : groupList;
+    a.G = numGroups < 0 ? 1 : (int)numGroups;
+    a.rows = (int)rows;
+    a.experts = (int)experts;
+    a.expert_base = expertBase;
+    if (a.G == 0) return MR_OK;
+    char* h = reinterpret_cast<char*>(workspace) + x_bytes;
+    a.x_scales = xScales;
+    a.xs_row = xScaleStride;
+    a.w_scales = w13Scales;
+    a.N = (int)inter;
+    a.y = h;
+    a.y_stride = wide_stride(inter) / 2;
+    a.y_dtype = MR_DTYPE_BF16;
+    const bool pair = use_pairs(rows, a.G);
+    Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, w13, ar, am, hidden, true};
+    MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, workspace, s));
+    mr_status st = run_product(p, a, pair, s);
+    if (st != MR_OK) return st;
+
+    p = Product{h, wide_stride(inter), kBf16, w2, br, bm, inter, false};
+    a.x_scales = nullptr;
+    a.w_scales = w2Scales;
+    a.N = (int)hidden;
+    a.y = y;
+    a.y_stride = yStride;
+    a.y_dtype = yDtype;
+    return run_product(p, a, pair, s);
+}

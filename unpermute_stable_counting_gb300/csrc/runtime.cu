@@ -88,6 +88,7 @@ namespace mr {
 cudaError_t mr_check_words_batching(unsigned* out, bool reset);
 cudaError_t mr_check_words_context(unsigned* out, bool reset);
 cudaError_t mr_check_words_grouped_matmul(unsigned* out, bool reset);
+cudaError_t mr_check_words_int8_matmul(unsigned* out, bool reset);
 cudaError_t mr_check_words_layer(unsigned* out, bool reset);
 cudaError_t mr_check_words_norm_bf16(unsigned* out, bool reset);
 cudaError_t mr_check_words_norm_f16(unsigned* out, bool reset);
@@ -103,7 +104,8 @@ extern "C" mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, 
 #ifdef MR_CHECKED
     if (!failures) return MR_ERR_PARAM_NULLPTR;
     cudaError_t (*readers[])(unsigned*, bool) = {mr::mr_check_words_batching, mr::mr_check_words_context,
-                                                 mr::mr_check_words_grouped_matmul, mr::mr_check_words_layer,
+                                                 mr::mr_check_words_grouped_matmul, mr::mr_check_words_int8_matmul,
+                                                 mr::mr_check_words_layer,
                                                  mr::mr_check_words_norm_bf16, mr::mr_check_words_norm_f16,
                                                  mr::mr_check_words_norm_f32,
                                                  mr::mr_check_words_permute, mr::mr_check_words_quantize,
@@ -128,12 +130,14 @@ extern "C" mr_status mr_checked_errors(uint32_t* failures, uint32_t* firstSite, 
 
 namespace mr {
 cudaError_t waits_out_grouped_matmul(unsigned* out, bool reset);
+cudaError_t waits_out_int8_matmul(unsigned* out, bool reset);
 cudaError_t waits_out_layer(unsigned* out, bool reset);
 }  // namespace mr
 
 extern "C" mr_status mr_waits_out(uint32_t* count, int32_t reset) {
     if (!count) return MR_ERR_PARAM_NULLPTR;
-    cudaError_t (*readers[])(unsigned*, bool) = {mr::waits_out_grouped_matmul, mr::waits_out_layer};
+    cudaError_t (*readers[])(unsigned*, bool) = {mr::waits_out_grouped_matmul, mr::waits_out_int8_matmul,
+                                                 mr::waits_out_layer};
     *count = 0u;
     // the copies below are in the legacy default stream's order, which streams that do not block it are not in
     MR_TRY_CUDA(cudaDeviceSynchronize());
