@@ -16,9 +16,9 @@
 //   warp 1       matrix instructions, 64 values of k a step
 //   warp 2       hands tiles to the warps below
 //   warp 3       TMA loads of 16-bit rows: a ring of 64 values of k
-//   warps 4-11   weights (and int8 rows) to 16 bits; each warpgroup has one half of a
-//                load's 128 values
-//   warps 12-19  results: scales, rounding, stores
+//   warps 4-11   weights to 16 bits; each warpgroup has one half of a load's 128 values
+//   warps 12-15  int8 rows to 16 bits (single blocks), or results
+//   warps 16-19  results: scales, rounding, stores
 // One persistent block per SM takes tiles round robin; a pair of blocks shares a tile
 // of 256 channels, where each converts its own 128 and loads half of the rows.
 #include "groups.cuh"
@@ -33,7 +33,7 @@ namespace {
 
 __device__ unsigned g_waits_out;  // blocks that left early, see mbar_wait
 
-constexpr int kThreads = 640, kConvertWarps = 8, kSumWarps = 8;
+constexpr int kThreads = 640, kConvertWarps = 8;
 constexpr int kWRows = 128, kWBytes = kWRows * 128;  // a load: 128 channels x 128 values
 
 struct Int8Args : Groups {
@@ -52,19 +52,26 @@ enum { kInt8 = 0, kF16 = 1, kBf16 = 2 };  // rows
 // factor are two planes of instructions with sums side by side.
 template <int XT, bool SWIGLU, bool PAIR> struct Cfg {
     static constexpr int kPlanes = SWIGLU ? 2 : 1;
-    static constexpr int kRows = PAIR ? (SWIGLU ? 128 : 256) : 64;  // rows of a tile
+    static constexpr int kRows = PAIR ? (SWIGLU ? 128 : 256) : 32;  // rows of a tile
     static constexpr int kLoadRows = PAIR ? kRows / 2 : kRows;      // of them, those this block loads
     static constexpr int kGrain = PAIR ? 64 : 16;                   // columns of an instruction are a multiple of this
-    static constexpr int kSteps = PAIR ? (SWIGLU ? 4 : 6) : 4;      // steps of converted weights (and 16-bit rows) held
+    // A step is 64 values of k, of single blocks 128: there the instructions are short, and what a step costs the
+    // thread that issues them (two waits and a commit) is what counts
+    static constexpr int kParts = PAIR ? 1 : 2;                     // of 64 values
+    // steps of converted weights and 16-bit rows held (16-bit rows come from L2 only when a step is free)
+    static constexpr int kSteps = PAIR ? (SWIGLU ? 4 : 6) : SWIGLU ? 3 : XT == kInt8 ? 4 : 6;
+    // warps of int8 rows, of results
+    static constexpr int kRowWarps = XT == kInt8 ? 4 : 0, kSumWarps = PAIR ? 8 : 4;
     static constexpr int kSumBufs = PAIR ? 1 : 2;
     static constexpr int kSumCols = kPlanes * kRows;
-    static constexpr int kACols = 256;                              // tensor memory: sums, then weights
-    static_assert(kSumCols * kSumBufs <= kACols && kSteps * 32 * kPlanes <= 256, "tensor memory");
-    static constexpr int kLoads = PAIR ? (SWIGLU ? 5 : 7) : XT == kInt8 ? (SWIGLU ? 4 : 7) : (SWIGLU ? 5 : 10);
+    static constexpr int kStepCols = 32 * kPlanes * kParts;         // tensor memory of a step's weights
+    static constexpr int kACols = kSumCols * kSumBufs;              // tensor memory: sums, then weights
+    static_assert(kACols + kSteps * kStepCols <= 512, "tensor memory");
+    static constexpr int kLoads = PAIR ? (SWIGLU ? 5 : 7) : XT == kInt8 ? (SWIGLU ? 5 : 9) : (SWIGLU ? 6 : 10);
     static constexpr int kLoadBytes = kPlanes * kWBytes + (XT == kInt8 ? kLoadRows * 128 : 0);
-    static constexpr int kStepBytes = kLoadRows * 128;
+    static constexpr int kPartBytes = kLoadRows * 128, kStepBytes = kPartBytes * kParts;
     static constexpr int kSmem = 1024 + kLoads * kLoadBytes + kSteps * kStepBytes;
-    static constexpr int kHalf = kRows / 2;                         // rows of a warpgroup of results
+    static constexpr int kHalf = PAIR ? kRows / 2 : kRows;          // rows of a warpgroup of results
 };
 
 // Matrix instruction with A in tensor memory.
@@ -149,17 +156,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kLoads; ++i)
-            mbar_init(smem_u32(&l_full[i]), 1), mbar_init(smem_u32(&l_empty[i]), kConvertWarps);
+            mbar_init(smem_u32(&l_full[i]), 1), mbar_init(smem_u32(&l_empty[i]), kConvertWarps + C::kRowWarps);
         for (int i = 0; i < C::kSteps; ++i) {
             mbar_init(smem_u32(&x_full[i]), 1);
-            mbar_init(smem_u32(&a_full[i]), kBlocks * kConvertWarps / 2);
+            mbar_init(smem_u32(&a_full[i]), kBlocks * kConvertWarps * C::kParts / 2 + C::kRowWarps);
             mbar_init(smem_u32(&a_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&t_full[i]), 1);
-            mbar_init(smem_u32(&t_empty[i]), kBlocks * kSumWarps);
+            mbar_init(smem_u32(&t_empty[i]), kBlocks * C::kSumWarps);
             mbar_init(smem_u32(&i_full[i]), 1);
-            mbar_init(smem_u32(&i_empty[i]), kConvertWarps + kSumWarps);
+            mbar_init(smem_u32(&i_empty[i]), kConvertWarps + C::kRowWarps + C::kSumWarps);
         }
         mbar_init(smem_u32(&drain_bar), 1);
         abort_word = 0u;
@@ -181,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tile tile;
     uint32_t it = 0;  // loads or steps that this warp has taken, over all of its tiles
     bool ok = true;
+    const int steps = 2 / C::kParts * a.KB;
     // columns of a tile's instructions, and boxes of 32 rows that this block loads
     auto columns = [&](int rows) { return (rows + C::kGrain - 1) / C::kGrain * C::kGrain; };
     auto boxes_of = [&](int rows) { return (columns(rows) / kBlocks + 31) / 32; };
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
                     ok = mbar_wait<PAIR>(smem_u32(&t_empty[buf]), ((n / C::kSumBufs) & 1) ^ 1, abort);
                     const uint32_t d = tmem + buf * C::kSumCols;
-                    for (int k = 0; ok && k < 2 * a.KB; ++k, ++it) {
+                    for (int k = 0; ok && k < steps; ++k, ++it) {
                         const uint32_t s = it % C::kSteps, parity = (it / C::kSteps) & 1;
                         ok = mbar_wait<PAIR>(smem_u32(&a_full[s]), parity, abort);
                         if (XT != kInt8) ok = ok && mbar_wait<PAIR>(smem_u32(&x_full[s]), parity, abort);
@@ -232,9 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int p = 0; p < C::kPlanes; ++p)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                mma_16_tmem<PAIR>(d + p * C::kRows, tmem + C::kACols + (s * C::kPlanes + p) * 32 + 8 * j,
-                                                  b + 2 * j, idesc, k > 0 || j > 0);
+                            for (int j = 0; j < 4 * C::kParts; ++j)
+                                mma_16_tmem<PAIR>(d + p * C::kRows,
+                                                  tmem + C::kACols + s * C::kStepCols + p * 32 * C::kParts + 8 * j,
+                                                  b + j / 4 * (C::kPartBytes / 16) + 2 * (j % 4), idesc, k > 0 || j > 0);
                         tc_commit<PAIR>(smem_u32(&a_empty[s]));
                     }
                     if (ok) tc_commit<PAIR>(smem_u32(&t_full[buf]));
@@ -263,15 +272,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int boxes = boxes_of(tile.rows);
                 const int row0 = tile.row0 + (int)rank * columns(tile.rows) / 2;
                 if (elect_one()) {
-                    for (int k = 0; k < 2 * a.KB; ++k, ++it) {
+                    for (int k = 0; k < steps; ++k, ++it) {
                         const uint32_t s = it % C::kSteps;
                         ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
                         if (!ok) break;
                         const uint32_t own = smem_u32(&x_full[s]), bar = PAIR ? map_cluster(own, 0) : own;
                         const uint32_t dst = smem_u32(rows16 + s * C::kStepBytes);
-                        if (rank == 0) mbar_expect(own, (uint32_t)(kBlocks * boxes * 32 * 128));
-                        for (int j = 0; j < boxes; ++j)
-                            tma_load_2d<PAIR>(dst + j * 32 * 128, &map_x, bar, k * 64, row0 + 32 * j);
+                        if (rank == 0) mbar_expect(own, (uint32_t)(kBlocks * C::kParts * boxes * 32 * 128));
+#pragma unroll
+                        for (int h = 0; h < C::kParts; ++h)
+                            for (int j = 0; j < boxes; ++j)
+                                tma_load_2d<PAIR>(dst + h * C::kPartBytes + j * 32 * 128, &map_x, bar,
+                                                  (k * C::kParts + h) * 64, row0 + 32 * j);
                     }
                 }
                 __syncwarp();
@@ -283,6 +295,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<80>();
         const int half = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t to = tmem + ((uint32_t)quarter << 21) + C::kACols;  // 32 lanes << 16
+        int pending = -1;  // step whose stores are on their way
+        auto hand_over = [&] {
+            if (pending < 0) return;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&a_full[pending]), 0));
+                else mbar_arrive(smem_u32(&a_full[pending]));
+            }
+            pending = -1;
+        };
         for (uint32_t n = 0;; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
             if (!ok) break;
@@ -294,43 +318,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t st = it % C::kLoads;
                 ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
                 if (!ok) break;
-                const uint8_t* src = loads + st * C::kLoadBytes;
-                uint4 w[C::kPlanes][4], x[XT == kInt8 ? C::kLoadRows / 32 : 1];
+                const uint8_t* src = loads + st * C::kLoadBytes + row * 128;
+                uint4 w[C::kPlanes][4];
 #pragma unroll
                 for (int p = 0; p < C::kPlanes; ++p)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        w[p][j] = *reinterpret_cast<const uint4*>(src + p * kWBytes + row * 128 +
-                                                                  (((half * 4 + j) ^ (row & 7)) << 4));
-                if constexpr (XT == kInt8) {
-#pragma unroll
-                    for (int i = 0; i < C::kLoadRows / 32; ++i)
-                        if (32 * i < rows)
-                            x[i] = *reinterpret_cast<const uint4*>(src + C::kPlanes * kWBytes + (32 * i + lane) * 128 +
-                                                                   (((half * 4 + quarter) ^ (lane & 7)) << 4));
-                }
+                        w[p][j] = *reinterpret_cast<const uint4*>(src + p * kWBytes + (((half * 4 + j) ^ (row & 7)) << 4));
+                hand_over();  // while these loads are on their way
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
-                const uint32_t k = 2 * it + half, s = k % C::kSteps;
+                const uint32_t k = C::kParts == 2 ? it : 2 * it + half, s = k % C::kSteps;
                 ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((k / C::kSteps) & 1) ^ 1, abort);
                 if (!ok) break;
                 tc_fence_after();
-                if constexpr (XT == kInt8) {
-                    uint8_t* dst = rows16 + s * C::kStepBytes;
-#pragma unroll
-                    for (int i = 0; i < C::kLoadRows / 32; ++i) {
-                        if (32 * i >= rows) continue;
-                        uint4 u, v;
-                        widen4<false>(x[i].x, u.x, u.y);
-                        widen4<false>(x[i].y, u.z, u.w);
-                        widen4<false>(x[i].z, v.x, v.y);
-                        widen4<false>(x[i].w, v.z, v.w);
-                        uint8_t* line = dst + (32 * i + lane) * 128;
-                        *reinterpret_cast<uint4*>(line + (((2 * quarter) ^ (lane & 7)) << 4)) = u;
-                        *reinterpret_cast<uint4*>(line + (((2 * quarter + 1) ^ (lane & 7)) << 4)) = v;
-                    }
-                    smem_proxy_fence();
-                }
 #pragma unroll
                 for (int p = 0; p < C::kPlanes; ++p) {
                     uint32_t v[32];
@@ -341,21 +342,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                         widen4<XT == kBf16>(w[p][j].z, v[8 * j + 4], v[8 * j + 5]);
                         widen4<XT == kBf16>(w[p][j].w, v[8 * j + 6], v[8 * j + 7]);
                     }
-                    tmem_st32(to + (s * C::kPlanes + p) * 32, v);
+                    tmem_st32(to + s * C::kStepCols + (p * C::kParts + (C::kParts == 2 ? half : 0)) * 32, v);
                 }
-                tmem_st_wait();
-                tc_fence_before();
+                pending = (int)s;
+            }
+            if (!ok) break;
+            hand_over();
+        }
+    } else if (warp < 4 + kConvertWarps + C::kRowWarps) {
+        regs_dec<80>();
+        const int quarter = warp & 3;  // of the pieces of a row's 64 values
+        for (uint32_t n = 0;; ++n) {
+            ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
+            if (!ok) break;
+            const int rows = info[n & 1].rows;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
+            if (rows == 0) break;
+            for (int kb = 0; kb < a.KB; ++kb, ++it) {
+                const uint32_t st = it % C::kLoads;
+                ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
+                if (!ok) break;
+                const uint8_t* src = loads + st * C::kLoadBytes + C::kPlanes * kWBytes + lane * 128;
+                uint4 x[2][C::kLoadRows / 32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < C::kLoadRows / 32; ++i)
+                        if (32 * i < rows)
+                            x[h][i] = *reinterpret_cast<const uint4*>(src + 32 * i * 128 + (((h * 4 + quarter) ^ (lane & 7)) << 4));
                 __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&a_full[s]), 0));
-                    else mbar_arrive(smem_u32(&a_full[s]));
+                if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
+                const uint32_t s = it % C::kSteps;
+                ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
+                if (!ok) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint8_t* dst = rows16 + s * C::kStepBytes + h * C::kPartBytes + lane * 128;
+#pragma unroll
+                    for (int i = 0; i < C::kLoadRows / 32; ++i) {
+                        if (32 * i >= rows) continue;
+                        uint4 u, v;
+                        widen4<false>(x[h][i].x, u.x, u.y);
+                        widen4<false>(x[h][i].y, u.z, u.w);
+                        widen4<false>(x[h][i].z, v.x, v.y);
+                        widen4<false>(x[h][i].w, v.z, v.w);
+                        uint8_t* line = dst + 32 * i * 128;
+                        *reinterpret_cast<uint4*>(line + (((2 * quarter) ^ (lane & 7)) << 4)) = u;
+                        *reinterpret_cast<uint4*>(line + (((2 * quarter + 1) ^ (lane & 7)) << 4)) = v;
+                    }
                 }
+                smem_proxy_fence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&a_full[s]));
             }
             if (!ok) break;
         }
-    } else {
+    } else if (warp >= 4 + kConvertWarps + 8 - C::kSumWarps) {
         regs_inc<136>();
-        const int half = (warp - 4 - kConvertWarps) >> 2, quarter = warp & 3;
+        const int half = PAIR ? (warp - 4 - kConvertWarps) >> 2 : 0, quarter = warp & 3;
         const uint32_t from = tmem + ((uint32_t)quarter << 21) + half * C::kHalf;
         for (uint32_t n = 0;; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
@@ -533,10 +578,10 @@ struct Product {
     bool swiglu;
 };
 
-bool use_pairs(int64_t rows, int64_t G) { return rows > 64 * std::min<int64_t>(G, rows); }
+bool use_pairs(int64_t rows, int64_t G) { return rows > 32 * std::min<int64_t>(G, rows); }
 
 mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
-    const int tile_m = pair ? (p.swiglu ? 128 : 256) : 64;
+    const int tile_m = pair ? (p.swiglu ? 128 : 256) : 32;
     const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G - 1, a.rows);  // or fewer
     a.n_tiles = ceil_div(a.N, pair ? 2 * kWRows : kWRows);
     a.KB = ceil_div(p.K, 128);
