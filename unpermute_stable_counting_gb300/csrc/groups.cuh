@@ -17,8 +17,9 @@ struct Tile {
 };
 
 // Walks the group list in tiles of TM rows. Every lane of the warp calls next()
-// with the same t, ascending over the calls.
-template <int TM> struct Walk {
+// with the same t, ascending over the calls. EVEN: a group's tiles have as many rows
+// each, to a multiple of 16, as its last one allows, so that tiles cost about the same.
+template <int TM, bool EVEN = false> struct Walk {
     int first, base_tile, total;      // window of 32 groups; tiles before it, tiles in it
     uint32_t base_row, window_rows;   // rows before it, rows in it
     int expert, count, row0, tiles;   // this lane's group
@@ -105,8 +106,9 @@ template <int TM> struct Walk {
         const int j = i - band * 8 * a.n_tiles;
         const int n = j / bm, m = 8 * band + j - n * bm;
         out.expert = __shfl_sync(0xffffffffu, expert, src);
-        out.row0 = __shfl_sync(0xffffffffu, row0, src) + m * TM;
-        out.rows = min(c - m * TM, TM);
+        const int rows = EVEN ? ((c + mt - 1) / mt + 15) / 16 * 16 : TM;
+        out.row0 = __shfl_sync(0xffffffffu, row0, src) + m * rows;
+        out.rows = min(c - m * rows, rows);
         out.n0 = n * bn;
         return true;
     }

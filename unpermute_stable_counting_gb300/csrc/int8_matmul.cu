@@ -13,9 +13,9 @@
 // store nor the instructions' reads. The rows of a group are the other operand (B):
 // an instruction has as many columns as the group has rows left, to the next 16.
 //   warp 0       TMA loads of the weights (and of int8 rows): a ring of 128 values of k
-//   warp 1       matrix instructions, 64 values of k a step
+//   warp 1       matrix instructions, 128 values of k a step
 //   warp 2       hands tiles to the warps below
-//   warp 3       TMA loads of 16-bit rows: a ring of 64 values of k
+//   warp 3       TMA loads of 16-bit rows: a ring of steps
 //   warps 4-11   weights to 16 bits; each warpgroup has one half of a load's 128 values
 //   warps 12-15  int8 rows to 16 bits (single blocks), or results
 //   warps 16-19  results: scales, rounding, stores
@@ -48,30 +48,30 @@ struct Int8Args : Groups {
 
 enum { kInt8 = 0, kF16 = 1, kBf16 = 2 };  // rows
 
-// XT: the rows' type. SWIGLU: the network's first product, whose gate and other
-// factor are two planes of instructions with sums side by side.
+// XT: the rows' type. SWIGLU: the network's first product; the upper half of a block's
+// 128 channels are the gate's, the lower half the same ones of the other factor.
 template <int XT, bool SWIGLU, bool PAIR> struct Cfg {
-    static constexpr int kPlanes = SWIGLU ? 2 : 1;
-    static constexpr int kRows = PAIR ? (SWIGLU ? 128 : 256) : 32;  // rows of a tile
-    static constexpr int kLoadRows = PAIR ? kRows / 2 : kRows;      // of them, those this block loads
-    static constexpr int kGrain = PAIR ? 64 : 16;                   // columns of an instruction are a multiple of this
-    // A step is 64 values of k, of single blocks 128: there the instructions are short, and what a step costs the
-    // thread that issues them (two waits and a commit) is what counts
-    static constexpr int kParts = PAIR ? 1 : 2;                     // of 64 values
-    // steps of converted weights and 16-bit rows held (16-bit rows come from L2 only when a step is free)
-    static constexpr int kSteps = PAIR ? (SWIGLU ? 4 : 6) : SWIGLU ? 3 : XT == kInt8 ? 4 : 6;
+    static constexpr int kRows = PAIR ? 256 : 32;                   // rows of a tile
+    static constexpr int kChannels = (PAIR ? 2 : 1) * (SWIGLU ? 64 : 128);
+    static constexpr int kLoadRows = PAIR ? kRows / 2 : kRows;      // of the rows, those this block loads
+    static constexpr int kBox = PAIR ? 64 : 32;                     // rows of a TMA load
+    // Steps of converted weights and of 16-bit rows held. (A step of 64 values costs the thread that issues the
+    // instructions its two waits and a commit twice: 16384 x 7168 x 7168 took 884 instead of 848 us, and 576 rows
+    // over 64 experts, 7168 -> 4096, 393 instead of 345.)
+    static constexpr int kSteps = PAIR ? 3 : XT == kInt8 ? 4 : 6;
     // warps of int8 rows, of results
     static constexpr int kRowWarps = XT == kInt8 ? 4 : 0, kSumWarps = PAIR ? 8 : 4;
     static constexpr int kSumBufs = PAIR ? 1 : 2;
-    static constexpr int kSumCols = kPlanes * kRows;
-    static constexpr int kStepCols = 32 * kPlanes * kParts;         // tensor memory of a step's weights
-    static constexpr int kACols = kSumCols * kSumBufs;              // tensor memory: sums, then weights
+    static constexpr int kStepCols = 64;                            // tensor memory of a step's weights
+    static constexpr int kACols = kRows * kSumBufs;                 // tensor memory: sums, then weights
     static_assert(kACols + kSteps * kStepCols <= 512, "tensor memory");
-    static constexpr int kLoads = PAIR ? (SWIGLU ? 5 : 7) : XT == kInt8 ? (SWIGLU ? 5 : 9) : (SWIGLU ? 6 : 10);
-    static constexpr int kLoadBytes = kPlanes * kWBytes + (XT == kInt8 ? kLoadRows * 128 : 0);
-    static constexpr int kPartBytes = kLoadRows * 128, kStepBytes = kPartBytes * kParts;
-    static constexpr int kSmem = 1024 + kLoads * kLoadBytes + kSteps * kStepBytes;
+    static constexpr int kLoads = PAIR ? (SWIGLU ? 6 : 7) : SWIGLU ? 8 : 9;
+    static constexpr int kLoadBytes = kWBytes + (XT == kInt8 ? kLoadRows * 128 : 0);
+    static constexpr int kPartBytes = kLoadRows * 128, kStepBytes = kPartBytes * 2;  // 64 values, 128
     static constexpr int kHalf = PAIR ? kRows / 2 : kRows;          // rows of a warpgroup of results
+    static constexpr int kChunk = 32;                               // of them, those read at once
+    static constexpr int kSwapBytes = SWIGLU ? 2 * kChunk / 2 * 128 : 0;  // of a warp of results
+    static constexpr int kSmem = 1024 + kLoads * kLoadBytes + kSteps * kStepBytes + kSumWarps * kSwapBytes;
 };
 
 // Matrix instruction with A in tensor memory.
@@ -144,12 +144,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t x_full[C::kSteps], a_full[C::kSteps], a_empty[C::kSteps];  // steps
     __shared__ __align__(8) uint64_t t_full[2], t_empty[2], i_full[2], i_empty[2];
     __shared__ Tile info[2];
-    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ __align__(8) uint64_t swap_bar[4], drain_bar;
     __shared__ uint32_t tmem_base, abort_word;
 
     uint8_t* loads = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     static_assert(C::kSmem + 1024 <= 232448, "shared memory of a block");
     uint8_t* rows16 = loads + C::kLoads * C::kLoadBytes;
+    float* swap = reinterpret_cast<float*>(rows16 + C::kSteps * C::kStepBytes);
     volatile uint32_t* abort = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kBlocks = PAIR ? 2 : 1;
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&l_full[i]), 1), mbar_init(smem_u32(&l_empty[i]), kConvertWarps + C::kRowWarps);
         for (int i = 0; i < C::kSteps; ++i) {
             mbar_init(smem_u32(&x_full[i]), 1);
-            mbar_init(smem_u32(&a_full[i]), kBlocks * kConvertWarps * C::kParts / 2 + C::kRowWarps);
+            mbar_init(smem_u32(&a_full[i]), kBlocks * kConvertWarps + C::kRowWarps);
             mbar_init(smem_u32(&a_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&i_full[i]), 1);
             mbar_init(smem_u32(&i_empty[i]), kConvertWarps + C::kRowWarps + C::kSumWarps);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&swap_bar[i]), 2);
         mbar_init(smem_u32(&drain_bar), 1);
         abort_word = 0u;
         mbar_init_fence();
@@ -184,21 +186,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
     pdl_enter();
 
-    Walk<C::kRows> walk;
+    Walk<C::kRows, true> walk;
     Tile tile;
     uint32_t it = 0;  // loads or steps that this warp has taken, over all of its tiles
     bool ok = true;
-    const int steps = 2 / C::kParts * a.KB;
-    // columns of a tile's instructions, and boxes of 32 rows that this block loads
-    auto columns = [&](int rows) { return (rows + C::kGrain - 1) / C::kGrain * C::kGrain; };
-    auto boxes_of = [&](int rows) { return (columns(rows) / kBlocks + 31) / 32; };
+    // columns of a tile's instructions, and boxes of rows that this block loads
+    auto columns = [](int rows) { return (rows + 15) / 16 * 16; };
+    auto boxes_of = [&](int rows) { return (columns(rows) / kBlocks + C::kBox - 1) / C::kBox; };
 
     if (warp < 4) {
         regs_dec<48>();
         if (warp == 0) {
             walk.begin(a, lane);
-            for (int t = first; ok && walk.next(a, lane, t, kWRows * kBlocks, tile); t += step) {
-                const int n0 = tile.n0 + (int)rank * kWRows;
+            for (int t = first; ok && walk.next(a, lane, t, C::kChannels, tile); t += step) {
+                const int n0 = tile.n0 + (int)rank * (C::kChannels / kBlocks);
                 const int boxes = XT == kInt8 ? boxes_of(tile.rows) : 0;
                 if (elect_one()) {
                     for (int kb = 0; kb < a.KB; ++kb, ++it) {
@@ -206,14 +207,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = mbar_wait<PAIR>(smem_u32(&l_empty[st]), ((it / C::kLoads) & 1) ^ 1, abort);
                         if (!ok) break;
                         const uint32_t bar = smem_u32(&l_full[st]), dst = smem_u32(loads + st * C::kLoadBytes);
-                        mbar_expect(bar, (uint32_t)(C::kPlanes * kWBytes + boxes * 32 * 128));
-#pragma unroll
-                        for (int p = 0; p < C::kPlanes; ++p)
-                            tma_load_3d(dst + p * kWBytes, &map_w, bar, kb * 128, n0, tile.expert * C::kPlanes + p);
+                        mbar_expect(bar, (uint32_t)(kWBytes + boxes * C::kBox * 128));
+                        if (SWIGLU) {
+                            tma_load_3d(dst, &map_w, bar, kb * 128, n0, tile.expert * 2);
+                            tma_load_3d(dst + kWBytes / 2, &map_w, bar, kb * 128, n0, tile.expert * 2 + 1);
+                        } else {
+                            tma_load_3d(dst, &map_w, bar, kb * 128, n0, tile.expert);
+                        }
                         if (XT == kInt8)
                             for (int j = 0; j < boxes; ++j)
-                                tma_load_2d(dst + C::kPlanes * kWBytes + j * 32 * 128, &map_x, bar, kb * 128,
-                                            tile.row0 + 32 * j);
+                                tma_load_2d(dst + kWBytes + j * C::kBox * 128, &map_x, bar, kb * 128,
+                                            tile.row0 + C::kBox * j);
                     }
                 }
                 __syncwarp();
@@ -224,13 +228,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = rank == 0;
             walk.begin(a, lane);
             uint32_t n = 0;
-            for (int t = first; ok && walk.next(a, lane, t, kWRows * kBlocks, tile); t += step, ++n) {
+            for (int t = first; ok && walk.next(a, lane, t, C::kChannels, tile); t += step, ++n) {
                 const uint32_t buf = n % C::kSumBufs;
                 const uint32_t idesc = idesc_16(kWRows * kBlocks, columns(tile.rows), XT == kBf16);
                 if (elect_one()) {
                     ok = mbar_wait<PAIR>(smem_u32(&t_empty[buf]), ((n / C::kSumBufs) & 1) ^ 1, abort);
-                    const uint32_t d = tmem + buf * C::kSumCols;
-                    for (int k = 0; ok && k < steps; ++k, ++it) {
+                    const uint32_t d = tmem + buf * C::kRows;
+                    for (int k = 0; ok && k < a.KB; ++k, ++it) {
                         const uint32_t s = it % C::kSteps, parity = (it / C::kSteps) & 1;
                         ok = mbar_wait<PAIR>(smem_u32(&a_full[s]), parity, abort);
                         if (XT != kInt8) ok = ok && mbar_wait<PAIR>(smem_u32(&x_full[s]), parity, abort);
@@ -238,12 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
                         const uint64_t b = smem_desc(smem_u32(rows16 + s * C::kStepBytes));
 #pragma unroll
-                        for (int p = 0; p < C::kPlanes; ++p)
-#pragma unroll
-                            for (int j = 0; j < 4 * C::kParts; ++j)
-                                mma_16_tmem<PAIR>(d + p * C::kRows,
-                                                  tmem + C::kACols + s * C::kStepCols + p * 32 * C::kParts + 8 * j,
-                                                  b + j / 4 * (C::kPartBytes / 16) + 2 * (j % 4), idesc, k > 0 || j > 0);
+                        for (int j = 0; j < 8; ++j)
+                            mma_16_tmem<PAIR>(d, tmem + C::kACols + s * C::kStepCols + 8 * j,
+                                              b + j / 4 * (C::kPartBytes / 16) + 2 * (j % 4), idesc, k > 0 || j > 0);
                         tc_commit<PAIR>(smem_u32(&a_empty[s]));
                     }
                     if (ok) tc_commit<PAIR>(smem_u32(&t_full[buf]));
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             walk.begin(a, lane);
             uint32_t n = 0;
             for (int t = first;; t += step, ++n) {
-                const bool more = walk.next(a, lane, t, kWRows * kBlocks, tile);
+                const bool more = walk.next(a, lane, t, C::kChannels, tile);
                 if (!mbar_wait<PAIR>(smem_u32(&i_empty[n & 1]), ((n >> 1) & 1) ^ 1, abort)) break;
                 if (lane == 0) {
                     if (!more) tile = Tile{0, 0, 0, 0};
@@ -268,22 +269,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (XT != kInt8) {
             walk.begin(a, lane);
-            for (int t = first; ok && walk.next(a, lane, t, kWRows * kBlocks, tile); t += step) {
+            for (int t = first; ok && walk.next(a, lane, t, C::kChannels, tile); t += step) {
                 const int boxes = boxes_of(tile.rows);
                 const int row0 = tile.row0 + (int)rank * columns(tile.rows) / 2;
                 if (elect_one()) {
-                    for (int k = 0; k < steps; ++k, ++it) {
+                    for (int k = 0; k < a.KB; ++k, ++it) {
                         const uint32_t s = it % C::kSteps;
                         ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
                         if (!ok) break;
                         const uint32_t own = smem_u32(&x_full[s]), bar = PAIR ? map_cluster(own, 0) : own;
                         const uint32_t dst = smem_u32(rows16 + s * C::kStepBytes);
-                        if (rank == 0) mbar_expect(own, (uint32_t)(kBlocks * C::kParts * boxes * 32 * 128));
+                        if (rank == 0) mbar_expect(own, (uint32_t)(kBlocks * 2 * boxes * C::kBox * 128));
 #pragma unroll
-                        for (int h = 0; h < C::kParts; ++h)
+                        for (int h = 0; h < 2; ++h)
                             for (int j = 0; j < boxes; ++j)
-                                tma_load_2d<PAIR>(dst + h * C::kPartBytes + j * 32 * 128, &map_x, bar,
-                                                  (k * C::kParts + h) * 64, row0 + 32 * j);
+                                tma_load_2d<PAIR>(dst + h * C::kPartBytes + j * C::kBox * 128, &map_x, bar,
+                                                  k * 128 + h * 64, row0 + C::kBox * j);
                     }
                 }
                 __syncwarp();
@@ -319,31 +320,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
                 if (!ok) break;
                 const uint8_t* src = loads + st * C::kLoadBytes + row * 128;
-                uint4 w[C::kPlanes][4];
+                uint4 w[4];
 #pragma unroll
-                for (int p = 0; p < C::kPlanes; ++p)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[p][j] = *reinterpret_cast<const uint4*>(src + p * kWBytes + (((half * 4 + j) ^ (row & 7)) << 4));
+                for (int j = 0; j < 4; ++j)
+                    w[j] = *reinterpret_cast<const uint4*>(src + (((half * 4 + j) ^ (row & 7)) << 4));
                 hand_over();  // while these loads are on their way
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
-                const uint32_t k = C::kParts == 2 ? it : 2 * it + half, s = k % C::kSteps;
-                ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((k / C::kSteps) & 1) ^ 1, abort);
+                const uint32_t s = it % C::kSteps;
+                ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
                 if (!ok) break;
                 tc_fence_after();
+                uint32_t v[32];
 #pragma unroll
-                for (int p = 0; p < C::kPlanes; ++p) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        widen4<XT == kBf16>(w[p][j].x, v[8 * j], v[8 * j + 1]);
-                        widen4<XT == kBf16>(w[p][j].y, v[8 * j + 2], v[8 * j + 3]);
-                        widen4<XT == kBf16>(w[p][j].z, v[8 * j + 4], v[8 * j + 5]);
-                        widen4<XT == kBf16>(w[p][j].w, v[8 * j + 6], v[8 * j + 7]);
-                    }
-                    tmem_st32(to + s * C::kStepCols + (p * C::kParts + (C::kParts == 2 ? half : 0)) * 32, v);
+                for (int j = 0; j < 4; ++j) {
+                    widen4<XT == kBf16>(w[j].x, v[8 * j], v[8 * j + 1]);
+                    widen4<XT == kBf16>(w[j].y, v[8 * j + 2], v[8 * j + 3]);
+                    widen4<XT == kBf16>(w[j].z, v[8 * j + 4], v[8 * j + 5]);
+                    widen4<XT == kBf16>(w[j].w, v[8 * j + 6], v[8 * j + 7]);
                 }
+                tmem_st32(to + s * C::kStepCols + half * 32, v);
                 pending = (int)s;
             }
             if (!ok) break;
@@ -363,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t st = it % C::kLoads;
                 ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
                 if (!ok) break;
-                const uint8_t* src = loads + st * C::kLoadBytes + C::kPlanes * kWBytes + lane * 128;
+                const uint8_t* src = loads + st * C::kLoadBytes + kWBytes + lane * 128;
                 uint4 x[2][C::kLoadRows / 32];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -401,7 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4 + kConvertWarps + 8 - C::kSumWarps) {
         regs_inc<136>();
         const int half = PAIR ? (warp - 4 - kConvertWarps) >> 2 : 0, quarter = warp & 3;
-        const uint32_t from = tmem + ((uint32_t)quarter << 21) + half * C::kHalf;
+        const uint32_t from = tmem + ((uint32_t)quarter << 21);
+        const int me = warp - (kThreads / 32 - C::kSumWarps);  // among the warps of results
+        uint32_t swaps = 0;
         for (uint32_t n = 0;; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
             if (!ok) break;
@@ -410,54 +408,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
             if (tile.rows == 0) break;
             if (!MR_IN_RANGE(tile.expert, a.experts, 911)) tile.expert = 0;
-            const int col = tile.n0 + (int)rank * kWRows + quarter * 32 + lane;
+            // this lane's channel; the network's: of the gate in the first two warps, of the other factor in the others
+            const int factor = SWIGLU ? quarter >> 1 : 0;
+            const int col = tile.n0 + (int)rank * (C::kChannels / kBlocks) + (SWIGLU ? quarter & 1 : quarter) * 32 + lane;
             const bool real = col < a.N;
-            const float* ws = a.w_scales + (int64_t)tile.expert * C::kPlanes * a.N + (real ? col : 0);
-            const float w0 = *ws, w1 = SWIGLU ? ws[a.N] : 0.0f;
-            const int mine = min(C::kHalf, tile.rows - half * C::kHalf);  // rows of this warp, may be none
-            int64_t row0 = (int64_t)tile.row0 + half * C::kHalf;
+            const float w_scale =
+                a.w_scales[((int64_t)tile.expert * (SWIGLU ? 2 : 1) + factor) * a.N + (real ? col : 0)];
+            // rows of this warp, may be none: those of half of the tile's columns
+            const int cols = PAIR ? (columns(tile.rows) / 2 + 15) / 16 * 16 : C::kHalf;
+            const int mine = min(cols, tile.rows - half * cols);
+            const int64_t row0 = (int64_t)tile.row0 + half * cols;
             const bool inside = mine <= 0 || MR_IN_RANGE(row0 + mine - 1, a.rows, 912);
-            float xs[(C::kHalf + 31) / 32];  // lane i: those of rows i, 32 + i, ...
+            float xs[C::kHalf / 32];  // lane i: those of rows i, 32 + i, ...
 #pragma unroll
-            for (int i = 0; i < (C::kHalf + 31) / 32; ++i)
+            for (int i = 0; i < C::kHalf / 32; ++i)
                 xs[i] = a.x_scales && inside && 32 * i + lane < mine ? a.x_scales[(row0 + 32 * i + lane) * a.xs_row] : 1.0f;
             const uint32_t buf = n % C::kSumBufs;
             ok = mbar_wait<PAIR>(smem_u32(&t_full[buf]), (n / C::kSumBufs) & 1, abort);
             if (!ok) break;
             tc_fence_after();
-            constexpr int kLd = 16;
+            constexpr int kLd = C::kChunk, kKeep = SWIGLU ? kLd / 2 : kLd;  // rows read at once, and of them this warp's
             const bool wide = !SWIGLU && a.y_dtype == MR_DTYPE_F32;
             const int elem = wide ? 4 : 2;
             char* y = reinterpret_cast<char*>(a.y) + (row0 * a.y_stride + col) * elem;
             const int64_t y_step = a.y_stride * elem;
-            uint32_t packed[C::kHalf / 2];
+            uint32_t packed[C::kHalf / kLd * kKeep / 2];
 #pragma unroll
             for (int c = 0; c < C::kHalf; c += kLd) {
                 if (c >= mine) break;
-                uint32_t v[kLd], u[SWIGLU ? kLd : 1];
-                const uint32_t at = from + buf * C::kSumCols + c;
-                tmem_load(v, at);
-                if constexpr (SWIGLU) {
-                    tmem_load(u, at + C::kRows);
-                    tmem_ld_wait(u);
-                }
+                uint32_t v[kLd];
+                tmem_load(v, from + buf * C::kRows + half * cols + c);
                 tmem_ld_wait(v);
                 float f[kLd];
 #pragma unroll
-                for (int j = 0; j < kLd; ++j) {
-                    const float s = __shfl_sync(0xffffffffu, xs[(c + j) / 32], (c + j) % 32);
-                    f[j] = __fmul_rn(__fmul_rn(__uint_as_float(v[j]), w0), s);
-                    if constexpr (SWIGLU) f[j] = silu(f[j]) * (__uint_as_float(u[j]) * w1 * s);
+                for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(__uint_as_float(v[j]), w_scale);
+                if (a.x_scales) {
+#pragma unroll
+                    for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, xs[(c + j) / 32], (c + j) % 32));
+                }
+                if constexpr (SWIGLU) {
+                    // Two warps have the two factors of the same channels: the first takes the chunk's first
+                    // rows, the second the others, each from the other's half of `swap`, two of them in turn.
+                    float* out = swap + ((me * 2 + (swaps & 1)) * kKeep) * 32 + lane;
+                    const float* in = swap + (((me ^ 2) * 2 + (swaps & 1)) * kKeep) * 32 + lane;
+                    const uint32_t bar = smem_u32(&swap_bar[half * 2 + (quarter & 1)]);
+#pragma unroll
+                    for (int j = 0; j < kKeep; ++j) out[j * 32] = factor ? f[j] : f[kKeep + j];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                    ok = mbar_wait<PAIR>(bar, swaps & 1, abort);
+                    ++swaps;
+                    if (!ok) break;
+#pragma unroll
+                    for (int j = 0; j < kKeep; ++j) {
+                        const float o = in[j * 32];
+                        f[j] = factor ? silu(o) * f[kKeep + j] : silu(f[j]) * o;
+                    }
                 }
                 if (wide) {
 #pragma unroll
-                    for (int j = 0; j < kLd; ++j)
+                    for (int j = 0; j < kKeep; ++j)
                         if (real && inside && c + j < mine) *reinterpret_cast<float*>(y + (c + j) * y_step) = f[j];
                 }
 #pragma unroll
-                for (int j = 0; j < kLd; j += 2)
-                    packed[(c + j) / 2] = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], f[j + 1]);
+                for (int j = 0; j < kKeep; j += 2)
+                    packed[(c / kLd * kKeep + j) / 2] = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], f[j + 1]);
             }
+            if (!ok) break;
             // everything is in registers: hand the sums back before the stores
             tc_fence_before();
             __syncwarp();
@@ -467,9 +484,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!wide && real && inside) {
 #pragma unroll
-                for (int j = 0; j < C::kHalf; ++j) {
-                    if (j < mine) *reinterpret_cast<uint16_t*>(y) = (uint16_t)(packed[j / 2] >> (16 * (j & 1)));
-                    y += y_step;
+                for (int c = 0; c < C::kHalf; c += kLd) {
+                    const int r = c + factor * kKeep;
+                    char* to = y + r * y_step;
+#pragma unroll
+                    for (int j = 0; j < kKeep; ++j) {
+                        if (r + j < mine)
+                            *reinterpret_cast<uint16_t*>(to) = (uint16_t)(packed[(c / kLd * kKeep + j) / 2] >> (16 * (j & 1)));
+                        to += y_step;
+                    }
                 }
             }
         }
@@ -581,19 +604,19 @@ struct Product {
 bool use_pairs(int64_t rows, int64_t G) { return rows > 32 * std::min<int64_t>(G, rows); }
 
 mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
-    const int tile_m = pair ? (p.swiglu ? 128 : 256) : 32;
+    const int tile_m = pair ? 256 : 32, channels = (pair ? 2 : 1) * (p.swiglu ? 64 : 128);
     const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G - 1, a.rows);  // or fewer
-    a.n_tiles = ceil_div(a.N, pair ? 2 * kWRows : kWRows);
+    a.n_tiles = ceil_div(a.N, channels);
     a.KB = ceil_div(p.K, 128);
     const int64_t tiles = m_tiles * a.n_tiles;
     if (tiles > INT32_MAX) return MR_ERR_PARAM_INVALID;
     CUtensorMap m[2];
     const bool eight = p.xt == kInt8;
     const uint64_t xd[2] = {(uint64_t)p.K, (uint64_t)a.rows}, xs[1] = {(uint64_t)p.x_stride};
-    const uint32_t xb[2] = {eight ? 128u : 64u, 32};
+    const uint32_t xb[2] = {eight ? 128u : 64u, pair ? 64u : 32u};
     const uint64_t wd[3] = {(uint64_t)p.K, (uint64_t)a.N, (uint64_t)a.experts * (p.swiglu ? 2 : 1)};
     const uint64_t ws[2] = {(uint64_t)p.w_row, (uint64_t)p.w_matrix};
-    const uint32_t wb[3] = {128, (uint32_t)kWRows, 1};
+    const uint32_t wb[3] = {128, (uint32_t)(p.swiglu ? kWRows / 2 : kWRows), 1};
     if (!make_tensor_map(&m[0], eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, eight ? 1 : 2, p.x, 2,
                          xd, xs, xb) ||
         !make_tensor_map(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, 3, wd, ws, wb))
