@@ -16,8 +16,10 @@
 //   warp 1       matrix instructions, 128 values of k a step
 //   warp 2       hands tiles to the warps below
 //   warp 3       TMA loads of 16-bit rows: a ring of steps
-//   warps 4-11   weights to 16 bits; each warpgroup has one half of a load's 128 values
-//   warps 12-15  int8 rows to 16 bits (single blocks), or results
+//   warps 4-11   weights to 16 bits; each warpgroup takes every other load, since what a
+//                load costs a warp is mostly latency (both on every load, half of it each:
+//                576 rows over 64 experts, 7168 -> 4096, 345 us, and XXX so)
+//   warps 12-15  int8 rows to 16 bits (single blocks), two on every other load; or results
 //   warps 16-19  results: scales, rounding, stores
 // One persistent block per SM takes tiles round robin; a pair of blocks shares a tile
 // of 256 channels, where each converts its own 128 and loads half of the rows.
@@ -48,29 +50,36 @@ struct Int8Args : Groups {
 
 enum { kInt8 = 0, kF16 = 1, kBf16 = 2 };  // rows
 
-// XT: the rows' type. SWIGLU: the network's first product; the upper half of a block's
-// 128 channels are the gate's, the lower half the same ones of the other factor.
+// XT: the rows' type. SWIGLU: the network's first product, with a gate's channels and
+// the same ones of the other factor in a tile. A single block has two operands of 128
+// channels a step, whose sums lie side by side: a plain product's 256 channels, or the
+// two factors. Of a pair each block has one: its half of 256 channels, or 64 of the
+// gate's above the same 64 of the other factor.
 template <int XT, bool SWIGLU, bool PAIR> struct Cfg {
-    static constexpr int kRows = PAIR ? 256 : 32;                   // rows of a tile
-    static constexpr int kChannels = (PAIR ? 2 : 1) * (SWIGLU ? 64 : 128);
+    static constexpr int kRows = PAIR ? 256 : 96;                   // rows of a tile
+    static constexpr int kChannels = SWIGLU ? 128 : 256;            // and channels of the result
+    static constexpr int kPlanes = PAIR ? 1 : 2;
     static constexpr int kLoadRows = PAIR ? kRows / 2 : kRows;      // of the rows, those this block loads
     static constexpr int kBox = PAIR ? 64 : 32;                     // rows of a TMA load
     // Steps of converted weights and of 16-bit rows held. (A step of 64 values costs the thread that issues the
-    // instructions its two waits and a commit twice: 16384 x 7168 x 7168 took 884 instead of 848 us, and 576 rows
-    // over 64 experts, 7168 -> 4096, 393 instead of 345.)
-    static constexpr int kSteps = PAIR ? 3 : XT == kInt8 ? 4 : 6;
+    // instructions its two waits and a commit twice: 16384 x 7168 x 7168 took 884 instead of 848 us.)
+    static constexpr int kSteps = PAIR ? 3 : 2;
     // warps of int8 rows, of results
     static constexpr int kRowWarps = XT == kInt8 ? 4 : 0, kSumWarps = PAIR ? 8 : 4;
-    static constexpr int kSumBufs = PAIR ? 1 : 2;
-    static constexpr int kStepCols = 64;                            // tensor memory of a step's weights
-    static constexpr int kACols = kRows * kSumBufs;                 // tensor memory: sums, then weights
+    static constexpr int kStepCols = 64 * kPlanes;                  // tensor memory of a step's weights
+    static constexpr int kACols = kRows * kPlanes;                  // tensor memory: sums, then weights
     static_assert(kACols + kSteps * kStepCols <= 512, "tensor memory");
-    static constexpr int kLoads = PAIR ? (SWIGLU ? 6 : 7) : SWIGLU ? 8 : 9;
-    static constexpr int kLoadBytes = kWBytes + (XT == kInt8 ? kLoadRows * 128 : 0);
+    static constexpr int kLoads = PAIR ? (SWIGLU ? 6 : 7) : XT == kInt8 ? 4 : 5;
+    static constexpr int kLoadBytes = kPlanes * kWBytes + (XT == kInt8 ? kLoadRows * 128 : 0);
     static constexpr int kPartBytes = kLoadRows * 128, kStepBytes = kPartBytes * 2;  // 64 values, 128
     static constexpr int kHalf = PAIR ? kRows / 2 : kRows;          // rows of a warpgroup of results
-    static constexpr int kChunk = 32;                               // of them, those read at once
-    static constexpr int kSwapBytes = SWIGLU ? 2 * kChunk / 2 * 128 : 0;  // of a warp of results
+    static constexpr int kChunk = PAIR ? 32 : 16;                   // of them, those read at once
+    static constexpr bool kSwap = SWIGLU && PAIR;                   // the factors meet in shared memory
+    static constexpr int kSwapBytes = kSwap ? 2 * kChunk / 2 * 128 : 0;  // of a warp of results
+    // registers of a thread of the first four warps, of the converters, of the next four warps and of the results;
+    // blocks are launched with 96 for each
+    static constexpr int kRegs[4] = {48, PAIR ? 80 : 112, PAIR ? 136 : 80, PAIR ? 136 : 128};
+    static_assert(kRegs[0] + 2 * kRegs[1] + kRegs[2] + kRegs[3] <= 5 * 96, "registers of a block");
     static constexpr int kSmem = 1024 + kLoads * kLoadBytes + kSteps * kStepBytes + kSumWarps * kSwapBytes;
 };
 
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t l_full[C::kLoads], l_empty[C::kLoads];                   // loads
     __shared__ __align__(8) uint64_t x_full[C::kSteps], a_full[C::kSteps], a_empty[C::kSteps];  // steps
-    __shared__ __align__(8) uint64_t t_full[2], t_empty[2], i_full[2], i_empty[2];
+    __shared__ __align__(8) uint64_t t_full, t_empty, i_full[2], i_empty[2];
     __shared__ Tile info[2];
     __shared__ __align__(8) uint64_t swap_bar[4], drain_bar;
     __shared__ uint32_t tmem_base, abort_word;
@@ -157,15 +166,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kLoads; ++i)
-            mbar_init(smem_u32(&l_full[i]), 1), mbar_init(smem_u32(&l_empty[i]), kConvertWarps + C::kRowWarps);
+            mbar_init(smem_u32(&l_full[i]), 1), mbar_init(smem_u32(&l_empty[i]), (kConvertWarps + C::kRowWarps) / 2);
         for (int i = 0; i < C::kSteps; ++i) {
             mbar_init(smem_u32(&x_full[i]), 1);
-            mbar_init(smem_u32(&a_full[i]), kBlocks * kConvertWarps + C::kRowWarps);
+            mbar_init(smem_u32(&a_full[i]), (kBlocks * kConvertWarps + C::kRowWarps) / 2);
             mbar_init(smem_u32(&a_empty[i]), 1);
         }
+        mbar_init(smem_u32(&t_full), 1);
+        mbar_init(smem_u32(&t_empty), kBlocks * C::kSumWarps);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&t_full[i]), 1);
-            mbar_init(smem_u32(&t_empty[i]), kBlocks * C::kSumWarps);
             mbar_init(smem_u32(&i_full[i]), 1);
             mbar_init(smem_u32(&i_empty[i]), kConvertWarps + C::kRowWarps + C::kSumWarps);
         }
@@ -195,11 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto boxes_of = [&](int rows) { return (columns(rows) / kBlocks + C::kBox - 1) / C::kBox; };
 
     if (warp < 4) {
-        regs_dec<48>();
+        regs_dec<C::kRegs[0]>();
         if (warp == 0) {
             walk.begin(a, lane);
             for (int t = first; ok && walk.next(a, lane, t, C::kChannels, tile); t += step) {
-                const int n0 = tile.n0 + (int)rank * (C::kChannels / kBlocks);
                 const int boxes = XT == kInt8 ? boxes_of(tile.rows) : 0;
                 if (elect_one()) {
                     for (int kb = 0; kb < a.KB; ++kb, ++it) {
@@ -207,16 +215,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = mbar_wait<PAIR>(smem_u32(&l_empty[st]), ((it / C::kLoads) & 1) ^ 1, abort);
                         if (!ok) break;
                         const uint32_t bar = smem_u32(&l_full[st]), dst = smem_u32(loads + st * C::kLoadBytes);
-                        mbar_expect(bar, (uint32_t)(kWBytes + boxes * C::kBox * 128));
-                        if (SWIGLU) {
-                            tma_load_3d(dst, &map_w, bar, kb * 128, n0, tile.expert * 2);
-                            tma_load_3d(dst + kWBytes / 2, &map_w, bar, kb * 128, n0, tile.expert * 2 + 1);
+                        mbar_expect(bar, (uint32_t)(C::kPlanes * kWBytes + boxes * C::kBox * 128));
+                        const int k = kb * 128, e = tile.expert;
+                        if (C::kSwap) {
+                            tma_load_3d(dst, &map_w, bar, k, tile.n0 + (int)rank * 64, 2 * e);
+                            tma_load_3d(dst + kWBytes / 2, &map_w, bar, k, tile.n0 + (int)rank * 64, 2 * e + 1);
+                        } else if (PAIR) {
+                            tma_load_3d(dst, &map_w, bar, k, tile.n0 + (int)rank * kWRows, e);
                         } else {
-                            tma_load_3d(dst, &map_w, bar, kb * 128, n0, tile.expert);
+                            tma_load_3d(dst, &map_w, bar, k, tile.n0, SWIGLU ? 2 * e : e);
+                            tma_load_3d(dst + kWBytes, &map_w, bar, k, SWIGLU ? tile.n0 : tile.n0 + kWRows,
+                                        SWIGLU ? 2 * e + 1 : e);
                         }
                         if (XT == kInt8)
                             for (int j = 0; j < boxes; ++j)
-                                tma_load_2d(dst + kWBytes + j * C::kBox * 128, &map_x, bar, kb * 128,
+                                tma_load_2d(dst + C::kPlanes * kWBytes + j * C::kBox * 128, &map_x, bar, k,
                                             tile.row0 + C::kBox * j);
                     }
                 }
@@ -229,11 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             walk.begin(a, lane);
             uint32_t n = 0;
             for (int t = first; ok && walk.next(a, lane, t, C::kChannels, tile); t += step, ++n) {
-                const uint32_t buf = n % C::kSumBufs;
                 const uint32_t idesc = idesc_16(kWRows * kBlocks, columns(tile.rows), XT == kBf16);
                 if (elect_one()) {
-                    ok = mbar_wait<PAIR>(smem_u32(&t_empty[buf]), ((n / C::kSumBufs) & 1) ^ 1, abort);
-                    const uint32_t d = tmem + buf * C::kRows;
+                    ok = mbar_wait<PAIR>(smem_u32(&t_empty), (n & 1) ^ 1, abort);
                     for (int k = 0; ok && k < a.KB; ++k, ++it) {
                         const uint32_t s = it % C::kSteps, parity = (it / C::kSteps) & 1;
                         ok = mbar_wait<PAIR>(smem_u32(&a_full[s]), parity, abort);
@@ -242,12 +253,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
                         const uint64_t b = smem_desc(smem_u32(rows16 + s * C::kStepBytes));
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            mma_16_tmem<PAIR>(d, tmem + C::kACols + s * C::kStepCols + 8 * j,
-                                              b + j / 4 * (C::kPartBytes / 16) + 2 * (j % 4), idesc, k > 0 || j > 0);
+                        for (int p = 0; p < C::kPlanes; ++p)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                mma_16_tmem<PAIR>(tmem + p * C::kRows, tmem + C::kACols + s * C::kStepCols + p * 64 + 8 * j,
+                                                  b + j / 4 * (C::kPartBytes / 16) + 2 * (j % 4), idesc, k > 0 || j > 0);
                         tc_commit<PAIR>(smem_u32(&a_empty[s]));
                     }
-                    if (ok) tc_commit<PAIR>(smem_u32(&t_full[buf]));
+                    if (ok) tc_commit<PAIR>(smem_u32(&t_full));
                 }
                 __syncwarp();
                 it = __reduce_max_sync(0xffffffffu, it);
@@ -293,22 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp < 4 + kConvertWarps) {
-        regs_dec<80>();
-        const int half = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        if constexpr (PAIR) regs_dec<C::kRegs[1]>();
+        else regs_inc<C::kRegs[1]>();
+        const uint32_t turn = (warp - 4) >> 2;
+        const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t to = tmem + ((uint32_t)quarter << 21) + C::kACols;  // 32 lanes << 16
-        int pending = -1;  // step whose stores are on their way
-        auto hand_over = [&] {
-            if (pending < 0) return;
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&a_full[pending]), 0));
-                else mbar_arrive(smem_u32(&a_full[pending]));
-            }
-            pending = -1;
-        };
-        for (uint32_t n = 0;; ++n) {
+        for (uint32_t n = 0; ok; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
             if (!ok) break;
             const int rows = info[n & 1].rows;
@@ -316,39 +319,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
             if (rows == 0) break;
             for (int kb = 0; kb < a.KB; ++kb, ++it) {
-                const uint32_t st = it % C::kLoads;
+                if ((it & 1) != turn) continue;
+                const uint32_t st = it % C::kLoads, s = it % C::kSteps;
                 ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
                 if (!ok) break;
                 const uint8_t* src = loads + st * C::kLoadBytes + row * 128;
-                uint4 w[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = *reinterpret_cast<const uint4*>(src + (((half * 4 + j) ^ (row & 7)) << 4));
-                hand_over();  // while these loads are on their way
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
-                const uint32_t s = it % C::kSteps;
-                ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t v[32];
+                for (int p = 0; p < C::kPlanes; ++p) {
+                    uint4 w[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    widen4<XT == kBf16>(w[j].x, v[8 * j], v[8 * j + 1]);
-                    widen4<XT == kBf16>(w[j].y, v[8 * j + 2], v[8 * j + 3]);
-                    widen4<XT == kBf16>(w[j].z, v[8 * j + 4], v[8 * j + 5]);
-                    widen4<XT == kBf16>(w[j].w, v[8 * j + 6], v[8 * j + 7]);
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = *reinterpret_cast<const uint4*>(src + p * kWBytes + ((j ^ (row & 7)) << 4));
+                    if (p == C::kPlanes - 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
+                    }
+                    if (p == 0) {
+                        ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            widen4<XT == kBf16>(w[4 * h + j].x, v[8 * j], v[8 * j + 1]);
+                            widen4<XT == kBf16>(w[4 * h + j].y, v[8 * j + 2], v[8 * j + 3]);
+                            widen4<XT == kBf16>(w[4 * h + j].z, v[8 * j + 4], v[8 * j + 5]);
+                            widen4<XT == kBf16>(w[4 * h + j].w, v[8 * j + 6], v[8 * j + 7]);
+                        }
+                        tmem_st32(to + s * C::kStepCols + p * 64 + h * 32, v);
+                    }
                 }
-                tmem_st32(to + s * C::kStepCols + half * 32, v);
-                pending = (int)s;
+                if (!ok) break;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&a_full[s]), 0));
+                    else mbar_arrive(smem_u32(&a_full[s]));
+                }
             }
-            if (!ok) break;
-            hand_over();
         }
-    } else if (warp < 4 + kConvertWarps + C::kRowWarps) {
-        regs_dec<80>();
-        const int quarter = warp & 3;  // of the pieces of a row's 64 values
-        for (uint32_t n = 0;; ++n) {
+    } else if (!PAIR && warp < 8 + kConvertWarps) {
+        regs_dec<C::kRegs[2]>();
+        const uint32_t turn = (warp >> 1) & 1;
+        const int h = warp & 1;  // half of a load's values
+        for (uint32_t n = 0; ok && XT == kInt8; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
             if (!ok) break;
             const int rows = info[n & 1].rows;
@@ -356,46 +374,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
             if (rows == 0) break;
             for (int kb = 0; kb < a.KB; ++kb, ++it) {
-                const uint32_t st = it % C::kLoads;
+                if ((it & 1) != turn) continue;
+                const uint32_t st = it % C::kLoads, s = it % C::kSteps;
                 ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
                 if (!ok) break;
-                const uint8_t* src = loads + st * C::kLoadBytes + kWBytes + lane * 128;
-                uint4 x[2][C::kLoadRows / 32];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < C::kLoadRows / 32; ++i)
-                        if (32 * i < rows)
-                            x[h][i] = *reinterpret_cast<const uint4*>(src + 32 * i * 128 + (((h * 4 + quarter) ^ (lane & 7)) << 4));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
-                const uint32_t s = it % C::kSteps;
+                const uint8_t* src = loads + st * C::kLoadBytes + C::kPlanes * kWBytes + lane * 128;
+                uint8_t* dst = rows16 + s * C::kStepBytes + h * C::kPartBytes + lane * 128;
                 ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
                 if (!ok) break;
+                for (int i = 0; i < rows; i += 32) {
+                    uint4 x[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint8_t* dst = rows16 + s * C::kStepBytes + h * C::kPartBytes + lane * 128;
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = *reinterpret_cast<const uint4*>(src + i * 128 + (((h * 4 + j) ^ (lane & 7)) << 4));
 #pragma unroll
-                    for (int i = 0; i < C::kLoadRows / 32; ++i) {
-                        if (32 * i >= rows) continue;
+                    for (int j = 0; j < 4; ++j) {
                         uint4 u, v;
-                        widen4<false>(x[h][i].x, u.x, u.y);
-                        widen4<false>(x[h][i].y, u.z, u.w);
-                        widen4<false>(x[h][i].z, v.x, v.y);
-                        widen4<false>(x[h][i].w, v.z, v.w);
-                        uint8_t* line = dst + 32 * i * 128;
-                        *reinterpret_cast<uint4*>(line + (((2 * quarter) ^ (lane & 7)) << 4)) = u;
-                        *reinterpret_cast<uint4*>(line + (((2 * quarter + 1) ^ (lane & 7)) << 4)) = v;
+                        widen4<false>(x[j].x, u.x, u.y);
+                        widen4<false>(x[j].y, u.z, u.w);
+                        widen4<false>(x[j].z, v.x, v.y);
+                        widen4<false>(x[j].w, v.z, v.w);
+                        *reinterpret_cast<uint4*>(dst + i * 128 + (((2 * j) ^ (lane & 7)) << 4)) = u;
+                        *reinterpret_cast<uint4*>(dst + i * 128 + (((2 * j + 1) ^ (lane & 7)) << 4)) = v;
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
                 smem_proxy_fence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&a_full[s]));
             }
-            if (!ok) break;
         }
-    } else if (warp >= 4 + kConvertWarps + 8 - C::kSumWarps) {
-        regs_inc<136>();
+    } else {
+        regs_inc<C::kRegs[3]>();
         const int half = PAIR ? (warp - 4 - kConvertWarps) >> 2 : 0, quarter = warp & 3;
         const uint32_t from = tmem + ((uint32_t)quarter << 21);
         const int me = warp - (kThreads / 32 - C::kSumWarps);  // among the warps of results
@@ -408,12 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
             if (tile.rows == 0) break;
             if (!MR_IN_RANGE(tile.expert, a.experts, 911)) tile.expert = 0;
-            // this lane's channel; the network's: of the gate in the first two warps, of the other factor in the others
-            const int factor = SWIGLU ? quarter >> 1 : 0;
-            const int col = tile.n0 + (int)rank * (C::kChannels / kBlocks) + (SWIGLU ? quarter & 1 : quarter) * 32 + lane;
+            // this lane's channel; a pair's network: of the gate in the first two warps, of the other factor in the others
+            const int factor = C::kSwap ? quarter >> 1 : 0;
+            const int col = tile.n0 + (C::kSwap ? (int)rank * 64 + (quarter & 1) * 32 : (int)rank * kWRows + quarter * 32) + lane;
+            const float* ws = a.w_scales + ((int64_t)tile.expert * (SWIGLU ? 2 : 1) + factor) * a.N;
             const bool real = col < a.N;
-            const float w_scale =
-                a.w_scales[((int64_t)tile.expert * (SWIGLU ? 2 : 1) + factor) * a.N + (real ? col : 0)];
             // rows of this warp, may be none: those of half of the tile's columns
             const int cols = PAIR ? (columns(tile.rows) / 2 + 15) / 16 * 16 : C::kHalf;
             const int mine = min(cols, tile.rows - half * cols);
@@ -423,75 +433,121 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < C::kHalf / 32; ++i)
                 xs[i] = a.x_scales && inside && 32 * i + lane < mine ? a.x_scales[(row0 + 32 * i + lane) * a.xs_row] : 1.0f;
-            const uint32_t buf = n % C::kSumBufs;
-            ok = mbar_wait<PAIR>(smem_u32(&t_full[buf]), (n / C::kSumBufs) & 1, abort);
-            if (!ok) break;
-            tc_fence_after();
-            constexpr int kLd = C::kChunk, kKeep = SWIGLU ? kLd / 2 : kLd;  // rows read at once, and of them this warp's
+            constexpr int kLd = C::kChunk, kKeep = C::kSwap ? kLd / 2 : kLd;  // rows read at once, and of them this warp's
             const bool wide = !SWIGLU && a.y_dtype == MR_DTYPE_F32;
             const int elem = wide ? 4 : 2;
             char* y = reinterpret_cast<char*>(a.y) + (row0 * a.y_stride + col) * elem;
             const int64_t y_step = a.y_stride * elem;
-            uint32_t packed[C::kHalf / kLd * kKeep / 2];
+            const float w_scale = ws[real ? col : 0];
+            auto scaled = [&](const uint32_t (&v)[kLd], float by, int c, float (&f)[kLd]) {
 #pragma unroll
-            for (int c = 0; c < C::kHalf; c += kLd) {
-                if (c >= mine) break;
-                uint32_t v[kLd];
-                tmem_load(v, from + buf * C::kRows + half * cols + c);
-                tmem_ld_wait(v);
-                float f[kLd];
-#pragma unroll
-                for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(__uint_as_float(v[j]), w_scale);
+                for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(__uint_as_float(v[j]), by);
                 if (a.x_scales) {
 #pragma unroll
-                    for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, xs[(c + j) / 32], (c + j) % 32));
+                    for (int j = 0; j < kLd; ++j)
+                        f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, xs[(c + j) / 32], (c + j) % 32));
                 }
-                if constexpr (SWIGLU) {
-                    // Two warps have the two factors of the same channels: the first takes the chunk's first
-                    // rows, the second the others, each from the other's half of `swap`, two of them in turn.
-                    float* out = swap + ((me * 2 + (swaps & 1)) * kKeep) * 32 + lane;
-                    const float* in = swap + (((me ^ 2) * 2 + (swaps & 1)) * kKeep) * 32 + lane;
-                    const uint32_t bar = smem_u32(&swap_bar[half * 2 + (quarter & 1)]);
-#pragma unroll
-                    for (int j = 0; j < kKeep; ++j) out[j * 32] = factor ? f[j] : f[kKeep + j];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar);
-                    ok = mbar_wait<PAIR>(bar, swaps & 1, abort);
-                    ++swaps;
-                    if (!ok) break;
-#pragma unroll
-                    for (int j = 0; j < kKeep; ++j) {
-                        const float o = in[j * 32];
-                        f[j] = factor ? silu(o) * f[kKeep + j] : silu(f[j]) * o;
-                    }
-                }
-                if (wide) {
-#pragma unroll
-                    for (int j = 0; j < kKeep; ++j)
-                        if (real && inside && c + j < mine) *reinterpret_cast<float*>(y + (c + j) * y_step) = f[j];
-                }
-#pragma unroll
-                for (int j = 0; j < kKeep; j += 2)
-                    packed[(c / kLd * kKeep + j) / 2] = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], f[j + 1]);
-            }
-            if (!ok) break;
-            // everything is in registers: hand the sums back before the stores
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&t_empty[buf]), 0));
-                else mbar_arrive(smem_u32(&t_empty[buf]));
-            }
-            if (!wide && real && inside) {
+            };
+            if constexpr (!PAIR) {
+                // the second operand's channels, or the same ones of the other factor
+                const int col1 = SWIGLU ? col : col + kWRows;
+                const bool real1 = col1 < a.N;
+                const float w_scale1 = ws[SWIGLU ? (real ? a.N + col : 0) : (real1 ? col1 : 0)];
+                ok = mbar_wait(smem_u32(&t_full), n & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < C::kHalf; c += kLd) {
-                    const int r = c + factor * kKeep;
-                    char* to = y + r * y_step;
+                    if (c >= mine) break;
+                    uint32_t v[kLd], u[kLd];
+                    tmem_load(v, from + c);
+                    tmem_ld_wait(v);
+                    tmem_load(u, from + C::kRows + c);
+                    float f[kLd], g[kLd];
+                    scaled(v, w_scale, c, f);
+                    tmem_ld_wait(u);
+                    if (c + kLd >= mine) {  // everything is in registers: hand the sums back before the last stores
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&t_empty));
+                    }
+                    scaled(u, w_scale1, c, g);
+                    if (SWIGLU) {
 #pragma unroll
-                    for (int j = 0; j < kKeep; ++j) {
-                        if (r + j < mine)
-                            *reinterpret_cast<uint16_t*>(to) = (uint16_t)(packed[(c / kLd * kKeep + j) / 2] >> (16 * (j & 1)));
-                        to += y_step;
+                        for (int j = 0; j < kLd; ++j) f[j] = silu(f[j]) * g[j];
+                    }
+                    if (!inside) continue;
+                    char* to = y + c * y_step;
+#pragma unroll
+                    for (int j = 0; j < kLd; ++j, to += y_step) {
+                        if (c + j >= mine) break;
+                        if (wide) {
+                            if (real) *reinterpret_cast<float*>(to) = f[j];
+                            if (real1) *reinterpret_cast<float*>(to + kWRows * 4) = g[j];
+                        } else {
+                            const uint32_t w = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], g[j]);
+                            if (real) *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
+                            if (!SWIGLU && real1) *reinterpret_cast<uint16_t*>(to + kWRows * 2) = (uint16_t)(w >> 16);
+                        }
+                    }
+                }
+            } else {
+                ok = mbar_wait<PAIR>(smem_u32(&t_full), n & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t packed[C::kHalf / kLd * kKeep / 2];
+#pragma unroll
+                for (int c = 0; c < C::kHalf; c += kLd) {
+                    if (c >= mine) break;
+                    uint32_t v[kLd];
+                    tmem_load(v, from + half * cols + c);
+                    tmem_ld_wait(v);
+                    float f[kLd];
+                    scaled(v, w_scale, c, f);
+                    if constexpr (C::kSwap) {
+                        // Two warps have the two factors of the same channels: the first takes the chunk's first
+                        // rows, the second the others, each from the other's half of `swap`, two of them in turn.
+                        float* out = swap + ((me * 2 + (swaps & 1)) * kKeep) * 32 + lane;
+                        const float* in = swap + (((me ^ 2) * 2 + (swaps & 1)) * kKeep) * 32 + lane;
+                        const uint32_t bar = smem_u32(&swap_bar[half * 2 + (quarter & 1)]);
+#pragma unroll
+                        for (int j = 0; j < kKeep; ++j) out[j * 32] = factor ? f[j] : f[kKeep + j];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar);
+                        ok = mbar_wait<PAIR>(bar, swaps & 1, abort);
+                        ++swaps;
+                        if (!ok) break;
+#pragma unroll
+                        for (int j = 0; j < kKeep; ++j) {
+                            const float o = in[j * 32];
+                            f[j] = factor ? silu(o) * f[kKeep + j] : silu(f[j]) * o;
+                        }
+                    }
+                    if (wide) {
+#pragma unroll
+                        for (int j = 0; j < kKeep; ++j)
+                            if (real && inside && c + j < mine) *reinterpret_cast<float*>(y + (c + j) * y_step) = f[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < kKeep; j += 2)
+                        packed[(c / kLd * kKeep + j) / 2] = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], f[j + 1]);
+                }
+                if (!ok) break;
+                // everything is in registers: hand the sums back before the stores
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_cluster(smem_u32(&t_empty), 0));
+                if (!wide && real && inside) {
+#pragma unroll
+                    for (int c = 0; c < C::kHalf; c += kLd) {
+                        const int r = c + factor * kKeep;
+                        char* to = y + r * y_step;
+#pragma unroll
+                        for (int j = 0; j < kKeep; ++j) {
+                            if (r + j < mine)
+                                *reinterpret_cast<uint16_t*>(to) = (uint16_t)(packed[(c / kLd * kKeep + j) / 2] >> (16 * (j & 1)));
+                            to += y_step;
+                        }
                     }
                 }
             }
@@ -601,10 +657,10 @@ struct Product {
     bool swiglu;
 };
 
-bool use_pairs(int64_t rows, int64_t G) { return rows > 32 * std::min<int64_t>(G, rows); }
+bool use_pairs(int64_t rows, int64_t G) { return rows > 96 * std::min<int64_t>(G, rows); }
 
 mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
-    const int tile_m = pair ? 256 : 32, channels = (pair ? 2 : 1) * (p.swiglu ? 64 : 128);
+    const int tile_m = pair ? 256 : 96, channels = p.swiglu ? 128 : 256;
     const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G - 1, a.rows);  // or fewer
     a.n_tiles = ceil_div(a.N, channels);
     a.KB = ceil_div(p.K, 128);
@@ -616,7 +672,7 @@ mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
     const uint32_t xb[2] = {eight ? 128u : 64u, pair ? 64u : 32u};
     const uint64_t wd[3] = {(uint64_t)p.K, (uint64_t)a.N, (uint64_t)a.experts * (p.swiglu ? 2 : 1)};
     const uint64_t ws[2] = {(uint64_t)p.w_row, (uint64_t)p.w_matrix};
-    const uint32_t wb[3] = {128, (uint32_t)(p.swiglu ? kWRows / 2 : kWRows), 1};
+    const uint32_t wb[3] = {128, (uint32_t)(p.swiglu && pair ? kWRows / 2 : kWRows), 1};
     if (!make_tensor_map(&m[0], eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, eight ? 1 : 2, p.x, 2,
                          xd, xs, xb) ||
         !make_tensor_map(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, 3, wd, ws, wb))
