@@ -675,12 +675,14 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
  *   x and weights start on 16 bytes and have row strides that are multiples of 16
  *   bytes, as 8-bit operands of the other expert products; a length that is not is
  *   padded by the stride, and the padding is never read as values.
- *   workspace     256-byte aligned; not needed (NULL) for 16-bit rows.
+ *   workspace     256-byte aligned, of the size that the first call gives for the
+ *                 current device (NULL where that is 0). It need not hold
+ *                 anything, and is the call's alone until the stream has passed it.
  *   Returns MR_OK, MR_ERR_PARAM_NULLPTR, MR_ERR_PARAM_INVALID,
  *   MR_ERR_WORKSPACE or MR_ERR_CUDA.
  */
-mr_status moe_grouped_matmul_int8_get_workspace_size(int64_t rows, int64_t cols, int32_t xDtype,
-                                                     uint64_t* workspaceSize);
+mr_status moe_grouped_matmul_int8_get_workspace_size(int64_t rows, int64_t numGroups, int64_t outCols,
+                                                     int64_t cols, int32_t xDtype, uint64_t* workspaceSize);
 mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int64_t xStride, const float* xScales,
                                   int64_t xScaleStride, const void* weights, const int64_t* weightStrides,
                                   const float* weightScales, const int64_t* groupList, int64_t numGroups,
@@ -701,11 +703,10 @@ mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int64_t xStride
  *   w2            int8 [experts, hidden, inter]; w2Strides as w13Strides.
  *   w2Scales      float32 [experts, hidden].
  *   y             [rows, hidden] of yDtype.
- *   The other arguments, limits and errors are moe_grouped_matmul_int8's; the
- *   workspace is always needed.
+ *   The other arguments, limits and errors are moe_grouped_matmul_int8's.
  */
-mr_status moe_expert_ffn_int8_get_workspace_size(int64_t rows, int64_t hidden, int64_t inter,
-                                                 int32_t xDtype, uint64_t* workspaceSize);
+mr_status moe_expert_ffn_int8_get_workspace_size(int64_t rows, int64_t numGroups, int64_t hidden,
+                                                 int64_t inter, int32_t xDtype, uint64_t* workspaceSize);
 mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t xStride, const float* xScales,
                               int64_t xScaleStride, const void* w13, const int64_t* w13Strides,
                               const float* w13Scales, const void* w2, const int64_t* w2Strides,

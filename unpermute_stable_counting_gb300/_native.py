@@ -53,10 +53,10 @@ SIGNATURES = {
     "moe_expert_ffn_get_workspace_size": (_I32, [_I64, _I64, _I64, _PU64]),
     "moe_expert_ffn": (_I32, [_P, _I32, _I64, _P, _PI64, _P, _PI64, _P, _P, _PI64, _P, _P, _I64, _P,
                               _I64, _I64, _I64, _I64, _I64, _P, _I32, _I64, _P, _U64, _P]),
-    "moe_grouped_matmul_int8_get_workspace_size": (_I32, [_I64, _I64, _I32, _PU64]),
+    "moe_grouped_matmul_int8_get_workspace_size": (_I32, [_I64, _I64, _I64, _I64, _I32, _PU64]),
     "moe_grouped_matmul_int8": (_I32, [_P, _I32, _I64, _P, _I64, _P, _PI64, _P, _P, _I64, _P, _I64, _I64, _I64, _I64,
                                        _I64, _P, _I32, _I64, _P, _U64, _P]),
-    "moe_expert_ffn_int8_get_workspace_size": (_I32, [_I64, _I64, _I64, _I32, _PU64]),
+    "moe_expert_ffn_int8_get_workspace_size": (_I32, [_I64, _I64, _I64, _I64, _I32, _PU64]),
     "moe_expert_ffn_int8": (_I32, [_P, _I32, _I64, _P, _I64, _P, _PI64, _P, _P, _PI64, _P, _P, _I64, _P, _I64, _I64,
                                    _I64, _I64, _I64, _P, _I32, _I64, _P, _U64, _P]),
     "moe_layer_get_workspace_size": (_I32, [_I64, _I64, _I64, _I64, _I64, _I32, _PU64]),

@@ -842,10 +842,16 @@ def moe_expert_ffn(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x_scal
 _INT8_ROWS = {torch.int8: DT_INT8, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
 
 
+def grouped_matmul_int8_workspace_size(rows: int, groups: int, out_cols: int, cols: int, x_dtype: int) -> int:
+    """Of the current device. groups: the group list's rows, -1 without a list."""
+    index = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _grouped_matmul_int8_workspace_size(index, rows, groups, out_cols, cols, x_dtype)
+
+
 @functools.lru_cache(maxsize=1024)
-def grouped_matmul_int8_workspace_size(rows: int, cols: int, x_dtype: int) -> int:
+def _grouped_matmul_int8_workspace_size(index, rows, groups, out_cols, cols, x_dtype):
     ws = ctypes.c_uint64(0)
-    _check(lib().moe_grouped_matmul_int8_get_workspace_size(rows, cols, x_dtype, ctypes.byref(ws)),
+    _check(lib().moe_grouped_matmul_int8_get_workspace_size(rows, groups, out_cols, cols, x_dtype, ctypes.byref(ws)),
            "moe_grouped_matmul_int8_get_workspace_size")
     return int(ws.value)
 
@@ -908,9 +914,9 @@ def moe_grouped_matmul_int8(x, weights, weight_scales, group_list=None, *, x_sca
     E, N = weights.shape[0], weights.shape[1]
     wa, wst, wsa = _int8_weights("weights", weights, weight_scales, (E, N, K), index)
     out, ya, ydt, yst = _out_rows(out, rows, N, out_dtype, index)
-    wsp, size = None, 0
-    if dt == DT_INT8 or workspace is not None:
-        workspace = _workspace(workspace, grouped_matmul_int8_workspace_size(rows, K, dt), index)
+    wsp, size = None, _grouped_matmul_int8_workspace_size(index, rows, groups, N, K, dt)
+    if size or workspace is not None:
+        workspace = _workspace(workspace, size, index)
         wsp, size = workspace.data_ptr(), workspace.numel()
     st = lib().moe_grouped_matmul_int8(x.data_ptr(), dt, xst, xsa, xss, wa, wst, wsa, ga, groups,
                                        _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, N, K,
@@ -919,10 +925,16 @@ def moe_grouped_matmul_int8(x, weights, weight_scales, group_list=None, *, x_sca
     return out
 
 
+def expert_ffn_int8_workspace_size(rows: int, groups: int, hidden: int, inter: int, x_dtype: int) -> int:
+    """Of the current device. groups: the group list's rows, -1 without a list."""
+    index = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _expert_ffn_int8_workspace_size(index, rows, groups, hidden, inter, x_dtype)
+
+
 @functools.lru_cache(maxsize=1024)
-def expert_ffn_int8_workspace_size(rows: int, hidden: int, inter: int, x_dtype: int) -> int:
+def _expert_ffn_int8_workspace_size(index, rows, groups, hidden, inter, x_dtype):
     ws = ctypes.c_uint64(0)
-    _check(lib().moe_expert_ffn_int8_get_workspace_size(rows, hidden, inter, x_dtype, ctypes.byref(ws)),
+    _check(lib().moe_expert_ffn_int8_get_workspace_size(rows, groups, hidden, inter, x_dtype, ctypes.byref(ws)),
            "moe_expert_ffn_int8_get_workspace_size")
     return int(ws.value)
 
@@ -945,7 +957,7 @@ def moe_expert_ffn_int8(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x
     if out_dtype is None:
         out_dtype = torch.bfloat16 if dt == DT_INT8 else x.dtype
     out, ya, ydt, yst = _out_rows(out, rows, H, out_dtype, index)
-    workspace = _workspace(workspace, expert_ffn_int8_workspace_size(rows, H, inter, dt), index)
+    workspace = _workspace(workspace, _expert_ffn_int8_workspace_size(index, rows, groups, H, inter, dt), index)
     st = lib().moe_expert_ffn_int8(x.data_ptr(), dt, xst, xsa, xss, a13, st13, s13, a2, st2, s2, ga, groups,
                                    _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, H,
                                    inter, ya, ydt, yst, workspace.data_ptr(), workspace.numel(), _raw_stream(index))

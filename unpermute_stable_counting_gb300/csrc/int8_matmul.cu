@@ -16,13 +16,15 @@
 //   warp 1       matrix instructions, 128 values of k a step
 //   warp 2       hands tiles to the warps below
 //   warp 3       TMA loads of 16-bit rows: a ring of steps
-//   warps 4-11   weights to 16 bits; each warpgroup takes every other load, since what a
-//                load costs a warp is mostly latency (both on every load, half of it each:
-//                576 rows over 64 experts, 7168 -> 4096, 345 us, and XXX so)
-//   warps 12-15  int8 rows to 16 bits (single blocks), two on every other load; or results
-//   warps 16-19  results: scales, rounding, stores
+//   warps 4-11   weights to 16 bits; of a pair each warpgroup takes every other load, of a
+//                single block one of a load's two operands
+//   four warps   int8 rows, where there are any, to 16 bits, two on every other load
+//   eight warps  results: scales, rounding, stores
 // One persistent block per SM takes tiles round robin; a pair of blocks shares a tile
-// of 256 channels, where each converts its own 128 and loads half of the rows.
+// of 256 channels, where each converts its own 128 and loads half of the rows. Where
+// single blocks would have few tiles each, they take equal shares of all tiles' loads
+// instead: a tile's sums may then come from several blocks, which leave them in the
+// workspace, and the last one to arrive adds them up, in the order of k.
 #include "groups.cuh"
 #include "tensor.cuh"
 
@@ -35,7 +37,7 @@ namespace {
 
 __device__ unsigned g_waits_out;  // blocks that left early, see mbar_wait
 
-constexpr int kThreads = 640, kConvertWarps = 8;
+constexpr int kConvertWarps = 8, kSumWarps = 8;
 constexpr int kWRows = 128, kWBytes = kWRows * 128;  // a load: 128 channels x 128 values
 
 struct Int8Args : Groups {
@@ -46,6 +48,63 @@ struct Int8Args : Groups {
     void* y;
     int64_t y_stride;
     int y_dtype;
+    // equal shares of the loads (NULL: whole tiles round robin)
+    float* parts;           // two to a block, of part_rows rows of 256 sums
+    int part_rows, part_loads;  // a share is this many loads at least
+    unsigned* tickets;      // of each tile: blocks that have left their sums, 0 at the start
+};
+
+constexpr int kMostShares = 256;  // groups of a list that is walked once more, for the number of its tiles
+
+// The tiles, or parts of tiles, that a block (pair) takes: loads [kb0, kb1) of tile t.
+// Every lane of the warp calls with the same values.
+template <typename W, bool SHARES> struct Items {
+    W walk;
+    Tile tile;
+    int t, kb0, kb1;
+    int at, end, total, blocks;   // shares: loads of all tiles (2^17 of each of 16 tiles for each SM, at most)
+
+    __device__ __forceinline__ void begin(const Int8Args& a, int lane, int first, int step) {
+        walk.begin(a, lane);
+        t = first - step;
+        if (!SHARES || !a.parts) return;
+        int tiles = walk.total;
+        if (a.G > 32) {
+            W all = walk;
+            for (int g = 32; g < a.G; g += 32) {
+                all.base_row = min(all.base_row + all.window_rows, (uint32_t)a.rows);
+                all.first = g;
+                all.load(a, lane);
+                tiles += all.total;
+            }
+        }
+        total = tiles * a.KB;
+        blocks = min((int)gridDim.x, total / a.part_loads + 1);
+        at = end = 0;
+        if (first < blocks) at = (int)((int64_t)first * total / blocks), end = (int)((int64_t)(first + 1) * total / blocks);
+    }
+    __device__ __forceinline__ bool next(const Int8Args& a, int lane, int channels, int step) {
+        if (SHARES && a.parts) {
+            if (at >= end) return false;
+            t = at / a.KB;
+            kb0 = at - t * a.KB;
+            kb1 = min(a.KB, kb0 + (end - at));
+            at += kb1 - kb0;
+        } else {
+            t += step;
+            kb0 = 0;
+            kb1 = a.KB;
+        }
+        return walk.next(a, lane, t, channels, tile);
+    }
+    __device__ __forceinline__ int owner(int load) const { return (int)(((int64_t)(load + 1) * blocks - 1) / total); }
+};
+
+// A tile, or the part of one: for the warps that do not walk the list.
+struct Item {
+    Tile tile;
+    int t, loads;
+    int first, last, block;  // blocks that have a part of the tile; this one
 };
 
 enum { kInt8 = 0, kF16 = 1, kBf16 = 2 };  // rows
@@ -61,26 +120,31 @@ template <int XT, bool SWIGLU, bool PAIR> struct Cfg {
     static constexpr int kPlanes = PAIR ? 1 : 2;
     static constexpr int kLoadRows = PAIR ? kRows / 2 : kRows;      // of the rows, those this block loads
     static constexpr int kBox = PAIR ? 64 : 32;                     // rows of a TMA load
-    // Steps of converted weights and of 16-bit rows held. (A step of 64 values costs the thread that issues the
-    // instructions its two waits and a commit twice: 16384 x 7168 x 7168 took 884 instead of 848 us.)
-    static constexpr int kSteps = PAIR ? 3 : 2;
-    // warps of int8 rows, of results
-    static constexpr int kRowWarps = XT == kInt8 ? 4 : 0, kSumWarps = PAIR ? 8 : 4;
-    static constexpr int kStepCols = 64 * kPlanes;                  // tensor memory of a step's weights
+    // Steps of converted weights held, one for each operand and load, and of 16-bit rows. The way round (converted,
+    // multiplied, free again) takes several steps' time: with three steps instead of four the dense 16384 x 7168 x
+    // 7168 took pairs 851 us instead of 835; with two of both operands single blocks took XXX for 576 rows over 64
+    // experts, 7168 -> 4096. (A step of 64 values costs the thread that issues the instructions its waits and
+    // commit twice: 884 instead of 848 us for the dense one.)
+    static constexpr int kSteps = PAIR ? 4 : 5, kRowSteps = PAIR ? 4 : 2;
+    static constexpr int kRowWarps = XT == kInt8 ? 4 : 0;           // warps of int8 rows
+    static constexpr int kWarps = 4 + kConvertWarps + kRowWarps + kSumWarps, kThreads = 32 * kWarps;
+    static constexpr int kStepCols = 64;                            // tensor memory of a step's weights
     static constexpr int kACols = kRows * kPlanes;                  // tensor memory: sums, then weights
     static_assert(kACols + kSteps * kStepCols <= 512, "tensor memory");
-    static constexpr int kLoads = PAIR ? (SWIGLU ? 6 : 7) : XT == kInt8 ? 4 : 5;
+    static constexpr int kLoads = PAIR ? (SWIGLU ? 4 : 6) : XT == kInt8 ? 4 : 5;
     static constexpr int kLoadBytes = kPlanes * kWBytes + (XT == kInt8 ? kLoadRows * 128 : 0);
     static constexpr int kPartBytes = kLoadRows * 128, kStepBytes = kPartBytes * 2;  // 64 values, 128
-    static constexpr int kHalf = PAIR ? kRows / 2 : kRows;          // rows of a warpgroup of results
+    static constexpr int kHalf = kRows / 2;                         // rows of a warpgroup of results
     static constexpr int kChunk = PAIR ? 32 : 16;                   // of them, those read at once
     static constexpr bool kSwap = SWIGLU && PAIR;                   // the factors meet in shared memory
     static constexpr int kSwapBytes = kSwap ? 2 * kChunk / 2 * 128 : 0;  // of a warp of results
-    // registers of a thread of the first four warps, of the converters, of the next four warps and of the results;
-    // blocks are launched with 96 for each
-    static constexpr int kRegs[4] = {48, PAIR ? 80 : 112, PAIR ? 136 : 80, PAIR ? 136 : 128};
-    static_assert(kRegs[0] + 2 * kRegs[1] + kRegs[2] + kRegs[3] <= 5 * 96, "registers of a block");
-    static constexpr int kSmem = 1024 + kLoads * kLoadBytes + kSteps * kStepBytes + kSumWarps * kSwapBytes;
+    // registers of a thread of the first four warps, of the converters, of int8 rows and of the results; blocks are
+    // launched with as many for all as there are
+    static constexpr int kRegs[4] = {PAIR ? 48 : 56, 80, 56, PAIR ? 136 : XT == kInt8 ? 104 : 128};
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static_assert(4 * kRegs[0] + kConvertWarps * kRegs[1] + kRowWarps * kRegs[2] + kSumWarps * kRegs[3] <=
+                  kWarps * kLaunchRegs, "registers of a block");
+    static constexpr int kSmem = 1024 + kLoads * kLoadBytes + kRowSteps * kStepBytes + kSumWarps * kSwapBytes;
 };
 
 // Matrix instruction with A in tensor memory.
@@ -144,41 +208,47 @@ __device__ __forceinline__ uint32_t pack2(int dt, float a, float b) {
 }
 
 template <int XT, bool SWIGLU, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
     int8_matmul_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const Int8Args a) {
     using C = Cfg<XT, SWIGLU, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t l_full[C::kLoads], l_empty[C::kLoads];                   // loads
-    __shared__ __align__(8) uint64_t x_full[C::kSteps], a_full[C::kSteps], a_empty[C::kSteps];  // steps
+    __shared__ __align__(8) uint64_t a_full[C::kSteps], a_empty[C::kSteps];                   // steps of weights
+    __shared__ __align__(8) uint64_t x_full[C::kRowSteps], x_empty[C::kRowSteps];             // and of rows
     __shared__ __align__(8) uint64_t t_full, t_empty, i_full[2], i_empty[2];
-    __shared__ Tile info[2];
+    __shared__ Item info[2];
+    __shared__ __align__(8) uint64_t part_bar[2];
+    __shared__ unsigned ticket;
     __shared__ __align__(8) uint64_t swap_bar[4], drain_bar;
     __shared__ uint32_t tmem_base, abort_word;
 
     uint8_t* loads = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     static_assert(C::kSmem + 1024 <= 232448, "shared memory of a block");
     uint8_t* rows16 = loads + C::kLoads * C::kLoadBytes;
-    float* swap = reinterpret_cast<float*>(rows16 + C::kSteps * C::kStepBytes);
+    float* swap = reinterpret_cast<float*>(rows16 + C::kRowSteps * C::kStepBytes);
     volatile uint32_t* abort = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kBlocks = PAIR ? 2 : 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kLoads; ++i)
-            mbar_init(smem_u32(&l_full[i]), 1), mbar_init(smem_u32(&l_empty[i]), (kConvertWarps + C::kRowWarps) / 2);
+            mbar_init(smem_u32(&l_full[i]), 1), mbar_init(smem_u32(&l_empty[i]), kConvertWarps / (PAIR ? 2 : 1) + C::kRowWarps / 2);
         for (int i = 0; i < C::kSteps; ++i) {
-            mbar_init(smem_u32(&x_full[i]), 1);
-            mbar_init(smem_u32(&a_full[i]), (kBlocks * kConvertWarps + C::kRowWarps) / 2);
+            mbar_init(smem_u32(&a_full[i]), kBlocks * kConvertWarps / 2);
             mbar_init(smem_u32(&a_empty[i]), 1);
         }
+        for (int i = 0; i < C::kRowSteps; ++i)
+            mbar_init(smem_u32(&x_full[i]), XT == kInt8 ? C::kRowWarps / 2 : 1), mbar_init(smem_u32(&x_empty[i]), 1);
         mbar_init(smem_u32(&t_full), 1);
-        mbar_init(smem_u32(&t_empty), kBlocks * C::kSumWarps);
+        mbar_init(smem_u32(&t_empty), kBlocks * kSumWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&i_full[i]), 1);
-            mbar_init(smem_u32(&i_empty[i]), kConvertWarps + C::kRowWarps + C::kSumWarps);
+            mbar_init(smem_u32(&i_empty[i]), kConvertWarps + C::kRowWarps + kSumWarps);
         }
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&swap_bar[i]), 2);
+        mbar_init(smem_u32(&part_bar[0]), kSumWarps);
+        mbar_init(smem_u32(&part_bar[1]), 1);
         mbar_init(smem_u32(&drain_bar), 1);
         abort_word = 0u;
         mbar_init_fence();
@@ -195,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
     pdl_enter();
 
-    Walk<C::kRows, true> walk;
-    Tile tile;
+    Items<Walk<C::kRows, true>, !PAIR> items;
+    const Tile& tile = items.tile;
     uint32_t it = 0;  // loads or steps that this warp has taken, over all of its tiles
     bool ok = true;
     // columns of a tile's instructions, and boxes of rows that this block loads
@@ -206,11 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         regs_dec<C::kRegs[0]>();
         if (warp == 0) {
-            walk.begin(a, lane);
-            for (int t = first; ok && walk.next(a, lane, t, C::kChannels, tile); t += step) {
+            items.begin(a, lane, first, step);
+            while (ok && items.next(a, lane, C::kChannels, step)) {
                 const int boxes = XT == kInt8 ? boxes_of(tile.rows) : 0;
                 if (elect_one()) {
-                    for (int kb = 0; kb < a.KB; ++kb, ++it) {
+                    for (int kb = items.kb0; kb < items.kb1; ++kb, ++it) {
                         const uint32_t st = it % C::kLoads;
                         ok = mbar_wait<PAIR>(smem_u32(&l_empty[st]), ((it / C::kLoads) & 1) ^ 1, abort);
                         if (!ok) break;
@@ -239,26 +309,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             ok = rank == 0;
-            walk.begin(a, lane);
-            uint32_t n = 0;
-            for (int t = first; ok && walk.next(a, lane, t, C::kChannels, tile); t += step, ++n) {
+            items.begin(a, lane, first, step);
+            for (uint32_t n = 0; ok && items.next(a, lane, C::kChannels, step); ++n) {
                 const uint32_t idesc = idesc_16(kWRows * kBlocks, columns(tile.rows), XT == kBf16);
                 if (elect_one()) {
                     ok = mbar_wait<PAIR>(smem_u32(&t_empty), (n & 1) ^ 1, abort);
-                    for (int k = 0; ok && k < a.KB; ++k, ++it) {
-                        const uint32_t s = it % C::kSteps, parity = (it / C::kSteps) & 1;
-                        ok = mbar_wait<PAIR>(smem_u32(&a_full[s]), parity, abort);
-                        if (XT != kInt8) ok = ok && mbar_wait<PAIR>(smem_u32(&x_full[s]), parity, abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t b = smem_desc(smem_u32(rows16 + s * C::kStepBytes));
+                    for (int k = items.kb0; ok && k < items.kb1; ++k, ++it) {
+                        const uint32_t r = it % C::kRowSteps;
+                        ok = mbar_wait<PAIR>(smem_u32(&x_full[r]), (it / C::kRowSteps) & 1, abort);
+                        const uint64_t b = smem_desc(smem_u32(rows16 + r * C::kStepBytes));
 #pragma unroll
-                        for (int p = 0; p < C::kPlanes; ++p)
+                        for (int p = 0; p < C::kPlanes; ++p) {
+                            const uint32_t i = it * C::kPlanes + p, s = i % C::kSteps;
+                            ok = ok && mbar_wait<PAIR>(smem_u32(&a_full[s]), (i / C::kSteps) & 1, abort);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                mma_16_tmem<PAIR>(tmem + p * C::kRows, tmem + C::kACols + s * C::kStepCols + p * 64 + 8 * j,
-                                                  b + j / 4 * (C::kPartBytes / 16) + 2 * (j % 4), idesc, k > 0 || j > 0);
-                        tc_commit<PAIR>(smem_u32(&a_empty[s]));
+                                mma_16_tmem<PAIR>(tmem + p * C::kRows, tmem + C::kACols + s * C::kStepCols + 8 * j,
+                                                  b + j / 4 * (C::kPartBytes / 16) + 2 * (j % 4), idesc,
+                                                  k > items.kb0 || j > 0);
+                            tc_commit<PAIR>(smem_u32(&a_empty[s]));
+                        }
+                        if (!ok) break;
+                        if (!PAIR) tc_commit(smem_u32(&x_empty[r]));
                     }
                     if (ok) tc_commit<PAIR>(smem_u32(&t_full));
                 }
@@ -268,27 +342,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 2) {
             // tiles for the warps below; one of no rows ends them
-            walk.begin(a, lane);
-            uint32_t n = 0;
-            for (int t = first;; t += step, ++n) {
-                const bool more = walk.next(a, lane, t, C::kChannels, tile);
+            items.begin(a, lane, first, step);
+            for (uint32_t n = 0;; ++n) {
+                const bool more = items.next(a, lane, C::kChannels, step);
                 if (!mbar_wait<PAIR>(smem_u32(&i_empty[n & 1]), ((n >> 1) & 1) ^ 1, abort)) break;
                 if (lane == 0) {
-                    if (!more) tile = Tile{0, 0, 0, 0};
-                    info[n & 1] = tile;
+                    Item& i = info[n & 1];
+                    i.tile = more ? tile : Tile{0, 0, 0, 0};
+                    if (more) {
+                        i.t = items.t;
+                        i.loads = items.kb1 - items.kb0;
+                        i.first = i.last = i.block = first;
+                        if (!PAIR && a.parts) {
+                            i.first = items.owner(items.t * a.KB);
+                            i.last = items.owner(items.t * a.KB + a.KB - 1);
+                        }
+                    }
                     mbar_arrive(smem_u32(&i_full[n & 1]));
                 }
                 if (!more) break;
             }
         } else if (XT != kInt8) {
-            walk.begin(a, lane);
-            for (int t = first; ok && walk.next(a, lane, t, C::kChannels, tile); t += step) {
+            items.begin(a, lane, first, step);
+            while (ok && items.next(a, lane, C::kChannels, step)) {
                 const int boxes = boxes_of(tile.rows);
                 const int row0 = tile.row0 + (int)rank * columns(tile.rows) / 2;
                 if (elect_one()) {
-                    for (int k = 0; k < a.KB; ++k, ++it) {
-                        const uint32_t s = it % C::kSteps;
-                        ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
+                    for (int k = items.kb0; k < items.kb1; ++k, ++it) {
+                        // (pairs' rows and weights have the same steps, and one commit for both)
+                        const uint32_t s = it % C::kRowSteps;
+                        static_assert(!PAIR || C::kRowSteps == C::kSteps, "steps of pairs");
+                        ok = mbar_wait<PAIR>(smem_u32(PAIR ? &a_empty[s] : &x_empty[s]), ((it / C::kRowSteps) & 1) ^ 1, abort);
                         if (!ok) break;
                         const uint32_t own = smem_u32(&x_full[s]), bar = PAIR ? map_cluster(own, 0) : own;
                         const uint32_t dst = smem_u32(rows16 + s * C::kStepBytes);
@@ -306,51 +390,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp < 4 + kConvertWarps) {
-        if constexpr (PAIR) regs_dec<C::kRegs[1]>();
-        else regs_inc<C::kRegs[1]>();
+        static_assert(C::kRegs[1] <= C::kLaunchRegs, "registers of the converters");
+        if constexpr (C::kRegs[1] < C::kLaunchRegs) regs_dec<C::kRegs[1]>();
         const uint32_t turn = (warp - 4) >> 2;
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t to = tmem + ((uint32_t)quarter << 21) + C::kACols;  // 32 lanes << 16
         for (uint32_t n = 0; ok; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
             if (!ok) break;
-            const int rows = info[n & 1].rows;
+            const int rows = info[n & 1].tile.rows, count = info[n & 1].loads;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
             if (rows == 0) break;
-            for (int kb = 0; kb < a.KB; ++kb, ++it) {
-                if ((it & 1) != turn) continue;
-                const uint32_t st = it % C::kLoads, s = it % C::kSteps;
+            for (int kb = 0; kb < count; ++kb, ++it) {
+                if (PAIR && (it & 1) != turn) continue;
+                const uint32_t st = it % C::kLoads, i = PAIR ? it : 2 * it + turn, s = i % C::kSteps;
                 ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
                 if (!ok) break;
-                const uint8_t* src = loads + st * C::kLoadBytes + row * 128;
+                const uint8_t* src = loads + st * C::kLoadBytes + (PAIR ? 0 : turn * kWBytes) + row * 128;
+                uint4 w[8];
 #pragma unroll
-                for (int p = 0; p < C::kPlanes; ++p) {
-                    uint4 w[8];
+                for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j] = *reinterpret_cast<const uint4*>(src + p * kWBytes + ((j ^ (row & 7)) << 4));
-                    if (p == C::kPlanes - 1) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        widen4<XT == kBf16>(w[4 * h + j].x, v[8 * j], v[8 * j + 1]);
+                        widen4<XT == kBf16>(w[4 * h + j].y, v[8 * j + 2], v[8 * j + 3]);
+                        widen4<XT == kBf16>(w[4 * h + j].z, v[8 * j + 4], v[8 * j + 5]);
+                        widen4<XT == kBf16>(w[4 * h + j].w, v[8 * j + 6], v[8 * j + 7]);
                     }
-                    if (p == 0) {
-                        ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
+                    if (h == 0) {  // (the first half is converted before the step is free)
+                        ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((i / C::kSteps) & 1) ^ 1, abort);
                         if (!ok) break;
                         tc_fence_after();
                     }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t v[32];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            widen4<XT == kBf16>(w[4 * h + j].x, v[8 * j], v[8 * j + 1]);
-                            widen4<XT == kBf16>(w[4 * h + j].y, v[8 * j + 2], v[8 * j + 3]);
-                            widen4<XT == kBf16>(w[4 * h + j].z, v[8 * j + 4], v[8 * j + 5]);
-                            widen4<XT == kBf16>(w[4 * h + j].w, v[8 * j + 6], v[8 * j + 7]);
-                        }
-                        tmem_st32(to + s * C::kStepCols + p * 64 + h * 32, v);
-                    }
+                    tmem_st32(to + s * C::kStepCols + h * 32, v);
                 }
                 if (!ok) break;
                 tmem_st_wait();
@@ -362,25 +440,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (!PAIR && warp < 8 + kConvertWarps) {
+    } else if (warp < 4 + kConvertWarps + C::kRowWarps) {
         regs_dec<C::kRegs[2]>();
         const uint32_t turn = (warp >> 1) & 1;
         const int h = warp & 1;  // half of a load's values
         for (uint32_t n = 0; ok && XT == kInt8; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
             if (!ok) break;
-            const int rows = info[n & 1].rows;
+            const int rows = info[n & 1].tile.rows, count = info[n & 1].loads;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
             if (rows == 0) break;
-            for (int kb = 0; kb < a.KB; ++kb, ++it) {
+            for (int kb = 0; kb < count; ++kb, ++it) {
                 if ((it & 1) != turn) continue;
-                const uint32_t st = it % C::kLoads, s = it % C::kSteps;
+                const uint32_t st = it % C::kLoads, s = it % C::kRowSteps;
                 ok = mbar_wait<PAIR>(smem_u32(&l_full[st]), (it / C::kLoads) & 1, abort);
                 if (!ok) break;
                 const uint8_t* src = loads + st * C::kLoadBytes + C::kPlanes * kWBytes + lane * 128;
                 uint8_t* dst = rows16 + s * C::kStepBytes + h * C::kPartBytes + lane * 128;
-                ok = mbar_wait<PAIR>(smem_u32(&a_empty[s]), ((it / C::kSteps) & 1) ^ 1, abort);
+                ok = mbar_wait<PAIR>(smem_u32(&x_empty[s]), ((it / C::kRowSteps) & 1) ^ 1, abort);
                 if (!ok) break;
                 for (int i = 0; i < rows; i += 32) {
                     uint4 x[4];
@@ -402,19 +480,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&l_empty[st]));
                 smem_proxy_fence();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&a_full[s]));
+                if (lane == 0) mbar_arrive(smem_u32(&x_full[s]));
             }
         }
     } else {
         regs_inc<C::kRegs[3]>();
-        const int half = PAIR ? (warp - 4 - kConvertWarps) >> 2 : 0, quarter = warp & 3;
+        const int me = warp - (C::kWarps - kSumWarps), half = me >> 2, quarter = warp & 3;
         const uint32_t from = tmem + ((uint32_t)quarter << 21);
-        const int me = warp - (kThreads / 32 - C::kSumWarps);  // among the warps of results
-        uint32_t swaps = 0;
+        uint32_t swaps = 0;  // of factors, or of tickets
         for (uint32_t n = 0;; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
             if (!ok) break;
-            tile = info[n & 1];
+            const Item item = info[n & 1];
+            Tile tile = item.tile;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&i_empty[n & 1]));
             if (tile.rows == 0) break;
@@ -425,13 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* ws = a.w_scales + ((int64_t)tile.expert * (SWIGLU ? 2 : 1) + factor) * a.N;
             const bool real = col < a.N;
             // rows of this warp, may be none: those of half of the tile's columns
-            const int cols = PAIR ? (columns(tile.rows) / 2 + 15) / 16 * 16 : C::kHalf;
+            const int cols = (columns(tile.rows) / 2 + 15) / 16 * 16;
             const int mine = min(cols, tile.rows - half * cols);
             const int64_t row0 = (int64_t)tile.row0 + half * cols;
             const bool inside = mine <= 0 || MR_IN_RANGE(row0 + mine - 1, a.rows, 912);
-            float xs[C::kHalf / 32];  // lane i: those of rows i, 32 + i, ...
+            constexpr int kGroups = (C::kHalf + 31) / 32;
+            float xs[kGroups];  // lane i: those of rows i, 32 + i, ...
 #pragma unroll
-            for (int i = 0; i < C::kHalf / 32; ++i)
+            for (int i = 0; i < kGroups; ++i)
                 xs[i] = a.x_scales && inside && 32 * i + lane < mine ? a.x_scales[(row0 + 32 * i + lane) * a.xs_row] : 1.0f;
             constexpr int kLd = C::kChunk, kKeep = C::kSwap ? kLd / 2 : kLd;  // rows read at once, and of them this warp's
             const bool wide = !SWIGLU && a.y_dtype == MR_DTYPE_F32;
@@ -443,9 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(__uint_as_float(v[j]), by);
                 if (a.x_scales) {
+                    float s = xs[0];
 #pragma unroll
-                    for (int j = 0; j < kLd; ++j)
-                        f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, xs[(c + j) / 32], (c + j) % 32));
+                    for (int i = 1; i < kGroups; ++i)
+                        if (c / 32 == i) s = xs[i];
+#pragma unroll
+                    for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, s, c % 32 + j));
                 }
             };
             if constexpr (!PAIR) {
@@ -456,38 +538,99 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait(smem_u32(&t_full), n & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < C::kHalf; c += kLd) {
-                    if (c >= mine) break;
-                    uint32_t v[kLd], u[kLd];
-                    tmem_load(v, from + c);
-                    tmem_ld_wait(v);
-                    tmem_load(u, from + C::kRows + c);
+                // rows c .. of the result from their sums
+                auto finish = [&](int c, const uint32_t (&v)[kLd], const uint32_t (&u)[kLd]) {
                     float f[kLd], g[kLd];
                     scaled(v, w_scale, c, f);
-                    tmem_ld_wait(u);
-                    if (c + kLd >= mine) {  // everything is in registers: hand the sums back before the last stores
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&t_empty));
-                    }
                     scaled(u, w_scale1, c, g);
                     if (SWIGLU) {
 #pragma unroll
                         for (int j = 0; j < kLd; ++j) f[j] = silu(f[j]) * g[j];
                     }
-                    if (!inside) continue;
+                    if (!inside) return;
                     char* to = y + c * y_step;
 #pragma unroll
                     for (int j = 0; j < kLd; ++j, to += y_step) {
-                        if (c + j >= mine) break;
+                        const bool in = c + j < mine;
                         if (wide) {
-                            if (real) *reinterpret_cast<float*>(to) = f[j];
-                            if (real1) *reinterpret_cast<float*>(to + kWRows * 4) = g[j];
+                            if (in && real) *reinterpret_cast<float*>(to) = f[j];
+                            if (in && real1) *reinterpret_cast<float*>(to + kWRows * 4) = g[j];
                         } else {
                             const uint32_t w = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], g[j]);
-                            if (real) *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
-                            if (!SWIGLU && real1) *reinterpret_cast<uint16_t*>(to + kWRows * 2) = (uint16_t)(w >> 16);
+                            if (in && real) *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
+                            if (!SWIGLU && in && real1) *reinterpret_cast<uint16_t*>(to + kWRows * 2) = (uint16_t)(w >> 16);
+                        }
+                    }
+                };
+                // where the block's sums of a tile in several parts go: its first part starts a tile, or is in one
+                const bool whole = item.first == item.last;
+                auto part_of = [&](int block) {
+                    return a.parts + (((int64_t)(2 * block + (block == item.first)) * a.part_rows + half * cols) << 8) +
+                           quarter * 32 + lane;
+                };
+                float* part = part_of(item.block);
+                auto hand_back = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&t_empty));
+                };
+                if (mine <= 0) hand_back();
+#pragma unroll
+                for (int c = 0; c < C::kHalf; c += kLd) {
+                    if (c >= mine) break;
+                    uint32_t v[kLd], u[kLd];
+                    tmem_load(v, from + half * cols + c);
+                    tmem_load(u, from + C::kRows + half * cols + c);
+                    tmem_ld_wait(v);
+                    tmem_ld_wait(u);
+                    if (c + kLd >= mine) hand_back();  // everything is in registers
+                    if (whole) {
+                        finish(c, v, u);
+                        continue;
+                    }
+#pragma unroll
+                    for (int j = 0; j < kLd; ++j)
+                        if (c + j < mine && MR_IN_RANGE(half * cols + c + j, a.part_rows, 913)) {
+                            __stcg(part + (c + j) * 256, __uint_as_float(v[j]));
+                            __stcg(part + (c + j) * 256 + 128, __uint_as_float(u[j]));
+                        }
+                }
+                if (!whole) {
+                    // the warps' sums are out, one of them takes a ticket for all
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&part_bar[0]));
+                    if (me == 0) {
+                        ok = mbar_wait(smem_u32(&part_bar[0]), swaps & 1, abort);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            ticket = atomicAdd(a.tickets + item.t, 1u);
+                            __threadfence();
+                            mbar_arrive(smem_u32(&part_bar[1]));
+                        }
+                    }
+                    ok = mbar_wait(smem_u32(&part_bar[1]), swaps & 1, abort);
+                    ++swaps;
+                    if (!ok) break;
+                    if (ticket == (unsigned)(item.last - item.first)) {
+                        __threadfence();
+                        for (int c = 0; c < mine; c += kLd) {
+                            float f[kLd], g[kLd];
+#pragma unroll
+                            for (int j = 0; j < kLd; ++j) f[j] = g[j] = 0.0f;
+                            for (int b = item.first; b <= item.last; ++b) {
+                                const float* from_b = part_of(b) + c * 256;
+#pragma unroll
+                                for (int j = 0; j < kLd; ++j)
+                                    if (c + j < mine) {
+                                        f[j] = __fadd_rn(f[j], __ldcg(from_b + j * 256));
+                                        g[j] = __fadd_rn(g[j], __ldcg(from_b + j * 256 + 128));
+                                    }
+                            }
+                            uint32_t v[kLd], u[kLd];
+#pragma unroll
+                            for (int j = 0; j < kLd; ++j) v[j] = __float_as_uint(f[j]), u[j] = __float_as_uint(g[j]);
+                            finish(c, v, u);
                         }
                     }
                 }
@@ -560,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t k = it > C::kLoads ? it - C::kLoads : 0; k < it; ++k)
                 mbar_drain(smem_u32(&l_full[k % C::kLoads]), (k / C::kLoads) & 1);
         if (XT != kInt8 && warp == 3 && rank == 0)
-            for (uint32_t k = it > C::kSteps ? it - C::kSteps : 0; k < it; ++k)
-                mbar_drain(smem_u32(&x_full[k % C::kSteps]), (k / C::kSteps) & 1);
+            for (uint32_t k = it > C::kRowSteps ? it - C::kRowSteps : 0; k < it; ++k)
+                mbar_drain(smem_u32(&x_full[k % C::kRowSteps]), (k / C::kRowSteps) & 1);
         if (warp == 1 && rank == 0) {
             if (elect_one()) tc_commit<PAIR>(smem_u32(&drain_bar));
             mbar_drain(smem_u32(&drain_bar), 0);
@@ -609,10 +752,11 @@ bool aligned16(const void* p) { return aligned(p, 16); }
 
 template <int XT, bool SWIGLU, bool PAIR>
 cudaError_t launch_int8(const CUtensorMap (&m)[2], const Int8Args& a, int64_t tiles, cudaStream_t s) {
+    if (a.parts) tiles = tiles * a.KB / a.part_loads + 1;
     auto kernel = int8_matmul_kernel<XT, SWIGLU, PAIR>;
     constexpr int smem = Cfg<XT, SWIGLU, PAIR>::kSmem;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Cfg<XT, SWIGLU, PAIR>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -657,14 +801,40 @@ struct Product {
     bool swiglu;
 };
 
-bool use_pairs(int64_t rows, int64_t G) { return rows > 96 * std::min<int64_t>(G, rows); }
+// The tiles of a product, or more.
+int64_t most_tiles(int64_t rows, int64_t G, int64_t N, bool pair, bool swiglu) {
+    const int64_t down = std::min<int64_t>((int64_t)ceil_div(rows, pair ? 256 : 96) + G - 1, rows);
+    return down * ceil_div(N, swiglu ? 128 : 256);
+}
+
+// Pairs of blocks where the products count, single blocks where the weights' way from HBM does: a tile for
+// each SM, of groups of few rows (int8 rows, 7168 -> 4096: 576 of 64 groups 310 us in single blocks, 365 in pairs;
+// 4096 -> 4096: 1000 rows of 16 groups 71 and 79; 4096 -> 2048: 4000 rows of 64 groups 128 and 133, 8000 195 and 167;
+// 515 rows of 6 groups through the network, 1080 / 712, 49 and 37). Up to 32 rows the blocks may share tiles (below).
+bool use_pairs(int64_t rows, int64_t G, int64_t N, bool swiglu) {
+    if (rows <= 32) return false;
+    return rows > 64 * std::min<int64_t>(G, rows) || most_tiles(rows, G, N, false, swiglu) < device_sm_count();
+}
+
+// Whether single blocks take equal shares of the loads: where few rows leave half of the SMs without a
+// tile of their own (rows x cols -> channels, with and without: 1 x 4096 -> 2048 18 and 25 us, 1 x 7168 -> 7168
+// 27 and 40, 32 x 7168 -> 4096 32 and 40). With a tile for each SM adding up costs more than it
+// gives (8 rows of 8 groups, 7168 -> 4096: 63 and 59), and so it does for short rows (1 x 1024 -> 1024: 15 and 13) and with
+// more sums to add up (1003 rows of 12 groups, 1000 -> 1100: 49 and 19).
+bool use_shares(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu) {
+    return rows <= 32 && K > 15 * 128 && G <= kMostShares &&
+           most_tiles(rows, G, N, false, swiglu) <= device_sm_count() / 2;
+}
+int64_t part_rows(int64_t rows) { return std::min<int64_t>(96, (rows + 15) / 16 * 16); }
+uint64_t part_bytes(int64_t rows) { return (uint64_t)2 * device_sm_count() * part_rows(rows) * 1024; }
+uint64_t ticket_bytes(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu) {
+    return use_shares(rows, G, N, K, swiglu) ? align_up((uint64_t)most_tiles(rows, G, N, false, swiglu) * 4, 256) : 0;
+}
 
 mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
-    const int tile_m = pair ? 256 : 96, channels = p.swiglu ? 128 : 256;
-    const int64_t m_tiles = std::min<int64_t>((int64_t)ceil_div(a.rows, tile_m) + a.G - 1, a.rows);  // or fewer
-    a.n_tiles = ceil_div(a.N, channels);
+    a.n_tiles = ceil_div(a.N, p.swiglu ? 128 : 256);
     a.KB = ceil_div(p.K, 128);
-    const int64_t tiles = m_tiles * a.n_tiles;
+    const int64_t tiles = most_tiles(a.rows, a.G, a.N, pair, p.swiglu);
     if (tiles > INT32_MAX) return MR_ERR_PARAM_INVALID;
     CUtensorMap m[2];
     const bool eight = p.xt == kInt8;
@@ -722,6 +892,36 @@ cudaError_t prepare_rows(Product& p, const Int8Args& a, bool pair, const int64_t
     return e;
 }
 
+// A call's workspace: wide rows, the network's h, then tickets of each product and sums of parts of tiles.
+struct Room {
+    uint64_t x, h, tickets[2], parts;
+    uint64_t total() const { return x + h + tickets[0] + tickets[1] + parts; }
+};
+Room matmul_room(int64_t rows, int64_t G, int64_t N, int64_t K, int32_t dt) {
+    Room r{dt == MR_DTYPE_INT8 && use_pairs(rows, G, N, false) ? wide_bytes(rows, K) : 0, 0, {ticket_bytes(rows, G, N, K, false), 0}, 0};
+    r.parts = r.tickets[0] ? part_bytes(rows) : 0;
+    return r;
+}
+Room ffn_room(int64_t rows, int64_t G, int64_t hidden, int64_t inter, int32_t dt) {
+    Room r{dt == MR_DTYPE_INT8 && use_pairs(rows, G, inter, true) ? wide_bytes(rows, hidden) : 0, wide_bytes(rows, inter),
+           {ticket_bytes(rows, G, inter, hidden, true), ticket_bytes(rows, G, hidden, inter, false)}, 0};
+    r.parts = r.tickets[0] || r.tickets[1] ? part_bytes(rows) : 0;
+    return r;
+}
+// Tickets at 0 (nothing keeps the workspace between calls), where products take some.
+cudaError_t clear_tickets(const Room& r, char* workspace, cudaStream_t s) {
+    const uint64_t n = r.tickets[0] + r.tickets[1];
+    return n ? cudaMemsetAsync(workspace + r.x + r.h, 0, n, s) : cudaSuccess;
+}
+// The product's share of the room.
+void take_room(Int8Args& a, const Room& r, char* workspace, int product) {
+    char* tickets = workspace + r.x + r.h;
+    a.parts = r.tickets[product] ? reinterpret_cast<float*>(tickets + r.tickets[0] + r.tickets[1]) : nullptr;
+    a.part_rows = (int)part_rows(a.rows);
+    a.part_loads = a.rows > 8 ? 8 : 4;  // (16 x 4096 -> 4096: 21 us, with 4 loads 24; 1 x 4096 -> 2048: 18, with 8 19)
+    a.tickets = reinterpret_cast<unsigned*>(tickets + (product ? r.tickets[0] : 0));
+}
+
 // Checks that both products make of their weights; wr, wm: byte strides.
 bool weight_strides(const int64_t* strides, int64_t matrices, int64_t N, int64_t K, int64_t* wr, int64_t* wm) {
     const int64_t top = INT64_C(1) << 40;
@@ -750,11 +950,11 @@ cudaError_t waits_out_int8_matmul(unsigned* out, bool reset) {
 
 using namespace mr;
 
-extern "C" mr_status moe_grouped_matmul_int8_get_workspace_size(int64_t rows, int64_t cols, int32_t xDtype,
-                                                                uint64_t* workspaceSize) {
-    if (!row_type(xDtype) || !common_sizes(rows, 1, 0, cols, 1)) return MR_ERR_PARAM_INVALID;
+extern "C" mr_status moe_grouped_matmul_int8_get_workspace_size(int64_t rows, int64_t numGroups, int64_t outCols,
+                                                                int64_t cols, int32_t xDtype, uint64_t* workspaceSize) {
+    if (!row_type(xDtype) || !common_sizes(rows, 1, numGroups, outCols, cols)) return MR_ERR_PARAM_INVALID;
     if (!workspaceSize) return MR_ERR_PARAM_NULLPTR;
-    *workspaceSize = xDtype == MR_DTYPE_INT8 ? wide_bytes(rows, cols) : 0;
+    *workspaceSize = rows && numGroups ? matmul_room(rows, numGroups < 0 ? 1 : numGroups, outCols, cols, xDtype).total() : 0;
     return MR_OK;
 }
 
@@ -776,10 +976,12 @@ extern "C" mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int6
     if (!weight_strides(weightStrides, experts, outCols, cols, &wr, &wm)) return MR_ERR_PARAM_INVALID;
     if (xScales && (xScaleStride < 0 || xScaleStride > top)) return MR_ERR_PARAM_INVALID;
     if (rows == 0) return MR_OK;
-    if (!x || !weights || !weightScales || !y || (eight && (!xScales || !workspace))) return MR_ERR_PARAM_NULLPTR;
-    if (eight && workspaceSize < wide_bytes(rows, cols)) return MR_ERR_WORKSPACE;
+    const Room room = numGroups ? matmul_room(rows, numGroups < 0 ? 1 : numGroups, outCols, cols, xDtype) : Room{};
+    if (!x || !weights || !weightScales || !y || (eight && !xScales) || (room.total() && !workspace))
+        return MR_ERR_PARAM_NULLPTR;
+    if (workspaceSize < room.total()) return MR_ERR_WORKSPACE;
     if (!aligned16(weights) || !aligned16(x) || (numGroups > 0 && !aligned16(groupList)) ||
-        (eight && !aligned(workspace, 256)) || !aligned(y, yDtype == MR_DTYPE_F32 ? 4 : 2) || !aligned(xScales, 4) ||
+        (room.total() && !aligned(workspace, 256)) || !aligned(y, yDtype == MR_DTYPE_F32 ? 4 : 2) || !aligned(xScales, 4) ||
         !aligned(weightScales, 4) || !aligned(numRows, 8))
         return MR_ERR_PARAM_INVALID;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -798,16 +1000,19 @@ extern "C" mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int6
     a.y_stride = yStride;
     a.y_dtype = yDtype;
     Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, weights, wr, wm, cols, false};
-    const bool pair = use_pairs(rows, a.G);
-    MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, workspace, s));
+    const bool pair = use_pairs(rows, a.G, outCols, false);
+    char* base = reinterpret_cast<char*>(workspace);
+    MR_TRY_CUDA(clear_tickets(room, base, s));
+    MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, base, s));
+    take_room(a, room, base, 0);
     return run_product(p, a, pair, s);
 }
 
-extern "C" mr_status moe_expert_ffn_int8_get_workspace_size(int64_t rows, int64_t hidden, int64_t inter,
-                                                            int32_t xDtype, uint64_t* workspaceSize) {
-    if (!row_type(xDtype) || !common_sizes(rows, 1, 0, hidden, inter)) return MR_ERR_PARAM_INVALID;
+extern "C" mr_status moe_expert_ffn_int8_get_workspace_size(int64_t rows, int64_t numGroups, int64_t hidden,
+                                                            int64_t inter, int32_t xDtype, uint64_t* workspaceSize) {
+    if (!row_type(xDtype) || !common_sizes(rows, 1, numGroups, hidden, inter)) return MR_ERR_PARAM_INVALID;
     if (!workspaceSize) return MR_ERR_PARAM_NULLPTR;
-    *workspaceSize = (xDtype == MR_DTYPE_INT8 ? wide_bytes(rows, hidden) : 0) + wide_bytes(rows, inter);
+    *workspaceSize = rows && numGroups ? ffn_room(rows, numGroups < 0 ? 1 : numGroups, hidden, inter, xDtype).total() : 0;
     return MR_OK;
 }
 
@@ -832,10 +1037,10 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
         return MR_ERR_PARAM_INVALID;
     if (xScales && (xScaleStride < 0 || xScaleStride > top)) return MR_ERR_PARAM_INVALID;
     if (rows == 0) return MR_OK;
-    if (!x || !w13 || !w13Scales || !w2 || !w2Scales || !y || !workspace || (eight && !xScales))
+    const Room room = numGroups ? ffn_room(rows, numGroups < 0 ? 1 : numGroups, hidden, inter, xDtype) : Room{};
+    if (!x || !w13 || !w13Scales || !w2 || !w2Scales || !y || (room.total() && !workspace) || (eight && !xScales))
         return MR_ERR_PARAM_NULLPTR;
-    const uint64_t x_bytes = eight ? wide_bytes(rows, hidden) : 0;
-    if (workspaceSize < x_bytes + wide_bytes(rows, inter)) return MR_ERR_WORKSPACE;
+    if (workspaceSize < room.total()) return MR_ERR_WORKSPACE;
     if (!aligned16(w13) || !aligned16(w2) || !aligned16(x) || (numGroups > 0 && !aligned16(groupList)) ||
         !aligned(workspace, 256) || !aligned(y, yDtype == MR_DTYPE_F32 ? 4 : 2) || !aligned(xScales, 4) ||
         !aligned(w13Scales, 4) || !aligned(w2Scales, 4) || !aligned(numRows, 8))
@@ -848,7 +1053,7 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     a.experts = (int)experts;
     a.expert_base = expertBase;
     if (a.G == 0) return MR_OK;
-    char* h = reinterpret_cast<char*>(workspace) + x_bytes;
+    char *base = reinterpret_cast<char*>(workspace), *h = base + room.x;
     a.x_scales = xScales;
     a.xs_row = xScaleStride;
     a.w_scales = w13Scales;
@@ -856,9 +1061,11 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     a.y = h;
     a.y_stride = wide_stride(inter) / 2;
     a.y_dtype = MR_DTYPE_BF16;
-    const bool pair = use_pairs(rows, a.G);
+    const bool pair = use_pairs(rows, a.G, inter, true);
     Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, w13, ar, am, hidden, true};
-    MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, workspace, s));
+    MR_TRY_CUDA(clear_tickets(room, base, s));
+    MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, base, s));
+    take_room(a, room, base, 0);
     mr_status st = run_product(p, a, pair, s);
     if (st != MR_OK) return st;
 
@@ -869,5 +1076,6 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     a.y = y;
     a.y_stride = yStride;
     a.y_dtype = yDtype;
-    return run_product(p, a, pair, s);
+    take_room(a, room, base, 1);
+    return run_product(p, a, use_pairs(rows, a.G, hidden, false), s);
 }
