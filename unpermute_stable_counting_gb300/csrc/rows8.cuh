@@ -160,10 +160,16 @@ __device__ __forceinline__ uint32_t int8x4(const float* v, float inv) {
     return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
-// TPR threads a row, 32 values each in pieces of 16 bytes TPR pieces apart. LONG:
-// rows of more than 32 TPR values.
+// TPR threads a row (32: eight rows a block), 32 values each in pieces of 16 bytes TPR
+// pieces apart. LONG: rows of more than 32 TPR values. Blocks of as few registers as
+// let an SM hold 1280 threads, 1024 with the norm, fp32 rows' as many as they want
+// (the norm of 16384 x 7168 bf16 rows: 191 us, with 768 threads 214, and with 1280, where it spills, 198;
+// 65536 x 4096 bf16 rows to int8 132 us, 144 with 1024). Persistent blocks whose next
+// row comes to shared memory meanwhile were slower (251 and 146).
 template <int DT, int TPR, bool NORM, bool LOOSE, bool LONG>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
+                                  DT == MR_DTYPE_F32 ? 1 : (NORM ? 1024 : 1280) / (TPR == 32 ? 256 : TPR))
+    rows_kernel(const RowArgs a) {
     using P = Piece<DT>;
     constexpr int V = P::kValues, kPieces = 32 / V, kWarps = TPR / 32;
     __shared__ float2 part_sum[kWarps];
@@ -224,16 +230,21 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_kernel(const RowAr
     if constexpr (NORM) {
         // scale 1, or 2^-80 where the squares pass fp32's range
         auto sums = [&](float f, bool first, float& s, float& e) {
-            s = e = 0.0f;
+            // four sums side by side: a step's six additions follow one another
+            float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             for (int64_t base = 0; base < a.K; base += step) {
                 if (LONG) fetch(base, first);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     const float u = f == 1.0f ? v[j] : v[j] * f, sq = __fmul_rn(u, u);
                     // (a square of 11 bits is exact)
-                    two_add(s, e, sq, DT == MR_DTYPE_F32 ? __fmaf_rn(u, u, -sq) : 0.0f);
+                    two_add(s4[j & 3], e4[j & 3], sq, DT == MR_DTYPE_F32 ? __fmaf_rn(u, u, -sq) : 0.0f);
                 }
             }
+            two_add(s4[0], e4[0], s4[1], e4[1]);
+            two_add(s4[2], e4[2], s4[3], e4[3]);
+            two_add(s4[0], e4[0], s4[2], e4[2]);
+            s = s4[0], e = e4[0];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
@@ -242,10 +253,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_kernel(const RowAr
             if (kWarps > 1) {
                 if (lane == 0) part_sum[warp] = make_float2(s, e);
                 __syncthreads();
-                const float2 p = lane < kWarps ? part_sum[lane] : make_float2(0.0f, 0.0f);
+                const float2 p = part_sum[lane % kWarps];
                 s = p.x, e = p.y;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
+                for (int o = kWarps / 2; o > 0; o >>= 1) {
                     const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
                     two_add(s, e, s2, e2);
                 }
