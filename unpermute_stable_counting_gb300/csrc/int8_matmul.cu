@@ -48,6 +48,10 @@ struct Int8Args : Groups {
     void* y;
     int64_t y_stride;
     int y_dtype;
+    // Loads whose products one sum takes. The tensor cores cut what a sum has below fp32's digits at every addition,
+    // and 16-bit rows' sums lose by it: f16 rows of 7168 values are off by 7e-6, of 1000 by 8e-7. Where the result is
+    // fp32 a tile is taken in several sums, each added to what stands in y.
+    int sum_loads;
     // equal shares of the loads (NULL: whole tiles round robin)
     float* parts;           // two to a block, of part_rows rows of 256 sums
     int part_rows, part_loads;  // a share is this many loads at least
@@ -67,6 +71,7 @@ template <typename W, bool SHARES> struct Items {
     __device__ __forceinline__ void begin(const Int8Args& a, int lane, int first, int step) {
         walk.begin(a, lane);
         t = first - step;
+        kb1 = a.KB;
         if (!SHARES || !a.parts) return;
         int tiles = walk.total;
         if (a.G > 32) {
@@ -91,9 +96,9 @@ template <typename W, bool SHARES> struct Items {
             kb1 = min(a.KB, kb0 + (end - at));
             at += kb1 - kb0;
         } else {
-            t += step;
-            kb0 = 0;
-            kb1 = a.KB;
+            if (kb1 == a.KB) t += step, kb1 = 0;
+            kb0 = kb1;
+            kb1 = min(a.KB, kb0 + a.sum_loads);
         }
         return walk.next(a, lane, t, channels, tile);
     }
@@ -104,6 +109,7 @@ template <typename W, bool SHARES> struct Items {
 struct Item {
     Tile tile;
     int t, loads;
+    bool again;              // the tile's sums that are not the first
     int first, last, block;  // blocks that have a part of the tile; this one
 };
 
@@ -205,6 +211,12 @@ __device__ __forceinline__ uint32_t pack2(int dt, float a, float b) {
     }
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return reinterpret_cast<const uint32_t&>(h);
+}
+
+// A value of y, or what is added to one that this thread has put there.
+__device__ __forceinline__ void put(char* y, float v, bool add) {
+    if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(y), "f"(v) : "memory");
+    else *reinterpret_cast<float*>(y) = v;
 }
 
 template <int XT, bool SWIGLU, bool PAIR>
@@ -352,6 +364,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     if (more) {
                         i.t = items.t;
                         i.loads = items.kb1 - items.kb0;
+                        i.again = items.kb0 > 0;
                         i.first = i.last = i.block = first;
                         if (!PAIR && a.parts) {
                             i.first = items.owner(items.t * a.KB);
@@ -553,8 +566,8 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     for (int j = 0; j < kLd; ++j, to += y_step) {
                         const bool in = c + j < mine;
                         if (wide) {
-                            if (in && real) *reinterpret_cast<float*>(to) = f[j];
-                            if (in && real1) *reinterpret_cast<float*>(to + kWRows * 4) = g[j];
+                            if (in && real) put(to, f[j], item.again);
+                            if (in && real1) put(to + kWRows * 4, g[j], item.again);
                         } else {
                             const uint32_t w = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], g[j]);
                             if (in && real) *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
@@ -669,7 +682,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     if (wide) {
 #pragma unroll
                         for (int j = 0; j < kKeep; ++j)
-                            if (real && inside && c + j < mine) *reinterpret_cast<float*>(y + (c + j) * y_step) = f[j];
+                            if (real && inside && c + j < mine) put(y + (c + j) * y_step, f[j], item.again);
                     }
 #pragma unroll
                     for (int j = 0; j < kKeep; j += 2)
@@ -799,6 +812,7 @@ struct Product {
     int64_t w_row, w_matrix;   // byte strides of a row and of a matrix [N, K]
     int64_t K;
     bool swiglu;
+    bool exact;                // rows of int8 values (whatever type holds them)
 };
 
 // The tiles of a product, or more.
@@ -834,6 +848,9 @@ uint64_t ticket_bytes(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu
 mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
     a.n_tiles = ceil_div(a.N, p.swiglu ? 128 : 256);
     a.KB = ceil_div(p.K, 128);
+    const int sums = a.y_dtype == MR_DTYPE_F32 && !p.swiglu && !p.exact ? ceil_div(a.KB, 8) : 1;
+    a.sum_loads = ceil_div(a.KB, sums);
+    if (a.sum_loads < a.KB) a.parts = nullptr;
     const int64_t tiles = most_tiles(a.rows, a.G, a.N, pair, p.swiglu);
     if (tiles > INT32_MAX) return MR_ERR_PARAM_INVALID;
     CUtensorMap m[2];
@@ -999,7 +1016,7 @@ extern "C" mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int6
     a.y = y;
     a.y_stride = yStride;
     a.y_dtype = yDtype;
-    Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, weights, wr, wm, cols, false};
+    Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, weights, wr, wm, cols, false, eight};
     const bool pair = use_pairs(rows, a.G, outCols, false);
     char* base = reinterpret_cast<char*>(workspace);
     MR_TRY_CUDA(clear_tickets(room, base, s));
@@ -1062,14 +1079,14 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     a.y_stride = wide_stride(inter) / 2;
     a.y_dtype = MR_DTYPE_BF16;
     const bool pair = use_pairs(rows, a.G, inter, true);
-    Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, w13, ar, am, hidden, true};
+    Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, w13, ar, am, hidden, true, eight};
     MR_TRY_CUDA(clear_tickets(room, base, s));
     MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, base, s));
     take_room(a, room, base, 0);
     mr_status st = run_product(p, a, pair, s);
     if (st != MR_OK) return st;
 
-    p = Product{h, wide_stride(inter), kBf16, w2, br, bm, inter, false};
+    p = Product{h, wide_stride(inter), kBf16, w2, br, bm, inter, false, false};
     a.x_scales = nullptr;
     a.w_scales = w2Scales;
     a.N = (int)hidden;
