@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     if (more) {
                         i.t = items.t;
                         i.loads = items.kb1 - items.kb0;
-                        i.again = items.kb0 > 0;
+                        i.again = !a.parts && items.kb0 > 0;
                         i.first = i.last = i.block = first;
                         if (!PAIR && a.parts) {
                             i.first = items.owner(items.t * a.KB);
@@ -617,6 +617,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                         ok = mbar_wait(smem_u32(&part_bar[0]), swaps & 1, abort);
                         if (!ok) break;
                         if (lane == 0) {
+                            __threadfence();
                             ticket = atomicAdd(a.tickets + item.t, 1u);
                             __threadfence();
                             mbar_arrive(smem_u32(&part_bar[1]));
@@ -852,7 +853,7 @@ mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
     a.sum_loads = ceil_div(a.KB, sums);
     if (a.sum_loads < a.KB) a.parts = nullptr;
     const int64_t tiles = most_tiles(a.rows, a.G, a.N, pair, p.swiglu);
-    if (tiles > INT32_MAX) return MR_ERR_PARAM_INVALID;
+    if (tiles > INT32_MAX - 4096) return MR_ERR_PARAM_INVALID;  // (a block's count of them goes one round past)
     CUtensorMap m[2];
     const bool eight = p.xt == kInt8;
     const uint64_t xd[2] = {(uint64_t)p.K, (uint64_t)a.rows}, xs[1] = {(uint64_t)p.x_stride};
