@@ -612,6 +612,13 @@ def moe_quantize_int8(x, *, num_rows=None, interleaved: bool = False, out: dict 
         out = _interleaved(rows, cols, index) if interleaved else dict(
             values=_wide_rows(shape[:-1], cols, index, torch.int8),
             scales=torch.empty(shape[:-1], dtype=torch.float32, device=_device(index)))
+        if dims == 2 and not interleaved:  # nothing of these to check
+            st = lib().moe_quantize_int8(x.data_ptr(), dt, 1, rows, cols, _Pair(0, _row_stride(shape, strides)), num_rows,
+                                         out["values"].data_ptr(), _Pair(0, -(-cols // 16) * 16), out["scales"].data_ptr(),
+                                         None, _raw_stream(index))
+            if st:
+                _check(st, "moe_quantize_int8")
+            return out
     values, scales = out["values"], out["scales"]
     vshape, vstrides = _rows_of("values", values, dims)
     if values.dtype != torch.int8 or vshape != shape:
@@ -667,37 +674,43 @@ def moe_add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quantize: s
     ra = rs = 0
     if residual is not None:
         ra, rs = _like_x("residual", residual, x, shape, index)
-    if out is None:
-        out = {}
-        if residual is not None:
-            out["residual"] = torch.empty((rows, cols), dtype=x.dtype, device=_device(index))
-        if with_y:
-            out["y"] = torch.empty((rows, cols), dtype=x.dtype, device=_device(index))
-        if interleaved:
-            out.update(_interleaved(rows, cols, index))
-        elif quantize is not None:
-            eight = quantize == "int8"
-            out["values"] = _wide_rows((rows,), cols, index, torch.int8 if eight else _E4M3)
-            out["scales"] = torch.empty((rows,) if eight else (rows, _blocks(cols)), dtype=torch.float32,
-                                        device=_device(index))
     ha = hs = ya = ys = va = vst = sa = 0
     ss = None
-    if residual is not None:
-        ha, hs = _like_x("residual", out["residual"], x, shape, index)
-    if with_y:
-        ya, ys = _like_x("y", out["y"], x, shape, index)
-    if quantize is not None:
-        values, scales = out["values"], out["scales"]
-        vshape, vstrides = _rows_of("values", values, 2)
-        if values.dtype != (torch.int8 if quantize == "int8" else _E4M3) or vshape != shape:
-            raise ValueError(f"values must be {quantize} of x's shape")
-        _same_device("values", values, index)
-        va, vst = values.data_ptr(), _row_stride(vshape, vstrides)
-        if quantize == "int8":
-            sa, step = _scales_of_rows(scales, rows, index)
-            ss = _Pair(step, 1)
-        else:
-            sa, ss = _block_scales(scales, (rows, _blocks(cols)), index)
+    if out is None:  # nothing of what is made here to check
+        out, device = {}, _device(index)
+        if residual is not None:
+            t = out["residual"] = torch.empty(shape, dtype=x.dtype, device=device)
+            ha, hs = t.data_ptr(), cols
+        if with_y:
+            t = out["y"] = torch.empty(shape, dtype=x.dtype, device=device)
+            ya, ys = t.data_ptr(), cols
+        if interleaved:
+            out.update(_interleaved(rows, cols, index))
+            va, vst = out["values"].data_ptr(), cols + 4
+            sa, ss = out["scales"].data_ptr(), _Pair(cols // 4 + 1, 1)
+        elif quantize is not None:
+            eight = quantize == "int8"
+            t = out["values"] = _wide_rows((rows,), cols, index, torch.int8 if eight else _E4M3)
+            va, vst = t.data_ptr(), -(-cols // 16) * 16
+            t = out["scales"] = torch.empty((rows,) if eight else (rows, _blocks(cols)), dtype=torch.float32, device=device)
+            sa = t.data_ptr()
+    else:
+        if residual is not None:
+            ha, hs = _like_x("residual", out["residual"], x, shape, index)
+        if with_y:
+            ya, ys = _like_x("y", out["y"], x, shape, index)
+        if quantize is not None:
+            values, scales = out["values"], out["scales"]
+            vshape, vstrides = _rows_of("values", values, 2)
+            if values.dtype != (torch.int8 if quantize == "int8" else _E4M3) or vshape != shape:
+                raise ValueError(f"values must be {quantize} of x's shape")
+            _same_device("values", values, index)
+            va, vst = values.data_ptr(), _row_stride(vshape, vstrides)
+            if quantize == "int8":
+                sa, step = _scales_of_rows(scales, rows, index)
+                ss = _Pair(step, 1)
+            else:
+                sa, ss = _block_scales(scales, (rows, _blocks(cols)), index)
     st = lib().moe_add_rms_norm(x.data_ptr(), dt, rows, cols, _row_stride(shape, strides), ra, rs, wa,
                                 _TORCH_TO_DT[weight.dtype], eps, num_rows, ha, hs, ya, ys, _QUANTIZED[quantize], va, vst,
                                 sa, ss, _raw_stream(index))

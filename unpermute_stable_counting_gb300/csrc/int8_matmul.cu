@@ -48,6 +48,7 @@ struct Int8Args : Groups {
     void* y;
     int64_t y_stride;
     int y_dtype;
+    int many;               // blocks may have several tiles
     // Loads whose products one sum takes. The tensor cores cut what a sum has below fp32's digits at every addition,
     // and 16-bit rows' sums lose by it: f16 rows of 7168 values are off by 7e-6, of 1000 by 8e-7. Where the result is
     // fp32 a tile is taken in several sums, each added to what stands in y.
@@ -543,14 +544,22 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, s, c % 32 + j));
                 }
             };
+            ok = mbar_wait<PAIR>(smem_u32(&t_full), n & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            auto hand_back = [&] {  // the sums
+                tc_fence_before();
+                __syncwarp();
+                if (lane != 0) return;
+                if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&t_empty), 0));
+                else mbar_arrive(smem_u32(&t_empty));
+            };
+            if (mine <= 0) hand_back();
             if constexpr (!PAIR) {
                 // the second operand's channels, or the same ones of the other factor
                 const int col1 = SWIGLU ? col : col + kWRows;
                 const bool real1 = col1 < a.N;
                 const float w_scale1 = ws[SWIGLU ? (real ? a.N + col : 0) : (real1 ? col1 : 0)];
-                ok = mbar_wait(smem_u32(&t_full), n & 1, abort);
-                if (!ok) break;
-                tc_fence_after();
                 // rows c .. of the result from their sums
                 auto finish = [&](int c, const uint32_t (&v)[kLd], const uint32_t (&u)[kLd]) {
                     float f[kLd], g[kLd];
@@ -582,15 +591,8 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                            quarter * 32 + lane;
                 };
                 float* part = part_of(item.block);
-                auto hand_back = [&] {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&t_empty));
-                };
-                if (mine <= 0) hand_back();
-#pragma unroll
-                for (int c = 0; c < C::kHalf; c += kLd) {
-                    if (c >= mine) break;
+#pragma unroll 1
+                for (int c = 0; c < mine; c += kLd) {
                     uint32_t v[kLd], u[kLd];
                     tmem_load(v, from + half * cols + c);
                     tmem_load(u, from + C::kRows + half * cols + c);
@@ -628,6 +630,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     if (!ok) break;
                     if (ticket == (unsigned)(item.last - item.first)) {
                         __threadfence();
+#pragma unroll 1
                         for (int c = 0; c < mine; c += kLd) {
                             float f[kLd], g[kLd];
 #pragma unroll
@@ -649,18 +652,43 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     }
                 }
             } else {
-                ok = mbar_wait<PAIR>(smem_u32(&t_full), n & 1, abort);
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t packed[C::kHalf / kLd * kKeep / 2];
+                if constexpr (!SWIGLU) {
+                    // With tiles to come the sums are handed back before the stores of 16-bit results, which wait in
+                    // registers (16384 x 7168 x 7168: 836 us, as below 869). In a launch of one tile a block what
+                    // this code costs is its own way from memory (1003 rows of 12 groups, 1000 -> 1100: 15.9 us, as
+                    // below 13.7).
+                    if (a.many && !wide) {
+                        uint32_t packed[C::kHalf / 2];
 #pragma unroll
-                for (int c = 0; c < C::kHalf; c += kLd) {
-                    if (c >= mine) break;
+                        for (int c = 0; c < C::kHalf; c += kLd) {
+                            if (c >= mine) break;
+                            uint32_t v[kLd];
+                            tmem_load(v, from + half * cols + c);
+                            tmem_ld_wait(v);
+                            float f[kLd];
+                            scaled(v, w_scale, c, f);
+#pragma unroll
+                            for (int j = 0; j < kLd; j += 2) packed[(c + j) / 2] = pack2(a.y_dtype, f[j], f[j + 1]);
+                        }
+                        if (mine > 0) hand_back();
+                        if (real && inside) {
+                            char* to = y;
+#pragma unroll
+                            for (int j = 0; j < C::kHalf; ++j, to += y_step)
+                                if (j < mine) *reinterpret_cast<uint16_t*>(to) = (uint16_t)(packed[j / 2] >> (16 * (j & 1)));
+                        }
+                        continue;
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; c < mine; c += kLd) {
                     uint32_t v[kLd];
                     tmem_load(v, from + half * cols + c);
                     tmem_ld_wait(v);
+                    if (c + kLd >= mine) hand_back();  // everything is in registers
                     float f[kLd];
                     scaled(v, w_scale, c, f);
+                    int r = c;
                     if constexpr (C::kSwap) {
                         // Two warps have the two factors of the same channels: the first takes the chunk's first
                         // rows, the second the others, each from the other's half of `swap`, two of them in turn.
@@ -679,34 +707,24 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                             const float o = in[j * 32];
                             f[j] = factor ? silu(o) * f[kKeep + j] : silu(f[j]) * o;
                         }
+                        r += factor * kKeep;
                     }
+                    if (!real || !inside) continue;
+                    char* to = y + r * y_step;
                     if (wide) {
 #pragma unroll
-                        for (int j = 0; j < kKeep; ++j)
-                            if (real && inside && c + j < mine) put(y + (c + j) * y_step, f[j], item.again);
-                    }
+                        for (int j = 0; j < kKeep; ++j, to += y_step)
+                            if (r + j < mine) put(to, f[j], item.again);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < kKeep; j += 2)
-                        packed[(c / kLd * kKeep + j) / 2] = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], f[j + 1]);
-                }
-                if (!ok) break;
-                // everything is in registers: hand the sums back before the stores
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_cluster(smem_u32(&t_empty), 0));
-                if (!wide && real && inside) {
-#pragma unroll
-                    for (int c = 0; c < C::kHalf; c += kLd) {
-                        const int r = c + factor * kKeep;
-                        char* to = y + r * y_step;
-#pragma unroll
-                        for (int j = 0; j < kKeep; ++j) {
-                            if (r + j < mine)
-                                *reinterpret_cast<uint16_t*>(to) = (uint16_t)(packed[(c / kLd * kKeep + j) / 2] >> (16 * (j & 1)));
-                            to += y_step;
+                        for (int j = 0; j < kKeep; j += 2, to += 2 * y_step) {
+                            const uint32_t w = pack2(SWIGLU ? (int)MR_DTYPE_BF16 : a.y_dtype, f[j], f[j + 1]);
+                            if (r + j < mine) *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
+                            if (r + j + 1 < mine) *reinterpret_cast<uint16_t*>(to + y_step) = (uint16_t)(w >> 16);
                         }
                     }
                 }
+                if (!ok) break;
             }
         }
     }
@@ -765,7 +783,7 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 bool aligned16(const void* p) { return aligned(p, 16); }
 
 template <int XT, bool SWIGLU, bool PAIR>
-cudaError_t launch_int8(const CUtensorMap (&m)[2], const Int8Args& a, int64_t tiles, cudaStream_t s) {
+cudaError_t launch_int8(const CUtensorMap (&m)[2], Int8Args a, int64_t tiles, cudaStream_t s) {
     if (a.parts) tiles = tiles * a.KB / a.part_loads + 1;
     auto kernel = int8_matmul_kernel<XT, SWIGLU, PAIR>;
     constexpr int smem = Cfg<XT, SWIGLU, PAIR>::kSmem;
@@ -800,6 +818,7 @@ cudaError_t launch_int8(const CUtensorMap (&m)[2], const Int8Args& a, int64_t ti
         resident[dev].store(n, std::memory_order_release);
     }
     cfg.gridDim = dim3((unsigned)(tiles < n ? tiles : n) * (PAIR ? 2 : 1));
+    a.many = tiles > n;
     return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], a);
 }
 
