@@ -417,3 +417,12 @@ def test_results_past_32_bits(usc):
         g = torch.tensor([[E - 1, rows]], dtype=torch.int64, device="cuda")
         y = usc.moe_grouped_matmul_int8(x, w, scales, g, x_scales=xs)["y"]
         assert_close(y, *product(values, weight(tail, ws)[0]))
+
+
+@pytest.mark.parametrize("x_dtype", [I8, BF16])
+def test_groups_of_few_and_many_rows_in_turn(usc, x_dtype):
+    """A block's tiles have their sums in halves of their room, or in all of it."""
+    sizes = [5, 90, 17, 33, 48, 49, 1, 96, 16, 97, 2, 64] * 4
+    g = torch.tensor([[i % 3, c] for i, c in enumerate(sizes)], dtype=torch.int64)
+    check_matmul(usc, sum(sizes), 3, 1500, 200, x_dtype, BF16, 9, g)
+    check_ffn(usc, sum(sizes), 3, 520, 300, x_dtype, seed=10, groups=g)

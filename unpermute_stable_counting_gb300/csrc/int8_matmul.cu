@@ -106,6 +106,24 @@ template <typename W, bool SHARES> struct Items {
     __device__ __forceinline__ int owner(int load) const { return (int)(((int64_t)(load + 1) * blocks - 1) / total); }
 };
 
+// Where a tile's sums lie: those of a single block's tiles of few rows in one half of
+// their room or the other, in turn, so that the next tile's instructions need not wait
+// for this one's results; others' in all of it. A half has barriers of its own.
+template <bool PAIR, int HALF> struct SumRoom {
+    uint32_t turn = 0, uses[2] = {0, 0};
+    bool both = false;
+    int half = 0;
+    __device__ __forceinline__ void next(int columns) {
+        both = !PAIR && columns > HALF;
+        half = PAIR || both ? 0 : (int)(turn++ & 1);
+    }
+    __device__ __forceinline__ uint32_t parity(int h) const { return (h ? uses[1] : uses[0]) & 1; }
+    __device__ __forceinline__ void used() {
+        if (both || half == 0) ++uses[0];
+        if (both || half == 1) ++uses[1];
+    }
+};
+
 // A tile, or the part of one: for the warps that do not walk the list.
 struct Item {
     Tile tile;
@@ -229,7 +247,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
     __shared__ __align__(8) uint64_t l_full[C::kLoads], l_empty[C::kLoads];                   // loads
     __shared__ __align__(8) uint64_t a_full[C::kSteps], a_empty[C::kSteps];                   // steps of weights
     __shared__ __align__(8) uint64_t x_full[C::kRowSteps], x_empty[C::kRowSteps];             // and of rows
-    __shared__ __align__(8) uint64_t t_full, t_empty, i_full[2], i_empty[2];
+    __shared__ __align__(8) uint64_t t_full[2], t_empty[2], i_full[2], i_empty[2];
     __shared__ Item info[2];
     __shared__ __align__(8) uint64_t part_bar[2];
     __shared__ unsigned ticket;
@@ -253,9 +271,9 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
         }
         for (int i = 0; i < C::kRowSteps; ++i)
             mbar_init(smem_u32(&x_full[i]), XT == kInt8 ? C::kRowWarps / 2 : 1), mbar_init(smem_u32(&x_empty[i]), 1);
-        mbar_init(smem_u32(&t_full), 1);
-        mbar_init(smem_u32(&t_empty), kBlocks * kSumWarps);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&t_full[i]), 1);
+            mbar_init(smem_u32(&t_empty[i]), kBlocks * kSumWarps);
             mbar_init(smem_u32(&i_full[i]), 1);
             mbar_init(smem_u32(&i_empty[i]), kConvertWarps + C::kRowWarps + kSumWarps);
         }
@@ -323,10 +341,14 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
         } else if (warp == 1) {
             ok = rank == 0;
             items.begin(a, lane, first, step);
-            for (uint32_t n = 0; ok && items.next(a, lane, C::kChannels, step); ++n) {
+            SumRoom<PAIR, C::kRows / 2> room;
+            while (ok && items.next(a, lane, C::kChannels, step)) {
+                room.next(columns(tile.rows));
+                const uint32_t d = tmem + room.half * (C::kRows / 2);
                 const uint32_t idesc = idesc_16(kWRows * kBlocks, columns(tile.rows), XT == kBf16);
                 if (elect_one()) {
-                    ok = mbar_wait<PAIR>(smem_u32(&t_empty), (n & 1) ^ 1, abort);
+                    ok = mbar_wait<PAIR>(smem_u32(&t_empty[room.half]), room.parity(room.half) ^ 1, abort);
+                    if (room.both) ok = ok && mbar_wait<PAIR>(smem_u32(&t_empty[1]), room.parity(1) ^ 1, abort);
                     for (int k = items.kb0; ok && k < items.kb1; ++k, ++it) {
                         const uint32_t r = it % C::kRowSteps;
                         ok = mbar_wait<PAIR>(smem_u32(&x_full[r]), (it / C::kRowSteps) & 1, abort);
@@ -339,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                             tc_fence_after();
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                mma_16_tmem<PAIR>(tmem + p * C::kRows, tmem + C::kACols + s * C::kStepCols + 8 * j,
+                                mma_16_tmem<PAIR>(d + p * C::kRows, tmem + C::kACols + s * C::kStepCols + 8 * j,
                                                   b + j / 4 * (C::kPartBytes / 16) + 2 * (j % 4), idesc,
                                                   k > items.kb0 || j > 0);
                             tc_commit<PAIR>(smem_u32(&a_empty[s]));
@@ -347,8 +369,10 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                         if (!ok) break;
                         if (!PAIR) tc_commit(smem_u32(&x_empty[r]));
                     }
-                    if (ok) tc_commit<PAIR>(smem_u32(&t_full));
+                    if (ok) tc_commit<PAIR>(smem_u32(&t_full[room.half]));
+                    if (ok && room.both) tc_commit<PAIR>(smem_u32(&t_full[1]));
                 }
+                room.used();
                 __syncwarp();
                 it = __reduce_max_sync(0xffffffffu, it);
                 ok = __all_sync(0xffffffffu, ok);
@@ -501,6 +525,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
         regs_inc<C::kRegs[3]>();
         const int me = warp - (C::kWarps - kSumWarps), half = me >> 2, quarter = warp & 3;
         const uint32_t from = tmem + ((uint32_t)quarter << 21);
+        SumRoom<PAIR, C::kRows / 2> room;
         uint32_t swaps = 0;  // of factors, or of tickets
         for (uint32_t n = 0;; ++n) {
             ok = mbar_wait<PAIR>(smem_u32(&i_full[n & 1]), (n >> 1) & 1, abort);
@@ -544,15 +569,23 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, s, c % 32 + j));
                 }
             };
-            ok = mbar_wait<PAIR>(smem_u32(&t_full), n & 1, abort);
+            room.next(columns(tile.rows));
+            ok = mbar_wait<PAIR>(smem_u32(&t_full[room.half]), room.parity(room.half), abort);
+            if (room.both) ok = ok && mbar_wait<PAIR>(smem_u32(&t_full[1]), room.parity(1), abort);
             if (!ok) break;
+            room.used();
             tc_fence_after();
-            auto hand_back = [&] {  // the sums
+            const uint32_t sums = from + room.half * (C::kRows / 2) + half * cols;
+            auto hand_back = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane != 0) return;
-                if (PAIR) mbar_arrive_cluster(map_cluster(smem_u32(&t_empty), 0));
-                else mbar_arrive(smem_u32(&t_empty));
+                if (PAIR) {
+                    mbar_arrive_cluster(map_cluster(smem_u32(&t_empty[0]), 0));
+                } else {
+                    mbar_arrive(smem_u32(&t_empty[room.half]));
+                    if (room.both) mbar_arrive(smem_u32(&t_empty[1]));
+                }
             };
             if (mine <= 0) hand_back();
             if constexpr (!PAIR) {
@@ -594,8 +627,8 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < mine; c += kLd) {
                     uint32_t v[kLd], u[kLd];
-                    tmem_load(v, from + half * cols + c);
-                    tmem_load(u, from + C::kRows + half * cols + c);
+                    tmem_load(v, sums + c);
+                    tmem_load(u, sums + C::kRows + c);
                     tmem_ld_wait(v);
                     tmem_ld_wait(u);
                     if (c + kLd >= mine) hand_back();  // everything is in registers
@@ -663,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                         for (int c = 0; c < C::kHalf; c += kLd) {
                             if (c >= mine) break;
                             uint32_t v[kLd];
-                            tmem_load(v, from + half * cols + c);
+                            tmem_load(v, sums + c);
                             tmem_ld_wait(v);
                             float f[kLd];
                             scaled(v, w_scale, c, f);
@@ -683,7 +716,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < mine; c += kLd) {
                     uint32_t v[kLd];
-                    tmem_load(v, from + half * cols + c);
+                    tmem_load(v, sums + c);
                     tmem_ld_wait(v);
                     if (c + kLd >= mine) hand_back();  // everything is in registers
                     float f[kLd];
