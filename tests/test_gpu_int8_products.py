@@ -426,3 +426,12 @@ def test_groups_of_few_and_many_rows_in_turn(usc, x_dtype):
     g = torch.tensor([[i % 3, c] for i, c in enumerate(sizes)], dtype=torch.int64)
     check_matmul(usc, sum(sizes), 3, 1500, 200, x_dtype, BF16, 9, g)
     check_ffn(usc, sum(sizes), 3, 520, 300, x_dtype, seed=10, groups=g)
+
+
+@pytest.mark.parametrize("x_dtype,out", [(I8, F32), (F16, BF16), (BF16, F32)])
+def test_more_tiles_than_sms_of_long_rows(usc, x_dtype, out):
+    for experts, per, N in ((40, 8, 1500), (34, 70, 1300), (170, 2, 700), (3, 60, 4000)):
+        g = torch.tensor([[i % 3, max(0, per - i % 5)] for i in range(experts)], dtype=torch.int64)
+        check_matmul(usc, int(g[:, 1].sum()), 3, N, 2100, x_dtype, out, experts, g)
+    g = torch.tensor([[i % 3, 1 + i % 14] for i in range(40)], dtype=torch.int64)
+    check_ffn(usc, int(g[:, 1].sum()), 3, 2100, 2000, x_dtype, seed=3, groups=g)

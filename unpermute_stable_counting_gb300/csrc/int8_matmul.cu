@@ -147,16 +147,16 @@ template <int XT, bool SWIGLU, bool PAIR> struct Cfg {
     static constexpr int kBox = PAIR ? 64 : 32;                     // rows of a TMA load
     // Steps of converted weights held, one for each operand and load, and of 16-bit rows. The way round (converted,
     // multiplied, free again) takes several steps' time: with three steps instead of four the dense 16384 x 7168 x
-    // 7168 took pairs 851 us instead of 835; with two of both operands single blocks took XXX for 576 rows over 64
-    // experts, 7168 -> 4096. (A step of 64 values costs the thread that issues the instructions its waits and
-    // commit twice: 884 instead of 848 us for the dense one.)
-    static constexpr int kSteps = PAIR ? 4 : 5, kRowSteps = PAIR ? 4 : 2;
+    // 7168 took pairs 851 us instead of 835. (A step of 64 values costs the thread that issues the instructions its
+    // waits and commit twice: 884 instead of 848 us.) 16-bit rows of single blocks come from L2 only when a step is
+    // free: with two of them 576 rows over 64 experts, 7168 -> 4096, take 328 us, with three 305.
+    static constexpr int kSteps = PAIR ? 4 : 5, kRowSteps = PAIR ? 4 : XT == kInt8 ? 2 : 3;
     static constexpr int kRowWarps = XT == kInt8 ? 4 : 0;           // warps of int8 rows
     static constexpr int kWarps = 4 + kConvertWarps + kRowWarps + kSumWarps, kThreads = 32 * kWarps;
     static constexpr int kStepCols = 64;                            // tensor memory of a step's weights
     static constexpr int kACols = kRows * kPlanes;                  // tensor memory: sums, then weights
     static_assert(kACols + kSteps * kStepCols <= 512, "tensor memory");
-    static constexpr int kLoads = PAIR ? (SWIGLU ? 4 : 6) : XT == kInt8 ? 4 : 5;
+    static constexpr int kLoads = PAIR && !SWIGLU ? 6 : 4;
     static constexpr int kLoadBytes = kPlanes * kWBytes + (XT == kInt8 ? kLoadRows * 128 : 0);
     static constexpr int kPartBytes = kLoadRows * 128, kStepBytes = kPartBytes * 2;  // 64 values, 128
     static constexpr int kHalf = kRows / 2;                         // rows of a warpgroup of results
