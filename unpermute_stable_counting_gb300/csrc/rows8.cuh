@@ -50,6 +50,14 @@ __device__ __forceinline__ void two_add(float& s, float& e, float v, float v_low
     s = t;
 }
 
+// The same for v >= 0 and s >= 0: the smaller one's lost digits, with two instructions less (the norm's time is
+// its instructions: it issues three quarters of what it could). A NaN is in s.
+__device__ __forceinline__ void two_add_positive(float& s, float& e, float v) {
+    const float t = __fadd_rn(s, v), hi = fmaxf(s, v), lo = fminf(s, v);
+    e = __fadd_rn(e, __fsub_rn(lo, __fsub_rn(t, hi)));
+    s = t;
+}
+
 // 1 / sqrt(v + v_low), v a normal number: a Newton step whose residual is formed without rounding
 __device__ __forceinline__ float rsqrt_rn(float v, float v_low) {
     if (!(v < __int_as_float(0x7F800000))) return v > 0.0f ? 0.0f : v;  // infinity, NaN
@@ -238,7 +246,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
                 for (int j = 0; j < 32; ++j) {
                     const float u = f == 1.0f ? v[j] : v[j] * f, sq = __fmul_rn(u, u);
                     // (a square of 11 bits is exact)
-                    two_add(s4[j & 3], e4[j & 3], sq, DT == MR_DTYPE_F32 ? __fmaf_rn(u, u, -sq) : 0.0f);
+                    two_add_positive(s4[j & 3], e4[j & 3], sq);
+                    if (DT == MR_DTYPE_F32) e4[j & 3] = __fadd_rn(e4[j & 3], __fmaf_rn(u, u, -sq));
                 }
             }
             two_add(s4[0], e4[0], s4[1], e4[1]);
