@@ -16,7 +16,8 @@
  * MoeUpdateExpert ("MoeUpdateExpert"), declared further down; and the experts
  * between the two: rows and weights in 8-bit blocks, the product of each
  * expert's rows with its weights, the experts' network, and a whole layer for a
- * few tokens.
+ * few tokens; the same products with 8-bit integers, as the batching's INT8 mode
+ * hands rows on, and the norm that makes such rows.
  *
  * Conventions shared by every entry point
  *  - Pointers named as device pointers must point to device memory of the
@@ -40,7 +41,8 @@
  *  - Argument errors are detected on the host before anything is enqueued;
  *    the call then returns the error and enqueues nothing. Errors that the
  *    CUDA runtime reports at launch return MR_ERR_CUDA.
- *  - Outputs must not alias inputs or each other.
+ *  - Outputs must not alias inputs or each other (moe_add_rms_norm's residualOut
+ *    excepted, see there).
  *  - Results are deterministic: identical inputs give identical bits.
  *  - Execute calls can be captured into a CUDA graph (stream capture): they
  *    only enqueue kernels (the not-padded moe_unpermute's maskedSelect and
@@ -660,7 +662,10 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
  *   y[r, n] = (sum_k x[r, k] w[e, n, k]) ws[e, n] xs[r]
  *   for the rows of each group. Products of int8 values are exact and so are
  *   their fp32 sums while they stay below 2^24; 16-bit rows multiply as they are.
- *   The result is rounded once to yDtype (each scale's product once to fp32).
+ *   The result is rounded once to yDtype (each scale's product once to fp32). With
+ *   16-bit rows of more than 1024 values an F32 result is the sum of the results of
+ *   equal parts of at most 1024 values, in their order; one of those below 2^-126
+ *   may count as 0.
  *
  *   x             [rows, cols] of xDtype: INT8 with xScales (the batching's y and
  *                 dynamicScale, or moe_quantize_int8's), or F16 or BF16, whose

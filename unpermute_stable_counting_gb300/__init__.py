@@ -15,7 +15,11 @@ CUDA kernels for sm_103a:
   with a scale per 128 values, the product of each group's rows with its
   expert's weights, and the experts' network between batching and unpermute;
 * moe_layer      -- a whole mixture-of-experts layer for up to 64 tokens
-  (router, experts, weighted sum) in one launch.
+  (router, experts, weighted sum) in one launch;
+* moe_quantize_int8, moe_add_rms_norm, moe_grouped_matmul_int8,
+  moe_expert_ffn_int8 -- the INT8 side: rows and weights as int8 values with a
+  scale per row or channel (the batching's INT8 mode), the norm that hands rows
+  on in 8 bits, and the experts' products with such weights.
 
 Importing the package does not load the CUDA library; the first call does,
 and fails loudly if the library was not built.
