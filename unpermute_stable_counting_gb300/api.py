@@ -897,7 +897,7 @@ def _int8_rows(x, x_scales, group_list):
 
 
 def _int8_weights(name, w, scales, shape, index):
-    """Address and strides of int8 weights of `shape`, address of their scales."""
+    """Address and strides (None: contiguous) of int8 weights of `shape`, address of their scales."""
     wshape, strides = _rows_of(name, w, len(shape))
     if w.dtype != torch.int8:
         raise TypeError(f"{name} must have dtype {torch.int8}, got {w.dtype}")
@@ -907,6 +907,8 @@ def _int8_weights(name, w, scales, shape, index):
     if scales is None:
         raise ValueError(f"{name} needs its scales")
     sa = _vector(name + "_scales", scales, torch.float32, index, shape[:-1])
+    if shape[-1] % 16 == 0 and w.is_contiguous():
+        return w.data_ptr(), None, sa
     return w.data_ptr(), _matrix_strides(name, wshape, strides), sa
 
 
@@ -934,7 +936,8 @@ def moe_grouped_matmul_int8(x, weights, weight_scales, group_list=None, *, x_sca
     st = lib().moe_grouped_matmul_int8(x.data_ptr(), dt, xst, xsa, xss, wa, wst, wsa, ga, groups,
                                        _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, N, K,
                                        ya, ydt, yst, wsp, size, _raw_stream(index))
-    _check(st, "moe_grouped_matmul_int8")
+    if st:
+        _check(st, "moe_grouped_matmul_int8")
     return out
 
 
@@ -974,7 +977,8 @@ def moe_expert_ffn_int8(x, w13, w13_scales, w2, w2_scales, group_list=None, *, x
     st = lib().moe_expert_ffn_int8(x.data_ptr(), dt, xst, xsa, xss, a13, st13, s13, a2, st2, s2, ga, groups,
                                    _vector("num_rows", num_rows, torch.int64, index), int(expert_base), rows, E, H,
                                    inter, ya, ydt, yst, workspace.data_ptr(), workspace.numel(), _raw_stream(index))
-    _check(st, "moe_expert_ffn_int8")
+    if st:
+        _check(st, "moe_expert_ffn_int8")
     return out
 
 

@@ -822,6 +822,12 @@ __global__ void __launch_bounds__(256)
     q[1] = b;
 }
 
+// Tickets to 0. (1 row, 4096 -> 2048: 14.9 us on the GPU, with a memset in front of the product 18.5.)
+__global__ void __launch_bounds__(256) clear_kernel(uint4* tickets, int n) {
+    pdl_enter();
+    for (int i = threadIdx.x; i < n; i += 256) tickets[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 bool aligned16(const void* p) { return aligned(p, 16); }
 
@@ -991,7 +997,8 @@ Room ffn_room(int64_t rows, int64_t G, int64_t hidden, int64_t inter, int32_t dt
 // Tickets at 0 (nothing keeps the workspace between calls), where products take some.
 cudaError_t clear_tickets(const Room& r, char* workspace, cudaStream_t s) {
     const uint64_t n = r.tickets[0] + r.tickets[1];
-    return n ? cudaMemsetAsync(workspace + r.x + r.h, 0, n, s) : cudaSuccess;
+    return n ? launch_pdl(clear_kernel, dim3(1), dim3(256), 0, s, reinterpret_cast<uint4*>(workspace + r.x + r.h), (int)(n / 16))
+             : cudaSuccess;
 }
 // The product's share of the room.
 void take_room(Int8Args& a, const Room& r, char* workspace, int product) {
