@@ -7,7 +7,7 @@ from _int8_util import e4m3_rows, int8_rows, norm
 pytestmark = pytest.mark.gpu
 
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
-COLS = [1, 7, 64, 100, 129, 1000, 1024, 1025, 2500, 4096, 4097, 7168, 8192, 9001, 16384, 16392, 20001]
+COLS = [1, 7, 64, 100, 129, 256, 257, 500, 513, 1000, 1024, 1025, 2048, 2050, 2500, 4096, 4097, 7168, 8192, 9001, 16384, 16392, 20001]
 
 
 @pytest.fixture(scope="module")

@@ -6,9 +6,9 @@
 //   out: y in x's type; int8 rows, q = round(y (127 / a)), s = a / 127 with
 //   a = max(max |y|, 2^-96) of the row; or e4m3 blocks as moe_quantize makes them
 //
-// A row's values stay in registers (32 a thread; a warp, 128, 256 or 512 threads a
-// row) from the load to the stores, so x and residual are read once. Rows of more
-// than 16384 values are read once more for each of the two sweeps that follow.
+// A row's values stay in registers (32 a thread, fewer of short rows and of fp32 ones; a warp, 128,
+// 256 or 512 threads a row) from the load to the stores, so x and residual are read once. Rows of more
+// than 16384 values (8192 in fp32) are read once more for each of the two sweeps that follow.
 //
 // The mean of squares is kept in two fp32 numbers (two-sum steps, the squares'
 // own rounding errors included), so that r is the correctly rounded value but for
@@ -86,16 +86,18 @@ template <int DT> __device__ __forceinline__ uint4 narrow(const float* v) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// 16 bytes of a row that starts anywhere, from the aligned words that hold them;
-// words outside [lo, hi) are left alone.
+// 16 bytes of a row that starts anywhere, from the aligned words that hold them; inside:
+// the 16 bytes on either side of the row belong to the tensor too, otherwise words
+// outside [lo, hi) are left alone.
 template <int DT>
-__device__ __forceinline__ uint4 load_any(const char* row, uint32_t col, int64_t K, const char* lo, const char* hi) {
+__device__ __forceinline__ uint4 load_any(const char* row, uint32_t col, int64_t K, bool inside, const char* lo,
+                                          const char* hi) {
     using P = Piece<DT>;
     const char* p = row + (int64_t)col * P::kElem;
     const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
     const char* q = p - off;
     const uint32_t next = off ? 16 : 0;
-    if (col + P::kValues <= K && q >= lo && q + next + 16 <= hi) {
+    if (col + P::kValues <= K && (inside || (q >= lo && q + next + 16 <= hi))) {
         const uint4 a = ld_stream_v4(q), b = ld_stream_v4(q + next);
         return P::shifted(a, b, off);
     }
@@ -168,18 +170,20 @@ __device__ __forceinline__ uint32_t int8x4(const float* v, float inv) {
     return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
-// TPR threads a row (32: eight rows a block), 32 values each in pieces of 16 bytes TPR
-// pieces apart. LONG: rows of more than 32 TPR values. Blocks of as few registers as
-// let an SM hold 1280 threads, 1024 with the norm, fp32 rows' as many as they want
+// TPR threads a row (32: eight rows a block), PER values each in pieces of 16 bytes TPR
+// pieces apart. LONG: rows of more than PER TPR values. Blocks of as few registers as
+// let an SM hold 1280 threads, 1024 with the norm or of fp32 rows
 // (the norm of 16384 x 7168 bf16 rows: 191 us, with 768 threads 214, and with 1280, where it spills, 198;
 // 65536 x 4096 bf16 rows to int8 132 us, 144 with 1024). Persistent blocks whose next
-// row comes to shared memory meanwhile were slower (251 and 146).
-template <int DT, int TPR, bool NORM, bool LOOSE, bool LONG>
+// row comes to shared memory meanwhile were slower (251 and 146), and so were 16 values
+// a thread (219 and 181); fp32 rows' norm has 16 (16384 x 7168: 415 us, with 32 847),
+// alone they have 32.
+template <int DT, int TPR, int PER, bool NORM, bool LOOSE, bool LONG>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
-                                  DT == MR_DTYPE_F32 ? 1 : (NORM ? 1024 : 1280) / (TPR == 32 ? 256 : TPR))
+                                  (NORM || DT == MR_DTYPE_F32 ? 1024 : 1280) / (TPR == 32 ? 256 : TPR))
     rows_kernel(const RowArgs a) {
     using P = Piece<DT>;
-    constexpr int V = P::kValues, kPieces = 32 / V, kWarps = TPR / 32;
+    constexpr int V = P::kValues, kPieces = PER / V, kWarps = TPR / 32;
     __shared__ float2 part_sum[kWarps];
     __shared__ uint32_t part_max[kWarps];
     pdl_enter();
@@ -196,10 +200,13 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
     uint8_t* qr = a.q + batch * a.q_batch + r_in * a.q_row;
     float* sr = a.scales + batch * a.s_batch + r_in * a.s_row;
 
-    float v[32];
+    float v[PER];
     auto column = [&](int64_t base, int i) { return (uint32_t)(base + (int64_t)(i * TPR + t) * V); };
+    // (rows before and behind it, whose 16 bytes next to it are rows' too)
+    const bool inside = LOOSE && !a.per_batch && row > 0 && row + 1 < a.rows && a.K * P::kElem >= 16 &&
+                        a.x_row >= a.K * P::kElem && (!NORM || !rr || a.residual_row >= a.K * P::kElem);
     auto piece = [&](const char* p, uint32_t col, const char* lo, const char* hi) {
-        if constexpr (LOOSE) return load_any<DT>(p, col, a.K, lo, hi);
+        if constexpr (LOOSE) return load_any<DT>(p, col, a.K, inside, lo, hi);
         return P::load(p, col, a.K, true);
     };
     // the values of h from `base` on; first: the first time, when h is also written
@@ -231,7 +238,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
             if (first && hr) store_piece<DT, LOOSE>(hr, column(base, i), a.K, h);
         }
     };
-    const int64_t step = LONG ? 32 * TPR : a.K;
+    const int64_t step = LONG ? PER * TPR : a.K;
     if (!LONG) fetch(0, true);
 
     float r = 1.0f;
@@ -243,7 +250,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
             for (int64_t base = 0; base < a.K; base += step) {
                 if (LONG) fetch(base, first);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
+                for (int j = 0; j < PER; ++j) {
                     const float u = f == 1.0f ? v[j] : v[j] * f, sq = __fmul_rn(u, u);
                     // (a square of 11 bits is exact)
                     two_add_positive(s4[j & 3], e4[j & 3], sq);
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
             if (LONG) fetch(base, false);
             norm(base);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) m = max_abs(m, v[j]);
+            for (int j = 0; j < PER; ++j) m = max_abs(m, v[j]);
         }
         uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu);
         if (kWarps > 1) {
@@ -380,20 +387,25 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
     }
 }
 
-template <int DT, int TPR, bool NORM, bool LONG>
+template <int DT, int TPR, int PER, bool NORM, bool LONG>
 cudaError_t launch_rows(const RowArgs& a, bool loose, cudaStream_t s) {
     const int64_t blocks = TPR == 32 ? (a.rows + 7) / 8 : a.rows;
     const dim3 grid((unsigned)blocks), block(TPR == 32 ? 256 : TPR);
-    return loose ? launch_pdl(rows_kernel<DT, TPR, NORM, true, LONG>, grid, block, 0, s, a)
-                 : launch_pdl(rows_kernel<DT, TPR, NORM, false, LONG>, grid, block, 0, s, a);
+    return loose ? launch_pdl(rows_kernel<DT, TPR, PER, NORM, true, LONG>, grid, block, 0, s, a)
+                 : launch_pdl(rows_kernel<DT, TPR, PER, NORM, false, LONG>, grid, block, 0, s, a);
 }
 
+// The fewest values a thread that hold a short row (32768 rows of 70 bf16 values, norm to int8: 48 us,
+// with 32 a thread 91; of 512: 38 and 50).
 template <int DT, bool NORM> cudaError_t launch_rows(const RowArgs& a, bool loose, cudaStream_t s) {
-    if (a.K <= 1024) return launch_rows<DT, 32, NORM, false>(a, loose, s);
-    if (a.K <= 4096) return launch_rows<DT, 128, NORM, false>(a, loose, s);
-    if (a.K <= 8192) return launch_rows<DT, 256, NORM, false>(a, loose, s);
-    if (a.K <= 16384) return launch_rows<DT, 512, NORM, false>(a, loose, s);
-    return launch_rows<DT, 512, NORM, true>(a, loose, s);
+    constexpr int P = DT == MR_DTYPE_F32 && NORM ? 16 : 32;
+    if (a.K <= 256) return launch_rows<DT, 32, 8, NORM, false>(a, loose, s);
+    if (a.K <= 512) return launch_rows<DT, 32, 16, NORM, false>(a, loose, s);
+    if (P == 32 && a.K <= 1024) return launch_rows<DT, 32, P, NORM, false>(a, loose, s);
+    if (a.K <= 128 * P) return launch_rows<DT, 128, P, NORM, false>(a, loose, s);
+    if (a.K <= 256 * P) return launch_rows<DT, 256, P, NORM, false>(a, loose, s);
+    if (a.K <= 512 * P) return launch_rows<DT, 512, P, NORM, false>(a, loose, s);
+    return launch_rows<DT, 512, P, NORM, true>(a, loose, s);
 }
 
 // Rows of one type, in a translation unit of their own (they compile side by side).
