@@ -30,7 +30,7 @@
 // 4096: tensor pipe active 71 % of 143 us; 16384 x 7168 -> 7168 takes 780 us, 2.16
 // PFLOP/s, beside 53 to make the rows f16). With few rows per group the weights' way
 // from HBM, and how long a load keeps its room: 576 rows over 64 experts, 7168 ->
-// 4096, 296 to 302 us, 0.94 to 0.96 of the copy rate; a load of 32 KB takes a block's
+// 4096, 298 us, 0.95 of the copy rate; a load of 32 KB takes a block's
 // converters about 1150 cycles (waits 300, shared memory and conversion 450, the way
 // to tensor memory 300), so that few tiles of long rows are bound by those. With few
 // loads in all, the start (1.8 us up to the first load: list, descriptors), the results and
