@@ -22,7 +22,7 @@
 //   eight warps  results: scales, rounding, stores
 // One persistent block per SM takes tiles round robin; a pair of blocks shares a tile
 // of 256 channels, where each converts its own 128 and loads half of the rows. Where
-// single blocks would have few tiles each, they take equal shares of all tiles' loads
+// few rows leave SMs without a tile, single blocks take equal shares of all tiles' loads
 // instead: a tile's sums may then come from several blocks, which leave them in the
 // workspace, and the last one to arrive adds them up, in the order of k.
 //
@@ -77,7 +77,7 @@ template <typename W, bool SHARES> struct Items {
     W walk;
     Tile tile;
     int t, kb0, kb1;
-    int at, end, total, blocks;   // shares: loads of all tiles (2^17 of each of 16 tiles for each SM, at most)
+    int at, end, total, blocks;   // shares: loads of all tiles (2^17 of each, and fewer tiles than SMs)
 
     __device__ __forceinline__ void begin(const Int8Args& a, int lane, int first, int step) {
         walk.begin(a, lane);
