@@ -662,10 +662,12 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
  *   y[r, n] = (sum_k x[r, k] w[e, n, k]) ws[e, n] xs[r]
  *   for the rows of each group. Products of int8 values are exact and so are
  *   their fp32 sums while they stay below 2^24; 16-bit rows multiply as they are.
- *   The result is rounded once to yDtype (each scale's product once to fp32). With
- *   16-bit rows of more than 1024 values an F32 result is the sum of the results of
- *   equal parts of at most 1024 values, in their order; one of those below 2^-126
- *   may count as 0.
+ *   The result is rounded once to yDtype (each scale's product once to fp32).
+ *   An F32 result of int8 rows is that of the 32-bit integer sum, rounded to fp32
+ *   once before the scales (2^17 cols and more: of exact sums of at most 1024
+ *   values, added in fp32 in a fixed order). With 16-bit rows of more than 1024
+ *   values an F32 result is the sum of the results of equal parts of at most 1024
+ *   values, in their order; one of those below 2^-126 may count as 0.
  *
  *   x             [rows, cols] of xDtype: INT8 with xScales (the batching's y and
  *                 dynamicScale, or moe_quantize_int8's), or F16 or BF16, whose

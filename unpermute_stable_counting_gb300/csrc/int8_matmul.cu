@@ -59,15 +59,19 @@ struct Int8Args : Groups {
     int64_t y_stride;
     int y_dtype;
     int many;               // blocks may have several tiles
-    // Loads whose products one sum takes. The tensor cores cut what a sum has below fp32's digits at every addition,
-    // and 16-bit rows' sums lose by it: f16 rows of 7168 values are off by 7e-6, of 1000 by 8e-7. Where the result is
-    // fp32 a tile is taken in several sums, each added to what stands in y.
-    int sum_loads;
+    // Loads whose products one sum takes. The tensor cores cut what a sum has below fp32's digits at every addition:
+    // f16 rows of 7168 values are off by 7e-6, of 1000 by 8e-7, and int8 rows of one sign, whose sums are exact up to
+    // 2^24 (1024 values), of 7168 by 1.2e-5. Where the result is fp32 a tile is taken in several sums, as `sums` says.
+    int sum_loads, sums;
     // equal shares of the loads (NULL: whole tiles round robin)
     float* parts;           // two to a block, of part_rows rows of 256 sums
     int part_rows, part_loads;  // a share is this many loads at least
     unsigned* tickets;      // of each tile: blocks that have left their sums, 0 at the start
 };
+
+// Several sums to a value: each scaled and added to y (16-bit rows), or put together before the scales, in y's place (int8
+// rows): as 32-bit integers, or, where those may not hold them, in fp32.
+enum { kOneSum = 0, kScaledSums, kIntSums, kFloatSums };
 
 constexpr int kMostShares = 256;  // groups of a list that is walked once more, for the number of its tiles
 
@@ -77,7 +81,8 @@ template <typename W, bool SHARES> struct Items {
     W walk;
     Tile tile;
     int t, kb0, kb1;
-    int at, end, total, blocks;   // shares: loads of all tiles (2^17 of each, and fewer tiles than SMs)
+    bool again, more;             // of the block's sums of the tile: not the first, not the last
+    int at, start, end, total, blocks;   // shares: loads of all tiles (2^17 of each, and fewer tiles than SMs)
 
     __device__ __forceinline__ void begin(const Int8Args& a, int lane, int first, int step) {
         walk.begin(a, lane);
@@ -98,18 +103,23 @@ template <typename W, bool SHARES> struct Items {
         blocks = min((int)gridDim.x, total / a.part_loads + 1);
         at = end = 0;
         if (first < blocks) at = (int)((int64_t)first * total / blocks), end = (int)((int64_t)(first + 1) * total / blocks);
+        start = at;
     }
     __device__ __forceinline__ bool next(const Int8Args& a, int lane, int channels, int step) {
         if (SHARES && a.parts) {
             if (at >= end) return false;
             t = at / a.KB;
             kb0 = at - t * a.KB;
-            kb1 = min(a.KB, kb0 + (end - at));
+            again = kb0 > 0 && at > start;
+            kb1 = min(a.KB, kb0 + min(end - at, a.sum_loads));
             at += kb1 - kb0;
+            more = kb1 < a.KB && at < end;
         } else {
             if (kb1 == a.KB) t += step, kb1 = 0;
             kb0 = kb1;
             kb1 = min(a.KB, kb0 + a.sum_loads);
+            again = kb0 > 0;
+            more = kb1 < a.KB;
         }
         return walk.next(a, lane, t, channels, tile);
     }
@@ -138,7 +148,7 @@ template <bool PAIR, int HALF> struct SumRoom {
 struct Item {
     Tile tile;
     int t, loads;
-    bool again;              // the tile's sums that are not the first
+    bool again, more;        // of the block's sums of the tile: not the first, not the last
     int first, last, block;  // blocks that have a part of the tile; this one
 };
 
@@ -255,6 +265,30 @@ template <int N> __device__ __forceinline__ void pack(bool f16, const float (&a)
 __device__ __forceinline__ void put(char* y, float v, bool add) {
     if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(y), "f"(v) : "memory");
     else *reinterpret_cast<float*>(y) = v;
+}
+
+// One of several sums to where they are put together, by the same thread every time; past L1, which does not see what
+// is added in L2.
+__device__ __forceinline__ void put_sum(void* to, uint32_t sum, bool ints, bool add) {
+    if (ints) {
+        const int v = __float2int_rn(__uint_as_float(sum));
+        if (add) asm volatile("red.global.add.s32 [%0], %1;" ::"l"(to), "r"(v) : "memory");
+        else asm volatile("st.global.cg.s32 [%0], %1;" ::"l"(to), "r"(v) : "memory");
+    } else {
+        if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to), "f"(__uint_as_float(sum)) : "memory");
+        else asm volatile("st.global.cg.f32 [%0], %1;" ::"l"(to), "f"(__uint_as_float(sum)) : "memory");
+    }
+}
+// The last one of them, and those before it.
+__device__ __forceinline__ uint32_t take_sum(const void* from, uint32_t sum, bool ints) {
+    uint32_t v;
+    asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(from) : "memory");
+    return __float_as_uint(ints ? __int2float_rn((int)v + __float2int_rn(__uint_as_float(sum)))
+                                : __fadd_rn(__uint_as_float(v), __uint_as_float(sum)));
+}
+
+__device__ __forceinline__ uint32_t sum_of_parts(uint32_t sum, float part, bool ints) {
+    return ints ? sum + __float_as_uint(part) : __float_as_uint(__fadd_rn(__uint_as_float(sum), part));
 }
 
 template <int XT, bool SWIGLU, bool PAIR>
@@ -408,7 +442,8 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     if (more) {
                         i.t = items.t;
                         i.loads = items.kb1 - items.kb0;
-                        i.again = !a.parts && items.kb0 > 0;
+                        i.again = items.again;
+                        i.more = items.more;
                         i.first = i.last = i.block = first;
                         if (!PAIR && a.parts) {
                             i.first = items.owner(items.t * a.KB);
@@ -572,20 +607,23 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                 xs[i] = a.x_scales && inside && 32 * i + lane < mine ? a.x_scales[(row0 + 32 * i + lane) * a.xs_row] : 1.0f;
             constexpr int kLd = C::kChunk, kKeep = C::kSwap ? kLd / 2 : kLd;  // rows read at once, and of them this warp's
             const bool wide = !SWIGLU && a.y_dtype == MR_DTYPE_F32;
+            const bool ints = wide && a.sums == kIntSums, several = wide && a.sums >= kIntSums;
+            const bool added = wide && a.sums == kScaledSums && item.again;
             const int elem = wide ? 4 : 2;
             char* y = reinterpret_cast<char*>(a.y) + (row0 * a.y_stride + col) * elem;
             const int64_t y_step = a.y_stride * elem;
             const float w_scale = ws[real ? col : 0];
-            auto scaled = [&](const uint32_t (&v)[kLd], float by, int c, float (&f)[kLd]) {
+            auto scaled = [&](const auto& v, float by, int c, auto& f) {
+                constexpr int kCount = sizeof(f) / sizeof(f[0]);
 #pragma unroll
-                for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(__uint_as_float(v[j]), by);
+                for (int j = 0; j < kCount; ++j) f[j] = __fmul_rn(__uint_as_float(v[j]), by);
                 if (a.x_scales) {
                     float s = xs[0];
 #pragma unroll
                     for (int i = 1; i < kGroups; ++i)
                         if (c / 32 == i) s = xs[i];
 #pragma unroll
-                    for (int j = 0; j < kLd; ++j) f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, s, c % 32 + j));
+                    for (int j = 0; j < kCount; ++j) f[j] = __fmul_rn(f[j], __shfl_sync(0xffffffffu, s, c % 32 + j));
                 }
             };
             room.next(columns(tile.rows));
@@ -626,8 +664,8 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     if (wide) {
 #pragma unroll
                         for (int j = 0; j < kLd; ++j, to += y_step) {
-                            if (c + j < mine && real) put(to, f[j], item.again);
-                            if (c + j < mine && real1) put(to + kWRows * 4, g[j], item.again);
+                            if (c + j < mine && real) put(to, f[j], added);
+                            if (c + j < mine && real1) put(to + kWRows * 4, g[j], added);
                         }
                         return;
                     }
@@ -656,17 +694,32 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     tmem_ld_wait(u);
                     if (c + kLd >= mine) hand_back();  // everything is in registers
                     if (whole) {
+                        if (several && (item.again || item.more)) {
+                            char* to = y + c * y_step;
+#pragma unroll
+                            for (int j = 0; j < kLd; ++j, to += y_step) {
+                                if (c + j >= mine || !inside) continue;
+                                if (item.more) {
+                                    if (real) put_sum(to, v[j], ints, item.again);
+                                    if (real1) put_sum(to + kWRows * 4, u[j], ints, item.again);
+                                } else {
+                                    if (real) v[j] = take_sum(to, v[j], ints);
+                                    if (real1) u[j] = take_sum(to + kWRows * 4, u[j], ints);
+                                }
+                            }
+                            if (item.more) continue;
+                        }
                         finish(c, v, u);
                         continue;
                     }
 #pragma unroll
                     for (int j = 0; j < kLd; ++j)
                         if (c + j < mine && MR_IN_RANGE(half * cols + c + j, a.part_rows, 913)) {
-                            __stcg(part + (c + j) * 256, __uint_as_float(v[j]));
-                            __stcg(part + (c + j) * 256 + 128, __uint_as_float(u[j]));
+                            put_sum(part + (c + j) * 256, v[j], ints, item.again);
+                            put_sum(part + (c + j) * 256 + 128, u[j], ints, item.again);
                         }
                 }
-                if (!whole) {
+                if (!whole && !item.more) {
                     // the warps' sums are out, one of them takes a ticket for all
                     __threadfence();
                     __syncwarp();
@@ -688,21 +741,23 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                         __threadfence();
 #pragma unroll 1
                         for (int c = 0; c < mine; c += kLd) {
-                            float f[kLd], g[kLd];
+                            uint32_t v[kLd], u[kLd];
 #pragma unroll
-                            for (int j = 0; j < kLd; ++j) f[j] = g[j] = 0.0f;
+                            for (int j = 0; j < kLd; ++j) v[j] = u[j] = 0u;
                             for (int b = item.first; b <= item.last; ++b) {
                                 const float* from_b = part_of(b) + c * 256;
 #pragma unroll
                                 for (int j = 0; j < kLd; ++j)
                                     if (c + j < mine) {
-                                        f[j] = __fadd_rn(f[j], __ldcg(from_b + j * 256));
-                                        g[j] = __fadd_rn(g[j], __ldcg(from_b + j * 256 + 128));
+                                        v[j] = sum_of_parts(v[j], __ldcg(from_b + j * 256), ints);
+                                        u[j] = sum_of_parts(u[j], __ldcg(from_b + j * 256 + 128), ints);
                                     }
                             }
-                            uint32_t v[kLd], u[kLd];
+                            if (ints) {
 #pragma unroll
-                            for (int j = 0; j < kLd; ++j) v[j] = __float_as_uint(f[j]), u[j] = __float_as_uint(g[j]);
+                                for (int j = 0; j < kLd; ++j)
+                                    v[j] = __float_as_uint(__int2float_rn((int)v[j])), u[j] = __float_as_uint(__int2float_rn((int)u[j]));
+                            }
                             finish(c, v, u);
                         }
                     }
@@ -740,6 +795,32 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                         }
                         continue;
                     }
+                    if (several) {
+                        constexpr int kFew = kLd / 2;  // (with kLd, whose earlier sums have registers, too, the kernel spills)
+#pragma unroll 1
+                        for (int c = 0; c < mine; c += kFew) {
+                            uint32_t v[kFew];
+                            tmem_load(v, sums + c);
+                            tmem_ld_wait(v);
+                            if (c + kFew >= mine) hand_back();
+                            char* to = y + c * y_step;
+                            const bool out = real && inside;
+                            float f[kFew];
+                            if (!item.more) {
+#pragma unroll
+                                for (int j = 0; j < kFew; ++j)
+                                    if (out && c + j < mine) v[j] = take_sum(to + j * y_step, v[j], ints);
+                                scaled(v, w_scale, c, f);
+                            }
+#pragma unroll
+                            for (int j = 0; j < kFew; ++j, to += y_step) {
+                                if (!out || c + j >= mine) continue;
+                                if (item.more) put_sum(to, v[j], ints, item.again);
+                                else put(to, f[j], false);
+                            }
+                        }
+                        continue;
+                    }
                 }
 #pragma unroll 1
                 for (int c = 0; c < mine; c += kLd) {
@@ -772,7 +853,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     }
                     if (!real || !inside) continue;
                     char* to = y + r * y_step;
-                    if (wide && item.again) {
+                    if (added) {
 #pragma unroll
                         for (int j = 0; j < kKeep; ++j, to += y_step)
                             if (r + j < mine) put(to, f[j], true);
@@ -941,9 +1022,11 @@ uint64_t ticket_bytes(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu
 mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
     a.n_tiles = ceil_div(a.N, p.swiglu ? 128 : 256);
     a.KB = ceil_div(p.K, 128);
-    const int sums = a.y_dtype == MR_DTYPE_F32 && !p.swiglu && !p.exact ? ceil_div(a.KB, 8) : 1;
+    const int sums = a.y_dtype == MR_DTYPE_F32 && !p.swiglu ? ceil_div(a.KB, 8) : 1;
     a.sum_loads = ceil_div(a.KB, sums);
-    if (a.sum_loads < a.KB) a.parts = nullptr;
+    // 2^17 products of int8 values reach 2^31
+    a.sums = sums == 1 ? kOneSum : !p.exact ? kScaledSums : p.K < (1 << 17) ? kIntSums : kFloatSums;
+    if (a.sums == kScaledSums) a.parts = nullptr;
     const int64_t tiles = most_tiles(a.rows, a.G, a.N, pair, p.swiglu);
     if (tiles > INT32_MAX - 4096) return MR_ERR_PARAM_INVALID;  // (a block's count of them goes one round past)
     CUtensorMap m[2];
