@@ -61,16 +61,18 @@ struct Int8Args : Groups {
     int many;               // blocks may have several tiles
     // Loads whose products one sum takes. The tensor cores cut what a sum has below fp32's digits at every addition:
     // f16 rows of 7168 values are off by 7e-6, of 1000 by 8e-7, and int8 rows of one sign, whose sums are exact up to
-    // 2^24 (1024 values), of 7168 by 1.2e-5. Where the result is fp32 a tile is taken in several sums, as `sums` says.
+    // 2^24 (1024 values), of 7168 by 1.2e-5. Where the result is fp32, or rows are long, a tile is taken in several sums,
+    // as `sums` says.
     int sum_loads, sums;
+    float* room;            // 16-bit results of several sums: a block's (pair's) tile of 256 sums to a row
     // equal shares of the loads (NULL: whole tiles round robin)
     float* parts;           // two to a block, of part_rows rows of 256 sums
     int part_rows, part_loads;  // a share is this many loads at least
     unsigned* tickets;      // of each tile: blocks that have left their sums, 0 at the start
 };
 
-// Several sums to a value: each scaled and added to y (16-bit rows), or put together before the scales, in y's place (int8
-// rows): as 32-bit integers, or, where those may not hold them, in fp32.
+// Several sums to a value: each scaled and added to y (fp32 results of 16-bit rows), or put together before the scales,
+// fp32 results in y's place: as 32-bit integers (fp32 results of int8 rows), or, where those may not hold them, in fp32.
 enum { kOneSum = 0, kScaledSums, kIntSums, kFloatSums };
 
 constexpr int kMostShares = 256;  // groups of a list that is walked once more, for the number of its tiles
@@ -607,7 +609,8 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                 xs[i] = a.x_scales && inside && 32 * i + lane < mine ? a.x_scales[(row0 + 32 * i + lane) * a.xs_row] : 1.0f;
             constexpr int kLd = C::kChunk, kKeep = C::kSwap ? kLd / 2 : kLd;  // rows read at once, and of them this warp's
             const bool wide = !SWIGLU && a.y_dtype == MR_DTYPE_F32;
-            const bool ints = wide && a.sums == kIntSums, several = wide && a.sums >= kIntSums;
+            const bool ints = wide && a.sums == kIntSums;
+            const bool several = a.sums >= kIntSums && (item.again || item.more);
             const bool added = wide && a.sums == kScaledSums && item.again;
             const int elem = wide ? 4 : 2;
             char* y = reinterpret_cast<char*>(a.y) + (row0 * a.y_stride + col) * elem;
@@ -694,10 +697,13 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     tmem_ld_wait(u);
                     if (c + kLd >= mine) hand_back();  // everything is in registers
                     if (whole) {
-                        if (several && (item.again || item.more)) {
-                            char* to = y + c * y_step;
+                        if (several) {
+                            float* room = a.parts ? part : a.room + (((int64_t)item.block * C::kRows + half * cols) << 8) +
+                                                               quarter * 32 + lane;
+                            char* to = wide ? y + c * y_step : reinterpret_cast<char*>(room + c * 256);
+                            const int64_t next = wide ? y_step : 1024;
 #pragma unroll
-                            for (int j = 0; j < kLd; ++j, to += y_step) {
+                            for (int j = 0; j < kLd; ++j, to += next) {
                                 if (c + j >= mine || !inside) continue;
                                 if (item.more) {
                                     if (real) put_sum(to, v[j], ints, item.again);
@@ -768,7 +774,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     // registers (16384 x 7168 x 7168: 836 us, as below 869). In a launch of one tile a block what
                     // this code costs is its own way from memory (1003 rows of 12 groups, 1000 -> 1100: 15.9 us, as
                     // below 13.7).
-                    if (a.many && !wide) {
+                    if (a.many && !wide && !several) {
                         uint32_t packed[C::kHalf / 2];
 #pragma unroll
                         for (int c = 0; c < C::kHalf; c += kLd) {
@@ -803,20 +809,30 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                             tmem_load(v, sums + c);
                             tmem_ld_wait(v);
                             if (c + kFew >= mine) hand_back();
-                            char* to = y + c * y_step;
+                            float* room = a.room + (((int64_t)first * C::kRows + half * cols + c) << 8) + (int)rank * kWRows +
+                                          quarter * 32 + lane;
+                            char* to = wide ? y + c * y_step : reinterpret_cast<char*>(room);
+                            const int64_t next = wide ? y_step : 1024;
                             const bool out = real && inside;
-                            float f[kFew];
-                            if (!item.more) {
+                            if (item.more) {
 #pragma unroll
-                                for (int j = 0; j < kFew; ++j)
-                                    if (out && c + j < mine) v[j] = take_sum(to + j * y_step, v[j], ints);
-                                scaled(v, w_scale, c, f);
+                                for (int j = 0; j < kFew; ++j, to += next)
+                                    if (out && c + j < mine) put_sum(to, v[j], ints, item.again);
+                                continue;
                             }
+#pragma unroll
+                            for (int j = 0; j < kFew; ++j, to += next)
+                                if (out && c + j < mine) v[j] = take_sum(to, v[j], ints);
+                            float f[kFew];
+                            scaled(v, w_scale, c, f);
+                            uint32_t w[kFew];
+                            if (!wide) pack(a.y_dtype == MR_DTYPE_F16, f, f, w);
+                            to = y + c * y_step;
 #pragma unroll
                             for (int j = 0; j < kFew; ++j, to += y_step) {
                                 if (!out || c + j >= mine) continue;
-                                if (item.more) put_sum(to, v[j], ints, item.again);
-                                else put(to, f[j], false);
+                                if (wide) put(to, f[j], false);
+                                else *reinterpret_cast<uint16_t*>(to) = (uint16_t)w[j];
                             }
                         }
                         continue;
@@ -989,6 +1005,10 @@ struct Product {
     bool exact;                // rows of int8 values (whatever type holds them)
 };
 
+// 16-bit results' values of k to a sum: what the tensor cores cut is 1e-4 of as many values of one sign (of 131072,
+// 7.6e-4: more than f16's rounding).
+constexpr int64_t kMostSum = 16384;
+
 // The tiles of a product, or more.
 int64_t most_tiles(int64_t rows, int64_t G, int64_t N, bool pair, bool swiglu) {
     const int64_t down = std::min<int64_t>((int64_t)ceil_div(rows, pair ? 256 : 96) + G - 1, rows);
@@ -999,8 +1019,9 @@ int64_t most_tiles(int64_t rows, int64_t G, int64_t N, bool pair, bool swiglu) {
 // each SM, of groups of few rows (int8 rows, 7168 -> 4096: 576 of 64 groups 310 us in single blocks, 365 in pairs;
 // 4096 -> 4096: 1000 rows of 16 groups 71 and 79; 4096 -> 2048: 4000 rows of 64 groups 128 and 133, 8000 195 and 167;
 // 515 rows of 6 groups through the network, 1080 / 712, 49 and 37). Up to 32 rows the blocks may share tiles (below).
-bool use_pairs(int64_t rows, int64_t G, int64_t N, bool swiglu) {
-    if (rows <= 32) return false;
+// The network's rows of several sums go to single blocks, whose two factors are in one warp.
+bool use_pairs(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu) {
+    if (rows <= 32 || (swiglu && K > kMostSum)) return false;
     return rows > 64 * std::min<int64_t>(G, rows) || most_tiles(rows, G, N, false, swiglu) < device_sm_count();
 }
 
@@ -1019,13 +1040,25 @@ uint64_t ticket_bytes(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu
     return use_shares(rows, G, N, K, swiglu) ? align_up((uint64_t)most_tiles(rows, G, N, false, swiglu) * 4, 256) : 0;
 }
 
+// The sums of a block's tile, where rows are long and blocks do not share tiles.
+uint64_t sum_bytes(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu) {
+    if (K <= kMostSum || use_shares(rows, G, N, K, swiglu)) return 0;
+    const bool pair = use_pairs(rows, G, N, K, swiglu);
+    return (uint64_t)std::min<int64_t>(most_tiles(rows, G, N, pair, swiglu), device_sm_count() / (pair ? 2 : 1)) *
+           (pair ? 256 : 96) * 1024;
+}
+
 mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
     a.n_tiles = ceil_div(a.N, p.swiglu ? 128 : 256);
     a.KB = ceil_div(p.K, 128);
-    const int sums = a.y_dtype == MR_DTYPE_F32 && !p.swiglu ? ceil_div(a.KB, 8) : 1;
+    const bool wide = a.y_dtype == MR_DTYPE_F32 && !p.swiglu;
+    const int sums = ceil_div(p.K, wide ? 1024 : kMostSum);
     a.sum_loads = ceil_div(a.KB, sums);
-    // 2^17 products of int8 values reach 2^31
-    a.sums = sums == 1 ? kOneSum : !p.exact ? kScaledSums : p.K < (1 << 17) ? kIntSums : kFloatSums;
+    // (2^17 products of int8 values reach 2^31)
+    a.sums = sums == 1                          ? kOneSum
+             : wide && !p.exact                 ? kScaledSums
+             : wide && p.K < (INT64_C(1) << 17) ? kIntSums
+                                                : kFloatSums;
     if (a.sums == kScaledSums) a.parts = nullptr;
     const int64_t tiles = most_tiles(a.rows, a.G, a.N, pair, p.swiglu);
     if (tiles > INT32_MAX - 4096) return MR_ERR_PARAM_INVALID;  // (a block's count of them goes one round past)
@@ -1085,19 +1118,22 @@ cudaError_t prepare_rows(Product& p, const Int8Args& a, bool pair, const int64_t
     return e;
 }
 
-// A call's workspace: wide rows, the network's h, then tickets of each product and sums of parts of tiles.
+// A call's workspace: wide rows, the network's h, then tickets of each product, sums of parts of tiles and of long rows.
 struct Room {
-    uint64_t x, h, tickets[2], parts;
-    uint64_t total() const { return x + h + tickets[0] + tickets[1] + parts; }
+    uint64_t x, h, tickets[2], parts, sums;
+    uint64_t total() const { return x + h + tickets[0] + tickets[1] + parts + sums; }
 };
 Room matmul_room(int64_t rows, int64_t G, int64_t N, int64_t K, int32_t dt) {
-    Room r{dt == MR_DTYPE_INT8 && use_pairs(rows, G, N, false) ? wide_bytes(rows, K) : 0, 0, {ticket_bytes(rows, G, N, K, false), 0}, 0};
+    Room r{dt == MR_DTYPE_INT8 && use_pairs(rows, G, N, K, false) ? wide_bytes(rows, K) : 0, 0,
+           {ticket_bytes(rows, G, N, K, false), 0}, 0, sum_bytes(rows, G, N, K, false)};
     r.parts = r.tickets[0] ? part_bytes(rows) : 0;
     return r;
 }
 Room ffn_room(int64_t rows, int64_t G, int64_t hidden, int64_t inter, int32_t dt) {
-    Room r{dt == MR_DTYPE_INT8 && use_pairs(rows, G, inter, true) ? wide_bytes(rows, hidden) : 0, wide_bytes(rows, inter),
-           {ticket_bytes(rows, G, inter, hidden, true), ticket_bytes(rows, G, hidden, inter, false)}, 0};
+    Room r{dt == MR_DTYPE_INT8 && use_pairs(rows, G, inter, hidden, true) ? wide_bytes(rows, hidden) : 0,
+           wide_bytes(rows, inter),
+           {ticket_bytes(rows, G, inter, hidden, true), ticket_bytes(rows, G, hidden, inter, false)}, 0,
+           std::max(sum_bytes(rows, G, inter, hidden, true), sum_bytes(rows, G, hidden, inter, false))};
     r.parts = r.tickets[0] || r.tickets[1] ? part_bytes(rows) : 0;
     return r;
 }
@@ -1114,6 +1150,7 @@ void take_room(Int8Args& a, const Room& r, char* workspace, int product) {
     a.part_rows = (int)part_rows(a.rows);
     a.part_loads = a.rows > 8 ? 8 : 4;  // (16 x 4096 -> 4096: 21 us, with 4 loads 24; 1 x 4096 -> 2048: 18, with 8 19)
     a.tickets = reinterpret_cast<unsigned*>(tickets + (product ? r.tickets[0] : 0));
+    a.room = reinterpret_cast<float*>(tickets + r.tickets[0] + r.tickets[1] + r.parts);
 }
 
 // Checks that both products make of their weights; wr, wm: byte strides.
@@ -1194,7 +1231,7 @@ extern "C" mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int6
     a.y_stride = yStride;
     a.y_dtype = yDtype;
     Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, weights, wr, wm, cols, false, eight};
-    const bool pair = use_pairs(rows, a.G, outCols, false);
+    const bool pair = use_pairs(rows, a.G, outCols, cols, false);
     char* base = reinterpret_cast<char*>(workspace);
     MR_TRY_CUDA(clear_tickets(room, base, s));
     MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, base, s));
@@ -1255,7 +1292,7 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     a.y = h;
     a.y_stride = wide_stride(inter) / 2;
     a.y_dtype = MR_DTYPE_BF16;
-    const bool pair = use_pairs(rows, a.G, inter, true);
+    const bool pair = use_pairs(rows, a.G, inter, hidden, true);
     Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, w13, ar, am, hidden, true, eight};
     MR_TRY_CUDA(clear_tickets(room, base, s));
     MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, base, s));
@@ -1271,5 +1308,5 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     a.y_stride = yStride;
     a.y_dtype = yDtype;
     take_room(a, room, base, 1);
-    return run_product(p, a, use_pairs(rows, a.G, hidden, false), s);
+    return run_product(p, a, use_pairs(rows, a.G, hidden, inter, false), s);
 }
