@@ -286,7 +286,9 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
         if (!small) {
             if (kWarps > 1) __syncthreads();
             sums(0x1p-80f, false, s, e);
-            eps_hi = eps_lo = 0.0f;  // nothing beside such squares
+            // (2^-160 is no fp32 number)
+            eps_hi = __fmul_rn(__fmul_rn(eps_hi, 0x1p-80f), 0x1p-80f);
+            eps_lo = __fmul_rn(__fmul_rn(eps_lo, 0x1p-80f), 0x1p-80f);
         }
         const bool finite = s < __int_as_float(0x7F800000);
         float m = __fdiv_rn(s, count), low = 0.0f;
