@@ -1059,7 +1059,6 @@ mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
              : wide && !p.exact                 ? kScaledSums
              : wide && p.K < (INT64_C(1) << 17) ? kIntSums
                                                 : kFloatSums;
-    if (a.sums == kScaledSums) a.parts = nullptr;
     const int64_t tiles = most_tiles(a.rows, a.G, a.N, pair, p.swiglu);
     if (tiles > INT32_MAX - 4096) return MR_ERR_PARAM_INVALID;  // (a block's count of them goes one round past)
     CUtensorMap m[2];
@@ -1090,6 +1089,10 @@ mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
     }
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
+
+// Results that take several scaled sums (kScaledSums, where rows are as long as those of shared tiles): their tiles have
+// no shares, although the size of the workspace, which does not go by y's type, has room for them.
+bool scaled_sums(int32_t yDtype, bool eight) { return yDtype == MR_DTYPE_F32 && !eight; }
 
 bool row_type(int32_t dt) { return dt == MR_DTYPE_INT8 || dt == MR_DTYPE_F16 || dt == MR_DTYPE_BF16; }
 bool out_type(int32_t dt) { return dt == MR_DTYPE_F16 || dt == MR_DTYPE_BF16 || dt == MR_DTYPE_F32; }
@@ -1137,16 +1140,16 @@ Room ffn_room(int64_t rows, int64_t G, int64_t hidden, int64_t inter, int32_t dt
     r.parts = r.tickets[0] || r.tickets[1] ? part_bytes(rows) : 0;
     return r;
 }
-// Tickets at 0 (nothing keeps the workspace between calls), where products take some.
-cudaError_t clear_tickets(const Room& r, char* workspace, cudaStream_t s) {
-    const uint64_t n = r.tickets[0] + r.tickets[1];
+// Tickets at 0 (nothing keeps the workspace between calls), where products take some. scaled: the last product does not.
+cudaError_t clear_tickets(const Room& r, bool scaled, bool network, char* workspace, cudaStream_t s) {
+    const uint64_t n = (scaled && !network ? 0 : r.tickets[0]) + (scaled ? 0 : r.tickets[1]);
     return n ? launch_pdl(clear_kernel, dim3(1), dim3(256), 0, s, reinterpret_cast<uint4*>(workspace + r.x + r.h), (int)(n / 16))
              : cudaSuccess;
 }
 // The product's share of the room.
-void take_room(Int8Args& a, const Room& r, char* workspace, int product) {
+void take_room(Int8Args& a, const Room& r, bool scaled, char* workspace, int product) {
     char* tickets = workspace + r.x + r.h;
-    a.parts = r.tickets[product] ? reinterpret_cast<float*>(tickets + r.tickets[0] + r.tickets[1]) : nullptr;
+    a.parts = r.tickets[product] && !scaled ? reinterpret_cast<float*>(tickets + r.tickets[0] + r.tickets[1]) : nullptr;
     a.part_rows = (int)part_rows(a.rows);
     a.part_loads = a.rows > 8 ? 8 : 4;  // (16 x 4096 -> 4096: 21 us, with 4 loads 24; 1 x 4096 -> 2048: 18, with 8 19)
     a.tickets = reinterpret_cast<unsigned*>(tickets + (product ? r.tickets[0] : 0));
@@ -1233,9 +1236,10 @@ extern "C" mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int6
     Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, weights, wr, wm, cols, false, eight};
     const bool pair = use_pairs(rows, a.G, outCols, cols, false);
     char* base = reinterpret_cast<char*>(workspace);
-    MR_TRY_CUDA(clear_tickets(room, base, s));
+    const bool scaled = scaled_sums(yDtype, eight);
+    MR_TRY_CUDA(clear_tickets(room, scaled, false, base, s));
     MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, base, s));
-    take_room(a, room, base, 0);
+    take_room(a, room, scaled, base, 0);
     return run_product(p, a, pair, s);
 }
 
@@ -1294,9 +1298,10 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     a.y_dtype = MR_DTYPE_BF16;
     const bool pair = use_pairs(rows, a.G, inter, hidden, true);
     Product p{x, xStride, eight ? kInt8 : xDtype == MR_DTYPE_BF16 ? kBf16 : kF16, w13, ar, am, hidden, true, eight};
-    MR_TRY_CUDA(clear_tickets(room, base, s));
+    const bool scaled = scaled_sums(yDtype, false);
+    MR_TRY_CUDA(clear_tickets(room, scaled, true, base, s));
     MR_TRY_CUDA(prepare_rows(p, a, pair, numRows, base, s));
-    take_room(a, room, base, 0);
+    take_room(a, room, false, base, 0);
     mr_status st = run_product(p, a, pair, s);
     if (st != MR_OK) return st;
 
@@ -1307,6 +1312,6 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     a.y = y;
     a.y_stride = yStride;
     a.y_dtype = yDtype;
-    take_room(a, room, base, 1);
+    take_room(a, room, scaled, base, 1);
     return run_product(p, a, use_pairs(rows, a.G, hidden, inter, false), s);
 }
