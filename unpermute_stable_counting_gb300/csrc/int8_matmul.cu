@@ -949,7 +949,8 @@ __global__ void __launch_bounds__(256) clear_kernel(uint4* tickets, int n) {
     for (int i = threadIdx.x; i < n; i += 256) tickets[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int ceil_div(int64_t a, int64_t b) { return (int)ceil_div64(a, b); }
 bool aligned16(const void* p) { return aligned(p, 16); }
 
 template <int XT, bool SWIGLU, bool PAIR>
@@ -1048,6 +1049,13 @@ uint64_t sum_bytes(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu) {
            (pair ? 256 : 96) * 1024;
 }
 
+// What counts a product's tiles, and the threads that widen its rows, holds them.
+bool countable(int64_t rows, int64_t G, int64_t N, int64_t K, bool swiglu, bool eight) {
+    const bool pair = use_pairs(rows, G, N, K, swiglu);
+    return most_tiles(rows, G, N, pair, swiglu) <= INT32_MAX - 4096 &&  // (a block's count of them goes one round past)
+           (!pair || !eight || ceil_div64(rows * ceil_div64(K, 16), 256) <= INT32_MAX);
+}
+
 mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
     a.n_tiles = ceil_div(a.N, p.swiglu ? 128 : 256);
     a.KB = ceil_div(p.K, 128);
@@ -1060,7 +1068,6 @@ mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
              : wide && p.K < (INT64_C(1) << 17) ? kIntSums
                                                 : kFloatSums;
     const int64_t tiles = most_tiles(a.rows, a.G, a.N, pair, p.swiglu);
-    if (tiles > INT32_MAX - 4096) return MR_ERR_PARAM_INVALID;  // (a block's count of them goes one round past)
     CUtensorMap m[2];
     const bool eight = p.xt == kInt8;
     const uint64_t xd[2] = {(uint64_t)p.K, (uint64_t)a.rows}, xs[1] = {(uint64_t)p.x_stride};
@@ -1218,6 +1225,7 @@ extern "C" mr_status moe_grouped_matmul_int8(const void* x, int32_t xDtype, int6
         (room.total() && !aligned(workspace, 256)) || !aligned(y, yDtype == MR_DTYPE_F32 ? 4 : 2) || !aligned(xScales, 4) ||
         !aligned(weightScales, 4) || !aligned(numRows, 8))
         return MR_ERR_PARAM_INVALID;
+    if (numGroups && !countable(rows, numGroups < 0 ? 1 : numGroups, outCols, cols, false, eight)) return MR_ERR_PARAM_INVALID;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     Int8Args a{};
     a.groups = numGroups < 0 ? nullptr : groupList;
@@ -1279,6 +1287,9 @@ extern "C" mr_status moe_expert_ffn_int8(const void* x, int32_t xDtype, int64_t 
     if (!aligned16(w13) || !aligned16(w2) || !aligned16(x) || (numGroups > 0 && !aligned16(groupList)) ||
         !aligned(workspace, 256) || !aligned(y, yDtype == MR_DTYPE_F32 ? 4 : 2) || !aligned(xScales, 4) ||
         !aligned(w13Scales, 4) || !aligned(w2Scales, 4) || !aligned(numRows, 8))
+        return MR_ERR_PARAM_INVALID;
+    const int64_t groups = numGroups < 0 ? 1 : numGroups;
+    if (groups && (!countable(rows, groups, inter, hidden, true, eight) || !countable(rows, groups, hidden, inter, false, false)))
         return MR_ERR_PARAM_INVALID;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     Int8Args a{};
