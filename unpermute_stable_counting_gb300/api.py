@@ -575,6 +575,19 @@ def _interleaved(rows, cols, index):
     return dict(rows=both, values=both[:, :cols], scales=both.view(torch.float32)[:, cols // 4])
 
 
+def _interleaved_out(out, rows, cols, row, scales, step):
+    """Whether values and scales that the caller gave (row and step: their strides) lie as _interleaved's; rows, if
+    not given, is a view of them."""
+    values, both = out["values"], out.get("rows")
+    if cols % 4 or values.data_ptr() + cols != scales or (rows > 1 and (row != cols + 4 or step != cols // 4 + 1)):
+        raise ValueError("interleaved: out's scales must stand behind their rows of values, a multiple of 4 columns")
+    if both is None:
+        out["rows"] = values.as_strided((rows, cols + 4), (cols + 4, 1))
+    elif (both.data_ptr() != values.data_ptr() or both.dtype != torch.int8 or both.shape != (rows, cols + 4)
+          or not both.is_contiguous()):
+        raise ValueError("interleaved: out's rows must be int8 [rows, cols + 4] that hold its values and scales")
+
+
 def _scales_of_rows(scales, rows, index):
     """Address and stride of float32 [rows], each scale with an element of its own."""
     if not isinstance(scales, torch.Tensor) or not scales.is_cuda or scales.dtype != torch.float32:
@@ -596,7 +609,7 @@ def moe_quantize_int8(x, *, num_rows=None, interleaved: bool = False, out: dict 
 
     interleaved (x of 2 dimensions, cols a multiple of 4): also rows [rows, cols + 4],
     each row's values and then its scale, the batching's token_data; values and scales
-    are views of it. num_rows (int64 [1] on the device, x of 2 dimensions): rows at or
+    are views of it, in out, too. num_rows (int64 [1] on the device, x of 2 dimensions): rows at or
     past it are not written."""
     dims = x.dim()
     if not 2 <= dims <= 4:
@@ -629,6 +642,8 @@ def moe_quantize_int8(x, *, num_rows=None, interleaved: bool = False, out: dict 
         xs, vs = _Pair(0, _row_stride(shape, strides)), _Pair(0, _row_stride(vshape, vstrides))
         sa, step = _scales_of_rows(scales, rows, index)
         ss = _Pair(0, step)
+        if interleaved and rows:
+            _interleaved_out(out, rows, cols, vs[1], sa, step)
     else:
         sa, ss = _vector("scales", scales, torch.float32, index, shape[:-1]), None
         if x.numel() == 0 and rows and cols:  # no matrices
@@ -709,6 +724,8 @@ def moe_add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quantize: s
             if quantize == "int8":
                 sa, step = _scales_of_rows(scales, rows, index)
                 ss = _Pair(step, 1)
+                if interleaved and rows:
+                    _interleaved_out(out, rows, cols, vst, sa, step)
             else:
                 sa, ss = _block_scales(scales, (rows, _blocks(cols)), index)
     st = lib().moe_add_rms_norm(x.data_ptr(), dt, rows, cols, _row_stride(shape, strides), ra, rs, wa,
