@@ -663,11 +663,10 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
  *   for the rows of each group. Products of int8 values are exact and so are
  *   their fp32 sums while they stay below 2^24; 16-bit rows multiply as they are.
  *   The result is rounded once to yDtype (each scale's product once to fp32).
- *   An F32 result of int8 rows is that of the 32-bit integer sum, rounded to fp32
- *   once before the scales (2^17 cols and more: of exact sums of at most 1024
- *   values, added in fp32 in a fixed order). With 16-bit rows of more than 1024
- *   values an F32 result is the sum of the results of equal parts of at most 1024
- *   values, in their order; one of those below 2^-126 may count as 0. A 16-bit
+ *   An F32 result of int8 rows is that of exact sums of at most 1024 values, which
+ *   are added in fp32 in a fixed order. With 16-bit rows of more than 1024 values an
+ *   F32 result is the sum of the results of equal parts of at most 1024 values, in
+ *   their order; one of those below 2^-126 may count as 0. A 16-bit
  *   result takes at most 16384 values into one sum of the tensor cores (which cut
  *   1e-4 of as many values of one sign), and adds such sums in fp32.
  *

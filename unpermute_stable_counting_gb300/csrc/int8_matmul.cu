@@ -71,9 +71,9 @@ struct Int8Args : Groups {
     unsigned* tickets;      // of each tile: blocks that have left their sums, 0 at the start
 };
 
-// Several sums to a value: each scaled and added to y (fp32 results of 16-bit rows), or put together before the scales,
-// fp32 results in y's place: as 32-bit integers (fp32 results of int8 rows), or, where those may not hold them, in fp32.
-enum { kOneSum = 0, kScaledSums, kIntSums, kFloatSums };
+// Several sums to a value: each scaled and added to y (fp32 results of 16-bit rows), or put together before the scales, of
+// fp32 results in y's place.
+enum { kOneSum = 0, kScaledSums, kPlainSums };
 
 constexpr int kMostShares = 256;  // groups of a list that is walked once more, for the number of its tiles
 
@@ -271,26 +271,15 @@ __device__ __forceinline__ void put(char* y, float v, bool add) {
 
 // One of several sums to where they are put together, by the same thread every time; past L1, which does not see what
 // is added in L2.
-__device__ __forceinline__ void put_sum(void* to, uint32_t sum, bool ints, bool add) {
-    if (ints) {
-        const int v = __float2int_rn(__uint_as_float(sum));
-        if (add) asm volatile("red.global.add.s32 [%0], %1;" ::"l"(to), "r"(v) : "memory");
-        else asm volatile("st.global.cg.s32 [%0], %1;" ::"l"(to), "r"(v) : "memory");
-    } else {
-        if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to), "f"(__uint_as_float(sum)) : "memory");
-        else asm volatile("st.global.cg.f32 [%0], %1;" ::"l"(to), "f"(__uint_as_float(sum)) : "memory");
-    }
+__device__ __forceinline__ void put_sum(void* to, uint32_t sum, bool add) {
+    if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to), "f"(__uint_as_float(sum)) : "memory");
+    else asm volatile("st.global.cg.u32 [%0], %1;" ::"l"(to), "r"(sum) : "memory");
 }
 // The last one of them, and those before it.
-__device__ __forceinline__ uint32_t take_sum(const void* from, uint32_t sum, bool ints) {
-    uint32_t v;
-    asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(from) : "memory");
-    return __float_as_uint(ints ? __int2float_rn((int)v + __float2int_rn(__uint_as_float(sum)))
-                                : __fadd_rn(__uint_as_float(v), __uint_as_float(sum)));
-}
-
-__device__ __forceinline__ uint32_t sum_of_parts(uint32_t sum, float part, bool ints) {
-    return ints ? sum + __float_as_uint(part) : __float_as_uint(__fadd_rn(__uint_as_float(sum), part));
+__device__ __forceinline__ uint32_t take_sum(const void* from, uint32_t sum) {
+    float v;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(from) : "memory");
+    return __float_as_uint(__fadd_rn(v, __uint_as_float(sum)));
 }
 
 template <int XT, bool SWIGLU, bool PAIR>
@@ -609,8 +598,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                 xs[i] = a.x_scales && inside && 32 * i + lane < mine ? a.x_scales[(row0 + 32 * i + lane) * a.xs_row] : 1.0f;
             constexpr int kLd = C::kChunk, kKeep = C::kSwap ? kLd / 2 : kLd;  // rows read at once, and of them this warp's
             const bool wide = !SWIGLU && a.y_dtype == MR_DTYPE_F32;
-            const bool ints = wide && a.sums == kIntSums;
-            const bool several = a.sums >= kIntSums && (item.again || item.more);
+            const bool several = a.sums == kPlainSums && (item.again || item.more);
             const bool added = wide && a.sums == kScaledSums && item.again;
             const int elem = wide ? 4 : 2;
             char* y = reinterpret_cast<char*>(a.y) + (row0 * a.y_stride + col) * elem;
@@ -706,11 +694,11 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                             for (int j = 0; j < kLd; ++j, to += next) {
                                 if (c + j >= mine || !inside) continue;
                                 if (item.more) {
-                                    if (real) put_sum(to, v[j], ints, item.again);
-                                    if (real1) put_sum(to + kWRows * 4, u[j], ints, item.again);
+                                    if (real) put_sum(to, v[j], item.again);
+                                    if (real1) put_sum(to + kWRows * 4, u[j], item.again);
                                 } else {
-                                    if (real) v[j] = take_sum(to, v[j], ints);
-                                    if (real1) u[j] = take_sum(to + kWRows * 4, u[j], ints);
+                                    if (real) v[j] = take_sum(to, v[j]);
+                                    if (real1) u[j] = take_sum(to + kWRows * 4, u[j]);
                                 }
                             }
                             if (item.more) continue;
@@ -721,8 +709,8 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kLd; ++j)
                         if (c + j < mine && MR_IN_RANGE(half * cols + c + j, a.part_rows, 913)) {
-                            put_sum(part + (c + j) * 256, v[j], ints, item.again);
-                            put_sum(part + (c + j) * 256 + 128, u[j], ints, item.again);
+                            put_sum(part + (c + j) * 256, v[j], item.again);
+                            put_sum(part + (c + j) * 256 + 128, u[j], item.again);
                         }
                 }
                 if (!whole && !item.more) {
@@ -747,23 +735,21 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                         __threadfence();
 #pragma unroll 1
                         for (int c = 0; c < mine; c += kLd) {
-                            uint32_t v[kLd], u[kLd];
+                            float f[kLd], g[kLd];
 #pragma unroll
-                            for (int j = 0; j < kLd; ++j) v[j] = u[j] = 0u;
+                            for (int j = 0; j < kLd; ++j) f[j] = g[j] = 0.0f;
                             for (int b = item.first; b <= item.last; ++b) {
                                 const float* from_b = part_of(b) + c * 256;
 #pragma unroll
                                 for (int j = 0; j < kLd; ++j)
                                     if (c + j < mine) {
-                                        v[j] = sum_of_parts(v[j], __ldcg(from_b + j * 256), ints);
-                                        u[j] = sum_of_parts(u[j], __ldcg(from_b + j * 256 + 128), ints);
+                                        f[j] = __fadd_rn(f[j], __ldcg(from_b + j * 256));
+                                        g[j] = __fadd_rn(g[j], __ldcg(from_b + j * 256 + 128));
                                     }
                             }
-                            if (ints) {
+                            uint32_t v[kLd], u[kLd];
 #pragma unroll
-                                for (int j = 0; j < kLd; ++j)
-                                    v[j] = __float_as_uint(__int2float_rn((int)v[j])), u[j] = __float_as_uint(__int2float_rn((int)u[j]));
-                            }
+                            for (int j = 0; j < kLd; ++j) v[j] = __float_as_uint(f[j]), u[j] = __float_as_uint(g[j]);
                             finish(c, v, u);
                         }
                     }
@@ -802,6 +788,36 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                         continue;
                     }
                     if (several) {
+                        // where row c's sums are put together. (Found anew for each chunk: 4096 x 7168 int8 -> 4096 fp32 275
+                        // us, from an address held for the tile 447; one sum, which is not exact, 170.)
+                        auto home = [&](int c) {
+                            float* room = a.room + (((int64_t)first * C::kRows + half * cols + c) << 8) + (int)rank * kWRows +
+                                          quarter * 32 + lane;
+                            return wide ? y + c * y_step : reinterpret_cast<char*>(room);
+                        };
+                        if (item.more) {
+#pragma unroll 1
+                            for (int c = 0; c < mine; c += kLd) {
+                                uint32_t v[kLd];
+                                tmem_load(v, sums + c);
+                                tmem_ld_wait(v);
+                                if (c + kLd >= mine) hand_back();
+                                char* to = home(c);
+                                const int64_t next = wide ? y_step : 1024;
+                                const bool out = real && inside;
+                                if (out && item.again) {
+#pragma unroll
+                                    for (int j = 0; j < kLd; ++j, to += next)
+                                        if (c + j < mine) put_sum(to, v[j], true);
+                                } else if (out) {
+#pragma unroll
+                                    for (int j = 0; j < kLd; ++j, to += next)
+                                        if (c + j < mine) put_sum(to, v[j], false);
+                                }
+                                __syncwarp();
+                            }
+                            continue;
+                        }
                         constexpr int kFew = kLd / 2;  // (with kLd, whose earlier sums have registers, too, the kernel spills)
 #pragma unroll 1
                         for (int c = 0; c < mine; c += kFew) {
@@ -809,20 +825,13 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                             tmem_load(v, sums + c);
                             tmem_ld_wait(v);
                             if (c + kFew >= mine) hand_back();
-                            float* room = a.room + (((int64_t)first * C::kRows + half * cols + c) << 8) + (int)rank * kWRows +
-                                          quarter * 32 + lane;
-                            char* to = wide ? y + c * y_step : reinterpret_cast<char*>(room);
+                            char* to = home(c);
                             const int64_t next = wide ? y_step : 1024;
                             const bool out = real && inside;
-                            if (item.more) {
-#pragma unroll
-                                for (int j = 0; j < kFew; ++j, to += next)
-                                    if (out && c + j < mine) put_sum(to, v[j], ints, item.again);
-                                continue;
-                            }
 #pragma unroll
                             for (int j = 0; j < kFew; ++j, to += next)
-                                if (out && c + j < mine) v[j] = take_sum(to, v[j], ints);
+                                if (out && c + j < mine) v[j] = take_sum(to, v[j]);
+                            __syncwarp();
                             float f[kFew];
                             scaled(v, w_scale, c, f);
                             uint32_t w[kFew];
@@ -834,6 +843,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                                 if (wide) put(to, f[j], false);
                                 else *reinterpret_cast<uint16_t*>(to) = (uint16_t)w[j];
                             }
+                            __syncwarp();
                         }
                         continue;
                     }
@@ -1062,11 +1072,7 @@ mr_status run_product(const Product& p, Int8Args a, bool pair, cudaStream_t s) {
     const bool wide = a.y_dtype == MR_DTYPE_F32 && !p.swiglu;
     const int sums = ceil_div(p.K, wide ? 1024 : kMostSum);
     a.sum_loads = ceil_div(a.KB, sums);
-    // (2^17 products of int8 values reach 2^31)
-    a.sums = sums == 1                          ? kOneSum
-             : wide && !p.exact                 ? kScaledSums
-             : wide && p.K < (INT64_C(1) << 17) ? kIntSums
-                                                : kFloatSums;
+    a.sums = sums == 1 ? kOneSum : wide && !p.exact ? kScaledSums : kPlainSums;
     const int64_t tiles = most_tiles(a.rows, a.G, a.N, pair, p.swiglu);
     CUtensorMap m[2];
     const bool eight = p.xt == kInt8;
