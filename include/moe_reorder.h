@@ -678,7 +678,8 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
  *                 matrix} byte strides, nullable (contiguous).
  *   weightScales  float32 [experts, outCols].
  *   numRows       device int64 [1], nullable: the rows in use (the batching's
- *                 actualTokenNum), so that no others are converted.
+ *                 actualTokenNum), so that no others are converted. Rows of y at or
+ *                 past it that a group covers all the same may hold anything.
  *   groupList, numGroups, expertBase, y and the limits are moe_grouped_matmul's.
  *   x and weights start on 16 bytes and have row strides that are multiples of 16
  *   bytes, as 8-bit operands of the other expert products; a length that is not is

@@ -6,7 +6,8 @@
 //
 // The tensor cores of sm_103a have no 8-bit integer products. An int8 value is
 // exact in f16 and in bf16, a product of two in the fp32 accumulators, and so is a
-// sum while it stays below 2^24. So the products run at the 16-bit rate, and the
+// sum while it stays below 2^24 (where results are fp32, or rows long, several sums make
+// a value, see Int8Args). So the products run at the 16-bit rate, and the
 // weights, which are the bulk of what is read, become 16 bits on their way to the
 // tensor cores: W is the operand with 128 rows (A), and its values go from shared
 // memory through registers to tensor memory, which costs shared memory neither the
@@ -27,7 +28,7 @@
 // workspace, and the last one to arrive adds them up, in the order of k.
 //
 // What bounds it: with many rows the tensor cores and the power limit (4096 x 7168 ->
-// 4096: tensor pipe active 71 % of 143 us; 16384 x 7168 -> 7168 takes 780 us, 2.16
+// 4096: tensor pipe active 71 % of 142 us; 16384 x 7168 -> 7168 takes 780 us, 2.16
 // PFLOP/s, beside 53 to make the rows f16). With few rows per group the weights' way
 // from HBM, and how long a load keeps its room: 576 rows over 64 experts, 7168 ->
 // 4096, 298 us, 0.95 of the copy rate; a load of 32 KB takes a block's
@@ -953,7 +954,7 @@ __global__ void __launch_bounds__(256)
     q[1] = b;
 }
 
-// Tickets to 0. (1 row, 4096 -> 2048: 14.9 us on the GPU, with a memset in front of the product 18.5.)
+// Tickets to 0. (1 row, 4096 -> 2048: 14.8 us on the GPU, with a memset in front of the product 18.5.)
 __global__ void __launch_bounds__(256) clear_kernel(uint4* tickets, int n) {
     pdl_enter();
     for (int i = threadIdx.x; i < n; i += 256) tickets[i] = make_uint4(0u, 0u, 0u, 0u);

@@ -8,7 +8,8 @@
 //
 // A row's values stay in registers (32 a thread, fewer of short rows and of fp32 ones; a warp, 128,
 // 256 or 512 threads a row) from the load to the stores, so x and residual are read once. Rows of more
-// than 16384 values (8192 in fp32) are read once more for each of the two sweeps that follow.
+// than 16384 values (8192 of fp32 rows' norm) are read once more for every sweep that follows the first: the
+// norm's sum is one, int8's maximum another, the stores the last.
 //
 // The mean of squares is kept in two fp32 numbers (two-sum steps, the squares'
 // own rounding errors included), so that r is the correctly rounded value but for
@@ -172,12 +173,13 @@ __device__ __forceinline__ uint32_t int8x4(const float* v, float inv) {
 
 // TPR threads a row (32: eight rows a block), PER values each in pieces of 16 bytes TPR
 // pieces apart. LONG: rows of more than PER TPR values. Blocks of as few registers as
-// let an SM hold 1280 threads, 1024 with the norm or of fp32 rows
-// (the norm of 16384 x 7168 bf16 rows: 191 us, with 768 threads 214, and with 1280, where it spills, 198;
-// 65536 x 4096 bf16 rows to int8 132 us, 144 with 1024). Persistent blocks whose next
+// let an SM hold 1280 threads, 1024 with the norm or of fp32 rows: threads in flight are worth a few spilled
+// words, but not many. (The norm of 16384 x 7168 bf16 rows with residual, bf16 and e4m3 results: 191 us, 64 registers
+// that spill 80 bytes; with 768 threads, 80 registers and no spills, 207; with 1280, 48 registers and 360 bytes, 249. The
+// same of fp32 rows: 410, with 768 threads 630. 65536 x 4096 bf16 rows to int8: 132, 48 registers that spill 20 bytes;
+// with 1024 threads and no spills 142.) Persistent blocks whose next
 // row comes to shared memory meanwhile were slower (251 and 146), and so were 16 values
-// a thread (219 and 181); fp32 rows' norm has 16 (16384 x 7168: 415 us, with 32 847),
-// alone they have 32.
+// a thread (219 and 181); fp32 rows' norm has 16 (with 32 847 us instead of 415), alone they have 32.
 template <int DT, int TPR, int PER, bool NORM, bool LOOSE, bool LONG>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
                                   (NORM || DT == MR_DTYPE_F32 ? 1024 : 1280) / (TPR == 32 ? 256 : TPR))
