@@ -59,10 +59,9 @@ def test_lengths_next_to_the_border(usc, rows, K, x_dtype):
 
 
 @pytest.mark.parametrize("x_dtype", [I8, F16, BF16])
-@pytest.mark.parametrize("rows", [3, 40])
-def test_the_networks_first_product(usc, rows, x_dtype):
+@pytest.mark.parametrize("rows,H,inter", [(3, 1 << 20, 70), (40, 1 << 20, 70), (3000, 16500, 700)])
+def test_the_networks_first_product(usc, rows, H, inter, x_dtype):
     """g, u > 0 and w2 > 0: what a sum loses is lost by every h and by y."""
-    H, inter = 1 << 20, 70
     x, xs = rows_of(rows, H, x_dtype, 5)
     w13 = one_sign((1, 2, inter, H), 6)
     s13 = scales((1, 2, inter), 7) / (64.0 * H) / (114.0 if x_dtype == I8 else 1.0)
@@ -76,7 +75,23 @@ def test_the_networks_first_product(usc, rows, x_dtype):
     dh = (1.1 * SUM * g / (g * torch.sigmoid(g)) + SUM + (16 + g) * 2.0**-23) * (1 + SUM) * h + 2.0**-8 * h
     wd = w2[0].double() * s2[0].double()[:, None]
     want, bound = h @ wd.T, dh @ wd.T
-    assert ((y - want).abs() <= bound * (1 + 1e-3) + want * (2.0**-11 + 80 * 2.0**-23)).all()
+    assert ((y - want).abs() <= bound * (1 + 1e-3) + want * (2.0**-11 + (inter + 10) * 2.0**-23)).all()
+
+
+@pytest.mark.parametrize("out", [F16, BF16])
+@pytest.mark.parametrize("rows,groups,N", [(600, 3, 7000), (300, 100, 700)])
+def test_several_tiles_for_each_block(usc, rows, groups, N, out):
+    """Pairs, single blocks: signs differ, no sum on the way leaves 24 bits, so that the bits are the integers'."""
+    K = 16500
+    x, w = one_sign((rows, K), 1, -127, 128), one_sign((2, N, K), 2, -127, 128)
+    xs, ws = scales((rows,), 3) / 4096.0, scales((2, N), 4) / 4096.0
+    lists = torch.tensor([[i % 2, rows // groups] for i in range(groups)])
+    sums = exact_sums(x, w, lists)
+    assert sums.abs().max() < 2**23
+    want = (sums.float() * ws[lists[:, 0].repeat_interleave(lists[:, 1]).cuda()] * xs[:, None]).to(out)
+    for _ in range(3):
+        y = usc.moe_grouped_matmul_int8(x, w, ws, lists.cuda(), x_scales=xs, out_dtype=out)["y"]
+        assert torch.equal(y, want)
 
 
 @pytest.mark.parametrize("rows", [3, 100])

@@ -65,7 +65,9 @@ struct Int8Args : Groups {
     // 2^24 (1024 values), of 7168 by 1.2e-5. Where the result is fp32, or rows are long, a tile is taken in several sums,
     // as `sums` says.
     int sum_loads, sums;
-    float* room;            // 16-bit results of several sums: a block's (pair's) tile of 256 sums to a row
+    // 16-bit results of several sums: kRows rows of 256 sums for each block (pair), of which a thread has the same words for
+    // every tile, so that no tile's sums wait for another warp's
+    float* room;
     // equal shares of the loads (NULL: whole tiles round robin)
     float* parts;           // two to a block, of part_rows rows of 256 sums
     int part_rows, part_loads;  // a share is this many loads at least
@@ -687,8 +689,8 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                     if (c + kLd >= mine) hand_back();  // everything is in registers
                     if (whole) {
                         if (several) {
-                            float* room = a.parts ? part : a.room + (((int64_t)item.block * C::kRows + half * cols) << 8) +
-                                                               quarter * 32 + lane;
+                            // (no whole tile is among those that blocks share: a share is at most 9 of 17 of a tile's loads)
+                            float* room = a.room + (((int64_t)item.block * C::kRows + half * C::kHalf) << 8) + quarter * 32 + lane;
                             char* to = wide ? y + c * y_step : reinterpret_cast<char*>(room + c * 256);
                             const int64_t next = wide ? y_step : 1024;
 #pragma unroll
@@ -792,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<XT, SWIGLU, PAIR>::kThreads, 1)
                         // where row c's sums are put together. (Found anew for each chunk: 4096 x 7168 int8 -> 4096 fp32 275
                         // us, from an address held for the tile 447; one sum, which is not exact, 170.)
                         auto home = [&](int c) {
-                            float* room = a.room + (((int64_t)first * C::kRows + half * cols + c) << 8) + (int)rank * kWRows +
+                            float* room = a.room + (((int64_t)first * C::kRows + half * C::kHalf + c) << 8) + (int)rank * kWRows +
                                           quarter * 32 + lane;
                             return wide ? y + c * y_step : reinterpret_cast<char*>(room);
                         };
