@@ -666,9 +666,10 @@ mr_status moe_expert_ffn(const void* x, int32_t xDtype, int64_t xStride, const f
  *   An F32 result of int8 rows is that of exact sums of at most 1024 values, which
  *   are added in fp32 in a fixed order. With 16-bit rows of more than 1024 values an
  *   F32 result is the sum of the results of equal parts of at most 1024 values, in
- *   their order; one of those below 2^-126 may count as 0. A 16-bit
- *   result takes at most 16384 values into one sum of the tensor cores (which cut
- *   1e-4 of as many values of one sign), and adds such sums in fp32.
+ *   their order; one of those below 2^-126 may count as 0, and one past fp32's range
+ *   is an infinity. A 16-bit result takes at most 16384 values into one sum of the
+ *   tensor cores (which cut 1e-4 of as many values of one sign), and adds such sums
+ *   in fp32.
  *
  *   x             [rows, cols] of xDtype: INT8 with xScales (the batching's y and
  *                 dynamicScale, or moe_quantize_int8's), or F16 or BF16, whose
